@@ -72,8 +72,11 @@ typedef enum {
   FLCE_ERR_LABEL = 4,        /* (err_word only) label outside [0, V)        */
   FLCE_ERR_TIMEOUT = 5,      /* (err_word only) a bounded device wait expired */
   FLCE_ERR_CUDA = 6,         /* a CUDA runtime/driver call failed           */
-  FLCE_ERR_BOUNDS = 7        /* (err_word only, debug build) an index check
+  FLCE_ERR_BOUNDS = 7,       /* (err_word only, debug build) an index check
                                 failed; the access was skipped              */
+  FLCE_ERR_INDEX = 8         /* (err_word only) sequence offsets that do not
+                                ascend within [0, tokens], or a position
+                                outside the rotation tables                 */
 } flce_status;
 
 typedef enum { FLCE_BF16 = 0, FLCE_FP32 = 1 } flce_dtype;
@@ -320,14 +323,103 @@ flce_status flce_backward_vocab_shard(const void* X, const void* W_shard, const 
                                       float* dW_shard, int accumulate_dW, void* workspace,
                                       size_t ws_bytes, int32_t* err_word, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention of the packed batch whose loss the calls above compute.  The
+ * conventions at the top hold here too: device pointers, the caller's memory,
+ * asynchronous on `stream`, argument errors returned, data errors in
+ * *err_word.  A head's head_dim values are contiguous; rows (tokens) and heads
+ * may lie any multiple of 8 elements apart, so q, k and v can be views of one
+ * fused projection.  Pointers to heads, weights and tables are 16-byte
+ * aligned.  Results do not change from run to run (no atomics).
+ * ------------------------------------------------------------------------ */
+
+/* RMS norm of every query and key head and the rotary position rotation of the
+ * result, in one pass:
+ *   n = x / sqrt(mean(x^2) + eps),  y = R(position) (weight * n)
+ * R turns each pair of the first rot_dim values by the angle whose cosine and
+ * sine stand in the tables (float, table_rows x rot_dim/2): the pairs are
+ * (j, j + rot_dim/2), or (2j, 2j + 1) when interleaved.  The other values are
+ * normed only. */
+typedef struct {
+  size_t struct_size;            /* sizeof(flce_qk_norm_rope_desc) */
+  int64_t tokens, q_heads, kv_heads;
+  int64_t head_dim;              /* a multiple of 8, at most 256 */
+  int64_t rot_dim;               /* a multiple of 8, 0 to head_dim */
+  int64_t table_rows;            /* rows of the cosine and sine tables */
+  flce_dtype dtype;              /* of q, k, the weights and the outputs */
+  float eps;
+  int interleaved;
+  int64_t q_row, q_head, k_row, k_head;  /* strides of q and k in elements */
+} flce_qk_norm_rope_desc;
+
+/* q_out and k_out are contiguous (tokens x heads x head_dim).  A weight of
+ * NULL counts as ones; positions (int64, one per token) of NULL as 0, 1, 2...
+ * A token whose position lies outside the tables is left unrotated and reported
+ * as FLCE_ERR_INDEX. */
+flce_status flce_qk_norm_rope_forward(const flce_qk_norm_rope_desc* desc, const void* q,
+                                      const void* k, const void* q_weight, const void* k_weight,
+                                      const float* cos_table, const float* sin_table,
+                                      const int64_t* positions, void* q_out, void* k_out,
+                                      int32_t* err_word, void* stream);
+
+/* Gradients of q, k (contiguous, dtype) and of both weights (float, head_dim,
+ * summed over tokens and heads; zero when tokens = 0), from the gradients of
+ * the outputs (contiguous) and the forward's inputs.  workspace: 256-byte aligned,
+ * flce_qk_norm_rope_workspace_size bytes (0 on an invalid desc), sized for the
+ * current device. */
+size_t flce_qk_norm_rope_workspace_size(const flce_qk_norm_rope_desc* desc);
+flce_status flce_qk_norm_rope_backward(const flce_qk_norm_rope_desc* desc, const void* dq_out,
+                                       const void* dk_out, const void* q, const void* k,
+                                       const void* q_weight, const void* k_weight,
+                                       const float* cos_table, const float* sin_table,
+                                       const int64_t* positions, void* dq, void* dk,
+                                       float* dq_weight, float* dk_weight, void* workspace,
+                                       size_t ws_bytes, int32_t* err_word, void* stream);
+
+/* Causal softmax attention within each packed sequence, query head h reading
+ * key / value head h / (q_heads / kv_heads):
+ *   s_ij = scale q_i . k_j  for j <= i in the same sequence
+ *   lse_i = log sum_j exp(s_ij),  out_i = sum_j exp(s_ij - lse_i) v_j
+ * cu_seqlens (device int32, sequences + 1) holds the sequences' offsets in the
+ * pack, ascending within [0, tokens]; sequences may be empty.  Rows outside
+ * [cu_seqlens[0], cu_seqlens[sequences]) belong to none: their out is 0, their
+ * lse -infinity, their gradients 0, and what they hold is not used.  Offsets
+ * that do not ascend are reported as FLCE_ERR_INDEX and every row then counts
+ * as belonging to none. */
+typedef struct {
+  size_t struct_size;            /* sizeof(flce_attention_desc) */
+  int64_t tokens, sequences;
+  int64_t q_heads, kv_heads;     /* q_heads a multiple of kv_heads */
+  int64_t head_dim;              /* a multiple of 8, at most 128 */
+  flce_dtype dtype;              /* FLCE_BF16 */
+  float scale;                   /* positive */
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head;  /* strides in elements */
+} flce_attention_desc;
+
+/* out: contiguous tokens x q_heads x head_dim; lse: float, q_heads x tokens. */
+flce_status flce_attention_forward(const flce_attention_desc* desc, const void* q, const void* k,
+                                   const void* v, const int32_t* cu_seqlens, void* out,
+                                   float* lse, int32_t* err_word, void* stream);
+
+/* Gradients of q, k and v (contiguous, dtype; those of a key / value head are
+ * summed over its query heads) from dout (contiguous) and the forward's inputs
+ * and results.  workspace: 256-byte aligned, flce_attention_workspace_size
+ * bytes (0 on an invalid desc). */
+size_t flce_attention_workspace_size(const flce_attention_desc* desc);
+flce_status flce_attention_backward(const flce_attention_desc* desc, const void* dout,
+                                    const void* q, const void* k, const void* v, const void* out,
+                                    const float* lse, const int32_t* cu_seqlens, void* dq,
+                                    void* dk, void* dv, void* workspace, size_t ws_bytes,
+                                    int32_t* err_word, void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* flce_status_string(flce_status s);
 
 /* Text of the last CUDA error this thread saw inside the library ("" if none). */
 const char* flce_last_cuda_error(void);
 
-/* Number of kernels the last flce_forward / flce_backward / flce_fwd_bwd call
- * on this thread enqueued. */
+/* Number of kernels the last forward or backward call on this thread (of the
+ * loss, the attention or the head norm) enqueued. */
 int flce_last_launch_count(void);
 
 /* Optional per-kernel timing.  While enabled (per host thread), every GEMM

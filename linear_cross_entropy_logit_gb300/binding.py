@@ -6,6 +6,7 @@ library is missing, ``lib()`` raises instead of falling back to anything.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -26,6 +27,7 @@ FLCE_ERR_LABEL = 4
 FLCE_ERR_TIMEOUT = 5
 FLCE_ERR_CUDA = 6
 FLCE_ERR_BOUNDS = 7
+FLCE_ERR_INDEX = 8
 
 FLCE_BF16 = 0
 FLCE_FP32 = 1
@@ -46,6 +48,8 @@ EXPORTED = (
     "flce_debug_wait_timeout", "flce_set_backward_merge", "flce_backward_merge",
     "flce_workspace_size_ex", "flce_vocab_chunk_ex", "flce_set_cluster_multicast",
     "flce_cluster_multicast", "flce_debug_last_multicast_launches",
+    "flce_qk_norm_rope_forward", "flce_qk_norm_rope_workspace_size", "flce_qk_norm_rope_backward",
+    "flce_attention_forward", "flce_attention_workspace_size", "flce_attention_backward",
 )
 
 PROFILE_KINDS = ("fwd_logits_lse", "bwd_dz_recompute", "bwd_dw_gemm", "bwd_dx_gemm",
@@ -63,6 +67,28 @@ class FlceOptions(ctypes.Structure):
                 ("cta_pair", ctypes.c_int), ("backward_merge", ctypes.c_int),
                 ("l2_hints", ctypes.c_int), ("vocab_chunk", ctypes.c_int64),
                 ("cluster_multicast", ctypes.c_int)]
+
+
+class FlceQkNormRopeDesc(ctypes.Structure):
+    """Mirror of ``flce_qk_norm_rope_desc`` in include/flce.h."""
+    _fields_ = [("struct_size", ctypes.c_size_t), ("tokens", ctypes.c_int64),
+                ("q_heads", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("rot_dim", ctypes.c_int64),
+                ("table_rows", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("interleaved", ctypes.c_int),
+                ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("k_row", ctypes.c_int64), ("k_head", ctypes.c_int64)]
+
+
+class FlceAttentionDesc(ctypes.Structure):
+    """Mirror of ``flce_attention_desc`` in include/flce.h."""
+    _fields_ = [("struct_size", ctypes.c_size_t), ("tokens", ctypes.c_int64),
+                ("sequences", ctypes.c_int64), ("q_heads", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("scale", ctypes.c_float),
+                ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("k_row", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("v_row", ctypes.c_int64), ("v_head", ctypes.c_int64)]
 
 
 class FlceError(RuntimeError):
@@ -176,6 +202,19 @@ def load(path: str) -> ctypes.CDLL:
     L.flce_cluster_multicast.restype = I32
     L.flce_debug_last_multicast_launches.argtypes = []
     L.flce_debug_last_multicast_launches.restype = I32
+    QD, AD = ctypes.POINTER(FlceQkNormRopeDesc), ctypes.POINTER(FlceAttentionDesc)
+    L.flce_qk_norm_rope_forward.argtypes = [QD, P, P, P, P, P, P, P, P, P, P, P]
+    L.flce_qk_norm_rope_forward.restype = I32
+    L.flce_qk_norm_rope_workspace_size.argtypes = [QD]
+    L.flce_qk_norm_rope_workspace_size.restype = SZ
+    L.flce_qk_norm_rope_backward.argtypes = [QD, P, P, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P, P]
+    L.flce_qk_norm_rope_backward.restype = I32
+    L.flce_attention_forward.argtypes = [AD, P, P, P, P, P, P, P, P]
+    L.flce_attention_forward.restype = I32
+    L.flce_attention_workspace_size.argtypes = [AD]
+    L.flce_attention_workspace_size.restype = SZ
+    L.flce_attention_backward.argtypes = [AD, P, P, P, P, P, P, P, P, P, P, P, SZ, P, P]
+    L.flce_attention_backward.restype = I32
     return L
 
 
@@ -567,6 +606,185 @@ def flce_forward_noalloc(X, W, labels, ignore_index: int = -100, smoothing: floa
     return loss, lse, valid_count, err_word
 
 
+def _on_stream(stream):
+    """Context in which new tensors belong to the stream the call runs on, so
+    the allocator does not hand their memory to another stream's work too early."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _heads(name, t, like=None):
+    """(row stride, head stride) of a [tokens, heads, head_dim] CUDA tensor whose
+    heads are contiguous; any number of tokens or heads may be 1."""
+    if not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, head_dim], got "
+                         f"{tuple(t.shape)} on {t.device}")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise TypeError(f"{name} must have the dtype and device of q: {t.dtype} on {t.device}")
+    T, H, D = t.shape
+    row, head, one = t.stride()
+    if D > 1 and one != 1:
+        raise ValueError(f"{name}: the head_dim values of a head must be contiguous")
+    return (row if T > 1 else H * D), (head if H > 1 else D)
+
+
+def _result(name, t, shape, dtype, device):
+    """An output buffer: the caller's (checked), or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.shape != torch.Size(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
+    return t
+
+
+def _operand(name, t, shape, dtype, device):
+    """A contiguous input of the given shape and type."""
+    if t.shape != torch.Size(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _workspace_bytes(buf, need: int, device):
+    """The caller's workspace, or a new one of the required size."""
+    return torch.empty(max(need, 256), dtype=torch.uint8, device=device) if buf is None else buf
+
+
+def _qk_norm_rope_desc(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+    q_row, q_head = _heads("q", q)
+    k_row, k_head = _heads("k", k, q)
+    T, HQ, D = q.shape
+    if k.shape[0] != T or k.shape[2] != D:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _operand(name, w, (D,), q.dtype, q.device)
+    rows = half = 0
+    if cos is not None or sin is not None:
+        if cos is None or sin is None or cos.dim() != 2:
+            raise ValueError("cos and sin must both be [positions, rot_dim / 2] tensors, or None")
+        rows, half = cos.shape
+        _operand("cos", cos, (rows, half), torch.float32, q.device)
+        _operand("sin", sin, (rows, half), torch.float32, q.device)
+    if positions is not None:
+        _operand("positions", positions, (T,), torch.int64, q.device)
+    return FlceQkNormRopeDesc(ctypes.sizeof(FlceQkNormRopeDesc), T, HQ, k.shape[1], D, 2 * half,
+                              rows, _dtype_code(q), eps, int(bool(interleaved)), q_row, q_head,
+                              k_row, k_head)
+
+
+def flce_qk_norm_rope_forward(q, k, q_weight, k_weight, cos, sin, positions=None,
+                              eps: float = 1e-6, *, interleaved: bool = False, q_out=None,
+                              k_out=None, err_word=None, stream=None):
+    """RMS norm of each head of q [T, Hq, D] and k [T, Hk, D], weighted and turned
+    to its position in one pass.  Returns (q_out, k_out, err_word), contiguous.
+
+    cos, sin: float32 [positions, rot_dim / 2], or None for no rotation; the
+    first rot_dim values of a head are turned, in pairs (j, j + rot_dim / 2), or
+    (2j, 2j + 1) when interleaved.  positions: int64 [T] or None (0, 1, 2, ...)."""
+    d = _qk_norm_rope_desc(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    with _on_stream(stream):
+        q_out = _result("q_out", q_out, q.shape, q.dtype, q.device)
+        k_out = _result("k_out", k_out, k.shape, q.dtype, q.device)
+        err_word = new_err_word(q.device) if err_word is None else err_word
+        st = lib().flce_qk_norm_rope_forward(
+            ctypes.byref(d), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(cos),
+            _ptr(sin), _ptr(positions), _ptr(q_out), _ptr(k_out), _ptr(err_word), _stream(stream))
+    _check(st, "flce_qk_norm_rope_forward")
+    return q_out, k_out, err_word
+
+
+def flce_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, positions=None,
+                               eps: float = 1e-6, *, interleaved: bool = False, dq=None, dk=None,
+                               dq_weight=None, dk_weight=None, workspace_buf=None, err_word=None,
+                               stream=None):
+    """Gradients of flce_qk_norm_rope_forward: (dq, dk in q's dtype, dq_weight,
+    dk_weight float32 [D], err_word)."""
+    d = _qk_norm_rope_desc(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    dev = q.device
+    _operand("dq_out", dq_out, q.shape, q.dtype, dev)
+    _operand("dk_out", dk_out, k.shape, q.dtype, dev)
+    with _on_stream(stream):
+        dq = _result("dq", dq, q.shape, q.dtype, dev)
+        dk = _result("dk", dk, k.shape, q.dtype, dev)
+        dq_weight = _result("dq_weight", dq_weight, (q.shape[2],), torch.float32, dev)
+        dk_weight = _result("dk_weight", dk_weight, (q.shape[2],), torch.float32, dev)
+        ws = _workspace_bytes(workspace_buf,
+                              lib().flce_qk_norm_rope_workspace_size(ctypes.byref(d)), dev)
+        err_word = new_err_word(dev) if err_word is None else err_word
+        st = lib().flce_qk_norm_rope_backward(
+            ctypes.byref(d), _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight),
+            _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions), _ptr(dq), _ptr(dk),
+            _ptr(dq_weight), _ptr(dk_weight), _ptr(ws), ws.numel(), _ptr(err_word),
+            _stream(stream))
+    _check(st, "flce_qk_norm_rope_backward")
+    return dq, dk, dq_weight, dk_weight, err_word
+
+
+def _attention_desc(q, k, v, cu_seqlens, scale):
+    q_row, q_head = _heads("q", q)
+    k_row, k_head = _heads("k", k, q)
+    v_row, v_head = _heads("v", v, q)
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"attention takes bfloat16 q, k and v, got {q.dtype}")
+    T, HQ, D = q.shape
+    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold the sequences' offsets, one more than sequences")
+    _operand("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, q.device)
+    scale = D ** -0.5 if scale is None else scale
+    return FlceAttentionDesc(ctypes.sizeof(FlceAttentionDesc), T, cu_seqlens.numel() - 1, HQ,
+                             k.shape[1], D, FLCE_BF16, scale, q_row, q_head, k_row, k_head, v_row,
+                             v_head)
+
+
+def flce_attention_forward(q, k, v, cu_seqlens, scale: Optional[float] = None, *, out=None,
+                           lse=None, err_word=None, stream=None):
+    """Causal attention within each packed sequence: q [T, Hq, D], k and v
+    [T, Hk, D] bf16 (views are fine), cu_seqlens int32 offsets.  Returns
+    (out [T, Hq, D] bf16, lse [Hq, T] float32, err_word); scale defaults to
+    D ** -0.5.  Rows outside the sequences get out 0 and lse -inf."""
+    d = _attention_desc(q, k, v, cu_seqlens, scale)
+    with _on_stream(stream):
+        out = _result("out", out, q.shape, q.dtype, q.device)
+        lse = _result("lse", lse, (q.shape[1], q.shape[0]), torch.float32, q.device)
+        err_word = new_err_word(q.device) if err_word is None else err_word
+        st = lib().flce_attention_forward(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v),
+                                          _ptr(cu_seqlens), _ptr(out), _ptr(lse), _ptr(err_word),
+                                          _stream(stream))
+    _check(st, "flce_attention_forward")
+    return out, lse, err_word
+
+
+def flce_attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale: Optional[float] = None, *,
+                            dq=None, dk=None, dv=None, workspace_buf=None, err_word=None,
+                            stream=None):
+    """Gradients (dq, dk, dv, err_word) of flce_attention_forward, contiguous bf16;
+    those of a key / value head are summed over the query heads that read it."""
+    d = _attention_desc(q, k, v, cu_seqlens, scale)
+    dev = q.device
+    _operand("dout", dout, q.shape, q.dtype, dev)
+    _operand("out", out, q.shape, q.dtype, dev)
+    _operand("lse", lse, (q.shape[1], q.shape[0]), torch.float32, dev)
+    with _on_stream(stream):
+        dq = _result("dq", dq, q.shape, q.dtype, dev)
+        dk = _result("dk", dk, k.shape, q.dtype, dev)
+        dv = _result("dv", dv, v.shape, q.dtype, dev)
+        ws = _workspace_bytes(workspace_buf,
+                              lib().flce_attention_workspace_size(ctypes.byref(d)), dev)
+        err_word = new_err_word(dev) if err_word is None else err_word
+        st = lib().flce_attention_backward(ctypes.byref(d), _ptr(dout), _ptr(q), _ptr(k), _ptr(v),
+                                           _ptr(out), _ptr(lse), _ptr(cu_seqlens), _ptr(dq),
+                                           _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(),
+                                           _ptr(err_word), _stream(stream))
+    _check(st, "flce_attention_backward")
+    return dq, dk, dv, err_word
+
+
 def last_launch_count() -> int:
     return int(lib().flce_last_launch_count())
 
@@ -621,3 +839,50 @@ def linear_cross_entropy(h, W, labels, ignore_index: int = -100, smoothing: floa
     return _LinearCrossEntropy.apply(h.reshape(-1, H).contiguous(), W.contiguous(),
                                      labels.reshape(-1).contiguous(), ignore_index, smoothing,
                                      reduction, z_loss)
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+        q_out, k_out, err = flce_qk_norm_rope_forward(q, k, q_weight, k_weight, cos, sin,
+                                                      positions, eps, interleaved=interleaved)
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions, err)
+        ctx.cfg = (eps, interleaved)
+        return q_out, k_out
+
+    @staticmethod
+    def backward(ctx, gq, gk):
+        q, k, wq, wk, cos, sin, positions, err = ctx.saved_tensors
+        eps, interleaved = ctx.cfg
+        dq, dk, dwq, dwk, _ = flce_qk_norm_rope_backward(
+            gq.contiguous(), gk.contiguous(), q, k, wq, wk, cos, sin, positions, eps,
+            interleaved=interleaved, err_word=err)
+        return (dq, dk, None if wq is None else dwq.to(wq.dtype),
+                None if wk is None else dwk.to(wk.dtype), None, None, None, None, None)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps: float = 1e-6,
+                 interleaved: bool = False):
+    """Autograd entry of flce_qk_norm_rope_forward: (q_out, k_out)."""
+    return _QkNormRope.apply(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+
+
+class _PackedAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens, scale):
+        out, lse, err = flce_attention_forward(q, k, v, cu_seqlens, scale)
+        ctx.save_for_backward(q, k, v, out, lse, cu_seqlens, err)
+        ctx.scale = scale
+        return out
+
+    @staticmethod
+    def backward(ctx, g):
+        q, k, v, out, lse, cu_seqlens, err = ctx.saved_tensors
+        dq, dk, dv, _ = flce_attention_backward(g.contiguous(), q, k, v, out, lse, cu_seqlens,
+                                                ctx.scale, err_word=err)
+        return dq, dk, dv, None, None
+
+
+def packed_attention(q, k, v, cu_seqlens, scale: Optional[float] = None):
+    """Autograd entry of flce_attention_forward: out [T, Hq, D]."""
+    return _PackedAttention.apply(q, k, v, cu_seqlens, scale)

@@ -27,7 +27,7 @@ LIBDIR = os.path.join(PKG, "_lib")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(LIBDIR, "libflce.so")
 DEBUG_LIB = os.path.join(LIBDIR, "libflce_debug.so")
-SOURCES = ["flce_api.cu", "flce_noalloc.cu"]
+SOURCES = ["flce_api.cu", "flce_noalloc.cu", "flce_attn.cu", "flce_qk_norm_rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # (library, extra nvcc flags)
 TARGETS = [(LIB, []), (DEBUG_LIB, ["-DFLCE_DEBUG"])]

@@ -36,6 +36,7 @@
 #include "aux_kernels.cuh"
 #include "bwd_fused.cuh"
 #include "gemm_core.cuh"
+#include "host_util.h"
 #include "ptx.cuh"
 
 using namespace flce;
@@ -1135,6 +1136,8 @@ const char* flce_status_string(flce_status s) {
     case FLCE_ERR_TIMEOUT: return "FLCE_ERR_TIMEOUT: a bounded device wait expired";
     case FLCE_ERR_CUDA: return "FLCE_ERR_CUDA: CUDA call failed";
     case FLCE_ERR_BOUNDS: return "FLCE_ERR_BOUNDS: an index check of the debug build failed";
+    case FLCE_ERR_INDEX:
+      return "FLCE_ERR_INDEX: sequence offsets not ascending or a position outside its table";
   }
   return "unknown flce_status";
 }
@@ -1307,6 +1310,22 @@ flce_options defaults(int64_t ignore_index, float smoothing, flce_reduction redu
 }
 
 }  // namespace
+
+namespace flce {
+namespace host {
+
+flce_status device(int* dev, int* sms) { return device_check(dev, sms); }
+flce_status fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+flce_status fail_text(const char* what) {
+  g_last_cuda_error = what;
+  return FLCE_ERR_CUDA;
+}
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() { return ::encode_fn(); }
+void reset_launches() { g_launches = 0; }
+void count_launch() { ++g_launches; }
+
+}  // namespace host
+}  // namespace flce
 
 extern "C" {
 

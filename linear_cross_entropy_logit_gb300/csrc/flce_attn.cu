@@ -1,0 +1,130 @@
+// C ABI of causal attention over packed sequences: argument checks, the
+// workspace plan and the launches.
+#include <climits>
+#include <cmath>
+
+#include "attn_simple.cuh"
+#include "host_util.h"
+
+using namespace flce;
+using host::aligned;
+
+namespace {
+
+bool shape_ok(const flce_attention_desc* d) {
+  if (!d || d->struct_size != sizeof(flce_attention_desc)) return false;
+  if (d->tokens < 0 || d->tokens > (int64_t)INT_MAX - 1024) return false;
+  if (d->sequences < 0 || d->sequences > (int64_t)INT_MAX - 1024) return false;
+  if (d->kv_heads <= 0 || d->q_heads <= 0 || d->q_heads % d->kv_heads) return false;
+  if (d->q_heads > 65535) return false;
+  if (d->head_dim <= 0 || d->head_dim % 8 || d->head_dim > 128) return false;
+  return true;
+}
+
+bool stride_ok(int64_t row, int64_t head, int64_t head_dim) {
+  return row % 8 == 0 && head % 8 == 0 && row > 0 && head >= head_dim && row < (1ll << 38) &&
+         head < (1ll << 38);
+}
+
+flce_status check(const flce_attention_desc* d, const void* const* ptrs, int n, const void* cu,
+                  const float* lse, const int32_t* err_word) {
+  if (!shape_ok(d)) return FLCE_ERR_ARG;
+  if (d->dtype != FLCE_BF16) return d->dtype == FLCE_FP32 ? FLCE_ERR_UNSUPPORTED : FLCE_ERR_ARG;
+  if (!(std::isfinite(d->scale) && d->scale > 0.f)) return FLCE_ERR_ARG;
+  if (!stride_ok(d->q_row, d->q_head, d->head_dim) ||
+      !stride_ok(d->k_row, d->k_head, d->head_dim) ||
+      !stride_ok(d->v_row, d->v_head, d->head_dim))
+    return FLCE_ERR_ARG;
+  if (!err_word || !aligned(err_word, 4) || !cu || !aligned(cu, 4)) return FLCE_ERR_ARG;
+  if (d->tokens == 0) return FLCE_OK;
+  if (!lse || !aligned(lse, 4)) return FLCE_ERR_ARG;
+  for (int i = 0; i < n; ++i)
+    if (!ptrs[i] || !aligned(ptrs[i], 16)) return FLCE_ERR_ARG;
+  return FLCE_OK;
+}
+
+AttnParams params(const flce_attention_desc* d, const int32_t* cu, int32_t* err_word) {
+  AttnParams p{};
+  p.cu = cu;
+  p.n_seqs = (int)d->sequences;
+  p.tokens = (int)d->tokens;
+  p.q_heads = (int)d->q_heads;
+  p.kv_heads = (int)d->kv_heads;
+  p.group = p.q_heads / p.kv_heads;
+  p.head_dim = (int)d->head_dim;
+  p.scale = d->scale;
+  p.q_row = d->q_row;
+  p.q_head = d->q_head;
+  p.k_row = d->k_row;
+  p.k_head = d->k_head;
+  p.v_row = d->v_row;
+  p.v_head = d->v_head;
+  p.err_word = err_word;
+  p.timeout_ns = host::kTimeoutNs;
+  return p;
+}
+
+size_t delta_bytes(const flce_attention_desc* d) {
+  return host::align_up((size_t)d->tokens * d->q_heads * sizeof(float));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t flce_attention_workspace_size(const flce_attention_desc* d) {
+  if (!shape_ok(d) || d->dtype != FLCE_BF16) return 0;
+  return host::kAlign + delta_bytes(d);
+}
+
+flce_status flce_attention_forward(const flce_attention_desc* d, const void* q, const void* k,
+                                   const void* v, const int32_t* cu_seqlens, void* out,
+                                   float* lse, int32_t* err_word, void* stream) {
+  host::reset_launches();
+  const void* ptrs[] = {q, k, v, out};
+  FLCE_HOST_TRY(check(d, ptrs, 4, cu_seqlens, lse, err_word));
+  if (d->tokens == 0) return FLCE_OK;
+  int dev, sms;
+  FLCE_HOST_TRY(host::device(&dev, &sms));
+  const dim3 grid((unsigned)host::ceil_div(d->tokens, 4), (unsigned)d->q_heads);
+  attn_simple_fwd<<<grid, 128, 0, static_cast<cudaStream_t>(stream)>>>(
+      params(d, cu_seqlens, err_word), static_cast<const bf16*>(q), static_cast<const bf16*>(k),
+      static_cast<const bf16*>(v), static_cast<bf16*>(out), lse);
+  host::count_launch();
+  FLCE_HOST_CUDA(cudaGetLastError());
+  return FLCE_OK;
+}
+
+flce_status flce_attention_backward(const flce_attention_desc* d, const void* dout, const void* q,
+                                    const void* k, const void* v, const void* out,
+                                    const float* lse, const int32_t* cu_seqlens, void* dq,
+                                    void* dk, void* dv, void* workspace, size_t ws_bytes,
+                                    int32_t* err_word, void* stream) {
+  host::reset_launches();
+  const void* ptrs[] = {dout, q, k, v, out, dq, dk, dv};
+  FLCE_HOST_TRY(check(d, ptrs, 8, cu_seqlens, lse, err_word));
+  if (!workspace || !aligned(workspace, host::kAlign) ||
+      ws_bytes < flce_attention_workspace_size(d))
+    return FLCE_ERR_WORKSPACE;
+  if (d->tokens == 0) return FLCE_OK;
+  int dev, sms;
+  FLCE_HOST_TRY(host::device(&dev, &sms));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  float* delta = reinterpret_cast<float*>(static_cast<char*>(workspace) + host::kAlign);
+  const AttnParams p = params(d, cu_seqlens, err_word);
+  const unsigned rows = (unsigned)host::ceil_div(d->tokens, 4);
+  attn_simple_dq<<<dim3(rows, (unsigned)d->q_heads), 128, 0, st>>>(
+      p, static_cast<const bf16*>(dout), static_cast<const bf16*>(q), static_cast<const bf16*>(k),
+      static_cast<const bf16*>(v), static_cast<const bf16*>(out), lse, delta,
+      static_cast<bf16*>(dq));
+  host::count_launch();
+  FLCE_HOST_CUDA(cudaGetLastError());
+  attn_simple_dkdv<<<dim3(rows, (unsigned)d->kv_heads), 128, 0, st>>>(
+      p, static_cast<const bf16*>(dout), static_cast<const bf16*>(q), static_cast<const bf16*>(k),
+      static_cast<const bf16*>(v), lse, delta, static_cast<bf16*>(dk), static_cast<bf16*>(dv));
+  host::count_launch();
+  FLCE_HOST_CUDA(cudaGetLastError());
+  return FLCE_OK;
+}
+
+}  // extern "C"

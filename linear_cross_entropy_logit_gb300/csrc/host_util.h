@@ -1,0 +1,47 @@
+// Host-side helpers shared by the library's translation units; defined in
+// flce_api.cu.
+#pragma once
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "flce.h"
+
+namespace flce {
+namespace host {
+
+constexpr int kMaxDevices = 64;
+constexpr size_t kAlign = 256;                           // workspace regions
+constexpr unsigned long long kTimeoutNs = 2000000000ull;  // bounded device waits
+
+// Current device and its SM count; FLCE_ERR_UNSUPPORTED off sm_103.
+flce_status device(int* dev, int* sms);
+// Keeps the error's text for flce_last_cuda_error and returns FLCE_ERR_CUDA.
+flce_status fail(cudaError_t e, const char* what);
+flce_status fail_text(const char* what);
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
+// flce_last_launch_count of the calling thread.
+void reset_launches();
+void count_launch();
+
+inline bool aligned(const void* p, size_t a) {
+  return (reinterpret_cast<uintptr_t>(p) % a) == 0;
+}
+inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace host
+}  // namespace flce
+
+#define FLCE_HOST_CUDA(call)                                          \
+  do {                                                                \
+    cudaError_t e_ = (call);                                          \
+    if (e_ != cudaSuccess) return ::flce::host::fail(e_, #call);      \
+  } while (0)
+#define FLCE_HOST_TRY(expr)              \
+  do {                                   \
+    flce_status s_ = (expr);             \
+    if (s_ != FLCE_OK) return s_;        \
+  } while (0)

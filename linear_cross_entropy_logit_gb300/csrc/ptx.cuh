@@ -12,7 +12,7 @@
 namespace flce {
 
 // Error codes shared with include/flce.h (kept numerically identical).
-enum : int { kErrLabel = 4, kErrTimeout = 5, kErrBounds = 7 };
+enum : int { kErrLabel = 4, kErrTimeout = 5, kErrBounds = 7, kErrIndex = 8 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
