@@ -1,10 +1,18 @@
-// Shared by the packed attention kernels: the call's parameters and the map
-// from rows to packed sequences.
+// Shared by the packed attention kernels: the call's parameters, the walk over
+// the work units of the packed sequences, and shared-memory helpers.
 #pragma once
+#include <cuda_bf16.h>
 #include <cstdint>
 #include "ptx.cuh"
 
 namespace flce {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kTile = 128;             // rows of a query or key tile (TMEM lanes)
+constexpr int kBoxBytes = kTile * 128; // one 64-column box of a tile, 128-byte rows
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
   const int32_t* cu;   // n_seqs + 1 offsets of the packed sequences
@@ -13,9 +21,163 @@ struct AttnParams {
   int q_heads, kv_heads, group;  // group = q_heads / kv_heads
   int head_dim;
   float scale;
-  int64_t q_row, q_head, k_row, k_head, v_row, v_head;  // strides in elements
+  bf16* out;           // tokens x q_heads x head_dim
+  float* lse;          // q_heads x tokens
+  const bf16* v;       // read directly where it holds non-finite values
+  int64_t v_row, v_head;
   int* err_word;
   unsigned long long timeout_ns;
 };
+
+// One work unit: rows [q0, q0 + unit rows) of the sequence [start, start +
+// len), or, with len = 0, `rows` rows from `start` that belong to no sequence.
+struct AttnUnit {
+  int start, len, q0, rows;
+  int head;
+};
+
+__device__ __forceinline__ int warp_add(int x) { return __reduce_add_sync(~0u, x); }
+__device__ __forceinline__ int warp_max(int x) { return __reduce_max_sync(~0u, x); }
+
+// The sequences of a pack cut into units of `rows` rows, numbered so that the
+// units with the most keys come first (unit i of a sequence sees i + 1 units'
+// worth of keys): dealt out in this order, the CTAs end together.  Every unit
+// number is mapped by one warp on its own from the offsets, so no list of units
+// is written and no launch goes before the attention.  Cost: about
+// log2(longest / rows) passes over the offsets, 32 at a time.
+struct UnitWalk {
+  const int32_t* cu;
+  int n, tokens, rows;
+  int longest;    // units of the longest sequence
+  int units;      // units of all sequences
+  int lead, gaps; // rows before the first sequence; units of all rows in none
+
+  __device__ __forceinline__ int count(int s) const {
+    return s < n ? (cu[s + 1] - cu[s] + rows - 1) / rows : 0;
+  }
+  // Units with index >= i within their sequence.
+  __device__ __forceinline__ int from(int i) const {
+    int t = 0;
+    for (int s = threadIdx.x & 31; s < n; s += 32) t += max(0, count(s) - i);
+    return warp_add(t);
+  }
+  // Executed by one whole warp.  Offsets that do not ascend within [0,
+  // tokens] leave every row in no sequence.
+  __device__ __forceinline__ void init(const AttnParams& p, int unit_rows) {
+    cu = p.cu;
+    n = p.n_seqs;
+    tokens = p.tokens;
+    rows = unit_rows;
+    int bad = 0, most = 0, sum = 0;
+    for (int s = threadIdx.x & 31; s <= n; s += 32) {
+      const int a = cu[s], b = s < n ? cu[s + 1] : a;
+      bad |= a < 0 || a > tokens || b < a || b > tokens;
+      if (!bad) {
+        const int c = (b - a + rows - 1) / rows;
+        most = max(most, c);
+        sum += c;
+      }
+    }
+    bad = __any_sync(~0u, bad);
+    if (bad) {
+      if (blockIdx.x == 0 && (threadIdx.x & 31) == 0) record_error(p.err_word, kErrIndex);
+      n = 0;
+    }
+    longest = bad ? 0 : warp_max(most);
+    units = bad ? 0 : warp_add(sum);
+    lead = bad ? 0 : cu[0];
+    const int tail = bad ? tokens : tokens - cu[n];
+    gaps = (lead + rows - 1) / rows + (tail + rows - 1) / rows;
+  }
+  __device__ __forceinline__ int total() const { return units + gaps; }
+
+  // Unit `rank` in [0, total()).  Executed by one whole warp.
+  __device__ __forceinline__ AttnUnit at(int rank) const {
+    AttnUnit u{};
+    if (rank >= units) {
+      const int g = rank - units, lead_units = (lead + rows - 1) / rows;
+      const int first = n > 0 || lead > 0 ? cu[n] : 0;
+      u.start = g < lead_units ? g * rows : first + (g - lead_units) * rows;
+      u.rows = min(rows, (g < lead_units ? lead : tokens) - u.start);
+      return u;
+    }
+    int lo = 0, hi = longest;  // from(lo) > rank >= from(hi)
+    int after = 0;             // from(lo + 1) once hi = lo + 1
+    while (hi - lo > 1) {
+      const int m = (lo + hi) >> 1, f = from(m);
+      if (f > rank) lo = m; else hi = m, after = f;
+    }
+    int nth = rank - after;  // among the sequences with more than lo units
+    for (int s0 = 0; s0 < n; s0 += 32) {
+      const int s = s0 + (threadIdx.x & 31);
+      const unsigned has = __ballot_sync(~0u, count(s) > lo);
+      const int c = __popc(has);
+      if (nth < c) {
+        const int q = s0 + (int)__fns(has, 0, nth + 1);
+        u.start = cu[q];
+        u.len = cu[q + 1] - u.start;
+        u.q0 = lo * rows;
+        return u;
+      }
+      nth -= c;
+    }
+    return u;  // not reached
+  }
+};
+
+// Unit number of round r of CTA c of g: every other round runs backwards, so
+// that a CTA with a long unit in one round gets a short one in the next.
+__device__ __forceinline__ int64_t dealt_unit(uint32_t r, int c, int g) {
+  return (int64_t)r * g + ((r & 1) ? g - 1 - c : c);
+}
+
+// mbar_wait by a whole warp: all its lanes get the same answer, so that they
+// leave a loop together.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const WaitCtx& ctx) {
+  return __all_sync(~0u, mbar_wait(bar, parity, ctx));
+}
+
+// K-major operand (rows x head values), step kk of 16 values.
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int kk) {
+  return smem_desc_sw128(tile + (kk >> 2) * kBoxBytes + (kk & 3) * 32, 16, 1024);
+}
+// MN-major operand (head values outermost for the MMA), step kk of 16 rows.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int kk) {
+  return smem_desc_sw128(tile + kk * 2048, kBoxBytes, 1024);
+}
+
+// Bits 15 and 31 set where a packed bf16 half is infinite or NaN.
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t x) {
+  return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+
+// Makes a tile fit to be multiplied by zeros: rows from `valid` on (another
+// sequence's, or none's) become zero; non-finite values become zero and their
+// row's bit is set in flags[4], for the caller to add them back where they are
+// visible.  Called by each of `warps` warps (w = 0 ..) with flags of its own.
+__device__ __forceinline__ void clean_tile(uint8_t* tile, int boxes, int valid, int w, int warps,
+                                           uint32_t* flags) {
+  const int lane = threadIdx.x & 31;
+  if (lane < 4) flags[lane] = 0;
+  __syncwarp();
+  for (int i = w * 32 + lane; i < boxes * kTile * 8; i += warps * 32) {
+    uint4* at = reinterpret_cast<uint4*>(tile) + i;
+    const int row = (i >> 3) & (kTile - 1);
+    if (row >= valid) {
+      *at = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    uint4 x = *at;
+    if ((nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w)) == 0) continue;
+    uint32_t* h = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t b = nonfinite2(h[e]);
+      h[e] &= (b & 0x8000u ? 0u : 0xffffu) | (b & 0x80000000u ? 0u : 0xffff0000u);
+    }
+    *at = x;
+    atomicOr(&flags[row >> 5], 1u << (row & 31));
+  }
+}
 
 }  // namespace flce

@@ -1,0 +1,443 @@
+// Forward of packed causal attention on the tensor cores.
+//
+//   s_ij = scale q_i . k_j,  m_i a running maximum,  p_ij = 2^((s_ij - m_i) log2 e)
+//   l_i = sum_j p_ij,  out_i = sum_j p_ij v_j / l_i,  lse_i = m_i + log l_i
+//
+// A persistent CTA takes units of 256 query rows of one sequence and head: two
+// tiles of 128, so that one tile's softmax runs beside the other's products.
+//   warps 0-3, 4-7  softmax of tile 0 / 1: a thread owns one row (TMEM lane)
+//   warp 8          issues the MMAs (one lane)
+//   warp 9          maps the units and loads Q, K and V by TMA
+//   warps 10-11     clean the value tile on the diagonal (see below)
+// TMEM: S of each tile (128 columns; P overwrites it as packed bf16) and O of
+// each tile.  S = Q K^T reads both operands from shared memory, O += P V reads
+// P from TMEM.  MMAs complete in order, so S of the next key tile may follow
+// the product that reads P out of the same columns, and a softmax that sees its
+// S also knows that every earlier product into its O is done.
+//
+// Key tiles run from the diagonal down: only the first tile of a query tile
+// needs a mask (key <= row).  The rest of a ragged last tile belongs to the
+// next sequence: its keys are masked by the same comparison, its values are
+// zeroed in shared memory, since 0 x NaN is NaN.  Non-finite values inside the
+// sequence that only some rows see are zeroed too and added back in the
+// epilogue to the rows that see them.
+//
+// The maximum is only moved when it grows by more than kMoveLog2 (2^8): until
+// then exponentials are relative to the old one, at most 2^8 in size, and O is
+// left alone.  l and m are fp32; P is rounded to bf16 (2^-9 each, the type of
+// V), and l sums it before that rounding.
+#pragma once
+#include "attn_common.cuh"
+
+namespace flce {
+
+constexpr int kFwdThreads = 384;
+constexpr int kFwdRows = 2 * kTile;
+constexpr float kMoveLog2 = 8.f;
+// Registers per thread of the two softmax warpgroups and of the third: a
+// softmax thread holds a row of 128 scores.
+constexpr int kFwdSoftmaxRegs = 200, kFwdOtherRegs = 104;
+static_assert(2 * kFwdSoftmaxRegs + kFwdOtherRegs == 3 * (65536 / kFwdThreads / 8 * 8),
+              "shares add up to what the block is launched with");
+
+template <int DP>
+struct FwdCfg {
+  static constexpr int kBoxes = DP / 64;
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;
+  static constexpr int kSlots = DP == 128 ? 4 : 8;  // K and V tiles in flight
+  static constexpr int kRing = 2 * kTileBytes;      // after the two Q tiles
+  static constexpr int kBars = kRing + kSlots * kTileBytes;
+  static constexpr int kSmem = kBars + 512 + 1024;  // + alignment of the base
+};
+
+struct FwdShared {
+  uint64_t full[8], empty[8];  // ring of K and V tiles
+  uint64_t qfull, qempty;
+  uint64_t sfull[2], pfull[2], ofull[2];
+  uint64_t clean[2][2];        // by unit parity and query tile: its diagonal value tile is fit for use
+  uint64_t ufull[2], uempty[2];
+  uint64_t mma_done;
+  AttnUnit unit[2];
+  uint32_t flags[2][2][2][4];  // by unit parity, diagonal tile and cleaning warp: non-finite rows
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(FwdShared) <= 512, "barrier area");
+
+// Tiles of a unit: key tiles of query tile 0 and 1 (0: it has no rows).
+__device__ __forceinline__ void unit_tiles(const AttnUnit& u, int& n0, int& n1) {
+  n0 = u.len > 0 ? u.q0 / kTile + 1 : 0;
+  n1 = u.q0 + kTile < u.len ? n0 + 1 : 0;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+         const __grid_constant__ CUtensorMap tv, const AttnParams p) {
+  using C = FwdCfg<DP>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = smem + C::kRing;
+  FwdShared& sh = *reinterpret_cast<FwdShared*>(smem + C::kBars);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const WaitCtx ctx{&sh.abort, p.err_word, p.timeout_ns};
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kSlots; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
+    mbar_init(&sh.qfull, 1);
+    mbar_init(&sh.qempty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.sfull[i], 1);
+      mbar_init(&sh.pfull[i], 4);
+      mbar_init(&sh.ofull[i], 1);
+      mbar_init(&sh.ufull[i], 1);
+      mbar_init(&sh.uempty[i], 11);  // 8 softmax warps, the MMA lane, 2 cleaning warps
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.clean[i >> 1][i & 1], 2);
+    mbar_init(&sh.mma_done, 1);
+    sh.abort = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp >= 8) regs_down<kFwdOtherRegs>();
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    regs_up<kFwdSoftmaxRegs>();
+    const int x = warp >> 2;           // query tile
+    const int row = threadIdx.x & 127; // row of the tile = TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // (32 * warp) << 16
+    const uint32_t ts = tmem + lanes + x * kTile;
+    const uint32_t to = tmem + lanes + 2 * kTile + x * DP;
+    const float c = p.scale * kLog2e;
+    uint32_t ns = 0, no = 0;  // tiles and units of this query tile so far
+    for (uint32_t it = 0;; ++it) {
+      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      const AttnUnit u = sh.unit[it & 1];
+      if (u.head < 0) break;
+      int n0, n1;
+      unit_tiles(u, n0, n1);
+      const int n = x ? n1 : n0;
+      if (u.len == 0) {  // rows of no sequence
+        const int r = x * kTile + row;
+        if (r < u.rows) {
+          const int64_t t = u.start + r;
+          p.lse[(int64_t)u.head * p.tokens + t] = -INFINITY;
+          uint4* o = reinterpret_cast<uint4*>(p.out + (t * p.q_heads + u.head) * p.head_dim);
+          for (int d = 0; d < p.head_dim / 8; ++d) o[d] = make_uint4(0, 0, 0, 0);
+        }
+      }
+      if (n == 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
+        continue;
+      }
+      float m = 0.f, l = 0.f;
+      bool ok = true;
+      for (int j = n - 1; j >= 0; --j, ++ns) {
+        if (!(ok = mbar_wait_warp(&sh.sfull[x], ns & 1, ctx))) break;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, s[i]);
+        tmem_ld_wait();
+        if (j == n - 1) {  // the diagonal
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i > row) s[i >> 5][i & 31] = 0xff800000u;  // -infinity
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mx[i] = __uint_as_float(s[i][0]);
+#pragma unroll
+          for (int e = 1; e < 31; e += 2)
+            mx[i] = fmax3(mx[i], __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
+          mx[i] = fmaxf(mx[i], __uint_as_float(s[i][31]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (j == n - 1) {
+          m = top;
+        } else {
+          const bool move = (top - m) * c > kMoveLog2;
+          if (__any_sync(~0u, move)) {
+            const float f = move ? ex2_approx((m - top) * c) : 1.f;
+            if (move) m = top;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DP; d += 32) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(to + d, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st_32x32b_x32(to + d, o);
+            }
+          }
+        }
+        const float b = m == -INFINITY ? 0.f : -m * c;  // no key so far: all p are 0
+        const uint64_t c2 = pack_f32x2(c, c), b2 = pack_f32x2(b, b);
+        uint64_t sum[4] = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float p0, p1;
+            unpack_f32x2(fma_f32x2(pack_u32x2(s[i][e], s[i][e + 1]), c2, b2), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            sum[(e >> 1) & 3] = add_f32x2(sum[(e >> 1) & 3], pack_f32x2(p0, p1));
+            pk[e >> 1] = pack_bf16x2(p0, p1);
+          }
+          tmem_st_32x32b_x16(ts + 16 * i, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.pfull[x]);
+        float l0, l1;
+        unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), l0, l1);
+        l += l0 + l1;
+      }
+      if (!ok || !mbar_wait_warp(&sh.ofull[x], no & 1, ctx)) break;
+      ++no;
+      tc_fence_after();
+      const uint32_t(&flags)[2][2][4] = sh.flags[it & 1];
+      uint32_t any = 0;  // non-finite rows of this and the tile before it
+      for (int f = 0; f <= x; ++f)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) any |= flags[f][i >> 2][i & 3];
+      const int r = u.q0 + x * kTile + row;  // row within the sequence
+      const int64_t t = u.start + r;
+      const float inv = 1.f / l;
+#pragma unroll
+      for (int d = 0; d < DP; d += 32) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(to + d, o);
+        tmem_ld_wait();
+        if (any && r < u.len) {  // add back the non-finite values this row sees
+          for (int f = 0; f <= x; ++f)
+            for (int w = 0; w < 4; ++w)
+              for (uint32_t b = flags[f][0][w] | flags[f][1][w]; b; b &= b - 1) {
+                const int key = u.q0 + f * kTile + w * 32 + __ffs(b) - 1;
+                if (key > r) continue;
+                const bf16* v = p.v + (int64_t)(u.start + key) * p.v_row +
+                                (u.head / p.group) * p.v_head + d;
+                for (int e = 0; e < 32; ++e) {
+                  if (d + e >= p.head_dim) break;
+                  const float val = __bfloat162float(v[e]);
+                  if (!isfinite(val)) {
+#pragma unroll
+                    for (int g = 0; g < 32; ++g)
+                      if (g == e) o[g] = __float_as_uint(__uint_as_float(o[g]) + val);
+                  }
+                }
+              }
+        }
+        if (r < u.len) {
+          bf16* out = p.out + (t * p.q_heads + u.head) * p.head_dim + d;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            if (d + e >= p.head_dim) break;
+            uint32_t w[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              w[g] = pack_bf16x2(__uint_as_float(o[e + 2 * g]) * inv,
+                                 __uint_as_float(o[e + 2 * g + 1]) * inv);
+            *reinterpret_cast<uint4*>(out + e) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      tc_fence_before();  // O is read before the next unit's first product into it
+      if (r < u.len) p.lse[(int64_t)u.head * p.tokens + t] = m * p.scale + logf(l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t ids = make_idesc(false, false, kTile, kTile);
+      constexpr uint32_t ido = make_idesc(false, true, kTile, DP);
+      const uint32_t q0 = smem_u32(smem);
+      uint32_t base = 0;  // ring position of the unit's first tile
+      uint32_t np[2] = {0, 0}, nq = 0, nclean = 0;  // bit 2 parity + tile of nclean: next phase
+      bool ok = true;
+      auto slot = [&](uint32_t pos) { return smem_u32(ring + (pos % C::kSlots) * C::kTileBytes); };
+      auto wait_tile = [&](uint32_t pos) {
+        ok = ok && mbar_wait(&sh.full[pos % C::kSlots], (pos / C::kSlots) & 1, ctx);
+        tc_fence_after();
+        return ok;
+      };
+      auto issue_s = [&](int x, uint32_t pos) {
+        const uint32_t kt = slot(pos);
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)
+          mma_issue(tmem + x * kTile, desc_k(q0 + x * C::kTileBytes, kk), desc_k(kt, kk), ids, kk != 0);
+        mma_commit(&sh.sfull[x]);
+      };
+      for (uint32_t it = 0; ok; ++it) {
+        if (!mbar_wait(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+        const AttnUnit u = sh.unit[it & 1];
+        if (u.head < 0) break;
+        if (u.len == 0) {
+          mbar_arrive(&sh.uempty[it & 1]);
+          continue;
+        }
+        int n0, n1;
+        unit_tiles(u, n0, n1);
+        const int last = max(n0, n1) - 1;  // key tile j sits at ring position base + 2 (last - j)
+        if (!mbar_wait(&sh.qfull, nq & 1, ctx)) break;
+        ++nq;
+        if (!wait_tile(base)) break;
+        issue_s(n1 ? 1 : 0, base);
+        mma_commit(&sh.empty[base % C::kSlots]);
+        if (n1) {
+          if (!wait_tile(base + 2)) break;
+          issue_s(0, base + 2);
+        }
+        if (last == 0) mma_commit(&sh.qempty);
+        for (int j = last; j >= 0 && ok; --j) {
+          const uint32_t kpos = base + 2 * (last - j), vpos = kpos + 1, knext = kpos + 2;
+          if (!wait_tile(vpos)) break;
+          if (j >= n0 - 1) {
+            const uint32_t f = j - (n0 - 1), bit = 2 * (it & 1) + f;
+            if (!(ok = mbar_wait(&sh.clean[it & 1][f], (nclean >> bit) & 1, ctx))) break;
+            nclean ^= 1u << bit;
+          }
+          if (j > 0 && !wait_tile(knext)) break;
+#pragma unroll
+          for (int x = 1; x >= 0; --x) {
+            if (j >= (x ? n1 : n0)) continue;
+            if (!(ok = mbar_wait(&sh.pfull[x], np[x] & 1, ctx))) break;
+            ++np[x];
+            tc_fence_after();
+            const uint32_t vt = slot(vpos);
+            const bool first = j == (x ? n1 : n0) - 1;
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_issue_ts(tmem + 2 * kTile + x * DP, tmem + x * kTile + kk * 8, desc_mn(vt, kk), ido,
+                           !(first && kk == 0));
+            // the key tile right below a pair's top one was multiplied with tile 0 at the start
+            const bool top = n1 && j == last;
+            if (j > 0) issue_s(x, knext);
+            else mma_commit(&sh.ofull[x]);
+            if (x == 0 || j >= n0) mma_commit(&sh.empty[vpos % C::kSlots]);
+            if (j > 0 && (x == 0 || top)) mma_commit(&sh.empty[knext % C::kSlots]);
+          }
+          if (j == 1) mma_commit(&sh.qempty);  // the last product that reads Q is issued
+        }
+        if (!ok) break;
+        mbar_arrive(&sh.uempty[it & 1]);
+        base += 2 * (last + 1);
+      }
+      mma_commit(&sh.mma_done);
+      mbar_wait_drain(&sh.mma_done, 0, p.timeout_ns);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ units, loads
+    if (lane == 0) {
+      prefetch_tensormap(&tq);
+      prefetch_tensormap(&tk);
+      prefetch_tensormap(&tv);
+    }
+    UnitWalk walk;
+    walk.init(p, kFwdRows);
+    const int64_t total = (int64_t)walk.total() * p.q_heads;
+    uint32_t pos = 0, nq = 0;
+    bool ok = true;
+    for (uint32_t it = 0; ok; ++it) {
+      const int64_t id = dealt_unit(it, blockIdx.x, gridDim.x);
+      AttnUnit u{};
+      u.head = -1;
+      if (id < total) {
+        u = walk.at((int)(id / p.q_heads));
+        u.head = (int)(id % p.q_heads);
+      }
+      if (lane == 0) {
+        ok = mbar_wait(&sh.uempty[it & 1], ((it >> 1) & 1) ^ 1, ctx);
+        if (ok) {
+          sh.unit[it & 1] = u;
+          mbar_arrive(&sh.ufull[it & 1]);
+        }
+        if (ok && u.len > 0) {
+          int n0, n1;
+          unit_tiles(u, n0, n1);
+          const int last = max(n0, n1) - 1, kvh = u.head / p.group;
+          auto load = [&](const CUtensorMap* map, int head, int r) {
+            const int s = pos % C::kSlots;
+            if (!(ok = mbar_wait(&sh.empty[s], ((pos / C::kSlots) & 1) ^ 1, ctx))) return;
+            mbar_arrive_expect_tx(&sh.full[s], C::kTileBytes);
+            for (int b = 0; b < C::kBoxes; ++b)
+              tma_load_3d(ring + s * C::kTileBytes + b * kBoxBytes, map, &sh.full[s], b * 64, head, r);
+            ++pos;
+          };
+          if ((ok = mbar_wait(&sh.qempty, (nq & 1) ^ 1, ctx))) {
+            mbar_arrive_expect_tx(&sh.qfull, (n1 ? 2 : 1) * C::kTileBytes);
+            for (int x = 0; x <= (n1 ? 1 : 0); ++x)
+              for (int b = 0; b < C::kBoxes; ++b)
+                tma_load_3d(smem + x * C::kTileBytes + b * kBoxBytes, &tq, &sh.qfull, b * 64, u.head,
+                            u.start + u.q0 + x * kTile);
+            ++nq;
+          }
+          for (int j = last; j >= 0 && ok; --j) {
+            load(&tk, kvh, u.start + j * kTile);
+            if (ok) load(&tv, kvh, u.start + j * kTile);
+          }
+        }
+      }
+      ok = __shfl_sync(~0u, ok, 0);
+      if (u.head < 0) break;
+    }
+    if (!ok && lane == 0) {
+      // copies in flight must land before the CTA's shared memory is given up
+      if (nq) mbar_wait_drain(&sh.qfull, (nq - 1) & 1, p.timeout_ns);
+      for (uint32_t i = pos > C::kSlots ? pos - C::kSlots : 0; i < pos; ++i)
+        mbar_wait_drain(&sh.full[i % C::kSlots], (i / C::kSlots) & 1, p.timeout_ns);
+    }
+  } else {
+    // ------------------------------------------------------------ diagonal value tiles
+    const int w = warp - 10;
+    uint32_t base = 0;
+    for (uint32_t it = 0;; ++it) {
+      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      const AttnUnit u = sh.unit[it & 1];
+      if (u.head < 0) break;
+      bool ok = true;
+      if (u.len > 0) {
+        int n0, n1;
+        unit_tiles(u, n0, n1);
+        const int last = max(n0, n1) - 1;
+        for (int j = last; j >= n0 - 1; --j) {
+          const uint32_t pos = base + 2 * (last - j) + 1;
+          const int f = j - (n0 - 1);
+          if (!(ok = mbar_wait_warp(&sh.full[pos % C::kSlots], (pos / C::kSlots) & 1, ctx))) break;
+          clean_tile(ring + (pos % C::kSlots) * C::kTileBytes, C::kBoxes, u.len - j * kTile, w, 2,
+                     sh.flags[it & 1][f][w]);
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.clean[it & 1][f]);
+        }
+        base += 2 * (last + 1);
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace flce

@@ -5,15 +5,16 @@
 //   delta_i = dout_i . out_i,  ds_ij = p_ij (dout_i . v_j - delta_i)
 //   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i
 #pragma once
-#include <cuda_bf16.h>
 #include "attn_common.cuh"
 
 namespace flce {
 
-using bf16 = __nv_bfloat16;
+struct AttnIn : AttnParams {
+  int64_t q_row, q_head, k_row, k_head;
+};
 
 // The sequence [lo, hi) holding `row`; empty when no sequence holds it.
-__device__ inline void attn_sequence_of(const AttnParams& p, int row, int& lo, int& hi) {
+__device__ inline void attn_sequence_of(const AttnIn& p, int row, int& lo, int& hi) {
   int a = 0, b = p.n_seqs;  // cu[a] <= row < cu[b] if both exist
   lo = hi = row;
   if (row < p.cu[0] || row >= p.cu[p.n_seqs]) return;
@@ -27,7 +28,7 @@ __device__ inline void attn_sequence_of(const AttnParams& p, int row, int& lo, i
 
 // Whether the offsets ascend within [0, tokens]; every thread of the block
 // gets the answer.
-__device__ inline bool attn_offsets_ok(const AttnParams& p) {
+__device__ inline bool attn_offsets_ok(const AttnIn& p) {
   bool bad = false;
   for (int s = threadIdx.x; s <= p.n_seqs; s += blockDim.x) {
     const int c = p.cu[s];
@@ -67,38 +68,7 @@ __device__ inline float dot_row(const float (&x)[kSimpleE], const float (&y)[kSi
   return warp_sum(s);
 }
 
-__global__ void attn_simple_fwd(AttnParams p, const bf16* q, const bf16* k, const bf16* v,
-                                bf16* out, float* lse) {
-  const bool ok = attn_offsets_ok(p);
-  const int lane = threadIdx.x & 31, h = blockIdx.y, D = p.head_dim;
-  const int i = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (i >= p.tokens) return;
-  int lo = i, hi = i;
-  if (ok) attn_sequence_of(p, i, lo, hi);
-  const int kvh = h / p.group;
-  float qi[kSimpleE], acc[kSimpleE] = {};
-  load_row(qi, q + i * p.q_row + h * p.q_head, D, lane);
-  float m = -INFINITY, l = 0.f;
-  for (int j = lo; j < hi && j <= i; ++j) {
-    float x[kSimpleE];
-    load_row(x, k + j * p.k_row + kvh * p.k_head, D, lane);
-    const float s = dot_row(qi, x) * p.scale;
-    const float mn = fmaxf(m, s);
-    const float c = expf(m - mn), w = expf(s - mn);
-    load_row(x, v + j * p.v_row + kvh * p.v_head, D, lane);
-    l = l * c + w;
-#pragma unroll
-    for (int e = 0; e < kSimpleE; ++e) acc[e] = acc[e] * c + w * x[e];
-    m = mn;
-  }
-  const float inv = lo < hi ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < kSimpleE; ++e) acc[e] *= inv;
-  store_row(out + ((int64_t)i * p.q_heads + h) * D, acc, D, lane);
-  if (lane == 0) lse[(int64_t)h * p.tokens + i] = lo < hi ? m + logf(l) : -INFINITY;
-}
-
-__global__ void attn_simple_dq(AttnParams p, const bf16* dout, const bf16* q, const bf16* k,
+__global__ void attn_simple_dq(AttnIn p, const bf16* dout, const bf16* q, const bf16* k,
                                const bf16* v, const bf16* out, const float* lse, float* delta,
                                bf16* dq) {
   const bool ok = attn_offsets_ok(p);
@@ -129,7 +99,7 @@ __global__ void attn_simple_dq(AttnParams p, const bf16* dout, const bf16* q, co
   store_row(dq + at, acc, D, lane);
 }
 
-__global__ void attn_simple_dkdv(AttnParams p, const bf16* dout, const bf16* q, const bf16* k,
+__global__ void attn_simple_dkdv(AttnIn p, const bf16* dout, const bf16* q, const bf16* k,
                                  const bf16* v, const float* lse, const float* delta, bf16* dk,
                                  bf16* dv) {
   const bool ok = attn_offsets_ok(p);

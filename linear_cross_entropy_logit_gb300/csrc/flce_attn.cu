@@ -1,8 +1,12 @@
 // C ABI of causal attention over packed sequences: argument checks, the
 // workspace plan and the launches.
+#include <algorithm>
 #include <climits>
 #include <cmath>
+#include <cstdio>
+#include <mutex>
 
+#include "attn_fwd.cuh"
 #include "attn_simple.cuh"
 #include "host_util.h"
 
@@ -43,8 +47,8 @@ flce_status check(const flce_attention_desc* d, const void* const* ptrs, int n, 
   return FLCE_OK;
 }
 
-AttnParams params(const flce_attention_desc* d, const int32_t* cu, int32_t* err_word) {
-  AttnParams p{};
+AttnIn params(const flce_attention_desc* d, const int32_t* cu, int32_t* err_word) {
+  AttnIn p{};
   p.cu = cu;
   p.n_seqs = (int)d->sequences;
   p.tokens = (int)d->tokens;
@@ -62,6 +66,45 @@ AttnParams params(const flce_attention_desc* d, const int32_t* cu, int32_t* err_
   p.err_word = err_word;
   p.timeout_ns = host::kTimeoutNs;
   return p;
+}
+
+// Work units of `rows` rows at most: every sequence's last and the gaps before
+// and after the sequences may be partial.
+int64_t most_units(const flce_attention_desc* d, int rows) {
+  return d->tokens / rows + d->sequences + 2;
+}
+
+// 3-D map (head value, head, token) with boxes of 64 values x 1 head x 128
+// tokens, 128-byte swizzle; values and tokens outside read as zero.
+flce_status map_heads(CUtensorMap* m, const void* base, const flce_attention_desc* d,
+                      int64_t heads, int64_t row, int64_t head) {
+  auto fn = host::encode_fn();
+  if (!fn) return host::fail_text("cuTensorMapEncodeTiled entry point unavailable");
+  cuuint64_t dims[3] = {(cuuint64_t)d->head_dim, (cuuint64_t)heads, (cuuint64_t)d->tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)head * 2, (cuuint64_t)row * 2};
+  cuuint32_t box[3] = {64, 1, kTile};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                  box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r == CUDA_SUCCESS) return FLCE_OK;
+  char buf[160];
+  snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled failed (%d): heads=%lld strides %lld, %lld",
+           (int)r, (long long)heads, (long long)row, (long long)head);
+  return host::fail_text(buf);
+}
+
+// A kernel's shared-memory limit, set once per device.
+struct Setup {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+};
+template <typename Kern>
+flce_status set_smem(Setup& s, Kern kern, int smem) {
+  std::call_once(s.once, [&] {
+    s.err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
+  return s.err == cudaSuccess ? FLCE_OK : host::fail(s.err, "cudaFuncSetAttribute");
 }
 
 size_t delta_bytes(const flce_attention_desc* d) {
@@ -86,10 +129,24 @@ flce_status flce_attention_forward(const flce_attention_desc* d, const void* q, 
   if (d->tokens == 0) return FLCE_OK;
   int dev, sms;
   FLCE_HOST_TRY(host::device(&dev, &sms));
-  const dim3 grid((unsigned)host::ceil_div(d->tokens, 4), (unsigned)d->q_heads);
-  attn_simple_fwd<<<grid, 128, 0, static_cast<cudaStream_t>(stream)>>>(
-      params(d, cu_seqlens, err_word), static_cast<const bf16*>(q), static_cast<const bf16*>(k),
-      static_cast<const bf16*>(v), static_cast<bf16*>(out), lse);
+  AttnParams p = params(d, cu_seqlens, err_word);
+  p.out = static_cast<bf16*>(out);
+  p.lse = lse;
+  p.v = static_cast<const bf16*>(v);
+  CUtensorMap tq, tk, tv;
+  FLCE_HOST_TRY(map_heads(&tq, q, d, d->q_heads, d->q_row, d->q_head));
+  FLCE_HOST_TRY(map_heads(&tk, k, d, d->kv_heads, d->k_row, d->k_head));
+  FLCE_HOST_TRY(map_heads(&tv, v, d, d->kv_heads, d->v_row, d->v_head));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int grid = (int)std::min<int64_t>(most_units(d, kFwdRows) * d->q_heads, sms);
+  static Setup setup[2][host::kMaxDevices];
+  if (d->head_dim <= 64) {
+    FLCE_HOST_TRY(set_smem(setup[0][dev], attn_fwd<64>, FwdCfg<64>::kSmem));
+    attn_fwd<64><<<grid, kFwdThreads, FwdCfg<64>::kSmem, st>>>(tq, tk, tv, p);
+  } else {
+    FLCE_HOST_TRY(set_smem(setup[1][dev], attn_fwd<128>, FwdCfg<128>::kSmem));
+    attn_fwd<128><<<grid, kFwdThreads, FwdCfg<128>::kSmem, st>>>(tq, tk, tv, p);
+  }
   host::count_launch();
   FLCE_HOST_CUDA(cudaGetLastError());
   return FLCE_OK;
@@ -111,7 +168,7 @@ flce_status flce_attention_backward(const flce_attention_desc* d, const void* do
   FLCE_HOST_TRY(host::device(&dev, &sms));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   float* delta = reinterpret_cast<float*>(static_cast<char*>(workspace) + host::kAlign);
-  const AttnParams p = params(d, cu_seqlens, err_word);
+  const AttnIn p = params(d, cu_seqlens, err_word);
   const unsigned rows = (unsigned)host::ceil_div(d->tokens, 4);
   attn_simple_dq<<<dim3(rows, (unsigned)d->q_heads), 128, 0, st>>>(
       p, static_cast<const bf16*>(dout), static_cast<const bf16*>(q), static_cast<const bf16*>(k),
