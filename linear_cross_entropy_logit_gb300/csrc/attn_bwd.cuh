@@ -1,0 +1,905 @@
+// Backward of packed causal attention on the tensor cores, in two kernels.
+//
+//   p_ij = exp(s_ij - lse_i),  delta_i = dout_i . out_i
+//   ds_ij = p_ij (dout_i . v_j - delta_i)
+//   dq_i = scale sum_j ds_ij k_j          attn_dq: a CTA owns 128 query rows
+//   dv_j = sum_i p_ij dout_i              attn_dkdv: a CTA owns 128 key rows and
+//   dk_j = scale sum_i ds_ij q_i          sums over the query heads that read them
+//
+// Each kernel recomputes S and dP = dout V^T, so that every sum stays in the
+// TMEM of the CTA that owns its rows: no fp32 gradient goes through memory, no
+// atomics, the same bits every run.  Seven products where one kernel for all
+// three gradients would take five, but that one has to add dq up in memory
+// across CTAs.
+//
+// Both: warps 0-7 compute (a thread owns one TMEM lane and 64 of the 128
+// columns), warp 8 issues MMAs, warp 9 maps units and loads, warps 12-15 clean
+// tiles (and attn_dq's compute delta).  P and dS are rounded to bf16 for the
+// products (their operands' type); everything else is fp32.  A masked entry is
+// set to zero after the multiplication, so that what it held does not matter;
+// its partner in the product (a row of another sequence, or a non-finite value)
+// is zeroed in shared memory, as in the forward.
+#pragma once
+#include "attn_common.cuh"
+
+namespace flce {
+
+constexpr int kBwdThreads = 512;
+constexpr int kBwdComputeRegs = 184, kBwdOtherRegs = 72;
+static_assert(2 * (kBwdComputeRegs + kBwdOtherRegs) == 4 * (65536 / kBwdThreads),
+              "shares add up to what the block is launched with");
+
+struct AttnBwdParams : AttnParams {
+  const bf16* dout;    // tokens x q_heads x head_dim
+  bf16 *dq, *dk, *dv;  // contiguous
+  float *nlse, *delta; // q_heads x tokens: -lse log2 e, delta (written by attn_dq)
+  float* partial;      // splits > 1: dk, dv partial sums, 2 x splits x tokens x kv_heads x head_dim
+  int splits;          // CTAs that share the query heads of a key / value head
+};
+
+// One thread's 64 scores and gradients of scores.
+__device__ __forceinline__ void load64(uint32_t (&r)[2][32], uint32_t at) {
+  tmem_ld_32x32b_x32(at, r[0]);
+  tmem_ld_32x32b_x32(at + 32, r[1]);
+  tmem_ld_wait();
+}
+__device__ __forceinline__ float as_f(uint32_t x) { return __uint_as_float(x); }
+
+// Writes `n` (a multiple of 8) fp32 values of a row as bf16, up to `limit`.
+template <int N>
+__device__ __forceinline__ void store_row(bf16* to, const uint32_t (&v)[N], float scale, int limit) {
+#pragma unroll
+  for (int e = 0; e < N; e += 8) {
+    if (e >= limit) break;
+    uint32_t w[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) w[g] = pack_bf16x2(as_f(v[e + 2 * g]) * scale, as_f(v[e + 2 * g + 1]) * scale);
+    *reinterpret_cast<uint4*>(to + e) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ----------------------------------------------------------------------------
+// dq
+// ----------------------------------------------------------------------------
+// TMEM: two S buffers (S of the next key tile is made while this one's is
+// read), dP (dS overwrites it), dQ.  Three K tiles are held: of this step (for
+// dQ += dS K), the next (S) and one in flight.
+template <int DP>
+struct DqCfg {
+  static constexpr int kBoxes = DP / 64;
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;
+  static constexpr int kK = DP == 128 ? 3 : 5, kV = DP == 128 ? 2 : 4;  // ring sizes
+  static constexpr int kRingK = 2 * kTileBytes;                        // after Q and dout
+  static constexpr int kRingV = kRingK + kK * kTileBytes;
+  static constexpr int kBars = kRingV + kV * kTileBytes;
+  static constexpr int kSmem = kBars + 512 + 2048;
+};
+
+struct DqShared {
+  uint64_t kfull[5], kempty[5], vfull[4], vempty[4];
+  uint64_t qfull, qempty;
+  uint64_t sfull[2], pfull, dsfull, accfull;
+  uint64_t clean[2], stats[2];
+  uint64_t ufull[2], uempty[2];
+  uint64_t mma_done;
+  AttnUnit unit[2];
+  uint32_t flags[4][4];
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(DqShared) <= 512, "barrier area");
+
+template <int DP>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+        const AttnBwdParams p) {
+  using C = DqCfg<DP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  DqShared& sh = *reinterpret_cast<DqShared*>(smem + C::kBars);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const WaitCtx ctx{&sh.abort, p.err_word, p.timeout_ns};
+
+  if (threadIdx.x == 0) {
+    // a K slot is given back by the MMAs and by the cleaning warps, which so see
+    // every K tile pass
+    for (int i = 0; i < C::kK; ++i) mbar_init(&sh.kfull[i], 1), mbar_init(&sh.kempty[i], 5);
+    for (int i = 0; i < C::kV; ++i) mbar_init(&sh.vfull[i], 1), mbar_init(&sh.vempty[i], 1);
+    mbar_init(&sh.qfull, 1);
+    mbar_init(&sh.qempty, 1);
+    mbar_init(&sh.pfull, 1);
+    mbar_init(&sh.dsfull, 8);
+    mbar_init(&sh.accfull, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.sfull[i], 1);
+      mbar_init(&sh.clean[i], 4);
+      mbar_init(&sh.stats[i], 4);
+      mbar_init(&sh.ufull[i], 1);
+      mbar_init(&sh.uempty[i], 13);  // 8 compute warps, the MMA lane, 4 cleaning warps
+    }
+    mbar_init(&sh.mma_done, 1);
+    sh.abort = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t t_dp = tmem + 2 * kTile, t_acc = tmem + 3 * kTile;
+  // per unit parity: -lse log2 e and delta of the 128 rows
+  float* stat = reinterpret_cast<float*>(smem + C::kBars + 512);
+
+  if (warp >= 8) regs_down<kBwdOtherRegs>();
+  if (warp < 8) {
+    // ------------------------------------------------------------ compute
+    regs_up<kBwdComputeRegs>();
+    const int half = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+    const float c = p.scale * kLog2e;
+    const uint64_t c2 = pack_f32x2(c, c);
+    uint32_t step = 0, units = 0;
+    for (uint32_t it = 0;; ++it) {
+      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      const AttnUnit u = sh.unit[it & 1];
+      if (u.head < 0) break;
+      bool ok = true;
+      if (u.len == 0) {  // rows of no sequence
+        if (half == 0 && row < u.rows) {
+          uint4* o = reinterpret_cast<uint4*>(
+              p.dq + ((int64_t)(u.start + row) * p.q_heads + u.head) * p.head_dim);
+          for (int d = 0; d < p.head_dim / 8; ++d) o[d] = make_uint4(0, 0, 0, 0);
+        }
+      } else {
+        if (!mbar_wait_warp(&sh.stats[it & 1], (it >> 1) & 1, ctx)) break;
+        const float nl = stat[(it & 1) * 256 + row], dl = -stat[(it & 1) * 256 + 128 + row];
+        const uint64_t nl2 = pack_f32x2(nl, nl), dl2 = pack_f32x2(dl, dl);
+        const int n = u.q0 / kTile + 1;
+        for (int j = n - 1; j >= 0; --j, ++step) {
+          if (!(ok = mbar_wait_warp(&sh.sfull[step & 1], (step >> 1) & 1, ctx))) break;
+          tc_fence_after();
+          uint32_t s[2][32], g[2][32];
+          load64(s, tmem + lanes + (step & 1) * kTile + half * 64);
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            float a, b;
+            unpack_f32x2(fma_f32x2(pack_u32x2(s[i >> 5][i & 31], s[i >> 5][(i & 31) + 1]), c2, nl2), a, b);
+            s[i >> 5][i & 31] = __float_as_uint(ex2_approx(a));
+            s[i >> 5][(i & 31) + 1] = __float_as_uint(ex2_approx(b));
+          }
+          if (!(ok = mbar_wait_warp(&sh.pfull, step & 1, ctx))) break;
+          tc_fence_after();
+          load64(g, t_dp + lanes + half * 64);
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            float a, b;
+            unpack_f32x2(add_f32x2(pack_u32x2(g[i >> 5][i & 31], g[i >> 5][(i & 31) + 1]), dl2), a, b);
+            s[i >> 5][i & 31] = __float_as_uint(a * as_f(s[i >> 5][i & 31]));
+            s[i >> 5][(i & 31) + 1] = __float_as_uint(b * as_f(s[i >> 5][(i & 31) + 1]));
+          }
+          if (j == n - 1) {  // the diagonal: keys after the row
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (half * 64 + i > row) s[i >> 5][i & 31] = 0;
+          }
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            pk[i] = pack_bf16x2(as_f(s[i >> 4][2 * (i & 15)]), as_f(s[i >> 4][2 * (i & 15) + 1]));
+          tmem_st_32x32b_x32(t_dp + lanes + half * 64, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.dsfull);
+        }
+        if (!ok || !mbar_wait_warp(&sh.accfull, units & 1, ctx)) break;
+        ++units;
+        tc_fence_after();
+        const int r = u.q0 + row;
+#pragma unroll
+        for (int d = 0; d < DP / 2; d += 32) {
+          uint32_t o[32];
+          const int d0 = half * (DP / 2) + d;
+          tmem_ld_32x32b_x32(t_acc + lanes + d0, o);
+          tmem_ld_wait();
+          if (r < u.len)
+            store_row(p.dq + ((int64_t)(u.start + r) * p.q_heads + u.head) * p.head_dim + d0, o,
+                      p.scale, p.head_dim - d0);
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t ids = make_idesc(false, false, kTile, kTile);
+      constexpr uint32_t idq = make_idesc(false, true, kTile, DP);
+      const uint32_t q0 = smem_u32(smem), do0 = q0 + C::kTileBytes;
+      const uint32_t kr = smem_u32(smem + C::kRingK), vr = smem_u32(smem + C::kRingV);
+      uint32_t base = 0, units = 0;  // steps before this unit
+      bool ok = true;
+      auto issue_s = [&](uint32_t t) {
+        if (!(ok = ok && mbar_wait(&sh.kfull[t % C::kK], (t / C::kK) & 1, ctx))) return;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)
+          mma_issue(tmem + (t & 1) * kTile, desc_k(q0, kk),
+                    desc_k(kr + (t % C::kK) * C::kTileBytes, kk), ids, kk != 0);
+        mma_commit(&sh.sfull[t & 1]);
+      };
+      auto issue_dp = [&](uint32_t t) {
+        if (!(ok = ok && mbar_wait(&sh.vfull[t % C::kV], (t / C::kV) & 1, ctx))) return;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)
+          mma_issue(t_dp, desc_k(do0, kk), desc_k(vr + (t % C::kV) * C::kTileBytes, kk), ids, kk != 0);
+        mma_commit(&sh.vempty[t % C::kV]);
+        mma_commit(&sh.pfull);
+      };
+      for (uint32_t it = 0; ok; ++it) {
+        if (!mbar_wait(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+        const AttnUnit u = sh.unit[it & 1];
+        if (u.head < 0) break;
+        if (u.len > 0) {
+          const int n = u.q0 / kTile + 1;
+          if (!mbar_wait(&sh.qfull, units & 1, ctx)) break;
+          // the diagonal key tile is cleaned before any product reads it
+          if (!mbar_wait(&sh.clean[it & 1], (it >> 1) & 1, ctx)) break;
+          issue_s(base);
+          issue_dp(base);
+          for (int i = 0; i < n && ok; ++i) {
+            const uint32_t t = base + i;
+            if (i + 1 < n) issue_s(t + 1);
+            if (!(ok = ok && mbar_wait(&sh.dsfull, t & 1, ctx))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_issue_ts(t_acc, t_dp + (kk >> 2) * 64 + (kk & 3) * 8,
+                           desc_mn(kr + (t % C::kK) * C::kTileBytes, kk), idq, (i | kk) != 0);
+            mma_commit(&sh.kempty[t % C::kK]);
+            if (i + 1 < n) issue_dp(t + 1);
+            // Q and dout are free once the last S and dP are done
+            if (i + 2 == n || n == 1) mma_commit(&sh.qempty);
+          }
+          if (!ok) break;
+          mma_commit(&sh.accfull);
+          base += n;
+          ++units;
+        } else {
+          // the phases of clean and stats go by units, empty ones included
+        }
+        mbar_arrive(&sh.uempty[it & 1]);
+      }
+      mma_commit(&sh.mma_done);
+      mbar_wait_drain(&sh.mma_done, 0, p.timeout_ns);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ units, loads
+    if (lane == 0) {
+      prefetch_tensormap(&tq);
+      prefetch_tensormap(&tk);
+      prefetch_tensormap(&tv);
+      prefetch_tensormap(&tdo);
+    }
+    UnitWalk walk;
+    walk.init(p, kTile);
+    const int64_t total = (int64_t)walk.total() * p.q_heads;
+    uint32_t t = 0, units = 0;
+    uint32_t loaded_k = 0, loaded_v = 0;
+    bool ok = true;
+    for (uint32_t it = 0; ok; ++it) {
+      const int64_t id = dealt_unit(it, blockIdx.x, gridDim.x);
+      AttnUnit u{};
+      u.head = -1;
+      if (id < total) {
+        u = walk.at((int)(id / p.q_heads));
+        u.head = (int)(id % p.q_heads);
+      }
+      if (lane == 0) {
+        ok = mbar_wait(&sh.uempty[it & 1], ((it >> 1) & 1) ^ 1, ctx);
+        if (ok) {
+          sh.unit[it & 1] = u;
+          mbar_arrive(&sh.ufull[it & 1]);
+        }
+        if (ok && u.len > 0) {
+          const int kvh = u.head / p.group;
+          if ((ok = mbar_wait(&sh.qempty, (units & 1) ^ 1, ctx))) {
+            mbar_arrive_expect_tx(&sh.qfull, 2 * C::kTileBytes);
+            for (int b = 0; b < C::kBoxes; ++b) {
+              tma_load_3d(smem + b * kBoxBytes, &tq, &sh.qfull, b * 64, u.head, u.start + u.q0);
+              tma_load_3d(smem + C::kTileBytes + b * kBoxBytes, &tdo, &sh.qfull, b * 64, u.head,
+                          u.start + u.q0);
+            }
+            ++units;
+          }
+          for (int j = u.q0 / kTile; j >= 0 && ok; --j, ++t) {
+            const int ks = t % C::kK, vs = t % C::kV, r = u.start + j * kTile;
+            if (!(ok = mbar_wait(&sh.kempty[ks], ((t / C::kK) & 1) ^ 1, ctx))) break;
+            mbar_arrive_expect_tx(&sh.kfull[ks], C::kTileBytes);
+            for (int b = 0; b < C::kBoxes; ++b)
+              tma_load_3d(smem + C::kRingK + ks * C::kTileBytes + b * kBoxBytes, &tk, &sh.kfull[ks],
+                          b * 64, kvh, r);
+            ++loaded_k;
+            if (!(ok = mbar_wait(&sh.vempty[vs], ((t / C::kV) & 1) ^ 1, ctx))) break;
+            mbar_arrive_expect_tx(&sh.vfull[vs], C::kTileBytes);
+            for (int b = 0; b < C::kBoxes; ++b)
+              tma_load_3d(smem + C::kRingV + vs * C::kTileBytes + b * kBoxBytes, &tv, &sh.vfull[vs],
+                          b * 64, kvh, r);
+            ++loaded_v;
+          }
+        }
+      }
+      ok = __shfl_sync(~0u, ok, 0);
+      if (u.head < 0) break;
+    }
+    if (!ok && lane == 0) {
+      if (units) mbar_wait_drain(&sh.qfull, (units - 1) & 1, p.timeout_ns);
+      for (uint32_t i = loaded_k > C::kK ? loaded_k - C::kK : 0; i < loaded_k; ++i)
+        mbar_wait_drain(&sh.kfull[i % C::kK], (i / C::kK) & 1, p.timeout_ns);
+      for (uint32_t i = loaded_v > C::kV ? loaded_v - C::kV : 0; i < loaded_v; ++i)
+        mbar_wait_drain(&sh.vfull[i % C::kV], (i / C::kV) & 1, p.timeout_ns);
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ delta, diagonal key tiles
+    const int w = warp - 12;
+    uint32_t t = 0;
+    for (uint32_t it = 0;; ++it) {
+      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      const AttnUnit u = sh.unit[it & 1];
+      if (u.head < 0) break;
+      if (u.len > 0) {
+        // lane r keeps row r's statistics; 16 lanes hold the 8 values each of a row
+        const int l = lane & 15, mine = u.q0 + w * 32 + lane;
+        const int64_t at = (int64_t)u.head * p.tokens + u.start;
+        const bool has = l * 8 < p.head_dim;
+        const float lse = mine < u.len ? p.lse[at + mine] : 0.f;
+        float delta = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < 32; i += 2) {
+          const int r = u.q0 + w * 32 + i + (lane >> 4);
+          uint4 a = make_uint4(0, 0, 0, 0), b = a;
+          if (has && r < u.len) {
+            const int64_t o = ((int64_t)(u.start + r) * p.q_heads + u.head) * p.head_dim + l * 8;
+            a = *reinterpret_cast<const uint4*>(p.out + o);
+            b = *reinterpret_cast<const uint4*>(p.dout + o);
+          }
+          const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sum = fmaf(as_f(x[e] << 16), as_f(y[e] << 16), sum);
+            sum = fmaf(as_f(x[e] & 0xffff0000u), as_f(y[e] & 0xffff0000u), sum);
+          }
+#pragma unroll
+          for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+          const float other = __shfl_xor_sync(~0u, sum, 16);
+          if (lane == i) delta = sum;            // lanes 0-15 hold row i,
+          if (lane == i + 1) delta = lane < 16 ? other : sum;  // 16-31 row i + 1
+          if (lane == i && lane >= 16) delta = other;
+        }
+        if (mine < u.len) {
+          const float nl = -lse * kLog2e;
+          stat[(it & 1) * 256 + w * 32 + lane] = nl;
+          stat[(it & 1) * 256 + 128 + w * 32 + lane] = delta;
+          p.nlse[at + mine] = nl;
+          p.delta[at + mine] = delta;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.stats[it & 1]);
+        bool ok = true;
+        for (int j = u.q0 / kTile; j >= 0; --j, ++t) {
+          const uint32_t s = t % C::kK;
+          if (!(ok = mbar_wait_warp(&sh.kfull[s], (t / C::kK) & 1, ctx))) break;
+          if (j == u.q0 / kTile) {
+            clean_tile(smem + C::kRingK + s * C::kTileBytes, C::kBoxes, u.len - u.q0, w, 4, sh.flags[w]);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.clean[it & 1]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.kempty[s]);
+        }
+        if (!ok) break;
+      } else if (lane == 0) {
+        mbar_arrive(&sh.stats[it & 1]);
+        mbar_arrive(&sh.clean[it & 1]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ----------------------------------------------------------------------------
+// dk, dv
+// ----------------------------------------------------------------------------
+// Products with keys as rows: S^T = K Q^T, dP^T = V dout^T (128 keys x 128
+// queries), dV += P^T dout, dK += dS^T Q with P^T and dS^T read from TMEM, where
+// they overwrite S^T and dP^T.  While the threads make P of a step, the tensor
+// cores run the last step's dK and this one's dP; while they make dS, this
+// step's dV and the next S.
+template <int DP>
+struct DkvCfg {
+  static constexpr int kBoxes = DP / 64;
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;
+  static constexpr int kStages = DP == 128 ? 2 : 4;  // Q and dout tiles
+  static constexpr int kRing = 2 * kTileBytes;       // after K and V; a stage is Q, dout
+  static constexpr int kBars = kRing + 2 * kStages * kTileBytes;
+  static constexpr int kStatStages = 4;              // -lse and delta of 128 queries
+  static constexpr int kSmem = kBars + kStatStages * 1024 + 1024;
+};
+
+struct DkvShared {
+  uint64_t qfull[4], qempty[4], gfull[4], gempty[4];  // Q and dout tiles
+  uint64_t tfull[4], tempty[4];                       // statistics
+  uint64_t kvfull, kvempty;
+  uint64_t sfull, dpfull, pfull, dsfull, accfull;
+  uint64_t clean[4];                                  // by stage
+  uint64_t ufull[2], uempty[2];
+  uint64_t mma_done;
+  AttnUnit unit[2];
+  uint32_t flags[4][2][4];
+  uint32_t dirty[2][4];  // by unit parity and cleaning warp: non-finite dout on the diagonal
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(DkvShared) <= 1024, "barrier area");
+
+// Whether the query tile `i` of a unit whose diagonal tile is `first` has to be
+// cleaned: the diagonal one, and a ragged last one.
+__device__ __forceinline__ bool dkv_cleaned(const AttnUnit& u, int i, int first) {
+  return i == first || u.len - i * kTile < kTile;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+          const AttnBwdParams p) {
+  using C = DkvCfg<DP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  DkvShared& sh = *reinterpret_cast<DkvShared*>(smem + C::kBars + C::kStatStages * 1024);
+  float* stat = reinterpret_cast<float*>(smem + C::kBars);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const WaitCtx ctx{&sh.abort, p.err_word, p.timeout_ns};
+  const int heads = p.kv_heads * p.splits, per_split = p.group / p.splits;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      // a Q slot is given back by the MMAs and by the cleaning warps once they have
+      // seen its step's tiles
+      mbar_init(&sh.qfull[i], 1), mbar_init(&sh.qempty[i], 5);
+      mbar_init(&sh.gfull[i], 1), mbar_init(&sh.gempty[i], 1);
+      mbar_init(&sh.clean[i], 4);
+    }
+    for (int i = 0; i < C::kStatStages; ++i) mbar_init(&sh.tfull[i], 1), mbar_init(&sh.tempty[i], 8);
+    mbar_init(&sh.kvfull, 1);
+    mbar_init(&sh.kvempty, 1);
+    mbar_init(&sh.sfull, 1);
+    mbar_init(&sh.dpfull, 1);
+    mbar_init(&sh.pfull, 8);
+    mbar_init(&sh.dsfull, 8);
+    mbar_init(&sh.accfull, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.ufull[i], 1);
+      mbar_init(&sh.uempty[i], 14);  // 8 compute, the MMA lane, statistics, 4 cleaning warps
+    }
+    mbar_init(&sh.mma_done, 1);
+    sh.abort = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t t_s = tmem, t_dp = tmem + kTile, t_dv = tmem + 2 * kTile, t_dk = tmem + 3 * kTile;
+
+  if (warp >= 8) regs_down<kBwdOtherRegs>();
+  if (warp < 8) {
+    // ------------------------------------------------------------ compute
+    regs_up<kBwdComputeRegs>();
+    const int half = warp >> 2, row = threadIdx.x & 127;  // 64 queries; a key
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+    const float c = p.scale * kLog2e;
+    const uint64_t c2 = pack_f32x2(c, c);
+    uint32_t step = 0, units = 0;
+    for (uint32_t it = 0;; ++it) {
+      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      const AttnUnit u = sh.unit[it & 1];
+      if (u.head < 0) break;
+      const int kvh = u.head / p.splits, split = u.head % p.splits;
+      bool ok = true;
+      if (u.len == 0) {  // rows of no sequence
+        if (row < u.rows) {
+          const int64_t at = ((int64_t)(u.start + row) * p.kv_heads + kvh) * p.head_dim;
+          const int64_t size = (int64_t)p.tokens * p.kv_heads * p.head_dim;
+          uint4* o = p.splits == 1
+                         ? reinterpret_cast<uint4*>((half ? p.dk : p.dv) + at)
+                         : reinterpret_cast<uint4*>(p.partial + (half ? 0 : p.splits) * size +
+                                                    split * size + at);
+          for (int d = 0; d < p.head_dim / (p.splits == 1 ? 8 : 4); ++d) o[d] = make_uint4(0, 0, 0, 0);
+        }
+      } else {
+        const int first = u.q0 / kTile, end = (u.len + kTile - 1) / kTile;
+        for (int h = 0; h < per_split && ok; ++h)
+          for (int i = first; i < end; ++i, ++step) {
+            const uint32_t ts = step % C::kStatStages;
+            if (!(ok = mbar_wait_warp(&sh.tfull[ts], (step / C::kStatStages) & 1, ctx))) break;
+            const float* nl = stat + ts * 256 + half * 64;
+            const bool diag = i == first, masked = dkv_cleaned(u, i, first);
+            const int limit = u.len - i * kTile - half * 64;  // queries of this sequence
+            const int from = diag ? row - half * 64 : 0;      // ... not before the key
+            if (!(ok = mbar_wait_warp(&sh.sfull, step & 1, ctx))) break;
+            tc_fence_after();
+            uint32_t s[2][32];
+            load64(s, t_s + lanes + half * 64);
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+              const float4 b = *reinterpret_cast<const float4*>(nl + e);
+              uint32_t(&r)[32] = s[e >> 5];
+              const int i0 = e & 31;
+              float x, y;
+              unpack_f32x2(fma_f32x2(pack_u32x2(r[i0], r[i0 + 1]), c2, pack_f32x2(b.x, b.y)), x, y);
+              r[i0] = __float_as_uint(ex2_approx(x));
+              r[i0 + 1] = __float_as_uint(ex2_approx(y));
+              unpack_f32x2(fma_f32x2(pack_u32x2(r[i0 + 2], r[i0 + 3]), c2, pack_f32x2(b.z, b.w)), x, y);
+              r[i0 + 2] = __float_as_uint(ex2_approx(x));
+              r[i0 + 3] = __float_as_uint(ex2_approx(y));
+            }
+            if (masked) {
+#pragma unroll
+              for (int e = 0; e < 64; ++e)
+                if (e < from || e >= limit) s[e >> 5][e & 31] = 0;
+            }
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              pk[e] = pack_bf16x2(as_f(s[e >> 4][2 * (e & 15)]), as_f(s[e >> 4][2 * (e & 15) + 1]));
+            tmem_st_32x32b_x32(t_s + lanes + half * 64, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.pfull);
+            if (!(ok = mbar_wait_warp(&sh.dpfull, step & 1, ctx))) break;
+            tc_fence_after();
+            uint32_t g[2][32];
+            load64(g, t_dp + lanes + half * 64);
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+              const float4 b = *reinterpret_cast<const float4*>(nl + 128 + e);
+              uint32_t(&r)[32] = g[e >> 5];
+              const uint32_t(&q)[32] = s[e >> 5];
+              const int i0 = e & 31;
+              r[i0] = __float_as_uint((as_f(r[i0]) - b.x) * as_f(q[i0]));
+              r[i0 + 1] = __float_as_uint((as_f(r[i0 + 1]) - b.y) * as_f(q[i0 + 1]));
+              r[i0 + 2] = __float_as_uint((as_f(r[i0 + 2]) - b.z) * as_f(q[i0 + 2]));
+              r[i0 + 3] = __float_as_uint((as_f(r[i0 + 3]) - b.w) * as_f(q[i0 + 3]));
+            }
+            if (masked) {
+#pragma unroll
+              for (int e = 0; e < 64; ++e)
+                if (e < from || e >= limit) g[e >> 5][e & 31] = 0;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              pk[e] = pack_bf16x2(as_f(g[e >> 4][2 * (e & 15)]), as_f(g[e >> 4][2 * (e & 15) + 1]));
+            tmem_st_32x32b_x32(t_dp + lanes + half * 64, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&sh.dsfull);
+              mbar_arrive(&sh.tempty[ts]);
+            }
+          }
+        if (!ok || !mbar_wait_warp(&sh.accfull, units & 1, ctx)) break;
+        ++units;
+        tc_fence_after();
+        // warps 0-3 write dV, warps 4-7 dK
+        const int r = u.q0 + row;
+        const bool live = r < u.len;
+        const int64_t at = ((int64_t)(u.start + r) * p.kv_heads + kvh) * p.head_dim;
+        const uint32_t* dw = sh.dirty[it & 1];
+        const bool dirty = half == 0 && (dw[0] | dw[1] | dw[2] | dw[3]);
+#pragma unroll
+        for (int d = 0; d < DP; d += 32) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32((half ? t_dk : t_dv) + lanes + d, o);
+          tmem_ld_wait();
+          if (!live) continue;
+          if (dirty) {  // add back the non-finite values of dout that this key sees
+            for (int h = 0; h < per_split; ++h)
+              for (int i = row; i < kTile && u.q0 + i < u.len; ++i) {
+                const bf16* g = p.dout + ((int64_t)(u.start + u.q0 + i) * p.q_heads + kvh * p.group +
+                                          split * per_split + h) * p.head_dim + d;
+                for (int e = 0; e < 32 && d + e < p.head_dim; ++e) {
+                  const float v = __bfloat162float(g[e]);
+                  if (!isfinite(v)) {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                      if (x == e) o[x] = __float_as_uint(as_f(o[x]) + v);
+                  }
+                }
+              }
+          }
+          const float scale = half ? p.scale : 1.f;
+          if (p.splits == 1) {
+            store_row((half ? p.dk : p.dv) + at + d, o, scale, p.head_dim - d);
+          } else {
+            const int64_t size = (int64_t)p.tokens * p.kv_heads * p.head_dim;
+            float* to = p.partial + ((half ? 0 : p.splits) + split) * size + at + d;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              if (d + e < p.head_dim)
+                *reinterpret_cast<float4*>(to + e) =
+                    make_float4(as_f(o[e]) * scale, as_f(o[e + 1]) * scale, as_f(o[e + 2]) * scale,
+                                as_f(o[e + 3]) * scale);
+          }
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t ids = make_idesc(false, false, kTile, kTile);
+      constexpr uint32_t idg = make_idesc(false, true, kTile, DP);
+      const uint32_t k0 = smem_u32(smem), v0 = k0 + C::kTileBytes;
+      const uint32_t ring = smem_u32(smem + C::kRing);
+      uint32_t base = 0, units = 0, nclean = 0;  // nclean: next phase of each stage's barrier
+      bool ok = true;
+      auto q_tile = [&](uint32_t t) { return ring + (t % C::kStages) * 2 * C::kTileBytes; };
+      // waits for step t's Q (S and later dK read it) and, if it is cleaned, for that
+      auto issue_s = [&](uint32_t t, bool cleaned) {
+        const uint32_t s = t % C::kStages;
+        if (!(ok = ok && mbar_wait(&sh.qfull[s], (t / C::kStages) & 1, ctx))) return;
+        if (cleaned) {
+          if (!(ok = mbar_wait(&sh.clean[s], (nclean >> s) & 1, ctx))) return;
+          nclean ^= 1u << s;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)
+          mma_issue(t_s, desc_k(k0, kk), desc_k(q_tile(t), kk), ids, kk != 0);
+        mma_commit(&sh.sfull);
+      };
+      auto issue_dp = [&](uint32_t t) {
+        const uint32_t s = t % C::kStages;
+        if (!(ok = ok && mbar_wait(&sh.gfull[s], (t / C::kStages) & 1, ctx))) return;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)
+          mma_issue(t_dp, desc_k(v0, kk), desc_k(q_tile(t) + C::kTileBytes, kk), ids, kk != 0);
+        mma_commit(&sh.dpfull);
+      };
+      for (uint32_t it = 0; ok; ++it) {
+        if (!mbar_wait(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+        const AttnUnit u = sh.unit[it & 1];
+        if (u.head < 0) break;
+        if (u.len > 0) {
+          const int first = u.q0 / kTile, tiles = (u.len + kTile - 1) / kTile - first;
+          const int n = tiles * per_split;
+          if (!mbar_wait(&sh.kvfull, units & 1, ctx)) break;
+          issue_s(base, true);
+          issue_dp(base);
+          int i = 0;  // query tile of step x within its head
+          for (int x = 0; x < n && ok; ++x) {
+            const uint32_t t = base + x;
+            if (!(ok = mbar_wait(&sh.pfull, t & 1, ctx))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_issue_ts(t_dv, t_s + (kk >> 2) * 64 + (kk & 3) * 8,
+                           desc_mn(q_tile(t) + C::kTileBytes, kk), idg, (x | kk) != 0);
+            mma_commit(&sh.gempty[t % C::kStages]);
+            if (++i == tiles) i = 0;
+            if (x + 1 < n) issue_s(t + 1, dkv_cleaned(u, first + i, first));
+            if (!(ok = ok && mbar_wait(&sh.dsfull, t & 1, ctx))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_issue_ts(t_dk, t_dp + (kk >> 2) * 64 + (kk & 3) * 8, desc_mn(q_tile(t), kk), idg,
+                           (x | kk) != 0);
+            mma_commit(&sh.qempty[t % C::kStages]);
+            if (x + 1 < n) issue_dp(t + 1);
+            if (x + 2 == n || n == 1) mma_commit(&sh.kvempty);
+          }
+          if (!ok) break;
+          mma_commit(&sh.accfull);
+          base += n;
+          ++units;
+        }
+        mbar_arrive(&sh.uempty[it & 1]);
+      }
+      mma_commit(&sh.mma_done);
+      mbar_wait_drain(&sh.mma_done, 0, p.timeout_ns);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ units, loads
+    if (lane == 0) {
+      prefetch_tensormap(&tq);
+      prefetch_tensormap(&tk);
+      prefetch_tensormap(&tv);
+      prefetch_tensormap(&tdo);
+    }
+    UnitWalk walk;
+    walk.init(p, kTile);
+    const int64_t total = (int64_t)walk.total() * heads;
+    uint32_t nq = 0, ng = 0, units = 0;
+    bool ok = true;
+    for (uint32_t it = 0; ok; ++it) {
+      const int64_t id = dealt_unit(it, blockIdx.x, gridDim.x);
+      AttnUnit u{};
+      u.head = -1;
+      if (id < total) {
+        u = walk.at((int)(id / heads));
+        u.head = (int)(id % heads);
+        // the walk counts from the sequence's start, key tiles have the most
+        // queries there: mirrored
+        if (u.len > 0) u.q0 = ((u.len + kTile - 1) / kTile - 1) * kTile - u.q0;
+      }
+      if (lane == 0) {
+        ok = mbar_wait(&sh.uempty[it & 1], ((it >> 1) & 1) ^ 1, ctx);
+        if (ok) {
+          sh.unit[it & 1] = u;
+          mbar_arrive(&sh.ufull[it & 1]);
+        }
+        if (ok && u.len > 0) {
+          const int kvh = u.head / p.splits;
+          const int h0 = kvh * p.group + (u.head % p.splits) * per_split;
+          if ((ok = mbar_wait(&sh.kvempty, (units & 1) ^ 1, ctx))) {
+            mbar_arrive_expect_tx(&sh.kvfull, 2 * C::kTileBytes);
+            for (int b = 0; b < C::kBoxes; ++b) {
+              tma_load_3d(smem + b * kBoxBytes, &tk, &sh.kvfull, b * 64, kvh, u.start + u.q0);
+              tma_load_3d(smem + C::kTileBytes + b * kBoxBytes, &tv, &sh.kvfull, b * 64, kvh,
+                          u.start + u.q0);
+            }
+            ++units;
+          }
+          for (int h = h0; h < h0 + per_split && ok; ++h)
+            for (int i = u.q0; i < u.len; i += kTile) {
+              const int s = nq % C::kStages, ph = ((nq / C::kStages) & 1) ^ 1;
+              uint8_t* at = smem + C::kRing + s * 2 * C::kTileBytes;
+              if (!(ok = mbar_wait(&sh.qempty[s], ph, ctx))) break;
+              mbar_arrive_expect_tx(&sh.qfull[s], C::kTileBytes);
+              for (int b = 0; b < C::kBoxes; ++b)
+                tma_load_3d(at + b * kBoxBytes, &tq, &sh.qfull[s], b * 64, h, u.start + i);
+              ++nq;
+              if (!(ok = mbar_wait(&sh.gempty[s], ph, ctx))) break;
+              mbar_arrive_expect_tx(&sh.gfull[s], C::kTileBytes);
+              for (int b = 0; b < C::kBoxes; ++b)
+                tma_load_3d(at + C::kTileBytes + b * kBoxBytes, &tdo, &sh.gfull[s], b * 64, h,
+                            u.start + i);
+              ++ng;
+            }
+        }
+      }
+      ok = __shfl_sync(~0u, ok, 0);
+      if (u.head < 0) break;
+    }
+    if (!ok && lane == 0) {
+      if (units) mbar_wait_drain(&sh.kvfull, (units - 1) & 1, p.timeout_ns);
+      for (uint32_t i = nq > C::kStages ? nq - C::kStages : 0; i < nq; ++i)
+        mbar_wait_drain(&sh.qfull[i % C::kStages], (i / C::kStages) & 1, p.timeout_ns);
+      for (uint32_t i = ng > C::kStages ? ng - C::kStages : 0; i < ng; ++i)
+        mbar_wait_drain(&sh.gfull[i % C::kStages], (i / C::kStages) & 1, p.timeout_ns);
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ statistics of the queries
+    uint32_t step = 0;
+    for (uint32_t it = 0;; ++it) {
+      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      const AttnUnit u = sh.unit[it & 1];
+      if (u.head < 0) break;
+      const int kvh = u.head / p.splits;
+      const int h0 = kvh * p.group + (u.head % p.splits) * per_split;
+      bool ok = true;
+      if (u.len > 0)
+        for (int h = h0; h < h0 + per_split && ok; ++h)
+          for (int i = u.q0; i < u.len; i += kTile, ++step) {
+            const uint32_t ts = step % C::kStatStages;
+            const int64_t at = (int64_t)h * p.tokens + u.start + i;
+            float nl[4], dl[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = e * 32 + lane;
+              const bool in = i + r < u.len;
+              nl[e] = in ? p.nlse[at + r] : 0.f;
+              dl[e] = in ? p.delta[at + r] : 0.f;
+            }
+            if (!(ok = mbar_wait_warp(&sh.tempty[ts], ((step / C::kStatStages) & 1) ^ 1, ctx))) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              stat[ts * 256 + e * 32 + lane] = nl[e];
+              stat[ts * 256 + 128 + e * 32 + lane] = dl[e];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.tfull[ts]);
+          }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ cleaned tiles
+    const int w = warp - 12;
+    uint32_t step = 0;
+    for (uint32_t it = 0;; ++it) {
+      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      const AttnUnit u = sh.unit[it & 1];
+      if (u.head < 0) break;
+      bool ok = true;
+      if (lane == 0) sh.dirty[it & 1][w] = 0;
+      if (u.len > 0) {
+        const int first = u.q0 / kTile, end = (u.len + kTile - 1) / kTile;
+        for (int h = 0; h < per_split && ok; ++h)
+          for (int i = first; i < end; ++i, ++step) {
+            const uint32_t s = step % C::kStages, ph = (step / C::kStages) & 1;
+            uint8_t* at = smem + C::kRing + s * 2 * C::kTileBytes;
+            const int valid = u.len - i * kTile;
+            if (!(ok = mbar_wait_warp(&sh.qfull[s], ph, ctx))) break;
+            if (i == first) clean_tile(at, C::kBoxes, valid, w, 4, sh.flags[w][0]);
+            else if (valid < kTile) zero_rows(at, C::kBoxes, valid, w, 4);
+            if (!(ok = mbar_wait_warp(&sh.gfull[s], ph, ctx))) break;
+            if (i == first) {
+              uint32_t* fl = sh.flags[w][1];
+              clean_tile(at + C::kTileBytes, C::kBoxes, valid, w, 4, fl);
+              __syncwarp();
+              if (lane == 0 && (fl[0] | fl[1] | fl[2] | fl[3])) sh.dirty[it & 1][w] = 1;
+            } else if (valid < kTile) {
+              zero_rows(at + C::kTileBytes, C::kBoxes, valid, w, 4);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              if (dkv_cleaned(u, i, first)) mbar_arrive(&sh.clean[s]);
+              mbar_arrive(&sh.qempty[s]);
+            }
+          }
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// dk, dv = sums of the splits' partial ones, in a fixed order.
+__global__ void __launch_bounds__(256) attn_sum_splits(const AttnBwdParams p) {
+  const int64_t size = (int64_t)p.tokens * p.kv_heads * p.head_dim;
+  const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
+  if (i >= size) return;
+  const float* from = p.partial + (int64_t)blockIdx.y * p.splits * size + i;
+  float4 t = *reinterpret_cast<const float4*>(from);
+  for (int s = 1; s < p.splits; ++s) {
+    const float4 x = *reinterpret_cast<const float4*>(from + s * size);
+    t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
+  }
+  *reinterpret_cast<uint2*>((blockIdx.y ? p.dv : p.dk) + i) =
+      make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+}
+
+}  // namespace flce

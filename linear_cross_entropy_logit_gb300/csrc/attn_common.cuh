@@ -180,4 +180,11 @@ __device__ __forceinline__ void clean_tile(uint8_t* tile, int boxes, int valid, 
   }
 }
 
+// The part of clean_tile that zeroes the rows from `valid` on.
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int boxes, int valid, int w, int warps) {
+  for (int i = w * 32 + (threadIdx.x & 31); i < boxes * kTile * 8; i += warps * 32)
+    if (((i >> 3) & (kTile - 1)) >= valid)
+      reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
+}
+
 }  // namespace flce

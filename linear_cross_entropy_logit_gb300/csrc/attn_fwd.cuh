@@ -47,7 +47,7 @@ struct FwdCfg {
   static constexpr int kSlots = DP == 128 ? 4 : 8;  // K and V tiles in flight
   static constexpr int kRing = 2 * kTileBytes;      // after the two Q tiles
   static constexpr int kBars = kRing + kSlots * kTileBytes;
-  static constexpr int kSmem = kBars + 512 + 1024;  // + alignment of the base
+  static constexpr int kSmem = kBars + 512;
 };
 
 struct FwdShared {
@@ -75,15 +75,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
          const __grid_constant__ CUtensorMap tv, const AttnParams p) {
   using C = FwdCfg<DP>;
-  extern __shared__ uint8_t raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + C::kRing;
   FwdShared& sh = *reinterpret_cast<FwdShared*>(smem + C::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtx ctx{&sh.abort, p.err_word, p.timeout_ns};
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kSlots; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
+    // K tiles lie in the even slots, V tiles in the odd ones; a V slot is given back
+    // by the MMAs and by both cleaning warps, which so see every V tile pass
+    for (int i = 0; i < C::kSlots; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], i & 1 ? 3 : 1);
     mbar_init(&sh.qfull, 1);
     mbar_init(&sh.qempty, 1);
     for (int i = 0; i < 2; ++i) {
@@ -415,15 +416,20 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
         int n0, n1;
         unit_tiles(u, n0, n1);
         const int last = max(n0, n1) - 1;
-        for (int j = last; j >= n0 - 1; --j) {
+        for (int j = last; j >= 0; --j) {
           const uint32_t pos = base + 2 * (last - j) + 1;
           const int f = j - (n0 - 1);
           if (!(ok = mbar_wait_warp(&sh.full[pos % C::kSlots], (pos / C::kSlots) & 1, ctx))) break;
-          clean_tile(ring + (pos % C::kSlots) * C::kTileBytes, C::kBoxes, u.len - j * kTile, w, 2,
-                     sh.flags[it & 1][f][w]);
-          fence_proxy_async_shared();
+          if (f >= 0) {
+            clean_tile(ring + (pos % C::kSlots) * C::kTileBytes, C::kBoxes, u.len - j * kTile, w, 2,
+                       sh.flags[it & 1][f][w]);
+            fence_proxy_async_shared();
+          }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.clean[it & 1][f]);
+          if (lane == 0) {
+            if (f >= 0) mbar_arrive(&sh.clean[it & 1][f]);
+            mbar_arrive(&sh.empty[pos % C::kSlots]);
+          }
         }
         base += 2 * (last + 1);
       }

@@ -1314,7 +1314,14 @@ flce_options defaults(int64_t ignore_index, float smoothing, flce_reduction redu
 namespace flce {
 namespace host {
 
-flce_status device(int* dev, int* sms) { return device_check(dev, sms); }
+flce_status device(int* dev, int* sms) {
+  const flce_status s = device_check(dev, sms);
+  if (s != FLCE_OK) return s;
+  // A thread that has made no runtime call yet (autograd's) has no context,
+  // which encoding a tensor map needs.
+  FLCE_CUDA(cudaSetDevice(*dev));
+  return FLCE_OK;
+}
 flce_status fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
 flce_status fail_text(const char* what) {
   g_last_cuda_error = what;

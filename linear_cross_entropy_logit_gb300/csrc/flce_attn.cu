@@ -6,8 +6,8 @@
 #include <cstdio>
 #include <mutex>
 
+#include "attn_bwd.cuh"
 #include "attn_fwd.cuh"
-#include "attn_simple.cuh"
 #include "host_util.h"
 
 using namespace flce;
@@ -47,8 +47,7 @@ flce_status check(const flce_attention_desc* d, const void* const* ptrs, int n, 
   return FLCE_OK;
 }
 
-AttnIn params(const flce_attention_desc* d, const int32_t* cu, int32_t* err_word) {
-  AttnIn p{};
+void fill(AttnParams& p, const flce_attention_desc* d, const int32_t* cu, int32_t* err_word) {
   p.cu = cu;
   p.n_seqs = (int)d->sequences;
   p.tokens = (int)d->tokens;
@@ -57,15 +56,10 @@ AttnIn params(const flce_attention_desc* d, const int32_t* cu, int32_t* err_word
   p.group = p.q_heads / p.kv_heads;
   p.head_dim = (int)d->head_dim;
   p.scale = d->scale;
-  p.q_row = d->q_row;
-  p.q_head = d->q_head;
-  p.k_row = d->k_row;
-  p.k_head = d->k_head;
   p.v_row = d->v_row;
   p.v_head = d->v_head;
   p.err_word = err_word;
   p.timeout_ns = host::kTimeoutNs;
-  return p;
 }
 
 // Work units of `rows` rows at most: every sequence's last and the gaps before
@@ -107,8 +101,62 @@ flce_status set_smem(Setup& s, Kern kern, int smem) {
   return s.err == cudaSuccess ? FLCE_OK : host::fail(s.err, "cudaFuncSetAttribute");
 }
 
-size_t delta_bytes(const flce_attention_desc* d) {
-  return host::align_up((size_t)d->tokens * d->q_heads * sizeof(float));
+// CTAs that share the query heads of one key / value head in attn_dkdv, each
+// summing its own (a divisor of their number): the fewest that give kDealt
+// units for every SM, without which the CTAs of a long sequence's first key
+// tiles run on after the others are done.
+constexpr int64_t kDealt = 2;
+int choose_splits(const flce_attention_desc* d, int sms) {
+  const int group = (int)(d->q_heads / d->kv_heads);
+  const int64_t units = std::max<int64_t>(1, d->tokens / kTile) * d->kv_heads;
+  for (int s = 1; s < group; ++s)
+    if (group % s == 0 && units * s >= kDealt * sms) return s;
+  return group;
+}
+
+struct BwdPlan {
+  int splits;
+  size_t off_delta, off_partial, total;
+};
+BwdPlan plan_backward(const flce_attention_desc* d, int sms) {
+  BwdPlan b;
+  const size_t rows = host::align_up((size_t)d->tokens * d->q_heads * sizeof(float));
+  b.splits = choose_splits(d, sms);
+  b.off_delta = rows;
+  b.off_partial = 2 * rows;
+  b.total = b.off_partial;
+  if (b.splits > 1)
+    b.total += host::align_up((size_t)2 * b.splits * d->tokens * d->kv_heads * d->head_dim * 4);
+  b.total = std::max(b.total, host::kAlign);
+  return b;
+}
+
+// SMs of the current device (152 when there is none to ask).
+int device_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess &&
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+    return sms;
+  (void)cudaGetLastError();
+  return 152;
+}
+
+template <int DP>
+flce_status launch_backward(const flce_attention_desc* d, const CUtensorMap (&m)[4],
+                            const AttnBwdParams& p, int dev, int sms, cudaStream_t st) {
+  static Setup setup[2][host::kMaxDevices];
+  FLCE_HOST_TRY(set_smem(setup[0][dev], attn_dq<DP>, DqCfg<DP>::kSmem));
+  FLCE_HOST_TRY(set_smem(setup[1][dev], attn_dkdv<DP>, DkvCfg<DP>::kSmem));
+  const int64_t units = most_units(d, kTile);
+  attn_dq<DP><<<(int)std::min<int64_t>(units * d->q_heads, sms), kBwdThreads, DqCfg<DP>::kSmem, st>>>(
+      m[0], m[1], m[2], m[3], p);
+  host::count_launch();
+  FLCE_HOST_CUDA(cudaGetLastError());
+  attn_dkdv<DP><<<(int)std::min<int64_t>(units * d->kv_heads * p.splits, sms), kBwdThreads,
+                  DkvCfg<DP>::kSmem, st>>>(m[0], m[1], m[2], m[3], p);
+  host::count_launch();
+  FLCE_HOST_CUDA(cudaGetLastError());
+  return FLCE_OK;
 }
 
 }  // namespace
@@ -117,7 +165,7 @@ extern "C" {
 
 size_t flce_attention_workspace_size(const flce_attention_desc* d) {
   if (!shape_ok(d) || d->dtype != FLCE_BF16) return 0;
-  return host::kAlign + delta_bytes(d);
+  return plan_backward(d, device_sms()).total;
 }
 
 flce_status flce_attention_forward(const flce_attention_desc* d, const void* q, const void* k,
@@ -129,7 +177,8 @@ flce_status flce_attention_forward(const flce_attention_desc* d, const void* q, 
   if (d->tokens == 0) return FLCE_OK;
   int dev, sms;
   FLCE_HOST_TRY(host::device(&dev, &sms));
-  AttnParams p = params(d, cu_seqlens, err_word);
+  AttnParams p{};
+  fill(p, d, cu_seqlens, err_word);
   p.out = static_cast<bf16*>(out);
   p.lse = lse;
   p.v = static_cast<const bf16*>(v);
@@ -166,21 +215,34 @@ flce_status flce_attention_backward(const flce_attention_desc* d, const void* do
   if (d->tokens == 0) return FLCE_OK;
   int dev, sms;
   FLCE_HOST_TRY(host::device(&dev, &sms));
+  const BwdPlan plan = plan_backward(d, sms);
+  char* ws = static_cast<char*>(workspace);
+  AttnBwdParams p{};
+  fill(p, d, cu_seqlens, err_word);
+  p.out = const_cast<bf16*>(static_cast<const bf16*>(out));
+  p.lse = const_cast<float*>(lse);
+  p.dout = static_cast<const bf16*>(dout);
+  p.dq = static_cast<bf16*>(dq);
+  p.dk = static_cast<bf16*>(dk);
+  p.dv = static_cast<bf16*>(dv);
+  p.nlse = reinterpret_cast<float*>(ws);
+  p.delta = reinterpret_cast<float*>(ws + plan.off_delta);
+  p.partial = reinterpret_cast<float*>(ws + plan.off_partial);
+  p.splits = plan.splits;
+  CUtensorMap m[4];
+  FLCE_HOST_TRY(map_heads(&m[0], q, d, d->q_heads, d->q_row, d->q_head));
+  FLCE_HOST_TRY(map_heads(&m[1], k, d, d->kv_heads, d->k_row, d->k_head));
+  FLCE_HOST_TRY(map_heads(&m[2], v, d, d->kv_heads, d->v_row, d->v_head));
+  FLCE_HOST_TRY(map_heads(&m[3], dout, d, d->q_heads, d->q_heads * d->head_dim, d->head_dim));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  float* delta = reinterpret_cast<float*>(static_cast<char*>(workspace) + host::kAlign);
-  const AttnIn p = params(d, cu_seqlens, err_word);
-  const unsigned rows = (unsigned)host::ceil_div(d->tokens, 4);
-  attn_simple_dq<<<dim3(rows, (unsigned)d->q_heads), 128, 0, st>>>(
-      p, static_cast<const bf16*>(dout), static_cast<const bf16*>(q), static_cast<const bf16*>(k),
-      static_cast<const bf16*>(v), static_cast<const bf16*>(out), lse, delta,
-      static_cast<bf16*>(dq));
-  host::count_launch();
-  FLCE_HOST_CUDA(cudaGetLastError());
-  attn_simple_dkdv<<<dim3(rows, (unsigned)d->kv_heads), 128, 0, st>>>(
-      p, static_cast<const bf16*>(dout), static_cast<const bf16*>(q), static_cast<const bf16*>(k),
-      static_cast<const bf16*>(v), lse, delta, static_cast<bf16*>(dk), static_cast<bf16*>(dv));
-  host::count_launch();
-  FLCE_HOST_CUDA(cudaGetLastError());
+  FLCE_HOST_TRY(d->head_dim <= 64 ? launch_backward<64>(d, m, p, dev, sms, st)
+                                  : launch_backward<128>(d, m, p, dev, sms, st));
+  if (p.splits > 1) {
+    const int64_t values = d->tokens * d->kv_heads * d->head_dim;
+    attn_sum_splits<<<dim3((unsigned)host::ceil_div(values, 1024), 2), 256, 0, st>>>(p);
+    host::count_launch();
+    FLCE_HOST_CUDA(cudaGetLastError());
+  }
   return FLCE_OK;
 }
 

@@ -16,7 +16,8 @@ constexpr int kMaxDevices = 64;
 constexpr size_t kAlign = 256;                           // workspace regions
 constexpr unsigned long long kTimeoutNs = 2000000000ull;  // bounded device waits
 
-// Current device and its SM count; FLCE_ERR_UNSUPPORTED off sm_103.
+// Current device, with its context on this thread, and its SM count;
+// FLCE_ERR_UNSUPPORTED off sm_103.
 flce_status device(int* dev, int* sms);
 // Keeps the error's text for flce_last_cuda_error and returns FLCE_ERR_CUDA.
 flce_status fail(cudaError_t e, const char* what);

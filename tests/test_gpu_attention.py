@@ -94,6 +94,21 @@ def test_many_sequences():
     check(*make(cu[-1] + 5, 2, 2, 64, seed=2), cu)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_units_for_each_sm(D):
+    """Several ragged units, one after the other, on every CTA, beside rows that hold NaN."""
+    lengths = [700, 130, 1, 0, 385, 64, 511, 257, 900, 33]
+    cu = np.concatenate([[0], np.cumsum(lengths)]).tolist()
+    q, k, v, g = make(cu[-1] + 77, 32, 16, D, seed=D)
+    for t in (q, k, v, g):
+        t[cu[-1]:] = float("nan")
+    got = run(q, k, v, g, cu)
+    n = cu[-1]
+    want = check(*[t[:n] for t in (q, k, v, g)], cu)
+    import torch
+    assert all(torch.equal(a[:n], b) for a, b in zip((got[0], *got[2:5]), (want[0], *want[2:5])))
+
+
 def test_rows_outside_the_sequences():
     """Rows before the first and after the last sequence: out 0, lse -inf, gradients 0,
     whatever they hold."""
