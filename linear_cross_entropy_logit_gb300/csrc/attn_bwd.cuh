@@ -181,6 +181,7 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
             s[i >> 5][(i & 31) + 1] = __float_as_uint(b * as_f(s[i >> 5][(i & 31) + 1]));
           }
           if (j == n - 1) {  // the diagonal: keys after the row
+            asm volatile("");  // kept a branch, as selects it would cost every tile
 #pragma unroll
             for (int i = 0; i < 64; ++i)
               if (half * 64 + i > row) s[i >> 5][i & 31] = 0;
@@ -216,68 +217,70 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t ids = make_idesc(false, false, kTile, kTile);
-      constexpr uint32_t idq = make_idesc(false, true, kTile, DP);
-      const uint32_t q0 = smem_u32(smem), do0 = q0 + C::kTileBytes;
-      const uint32_t kr = smem_u32(smem + C::kRingK), vr = smem_u32(smem + C::kRingV);
-      uint32_t base = 0, units = 0;  // steps before this unit
-      bool ok = true;
-      auto issue_s = [&](uint32_t t) {
-        if (!(ok = ok && mbar_wait(&sh.kfull[t % C::kK], (t / C::kK) & 1, ctx))) return;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)
-          mma_issue(tmem + (t & 1) * kTile, desc_k(q0, kk),
-                    desc_k(kr + (t % C::kK) * C::kTileBytes, kk), ids, kk != 0);
+    const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+    const uint32_t dp = tm + 2 * kTile, acc = tm + 3 * kTile;
+    const uint32_t q0 = smem_u32(smem), do0 = q0 + C::kTileBytes;
+    const uint32_t kr = smem_u32(smem + C::kRingK), vr = smem_u32(smem + C::kRingV);
+    uint32_t base = 0, units = 0;  // steps before this unit
+    bool ok = true;
+    auto issue_s = [&](uint32_t t) {
+      if (!(ok = ok && mbar_wait_warp(&sh.kfull[t % C::kK], (t / C::kK) & 1, ctx))) return;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_tiles<DP>(tm + (t & 1) * kTile, q0, kr + (t % C::kK) * C::kTileBytes);
         mma_commit(&sh.sfull[t & 1]);
-      };
-      auto issue_dp = [&](uint32_t t) {
-        if (!(ok = ok && mbar_wait(&sh.vfull[t % C::kV], (t / C::kV) & 1, ctx))) return;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)
-          mma_issue(t_dp, desc_k(do0, kk), desc_k(vr + (t % C::kV) * C::kTileBytes, kk), ids, kk != 0);
-        mma_commit(&sh.vempty[t % C::kV]);
-        mma_commit(&sh.pfull);
-      };
-      for (uint32_t it = 0; ok; ++it) {
-        if (!mbar_wait(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
-        const AttnUnit u = sh.unit[it & 1];
-        if (u.head < 0) break;
-        if (u.len > 0) {
-          const int n = u.q0 / kTile + 1;
-          if (!mbar_wait(&sh.qfull, units & 1, ctx)) break;
-          // the diagonal key tile is cleaned before any product reads it
-          if (!mbar_wait(&sh.clean[it & 1], (it >> 1) & 1, ctx)) break;
-          issue_s(base);
-          issue_dp(base);
-          for (int i = 0; i < n && ok; ++i) {
-            const uint32_t t = base + i;
-            if (i + 1 < n) issue_s(t + 1);
-            if (!(ok = ok && mbar_wait(&sh.dsfull, t & 1, ctx))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_issue_ts(t_acc, t_dp + (kk >> 2) * 64 + (kk & 3) * 8,
-                           desc_mn(kr + (t % C::kK) * C::kTileBytes, kk), idq, (i | kk) != 0);
-            mma_commit(&sh.kempty[t % C::kK]);
-            if (i + 1 < n) issue_dp(t + 1);
-            // Q and dout are free once the last S and dP are done
-            if (i + 2 == n || n == 1) mma_commit(&sh.qempty);
-          }
-          if (!ok) break;
-          mma_commit(&sh.accfull);
-          base += n;
-          ++units;
-        } else {
-          // the phases of clean and stats go by units, empty ones included
-        }
-        mbar_arrive(&sh.uempty[it & 1]);
       }
+      __syncwarp();
+    };
+    auto issue_dp = [&](uint32_t t) {
+      if (!(ok = ok && mbar_wait_warp(&sh.vfull[t % C::kV], (t / C::kV) & 1, ctx))) return;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_tiles<DP>(dp, do0, vr + (t % C::kV) * C::kTileBytes);
+        mma_commit(&sh.pfull);
+        mma_commit(&sh.vempty[t % C::kV]);
+      }
+      __syncwarp();
+    };
+    for (uint32_t it = 0; ok; ++it) {
+      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      const AttnUnit u = uniform(sh.unit[it & 1]);
+      if (u.head < 0) break;
+      if (u.len > 0) {
+        const int n = u.q0 / kTile + 1;
+        if (!mbar_wait_warp(&sh.qfull, units & 1, ctx)) break;
+        // the diagonal key tile is cleaned before any product reads it
+        if (!mbar_wait_warp(&sh.clean[it & 1], (it >> 1) & 1, ctx)) break;
+        issue_s(base);
+        issue_dp(base);
+        for (int i = 0; i < n && ok; ++i) {
+          const uint32_t t = base + i;
+          if (i + 1 < n) issue_s(t + 1);
+          if (!(ok = ok && mbar_wait_warp(&sh.dsfull, t & 1, ctx))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            mma_tmem_tile<DP>(acc, dp, 64, kr + (t % C::kK) * C::kTileBytes, i != 0);
+            mma_commit(&sh.kempty[t % C::kK]);
+          }
+          __syncwarp();
+          if (i + 1 < n) issue_dp(t + 1);
+          // Q and dout are free once the last S and dP are done
+          if ((i + 2 == n || n == 1) && elect_one()) mma_commit(&sh.qempty);
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) mma_commit(&sh.accfull);
+        base += n;
+        ++units;
+      }
+      if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
+      __syncwarp();
+    }
+    if (elect_one()) {
       mma_commit(&sh.mma_done);
       mbar_wait_drain(&sh.mma_done, 0, p.timeout_ns);
     }
+    __syncwarp();
   } else if (warp == 9) {
     // ------------------------------------------------------------ units, loads
     if (lane == 0) {
@@ -562,6 +565,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
               r[i0 + 3] = __float_as_uint(ex2_approx(y));
             }
             if (masked) {
+              asm volatile("");  // kept a branch, as selects it would cost every tile
 #pragma unroll
               for (int e = 0; e < 64; ++e)
                 if (e < from || e >= limit) s[e >> 5][e & 31] = 0;
@@ -591,6 +595,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
               r[i0 + 3] = __float_as_uint((as_f(r[i0 + 3]) - b.w) * as_f(q[i0 + 3]));
             }
             if (masked) {
+              asm volatile("");  // kept a branch, as selects it would cost every tile
 #pragma unroll
               for (int e = 0; e < 64; ++e)
                 if (e < from || e >= limit) g[e >> 5][e & 31] = 0;
@@ -658,79 +663,84 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t ids = make_idesc(false, false, kTile, kTile);
-      constexpr uint32_t idg = make_idesc(false, true, kTile, DP);
-      const uint32_t k0 = smem_u32(smem), v0 = k0 + C::kTileBytes;
-      const uint32_t ring = smem_u32(smem + C::kRing);
-      uint32_t base = 0, units = 0, nclean = 0;  // nclean: next phase of each stage's barrier
-      bool ok = true;
-      auto q_tile = [&](uint32_t t) { return ring + (t % C::kStages) * 2 * C::kTileBytes; };
-      // waits for step t's Q (S and later dK read it) and, if it is cleaned, for that
-      auto issue_s = [&](uint32_t t, bool cleaned) {
-        const uint32_t s = t % C::kStages;
-        if (!(ok = ok && mbar_wait(&sh.qfull[s], (t / C::kStages) & 1, ctx))) return;
-        if (cleaned) {
-          if (!(ok = mbar_wait(&sh.clean[s], (nclean >> s) & 1, ctx))) return;
-          nclean ^= 1u << s;
-        }
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)
-          mma_issue(t_s, desc_k(k0, kk), desc_k(q_tile(t), kk), ids, kk != 0);
-        mma_commit(&sh.sfull);
-      };
-      auto issue_dp = [&](uint32_t t) {
-        const uint32_t s = t % C::kStages;
-        if (!(ok = ok && mbar_wait(&sh.gfull[s], (t / C::kStages) & 1, ctx))) return;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)
-          mma_issue(t_dp, desc_k(v0, kk), desc_k(q_tile(t) + C::kTileBytes, kk), ids, kk != 0);
-        mma_commit(&sh.dpfull);
-      };
-      for (uint32_t it = 0; ok; ++it) {
-        if (!mbar_wait(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
-        const AttnUnit u = sh.unit[it & 1];
-        if (u.head < 0) break;
-        if (u.len > 0) {
-          const int first = u.q0 / kTile, tiles = (u.len + kTile - 1) / kTile - first;
-          const int n = tiles * per_split;
-          if (!mbar_wait(&sh.kvfull, units & 1, ctx)) break;
-          issue_s(base, true);
-          issue_dp(base);
-          int i = 0;  // query tile of step x within its head
-          for (int x = 0; x < n && ok; ++x) {
-            const uint32_t t = base + x;
-            if (!(ok = mbar_wait(&sh.pfull, t & 1, ctx))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_issue_ts(t_dv, t_s + (kk >> 2) * 64 + (kk & 3) * 8,
-                           desc_mn(q_tile(t) + C::kTileBytes, kk), idg, (x | kk) != 0);
-            mma_commit(&sh.gempty[t % C::kStages]);
-            if (++i == tiles) i = 0;
-            if (x + 1 < n) issue_s(t + 1, dkv_cleaned(u, first + i, first));
-            if (!(ok = ok && mbar_wait(&sh.dsfull, t & 1, ctx))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_issue_ts(t_dk, t_dp + (kk >> 2) * 64 + (kk & 3) * 8, desc_mn(q_tile(t), kk), idg,
-                           (x | kk) != 0);
-            mma_commit(&sh.qempty[t % C::kStages]);
-            if (x + 1 < n) issue_dp(t + 1);
-            if (x + 2 == n || n == 1) mma_commit(&sh.kvempty);
-          }
-          if (!ok) break;
-          mma_commit(&sh.accfull);
-          base += n;
-          ++units;
-        }
-        mbar_arrive(&sh.uempty[it & 1]);
+    const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+    const uint32_t a_s = tm, a_dp = tm + kTile, a_dv = tm + 2 * kTile, a_dk = tm + 3 * kTile;
+    const uint32_t k0 = smem_u32(smem), v0 = k0 + C::kTileBytes;
+    const uint32_t ring = smem_u32(smem + C::kRing);
+    uint32_t base = 0, units = 0, nclean = 0;  // nclean: next phase of each stage's barrier
+    bool ok = true;
+    auto q_tile = [&](uint32_t t) { return ring + (t % C::kStages) * 2 * C::kTileBytes; };
+    // waits for step t's Q (S and later dK read it) and, if it is cleaned, for that
+    auto issue_s = [&](uint32_t t, bool cleaned) {
+      const uint32_t s = t % C::kStages;
+      if (!(ok = ok && mbar_wait_warp(&sh.qfull[s], (t / C::kStages) & 1, ctx))) return;
+      if (cleaned) {
+        if (!(ok = mbar_wait_warp(&sh.clean[s], (nclean >> s) & 1, ctx))) return;
+        nclean ^= 1u << s;
       }
+      tc_fence_after();
+      if (elect_one()) {
+        mma_tiles<DP>(a_s, k0, q_tile(t));
+        mma_commit(&sh.sfull);
+      }
+      __syncwarp();
+    };
+    auto issue_dp = [&](uint32_t t) {
+      const uint32_t s = t % C::kStages;
+      if (!(ok = ok && mbar_wait_warp(&sh.gfull[s], (t / C::kStages) & 1, ctx))) return;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_tiles<DP>(a_dp, v0, q_tile(t) + C::kTileBytes);
+        mma_commit(&sh.dpfull);
+      }
+      __syncwarp();
+    };
+    for (uint32_t it = 0; ok; ++it) {
+      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      const AttnUnit u = uniform(sh.unit[it & 1]);
+      if (u.head < 0) break;
+      if (u.len > 0) {
+        const int first = u.q0 / kTile, tiles = (u.len + kTile - 1) / kTile - first;
+        const int n = tiles * per_split;
+        if (!mbar_wait_warp(&sh.kvfull, units & 1, ctx)) break;
+        issue_s(base, true);
+        issue_dp(base);
+        int i = 0;  // query tile of step x within its head
+        for (int x = 0; x < n && ok; ++x) {
+          const uint32_t t = base + x;
+          if (!(ok = mbar_wait_warp(&sh.pfull, t & 1, ctx))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            mma_tmem_tile<DP>(a_dv, a_s, 64, q_tile(t) + C::kTileBytes, x != 0);
+            mma_commit(&sh.gempty[t % C::kStages]);
+          }
+          __syncwarp();
+          if (++i == tiles) i = 0;
+          if (x + 1 < n) issue_s(t + 1, dkv_cleaned(u, first + i, first));
+          if (!(ok = ok && mbar_wait_warp(&sh.dsfull, t & 1, ctx))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            mma_tmem_tile<DP>(a_dk, a_dp, 64, q_tile(t), x != 0);
+            mma_commit(&sh.qempty[t % C::kStages]);
+          }
+          __syncwarp();
+          if (x + 1 < n) issue_dp(t + 1);
+          if ((x + 2 == n || n == 1) && elect_one()) mma_commit(&sh.kvempty);
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) mma_commit(&sh.accfull);
+        base += n;
+        ++units;
+      }
+      if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
+      __syncwarp();
+    }
+    if (elect_one()) {
       mma_commit(&sh.mma_done);
       mbar_wait_drain(&sh.mma_done, 0, p.timeout_ns);
     }
+    __syncwarp();
   } else if (warp == 9) {
     // ------------------------------------------------------------ units, loads
     if (lane == 0) {

@@ -137,13 +137,44 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, c
   return __all_sync(~0u, mbar_wait(bar, parity, ctx));
 }
 
-// K-major operand (rows x head values), step kk of 16 values.
-__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int kk) {
-  return smem_desc_sw128(tile + (kk >> 2) * kBoxBytes + (kk & 3) * 32, 16, 1024);
+// Products of whole tiles, issued by the elected lane of a converged warp.  The
+// whole warp keeps the issuing loop's state, in uniform registers: an
+// instruction takes 64 tensor cycles at N = 128, and with the state in one
+// lane's registers issuing one took longer than that (1.4x slower kernels).
+//
+// d (+)= A B^T over DP head values; A and B are 128-row tiles in shared memory.
+template <int DP>
+__device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t a_tile, uint32_t b_tile) {
+  constexpr uint32_t idesc = make_idesc(false, false, kTile, kTile);
+  const uint32_t a = desc_lo(a_tile, 16), b = desc_lo(b_tile, 16);
+#pragma unroll
+  for (int kk = 0; kk < DP / 16; ++kk) {
+    const uint32_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+    mma_issue_lo(d, a + off, b + off, idesc, kk != 0);
+  }
 }
-// MN-major operand (head values outermost for the MMA), step kk of 16 rows.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int kk) {
-  return smem_desc_sw128(tile + kk * 2048, kBoxBytes, 1024);
+// d (+)= A B over 128 rows of the tile B (128 x DP); A is packed bf16 in TMEM,
+// `gap` columns from one run of 64 k to the next (32 when they are adjacent).
+template <int DP>
+__device__ __forceinline__ void mma_tmem_tile(uint32_t d, uint32_t a, int gap, uint32_t b_tile,
+                                              bool accumulate) {
+  constexpr uint32_t idesc = make_idesc(false, true, kTile, DP);
+  const uint32_t b = desc_lo(b_tile, kBoxBytes);
+#pragma unroll
+  for (int kk = 0; kk < kTile / 16; ++kk)
+    mma_issue_ts(d, a + (kk >> 2) * gap + (kk & 3) * 8, b + ((kk * 2048) >> 4), idesc,
+                 kk != 0 || accumulate);
+}
+
+// A unit read from shared memory by a whole warp, the same in all its lanes.
+__device__ __forceinline__ AttnUnit uniform(const AttnUnit& from) {
+  AttnUnit u;
+  u.start = __shfl_sync(~0u, from.start, 0);
+  u.len = __shfl_sync(~0u, from.len, 0);
+  u.q0 = __shfl_sync(~0u, from.q0, 0);
+  u.rows = __shfl_sync(~0u, from.rows, 0);
+  u.head = __shfl_sync(~0u, from.head, 0);
+  return u;
 }
 
 // Bits 15 and 31 set where a packed bf16 half is infinite or NaN.

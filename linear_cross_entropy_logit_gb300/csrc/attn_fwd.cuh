@@ -150,6 +150,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
         for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, s[i]);
         tmem_ld_wait();
         if (j == n - 1) {  // the diagonal
+          asm volatile("");  // a branch: as selects it would cost every tile 128 of them
 #pragma unroll
           for (int i = 0; i < 128; ++i)
             if (i > row) s[i >> 5][i & 31] = 0xff800000u;  // -infinity
@@ -264,84 +265,89 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t ids = make_idesc(false, false, kTile, kTile);
-      constexpr uint32_t ido = make_idesc(false, true, kTile, DP);
-      const uint32_t q0 = smem_u32(smem);
-      uint32_t base = 0;  // ring position of the unit's first tile
-      uint32_t np[2] = {0, 0}, nq = 0, nclean = 0;  // bit 2 parity + tile of nclean: next phase
-      bool ok = true;
-      auto slot = [&](uint32_t pos) { return smem_u32(ring + (pos % C::kSlots) * C::kTileBytes); };
-      auto wait_tile = [&](uint32_t pos) {
-        ok = ok && mbar_wait(&sh.full[pos % C::kSlots], (pos / C::kSlots) & 1, ctx);
-        tc_fence_after();
-        return ok;
-      };
-      auto issue_s = [&](int x, uint32_t pos) {
-        const uint32_t kt = slot(pos);
-#pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk)
-          mma_issue(tmem + x * kTile, desc_k(q0 + x * C::kTileBytes, kk), desc_k(kt, kk), ids, kk != 0);
-        mma_commit(&sh.sfull[x]);
-      };
-      for (uint32_t it = 0; ok; ++it) {
-        if (!mbar_wait(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
-        const AttnUnit u = sh.unit[it & 1];
-        if (u.head < 0) break;
-        if (u.len == 0) {
-          mbar_arrive(&sh.uempty[it & 1]);
-          continue;
-        }
+    const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+    const uint32_t q0 = smem_u32(smem);
+    uint32_t base = 0;  // ring position of the unit's first tile
+    uint32_t np[2] = {0, 0}, nq = 0, nclean = 0;  // bit 2 parity + tile of nclean: next phase
+    bool ok = true;
+    auto slot = [&](uint32_t pos) { return smem_u32(ring) + (pos % C::kSlots) * C::kTileBytes; };
+    auto wait_tile = [&](uint32_t pos) {
+      ok = ok && mbar_wait_warp(&sh.full[pos % C::kSlots], (pos / C::kSlots) & 1, ctx);
+      tc_fence_after();
+      return ok;
+    };
+    for (uint32_t it = 0; ok; ++it) {
+      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      const AttnUnit u = uniform(sh.unit[it & 1]);
+      if (u.head < 0) break;
+      if (u.len > 0) {
         int n0, n1;
         unit_tiles(u, n0, n1);
         const int last = max(n0, n1) - 1;  // key tile j sits at ring position base + 2 (last - j)
-        if (!mbar_wait(&sh.qfull, nq & 1, ctx)) break;
+        if (!mbar_wait_warp(&sh.qfull, nq & 1, ctx)) break;
         ++nq;
         if (!wait_tile(base)) break;
-        issue_s(n1 ? 1 : 0, base);
-        mma_commit(&sh.empty[base % C::kSlots]);
+        if (elect_one()) {
+          const int x = n1 ? 1 : 0;
+          mma_tiles<DP>(tm + x * kTile, q0 + x * C::kTileBytes, slot(base));
+          mma_commit(&sh.sfull[x]);
+          mma_commit(&sh.empty[base % C::kSlots]);
+          if (last == 0) mma_commit(&sh.qempty);
+        }
+        __syncwarp();
         if (n1) {
           if (!wait_tile(base + 2)) break;
-          issue_s(0, base + 2);
+          if (elect_one()) {
+            mma_tiles<DP>(tm, q0, slot(base + 2));
+            mma_commit(&sh.sfull[0]);
+          }
+          __syncwarp();
         }
-        if (last == 0) mma_commit(&sh.qempty);
         for (int j = last; j >= 0 && ok; --j) {
           const uint32_t kpos = base + 2 * (last - j), vpos = kpos + 1, knext = kpos + 2;
           if (!wait_tile(vpos)) break;
           if (j >= n0 - 1) {
             const uint32_t f = j - (n0 - 1), bit = 2 * (it & 1) + f;
-            if (!(ok = mbar_wait(&sh.clean[it & 1][f], (nclean >> bit) & 1, ctx))) break;
+            if (!(ok = mbar_wait_warp(&sh.clean[it & 1][f], (nclean >> bit) & 1, ctx))) break;
             nclean ^= 1u << bit;
           }
           if (j > 0 && !wait_tile(knext)) break;
 #pragma unroll
           for (int x = 1; x >= 0; --x) {
-            if (j >= (x ? n1 : n0)) continue;
-            if (!(ok = mbar_wait(&sh.pfull[x], np[x] & 1, ctx))) break;
+            const int n = x ? n1 : n0;
+            if (j >= n) continue;
+            if (!(ok = mbar_wait_warp(&sh.pfull[x], np[x] & 1, ctx))) break;
             ++np[x];
             tc_fence_after();
-            const uint32_t vt = slot(vpos);
-            const bool first = j == (x ? n1 : n0) - 1;
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_issue_ts(tmem + 2 * kTile + x * DP, tmem + x * kTile + kk * 8, desc_mn(vt, kk), ido,
-                           !(first && kk == 0));
-            // the key tile right below a pair's top one was multiplied with tile 0 at the start
-            const bool top = n1 && j == last;
-            if (j > 0) issue_s(x, knext);
-            else mma_commit(&sh.ofull[x]);
-            if (x == 0 || j >= n0) mma_commit(&sh.empty[vpos % C::kSlots]);
-            if (j > 0 && (x == 0 || top)) mma_commit(&sh.empty[knext % C::kSlots]);
+            if (elect_one()) {
+              mma_tmem_tile<DP>(tm + 2 * kTile + x * DP, tm + x * kTile, 32, slot(vpos), j < n - 1);
+              // the key tile right below a pair's top one was multiplied with tile 0 at the start
+              const bool top = n1 && j == last;
+              if (j > 0) {
+                mma_tiles<DP>(tm + x * kTile, q0 + x * C::kTileBytes, slot(knext));
+                mma_commit(&sh.sfull[x]);
+              } else {
+                mma_commit(&sh.ofull[x]);
+              }
+              if (x == 0 || j >= n0) mma_commit(&sh.empty[vpos % C::kSlots]);
+              if (j > 0 && (x == 0 || top)) mma_commit(&sh.empty[knext % C::kSlots]);
+              // the last product that reads Q is issued
+              if (j == 1 && (x == 0 || n0 == 1)) mma_commit(&sh.qempty);
+            }
+            __syncwarp();
           }
-          if (j == 1) mma_commit(&sh.qempty);  // the last product that reads Q is issued
         }
         if (!ok) break;
-        mbar_arrive(&sh.uempty[it & 1]);
         base += 2 * (last + 1);
       }
+      if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
+      __syncwarp();
+    }
+    if (elect_one()) {
       mma_commit(&sh.mma_done);
       mbar_wait_drain(&sh.mma_done, 0, p.timeout_ns);
     }
+    __syncwarp();
   } else if (warp == 9) {
     // ------------------------------------------------------------ units, loads
     if (lane == 0) {
