@@ -1,12 +1,12 @@
-// Backward of packed causal attention on the tensor cores, in two kernels.
+// Backward of packed causal attention on the tensor cores.
 //
-//   p_ij = exp(s_ij - lse_i),  delta_i = dout_i . out_i
+//   p_ij = exp(s_ij - lse_i),  delta_i = dout_i . out_i   attn_delta
 //   ds_ij = p_ij (dout_i . v_j - delta_i)
 //   dq_i = scale sum_j ds_ij k_j          attn_dq: a CTA owns 128 query rows
 //   dv_j = sum_i p_ij dout_i              attn_dkdv: a CTA owns 128 key rows and
 //   dk_j = scale sum_i ds_ij q_i          sums over the query heads that read them
 //
-// Each kernel recomputes S and dP = dout V^T, so that every sum stays in the
+// The last two recompute S and dP = dout V^T, so that every sum stays in the
 // TMEM of the CTA that owns its rows: no fp32 gradient goes through memory, no
 // atomics, the same bits every run.  Seven products where one kernel for all
 // three gradients would take five, but that one has to add dq up in memory
@@ -32,7 +32,7 @@ static_assert(2 * (kBwdComputeRegs + kBwdOtherRegs) == 4 * (65536 / kBwdThreads)
 struct AttnBwdParams : AttnParams {
   const bf16* dout;    // tokens x q_heads x head_dim
   bf16 *dq, *dk, *dv;  // contiguous
-  float *nlse, *delta; // q_heads x tokens: -lse log2 e, delta (written by attn_dq)
+  float *nlse, *delta; // q_heads x tokens: -lse log2 e, delta (written by attn_delta)
   float* partial;      // splits > 1: dk, dv partial sums, 2 x splits x tokens x kv_heads x head_dim
   int splits;          // CTAs that share the query heads of a key / value head
 };
@@ -59,11 +59,62 @@ __device__ __forceinline__ void store_row(bf16* to, const uint32_t (&v)[N], floa
 }
 
 // ----------------------------------------------------------------------------
+// delta
+// ----------------------------------------------------------------------------
+// Bound by reading out and dout once.  Eight lanes hold a row, 16 values each
+// (two of the 8 x 16 byte pieces), four rows a lane: 16 loads in flight.  A
+// kernel of its own rather than attn_dq's work: there its loads stood
+// before every unit, 3-4 us each (145 us against 12 + 48 for 61 ragged sequences of 9999
+// tokens, 16 heads of 64).
+constexpr int kDeltaRows = 128;  // tokens of one head per block of 256 threads
+__global__ void __launch_bounds__(256) attn_delta(const AttnBwdParams p) {
+  const int lane = threadIdx.x & 7, slot = threadIdx.x >> 3, h = blockIdx.y;
+  const int64_t t0 = (int64_t)blockIdx.x * kDeltaRows + slot;
+  uint4 a[4][2], b[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int64_t t = t0 + 32 * i;
+      const int d = lane * 8 + 64 * e;
+      a[i][e] = b[i][e] = make_uint4(0, 0, 0, 0);
+      if (t < p.tokens && d < p.head_dim) {
+        const int64_t at = (t * p.q_heads + h) * p.head_dim + d;
+        a[i][e] = *reinterpret_cast<const uint4*>(p.out + at);
+        b[i][e] = *reinterpret_cast<const uint4*>(p.dout + at);
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t x[4] = {a[i][e].x, a[i][e].y, a[i][e].z, a[i][e].w};
+      const uint32_t y[4] = {b[i][e].x, b[i][e].y, b[i][e].z, b[i][e].w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        sum = fmaf(as_f(x[w] << 16), as_f(y[w] << 16), sum);
+        sum = fmaf(as_f(x[w] & 0xffff0000u), as_f(y[w] & 0xffff0000u), sum);
+      }
+    }
+#pragma unroll
+    for (int o = 4; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    const int64_t t = t0 + 32 * i;
+    if (lane == 0 && t < p.tokens) {
+      const int64_t at = (int64_t)h * p.tokens + t;
+      p.nlse[at] = -p.lse[at] * kLog2e;
+      p.delta[at] = sum;
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------
 // dq
 // ----------------------------------------------------------------------------
-// TMEM: two S buffers (S of the next key tile is made while this one's is
-// read), dP (dS overwrites it), dQ.  Three K tiles are held: of this step (for
-// dQ += dS K), the next (S) and one in flight.
+// TMEM: S, two dP buffers (dS overwrites its own), dQ.  S of the next key tile
+// follows as soon as this one's is in registers, and its dP goes to the other
+// buffer, so the tensor cores never wait for a dS other than dQ's own.  Three K
+// tiles are held: of this step (for dQ += dS K), the next (S) and one in flight.
 template <int DP>
 struct DqCfg {
   static constexpr int kBoxes = DP / 64;
@@ -72,14 +123,14 @@ struct DqCfg {
   static constexpr int kRingK = 2 * kTileBytes;                        // after Q and dout
   static constexpr int kRingV = kRingK + kK * kTileBytes;
   static constexpr int kBars = kRingV + kV * kTileBytes;
-  static constexpr int kSmem = kBars + 512 + 2048;
+  static constexpr int kSmem = kBars + 512;
 };
 
 struct DqShared {
   uint64_t kfull[5], kempty[5], vfull[4], vempty[4];
   uint64_t qfull, qempty;
-  uint64_t sfull[2], pfull, dsfull, accfull;
-  uint64_t clean[2], stats[2];
+  uint64_t sfull, sread, dpfull[2], dsfull, accfull;
+  uint64_t clean[2];
   uint64_t ufull[2], uempty[2];
   uint64_t mma_done;
   AttnUnit unit[2];
@@ -107,13 +158,13 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
     for (int i = 0; i < C::kV; ++i) mbar_init(&sh.vfull[i], 1), mbar_init(&sh.vempty[i], 1);
     mbar_init(&sh.qfull, 1);
     mbar_init(&sh.qempty, 1);
-    mbar_init(&sh.pfull, 1);
+    mbar_init(&sh.sfull, 1);
+    mbar_init(&sh.sread, 8);
     mbar_init(&sh.dsfull, 8);
     mbar_init(&sh.accfull, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.sfull[i], 1);
+      mbar_init(&sh.dpfull[i], 1);
       mbar_init(&sh.clean[i], 4);
-      mbar_init(&sh.stats[i], 4);
       mbar_init(&sh.ufull[i], 1);
       mbar_init(&sh.uempty[i], 13);  // 8 compute warps, the MMA lane, 4 cleaning warps
     }
@@ -129,9 +180,7 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const uint32_t t_dp = tmem + 2 * kTile, t_acc = tmem + 3 * kTile;
-  // per unit parity: -lse log2 e and delta of the 128 rows
-  float* stat = reinterpret_cast<float*>(smem + C::kBars + 512);
+  const uint32_t t_acc = tmem + 3 * kTile;
 
   if (warp >= 8) regs_down<kBwdOtherRegs>();
   if (warp < 8) {
@@ -143,7 +192,7 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
     const uint64_t c2 = pack_f32x2(c, c);
     uint32_t step = 0, units = 0;
     for (uint32_t it = 0;; ++it) {
-      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      if (!wait_bar_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
       const AttnUnit u = sh.unit[it & 1];
       if (u.head < 0) break;
       bool ok = true;
@@ -154,15 +203,20 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
           for (int d = 0; d < p.head_dim / 8; ++d) o[d] = make_uint4(0, 0, 0, 0);
         }
       } else {
-        if (!mbar_wait_warp(&sh.stats[it & 1], (it >> 1) & 1, ctx)) break;
-        const float nl = stat[(it & 1) * 256 + row], dl = -stat[(it & 1) * 256 + 128 + row];
+        const bool live = u.q0 + row < u.len;
+        const int64_t at = (int64_t)u.head * p.tokens + u.start + u.q0 + row;
+        const float nl = live ? p.nlse[at] : 0.f, dl = live ? -p.delta[at] : 0.f;
         const uint64_t nl2 = pack_f32x2(nl, nl), dl2 = pack_f32x2(dl, dl);
         const int n = u.q0 / kTile + 1;
         for (int j = n - 1; j >= 0; --j, ++step) {
-          if (!(ok = mbar_wait_warp(&sh.sfull[step & 1], (step >> 1) & 1, ctx))) break;
+          const uint32_t t_dp = tmem + (1 + (step & 1)) * kTile + lanes + half * 64;
+          if (!(ok = wait_bar_warp(&sh.sfull, step & 1, ctx))) break;
           tc_fence_after();
           uint32_t s[2][32], g[2][32];
-          load64(s, tmem + lanes + (step & 1) * kTile + half * 64);
+          load64(s, tmem + lanes + half * 64);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.sread);
 #pragma unroll
           for (int i = 0; i < 64; i += 2) {
             float a, b;
@@ -170,9 +224,9 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
             s[i >> 5][i & 31] = __float_as_uint(ex2_approx(a));
             s[i >> 5][(i & 31) + 1] = __float_as_uint(ex2_approx(b));
           }
-          if (!(ok = mbar_wait_warp(&sh.pfull, step & 1, ctx))) break;
+          if (!(ok = wait_bar_warp(&sh.dpfull[step & 1], (step >> 1) & 1, ctx))) break;
           tc_fence_after();
-          load64(g, t_dp + lanes + half * 64);
+          load64(g, t_dp);
 #pragma unroll
           for (int i = 0; i < 64; i += 2) {
             float a, b;
@@ -190,17 +244,17 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             pk[i] = pack_bf16x2(as_f(s[i >> 4][2 * (i & 15)]), as_f(s[i >> 4][2 * (i & 15) + 1]));
-          tmem_st_32x32b_x32(t_dp + lanes + half * 64, pk);
+          tmem_st_32x32b_x32(t_dp, pk);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.dsfull);
         }
-        if (!ok || !mbar_wait_warp(&sh.accfull, units & 1, ctx)) break;
+        if (!ok || !wait_bar_warp(&sh.accfull, units & 1, ctx)) break;
         ++units;
         tc_fence_after();
         const int r = u.q0 + row;
-#pragma unroll
+#pragma unroll 1
         for (int d = 0; d < DP / 2; d += 32) {
           uint32_t o[32];
           const int d0 = half * (DP / 2) + d;
@@ -217,67 +271,62 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMA issuer
-    const uint32_t tm = __shfl_sync(~0u, tmem, 0);
-    const uint32_t dp = tm + 2 * kTile, acc = tm + 3 * kTile;
+    const uint32_t tm = __shfl_sync(~0u, tmem, 0), el = elect_one();
+    const uint32_t acc = tm + 3 * kTile;
+    auto dp = [&](uint32_t t) { return tm + (1 + (t & 1)) * kTile; };
     const uint32_t q0 = smem_u32(smem), do0 = q0 + C::kTileBytes;
     const uint32_t kr = smem_u32(smem + C::kRingK), vr = smem_u32(smem + C::kRingV);
     uint32_t base = 0, units = 0;  // steps before this unit
     bool ok = true;
     auto issue_s = [&](uint32_t t) {
-      if (!(ok = ok && mbar_wait_warp(&sh.kfull[t % C::kK], (t / C::kK) & 1, ctx))) return;
-      tc_fence_after();
-      if (elect_one()) {
-        mma_tiles<DP>(tm + (t & 1) * kTile, q0, kr + (t % C::kK) * C::kTileBytes);
-        mma_commit(&sh.sfull[t & 1]);
-      }
-      __syncwarp();
+      if (!(ok = ok && wait_bar_warp(&sh.kfull[t % C::kK], (t / C::kK) & 1, ctx))) return;
+      mma_tiles<DP>(el, tm, q0, kr + (t % C::kK) * C::kTileBytes);
+      mma_commit_if(el, &sh.sfull);
     };
     auto issue_dp = [&](uint32_t t) {
-      if (!(ok = ok && mbar_wait_warp(&sh.vfull[t % C::kV], (t / C::kV) & 1, ctx))) return;
-      tc_fence_after();
-      if (elect_one()) {
-        mma_tiles<DP>(dp, do0, vr + (t % C::kV) * C::kTileBytes);
-        mma_commit(&sh.pfull);
-        mma_commit(&sh.vempty[t % C::kV]);
-      }
-      __syncwarp();
+      if (!(ok = ok && wait_bar_warp(&sh.vfull[t % C::kV], (t / C::kV) & 1, ctx))) return;
+      mma_tiles<DP>(el, dp(t), do0, vr + (t % C::kV) * C::kTileBytes);
+      mma_commit_if(el, &sh.dpfull[t & 1]);
+      mma_commit_if(el, &sh.vempty[t % C::kV]);
     };
     for (uint32_t it = 0; ok; ++it) {
-      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      if (!wait_bar_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
       const AttnUnit u = uniform(sh.unit[it & 1]);
       if (u.head < 0) break;
       if (u.len > 0) {
         const int n = u.q0 / kTile + 1;
-        if (!mbar_wait_warp(&sh.qfull, units & 1, ctx)) break;
+        if (!wait_bar_warp(&sh.qfull, units & 1, ctx)) break;
         // the diagonal key tile is cleaned before any product reads it
-        if (!mbar_wait_warp(&sh.clean[it & 1], (it >> 1) & 1, ctx)) break;
+        if (!wait_bar_warp(&sh.clean[it & 1], (it >> 1) & 1, ctx)) break;
         issue_s(base);
         issue_dp(base);
         for (int i = 0; i < n && ok; ++i) {
           const uint32_t t = base + i;
-          if (i + 1 < n) issue_s(t + 1);
-          if (!(ok = ok && mbar_wait_warp(&sh.dsfull, t & 1, ctx))) break;
+          if (!(ok = wait_bar_warp(&sh.sread, t & 1, ctx))) break;
           tc_fence_after();
-          if (elect_one()) {
-            mma_tmem_tile<DP>(acc, dp, 64, kr + (t % C::kK) * C::kTileBytes, i != 0);
-            mma_commit(&sh.kempty[t % C::kK]);
+          if (i + 1 < n) {
+            issue_s(t + 1);
+            issue_dp(t + 1);
           }
-          __syncwarp();
-          if (i + 1 < n) issue_dp(t + 1);
           // Q and dout are free once the last S and dP are done
-          if ((i + 2 == n || n == 1) && elect_one()) mma_commit(&sh.qempty);
-          __syncwarp();
+          if (i + 2 == n || n == 1) {
+            mma_commit_if(el, &sh.qempty);
+          }
+          if (!(ok = ok && wait_bar_warp(&sh.dsfull, t & 1, ctx))) break;
+          tc_fence_after();
+          mma_tmem_tile<DP>(el, acc, dp(t), 64, kr + (t % C::kK) * C::kTileBytes, i != 0);
+          mma_commit_if(el, &sh.kempty[t % C::kK]);
         }
         if (!ok) break;
-        if (elect_one()) mma_commit(&sh.accfull);
+        mma_commit_if(el, &sh.accfull);
         base += n;
         ++units;
       }
       if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
       __syncwarp();
     }
-    if (elect_one()) {
-      mma_commit(&sh.mma_done);
+    mma_commit_if(el, &sh.mma_done);
+    if (el) {
       mbar_wait_drain(&sh.mma_done, 0, p.timeout_ns);
     }
     __syncwarp();
@@ -289,8 +338,8 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
       prefetch_tensormap(&tv);
       prefetch_tensormap(&tdo);
     }
-    UnitWalk walk;
-    walk.init(p, kTile);
+    UnitWalk<kTile> walk;
+    walk.init(p);
     const int64_t total = (int64_t)walk.total() * p.q_heads;
     uint32_t t = 0, units = 0;
     uint32_t loaded_k = 0, loaded_v = 0;
@@ -304,14 +353,14 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
         u.head = (int)(id % p.q_heads);
       }
       if (lane == 0) {
-        ok = mbar_wait(&sh.uempty[it & 1], ((it >> 1) & 1) ^ 1, ctx);
+        ok = wait_bar(&sh.uempty[it & 1], ((it >> 1) & 1) ^ 1, ctx);
         if (ok) {
           sh.unit[it & 1] = u;
           mbar_arrive(&sh.ufull[it & 1]);
         }
         if (ok && u.len > 0) {
           const int kvh = u.head / p.group;
-          if ((ok = mbar_wait(&sh.qempty, (units & 1) ^ 1, ctx))) {
+          if ((ok = wait_bar(&sh.qempty, (units & 1) ^ 1, ctx))) {
             mbar_arrive_expect_tx(&sh.qfull, 2 * C::kTileBytes);
             for (int b = 0; b < C::kBoxes; ++b) {
               tma_load_3d(smem + b * kBoxBytes, &tq, &sh.qfull, b * 64, u.head, u.start + u.q0);
@@ -322,13 +371,13 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
           }
           for (int j = u.q0 / kTile; j >= 0 && ok; --j, ++t) {
             const int ks = t % C::kK, vs = t % C::kV, r = u.start + j * kTile;
-            if (!(ok = mbar_wait(&sh.kempty[ks], ((t / C::kK) & 1) ^ 1, ctx))) break;
+            if (!(ok = wait_bar(&sh.kempty[ks], ((t / C::kK) & 1) ^ 1, ctx))) break;
             mbar_arrive_expect_tx(&sh.kfull[ks], C::kTileBytes);
             for (int b = 0; b < C::kBoxes; ++b)
               tma_load_3d(smem + C::kRingK + ks * C::kTileBytes + b * kBoxBytes, &tk, &sh.kfull[ks],
                           b * 64, kvh, r);
             ++loaded_k;
-            if (!(ok = mbar_wait(&sh.vempty[vs], ((t / C::kV) & 1) ^ 1, ctx))) break;
+            if (!(ok = wait_bar(&sh.vempty[vs], ((t / C::kV) & 1) ^ 1, ctx))) break;
             mbar_arrive_expect_tx(&sh.vfull[vs], C::kTileBytes);
             for (int b = 0; b < C::kBoxes; ++b)
               tma_load_3d(smem + C::kRingV + vs * C::kTileBytes + b * kBoxBytes, &tv, &sh.vfull[vs],
@@ -348,56 +397,18 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
         mbar_wait_drain(&sh.vfull[i % C::kV], (i / C::kV) & 1, p.timeout_ns);
     }
   } else if (warp >= 12) {
-    // ------------------------------------------------------------ delta, diagonal key tiles
+    // ------------------------------------------------------------ diagonal key tiles
     const int w = warp - 12;
     uint32_t t = 0;
     for (uint32_t it = 0;; ++it) {
-      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      if (!wait_bar_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
       const AttnUnit u = sh.unit[it & 1];
       if (u.head < 0) break;
       if (u.len > 0) {
-        // lane r keeps row r's statistics; 16 lanes hold the 8 values each of a row
-        const int l = lane & 15, mine = u.q0 + w * 32 + lane;
-        const int64_t at = (int64_t)u.head * p.tokens + u.start;
-        const bool has = l * 8 < p.head_dim;
-        const float lse = mine < u.len ? p.lse[at + mine] : 0.f;
-        float delta = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < 32; i += 2) {
-          const int r = u.q0 + w * 32 + i + (lane >> 4);
-          uint4 a = make_uint4(0, 0, 0, 0), b = a;
-          if (has && r < u.len) {
-            const int64_t o = ((int64_t)(u.start + r) * p.q_heads + u.head) * p.head_dim + l * 8;
-            a = *reinterpret_cast<const uint4*>(p.out + o);
-            b = *reinterpret_cast<const uint4*>(p.dout + o);
-          }
-          const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-          float sum = 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            sum = fmaf(as_f(x[e] << 16), as_f(y[e] << 16), sum);
-            sum = fmaf(as_f(x[e] & 0xffff0000u), as_f(y[e] & 0xffff0000u), sum);
-          }
-#pragma unroll
-          for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-          const float other = __shfl_xor_sync(~0u, sum, 16);
-          if (lane == i) delta = sum;            // lanes 0-15 hold row i,
-          if (lane == i + 1) delta = lane < 16 ? other : sum;  // 16-31 row i + 1
-          if (lane == i && lane >= 16) delta = other;
-        }
-        if (mine < u.len) {
-          const float nl = -lse * kLog2e;
-          stat[(it & 1) * 256 + w * 32 + lane] = nl;
-          stat[(it & 1) * 256 + 128 + w * 32 + lane] = delta;
-          p.nlse[at + mine] = nl;
-          p.delta[at + mine] = delta;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.stats[it & 1]);
         bool ok = true;
         for (int j = u.q0 / kTile; j >= 0; --j, ++t) {
           const uint32_t s = t % C::kK;
-          if (!(ok = mbar_wait_warp(&sh.kfull[s], (t / C::kK) & 1, ctx))) break;
+          if (!(ok = wait_bar_warp(&sh.kfull[s], (t / C::kK) & 1, ctx))) break;
           if (j == u.q0 / kTile) {
             clean_tile(smem + C::kRingK + s * C::kTileBytes, C::kBoxes, u.len - u.q0, w, 4, sh.flags[w]);
             fence_proxy_async_shared();
@@ -409,7 +420,6 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
         }
         if (!ok) break;
       } else if (lane == 0) {
-        mbar_arrive(&sh.stats[it & 1]);
         mbar_arrive(&sh.clean[it & 1]);
       }
       __syncwarp();
@@ -436,11 +446,13 @@ template <int DP>
 struct DkvCfg {
   static constexpr int kBoxes = DP / 64;
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
-  static constexpr int kStages = DP == 128 ? 2 : 4;  // Q and dout tiles
-  static constexpr int kRing = 2 * kTileBytes;       // after K and V; a stage is Q, dout
-  static constexpr int kBars = kRing + 2 * kStages * kTileBytes;
-  static constexpr int kStatStages = 4;              // -lse and delta of 128 queries
-  static constexpr int kSmem = kBars + kStatStages * 1024 + 1024;
+  // Q tiles (read by S and, last of a step, by dK) and dout tiles (dP, dV)
+  static constexpr int kQ = DP == 128 ? 3 : 4, kG = DP == 128 ? 2 : 4;
+  static constexpr int kRingQ = 2 * kTileBytes;      // after K and V
+  static constexpr int kRingG = kRingQ + kQ * kTileBytes;
+  static constexpr int kBars = kRingG + kG * kTileBytes;
+  static constexpr int kStatStages = 2;              // -lse and delta of 128 queries
+  static constexpr int kSmem = kBars + kStatStages * 1024 + 1024;  // 227 KB at 128
 };
 
 struct DkvShared {
@@ -479,13 +491,13 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
   const int heads = p.kv_heads * p.splits, per_split = p.group / p.splits;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      // a Q slot is given back by the MMAs and by the cleaning warps once they have
-      // seen its step's tiles
+    // slots are given back by the MMAs and by the cleaning warps, which so see
+    // every tile pass
+    for (int i = 0; i < C::kQ; ++i) {
       mbar_init(&sh.qfull[i], 1), mbar_init(&sh.qempty[i], 5);
-      mbar_init(&sh.gfull[i], 1), mbar_init(&sh.gempty[i], 1);
       mbar_init(&sh.clean[i], 4);
     }
+    for (int i = 0; i < C::kG; ++i) mbar_init(&sh.gfull[i], 1), mbar_init(&sh.gempty[i], 5);
     for (int i = 0; i < C::kStatStages; ++i) mbar_init(&sh.tfull[i], 1), mbar_init(&sh.tempty[i], 8);
     mbar_init(&sh.kvfull, 1);
     mbar_init(&sh.kvempty, 1);
@@ -522,7 +534,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
     const uint64_t c2 = pack_f32x2(c, c);
     uint32_t step = 0, units = 0;
     for (uint32_t it = 0;; ++it) {
-      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      if (!wait_bar_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
       const AttnUnit u = sh.unit[it & 1];
       if (u.head < 0) break;
       const int kvh = u.head / p.splits, split = u.head % p.splits;
@@ -542,12 +554,12 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
         for (int h = 0; h < per_split && ok; ++h)
           for (int i = first; i < end; ++i, ++step) {
             const uint32_t ts = step % C::kStatStages;
-            if (!(ok = mbar_wait_warp(&sh.tfull[ts], (step / C::kStatStages) & 1, ctx))) break;
+            if (!(ok = wait_bar_warp(&sh.tfull[ts], (step / C::kStatStages) & 1, ctx))) break;
             const float* nl = stat + ts * 256 + half * 64;
             const bool diag = i == first, masked = dkv_cleaned(u, i, first);
             const int limit = u.len - i * kTile - half * 64;  // queries of this sequence
             const int from = diag ? row - half * 64 : 0;      // ... not before the key
-            if (!(ok = mbar_wait_warp(&sh.sfull, step & 1, ctx))) break;
+            if (!(ok = wait_bar_warp(&sh.sfull, step & 1, ctx))) break;
             tc_fence_after();
             uint32_t s[2][32];
             load64(s, t_s + lanes + half * 64);
@@ -579,7 +591,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.pfull);
-            if (!(ok = mbar_wait_warp(&sh.dpfull, step & 1, ctx))) break;
+            if (!(ok = wait_bar_warp(&sh.dpfull, step & 1, ctx))) break;
             tc_fence_after();
             uint32_t g[2][32];
             load64(g, t_dp + lanes + half * 64);
@@ -612,7 +624,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
               mbar_arrive(&sh.tempty[ts]);
             }
           }
-        if (!ok || !mbar_wait_warp(&sh.accfull, units & 1, ctx)) break;
+        if (!ok || !wait_bar_warp(&sh.accfull, units & 1, ctx)) break;
         ++units;
         tc_fence_after();
         // warps 0-3 write dV, warps 4-7 dK
@@ -621,7 +633,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
         const int64_t at = ((int64_t)(u.start + r) * p.kv_heads + kvh) * p.head_dim;
         const uint32_t* dw = sh.dirty[it & 1];
         const bool dirty = half == 0 && (dw[0] | dw[1] | dw[2] | dw[3]);
-#pragma unroll
+#pragma unroll 1
         for (int d = 0; d < DP; d += 32) {
           uint32_t o[32];
           tmem_ld_32x32b_x32((half ? t_dk : t_dv) + lanes + d, o);
@@ -663,81 +675,66 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMA issuer
-    const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+    const uint32_t tm = __shfl_sync(~0u, tmem, 0), el = elect_one();
     const uint32_t a_s = tm, a_dp = tm + kTile, a_dv = tm + 2 * kTile, a_dk = tm + 3 * kTile;
     const uint32_t k0 = smem_u32(smem), v0 = k0 + C::kTileBytes;
-    const uint32_t ring = smem_u32(smem + C::kRing);
-    uint32_t base = 0, units = 0, nclean = 0;  // nclean: next phase of each stage's barrier
+    const uint32_t ring_q = smem_u32(smem + C::kRingQ), ring_g = smem_u32(smem + C::kRingG);
+    uint32_t base = 0, units = 0, nclean = 0;  // nclean: next phase of each Q slot's barrier
     bool ok = true;
-    auto q_tile = [&](uint32_t t) { return ring + (t % C::kStages) * 2 * C::kTileBytes; };
+    auto q_tile = [&](uint32_t t) { return ring_q + (t % C::kQ) * C::kTileBytes; };
+    auto g_tile = [&](uint32_t t) { return ring_g + (t % C::kG) * C::kTileBytes; };
     // waits for step t's Q (S and later dK read it) and, if it is cleaned, for that
     auto issue_s = [&](uint32_t t, bool cleaned) {
-      const uint32_t s = t % C::kStages;
-      if (!(ok = ok && mbar_wait_warp(&sh.qfull[s], (t / C::kStages) & 1, ctx))) return;
+      const uint32_t s = t % C::kQ;
+      if (!(ok = ok && wait_bar_warp(&sh.qfull[s], (t / C::kQ) & 1, ctx))) return;
       if (cleaned) {
-        if (!(ok = mbar_wait_warp(&sh.clean[s], (nclean >> s) & 1, ctx))) return;
+        if (!(ok = wait_bar_warp(&sh.clean[s], (nclean >> s) & 1, ctx))) return;
         nclean ^= 1u << s;
       }
-      tc_fence_after();
-      if (elect_one()) {
-        mma_tiles<DP>(a_s, k0, q_tile(t));
-        mma_commit(&sh.sfull);
-      }
-      __syncwarp();
+      mma_tiles<DP>(el, a_s, k0, q_tile(t));
+      mma_commit_if(el, &sh.sfull);
     };
     auto issue_dp = [&](uint32_t t) {
-      const uint32_t s = t % C::kStages;
-      if (!(ok = ok && mbar_wait_warp(&sh.gfull[s], (t / C::kStages) & 1, ctx))) return;
-      tc_fence_after();
-      if (elect_one()) {
-        mma_tiles<DP>(a_dp, v0, q_tile(t) + C::kTileBytes);
-        mma_commit(&sh.dpfull);
-      }
-      __syncwarp();
+      if (!(ok = ok && wait_bar_warp(&sh.gfull[t % C::kG], (t / C::kG) & 1, ctx))) return;
+      mma_tiles<DP>(el, a_dp, v0, g_tile(t));
+      mma_commit_if(el, &sh.dpfull);
     };
     for (uint32_t it = 0; ok; ++it) {
-      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      if (!wait_bar_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
       const AttnUnit u = uniform(sh.unit[it & 1]);
       if (u.head < 0) break;
       if (u.len > 0) {
         const int first = u.q0 / kTile, tiles = (u.len + kTile - 1) / kTile - first;
         const int n = tiles * per_split;
-        if (!mbar_wait_warp(&sh.kvfull, units & 1, ctx)) break;
+        if (!wait_bar_warp(&sh.kvfull, units & 1, ctx)) break;
         issue_s(base, true);
         issue_dp(base);
         int i = 0;  // query tile of step x within its head
         for (int x = 0; x < n && ok; ++x) {
           const uint32_t t = base + x;
-          if (!(ok = mbar_wait_warp(&sh.pfull, t & 1, ctx))) break;
+          if (!(ok = wait_bar_warp(&sh.pfull, t & 1, ctx))) break;
           tc_fence_after();
-          if (elect_one()) {
-            mma_tmem_tile<DP>(a_dv, a_s, 64, q_tile(t) + C::kTileBytes, x != 0);
-            mma_commit(&sh.gempty[t % C::kStages]);
-          }
-          __syncwarp();
+          mma_tmem_tile<DP>(el, a_dv, a_s, 64, g_tile(t), x != 0);
+          mma_commit_if(el, &sh.gempty[t % C::kG]);
           if (++i == tiles) i = 0;
           if (x + 1 < n) issue_s(t + 1, dkv_cleaned(u, first + i, first));
-          if (!(ok = ok && mbar_wait_warp(&sh.dsfull, t & 1, ctx))) break;
+          if (!(ok = ok && wait_bar_warp(&sh.dsfull, t & 1, ctx))) break;
           tc_fence_after();
-          if (elect_one()) {
-            mma_tmem_tile<DP>(a_dk, a_dp, 64, q_tile(t), x != 0);
-            mma_commit(&sh.qempty[t % C::kStages]);
-          }
-          __syncwarp();
+          mma_tmem_tile<DP>(el, a_dk, a_dp, 64, q_tile(t), x != 0);
+          mma_commit_if(el, &sh.qempty[t % C::kQ]);
           if (x + 1 < n) issue_dp(t + 1);
-          if ((x + 2 == n || n == 1) && elect_one()) mma_commit(&sh.kvempty);
-          __syncwarp();
+          if (x + 2 == n || n == 1) mma_commit_if(el, &sh.kvempty);
         }
         if (!ok) break;
-        if (elect_one()) mma_commit(&sh.accfull);
+        mma_commit_if(el, &sh.accfull);
         base += n;
         ++units;
       }
       if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
       __syncwarp();
     }
-    if (elect_one()) {
-      mma_commit(&sh.mma_done);
+    mma_commit_if(el, &sh.mma_done);
+    if (el) {
       mbar_wait_drain(&sh.mma_done, 0, p.timeout_ns);
     }
     __syncwarp();
@@ -749,8 +746,8 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
       prefetch_tensormap(&tv);
       prefetch_tensormap(&tdo);
     }
-    UnitWalk walk;
-    walk.init(p, kTile);
+    UnitWalk<kTile> walk;
+    walk.init(p);
     const int64_t total = (int64_t)walk.total() * heads;
     uint32_t nq = 0, ng = 0, units = 0;
     bool ok = true;
@@ -766,7 +763,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
         if (u.len > 0) u.q0 = ((u.len + kTile - 1) / kTile - 1) * kTile - u.q0;
       }
       if (lane == 0) {
-        ok = mbar_wait(&sh.uempty[it & 1], ((it >> 1) & 1) ^ 1, ctx);
+        ok = wait_bar(&sh.uempty[it & 1], ((it >> 1) & 1) ^ 1, ctx);
         if (ok) {
           sh.unit[it & 1] = u;
           mbar_arrive(&sh.ufull[it & 1]);
@@ -774,7 +771,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
         if (ok && u.len > 0) {
           const int kvh = u.head / p.splits;
           const int h0 = kvh * p.group + (u.head % p.splits) * per_split;
-          if ((ok = mbar_wait(&sh.kvempty, (units & 1) ^ 1, ctx))) {
+          if ((ok = wait_bar(&sh.kvempty, (units & 1) ^ 1, ctx))) {
             mbar_arrive_expect_tx(&sh.kvfull, 2 * C::kTileBytes);
             for (int b = 0; b < C::kBoxes; ++b) {
               tma_load_3d(smem + b * kBoxBytes, &tk, &sh.kvfull, b * 64, kvh, u.start + u.q0);
@@ -785,18 +782,18 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
           }
           for (int h = h0; h < h0 + per_split && ok; ++h)
             for (int i = u.q0; i < u.len; i += kTile) {
-              const int s = nq % C::kStages, ph = ((nq / C::kStages) & 1) ^ 1;
-              uint8_t* at = smem + C::kRing + s * 2 * C::kTileBytes;
-              if (!(ok = mbar_wait(&sh.qempty[s], ph, ctx))) break;
-              mbar_arrive_expect_tx(&sh.qfull[s], C::kTileBytes);
+              const int qs = nq % C::kQ, gs = ng % C::kG;
+              if (!(ok = wait_bar(&sh.qempty[qs], ((nq / C::kQ) & 1) ^ 1, ctx))) break;
+              mbar_arrive_expect_tx(&sh.qfull[qs], C::kTileBytes);
               for (int b = 0; b < C::kBoxes; ++b)
-                tma_load_3d(at + b * kBoxBytes, &tq, &sh.qfull[s], b * 64, h, u.start + i);
+                tma_load_3d(smem + C::kRingQ + qs * C::kTileBytes + b * kBoxBytes, &tq, &sh.qfull[qs],
+                            b * 64, h, u.start + i);
               ++nq;
-              if (!(ok = mbar_wait(&sh.gempty[s], ph, ctx))) break;
-              mbar_arrive_expect_tx(&sh.gfull[s], C::kTileBytes);
+              if (!(ok = wait_bar(&sh.gempty[gs], ((ng / C::kG) & 1) ^ 1, ctx))) break;
+              mbar_arrive_expect_tx(&sh.gfull[gs], C::kTileBytes);
               for (int b = 0; b < C::kBoxes; ++b)
-                tma_load_3d(at + C::kTileBytes + b * kBoxBytes, &tdo, &sh.gfull[s], b * 64, h,
-                            u.start + i);
+                tma_load_3d(smem + C::kRingG + gs * C::kTileBytes + b * kBoxBytes, &tdo, &sh.gfull[gs],
+                            b * 64, h, u.start + i);
               ++ng;
             }
         }
@@ -806,16 +803,16 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
     }
     if (!ok && lane == 0) {
       if (units) mbar_wait_drain(&sh.kvfull, (units - 1) & 1, p.timeout_ns);
-      for (uint32_t i = nq > C::kStages ? nq - C::kStages : 0; i < nq; ++i)
-        mbar_wait_drain(&sh.qfull[i % C::kStages], (i / C::kStages) & 1, p.timeout_ns);
-      for (uint32_t i = ng > C::kStages ? ng - C::kStages : 0; i < ng; ++i)
-        mbar_wait_drain(&sh.gfull[i % C::kStages], (i / C::kStages) & 1, p.timeout_ns);
+      for (uint32_t i = nq > C::kQ ? nq - C::kQ : 0; i < nq; ++i)
+        mbar_wait_drain(&sh.qfull[i % C::kQ], (i / C::kQ) & 1, p.timeout_ns);
+      for (uint32_t i = ng > C::kG ? ng - C::kG : 0; i < ng; ++i)
+        mbar_wait_drain(&sh.gfull[i % C::kG], (i / C::kG) & 1, p.timeout_ns);
     }
   } else if (warp == 10) {
     // ------------------------------------------------------------ statistics of the queries
     uint32_t step = 0;
     for (uint32_t it = 0;; ++it) {
-      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      if (!wait_bar_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
       const AttnUnit u = sh.unit[it & 1];
       if (u.head < 0) break;
       const int kvh = u.head / p.splits;
@@ -834,7 +831,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
               nl[e] = in ? p.nlse[at + r] : 0.f;
               dl[e] = in ? p.delta[at + r] : 0.f;
             }
-            if (!(ok = mbar_wait_warp(&sh.tempty[ts], ((step / C::kStatStages) & 1) ^ 1, ctx))) break;
+            if (!(ok = wait_bar_warp(&sh.tempty[ts], ((step / C::kStatStages) & 1) ^ 1, ctx))) break;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               stat[ts * 256 + e * 32 + lane] = nl[e];
@@ -852,7 +849,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
     const int w = warp - 12;
     uint32_t step = 0;
     for (uint32_t it = 0;; ++it) {
-      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      if (!wait_bar_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
       const AttnUnit u = sh.unit[it & 1];
       if (u.head < 0) break;
       bool ok = true;
@@ -861,26 +858,28 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
         const int first = u.q0 / kTile, end = (u.len + kTile - 1) / kTile;
         for (int h = 0; h < per_split && ok; ++h)
           for (int i = first; i < end; ++i, ++step) {
-            const uint32_t s = step % C::kStages, ph = (step / C::kStages) & 1;
-            uint8_t* at = smem + C::kRing + s * 2 * C::kTileBytes;
+            const uint32_t qs = step % C::kQ, gs = step % C::kG;
+            uint8_t* q = smem + C::kRingQ + qs * C::kTileBytes;
+            uint8_t* g = smem + C::kRingG + gs * C::kTileBytes;
             const int valid = u.len - i * kTile;
-            if (!(ok = mbar_wait_warp(&sh.qfull[s], ph, ctx))) break;
-            if (i == first) clean_tile(at, C::kBoxes, valid, w, 4, sh.flags[w][0]);
-            else if (valid < kTile) zero_rows(at, C::kBoxes, valid, w, 4);
-            if (!(ok = mbar_wait_warp(&sh.gfull[s], ph, ctx))) break;
+            if (!(ok = wait_bar_warp(&sh.qfull[qs], (step / C::kQ) & 1, ctx))) break;
+            if (i == first) clean_tile(q, C::kBoxes, valid, w, 4, sh.flags[w][0]);
+            else if (valid < kTile) zero_rows(q, C::kBoxes, valid, w, 4);
+            if (!(ok = wait_bar_warp(&sh.gfull[gs], (step / C::kG) & 1, ctx))) break;
             if (i == first) {
               uint32_t* fl = sh.flags[w][1];
-              clean_tile(at + C::kTileBytes, C::kBoxes, valid, w, 4, fl);
+              clean_tile(g, C::kBoxes, valid, w, 4, fl);
               __syncwarp();
               if (lane == 0 && (fl[0] | fl[1] | fl[2] | fl[3])) sh.dirty[it & 1][w] = 1;
             } else if (valid < kTile) {
-              zero_rows(at + C::kTileBytes, C::kBoxes, valid, w, 4);
+              zero_rows(g, C::kBoxes, valid, w, 4);
             }
             fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) {
-              if (dkv_cleaned(u, i, first)) mbar_arrive(&sh.clean[s]);
-              mbar_arrive(&sh.qempty[s]);
+              if (dkv_cleaned(u, i, first)) mbar_arrive(&sh.clean[qs]);
+              mbar_arrive(&sh.qempty[qs]);
+              mbar_arrive(&sh.gempty[gs]);
             }
           }
       }

@@ -39,55 +39,77 @@ struct AttnUnit {
 __device__ __forceinline__ int warp_add(int x) { return __reduce_add_sync(~0u, x); }
 __device__ __forceinline__ int warp_max(int x) { return __reduce_max_sync(~0u, x); }
 
-// The sequences of a pack cut into units of `rows` rows, numbered so that the
+// The sequences of a pack cut into units of ROWS rows, numbered so that the
 // units with the most keys come first (unit i of a sequence sees i + 1 units'
 // worth of keys): dealt out in this order, the CTAs end together.  Every unit
 // number is mapped by one warp on its own from the offsets, so no list of units
 // is written and no launch goes before the attention.  Cost: about
-// log2(longest / rows) passes over the offsets, 32 at a time.
+// log2(longest / ROWS) passes over the sequences, 32 at a time; the first
+// 32 * kHeld are held in the warp's registers, the offsets of more are read again
+// in every pass.
+template <int ROWS>
 struct UnitWalk {
+  static constexpr int kHeld = 4;
   const int32_t* cu;
-  int n, tokens, rows;
+  int n, tokens;
   int longest;    // units of the longest sequence
   int units;      // units of all sequences
   int lead, gaps; // rows before the first sequence; units of all rows in none
+  int tail_start;
+  int start[kHeld], len[kHeld];  // of sequences lane + 32 k
 
-  __device__ __forceinline__ int count(int s) const {
-    return s < n ? (cu[s + 1] - cu[s] + rows - 1) / rows : 0;
+  static __device__ __forceinline__ int cut(int rows) { return (rows + ROWS - 1) / ROWS; }
+  // Units of sequence lane + 32 k.
+  __device__ __forceinline__ int count(int k) const {
+    const int s = 32 * k + (threadIdx.x & 31);
+    return s < n ? cut(cu[s + 1] - cu[s]) : 0;
   }
   // Units with index >= i within their sequence.
   __device__ __forceinline__ int from(int i) const {
     int t = 0;
-    for (int s = threadIdx.x & 31; s < n; s += 32) t += max(0, count(s) - i);
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) t += max(0, cut(len[k]) - i);
+    for (int k = kHeld; 32 * k < n; ++k) t += max(0, count(k) - i);
     return warp_add(t);
   }
   // Executed by one whole warp.  Offsets that do not ascend within [0,
   // tokens] leave every row in no sequence.
-  __device__ __forceinline__ void init(const AttnParams& p, int unit_rows) {
+  __device__ __forceinline__ void init(const AttnParams& p) {
+    const int lane = threadIdx.x & 31;
     cu = p.cu;
     n = p.n_seqs;
     tokens = p.tokens;
-    rows = unit_rows;
-    int bad = 0, most = 0, sum = 0;
-    for (int s = threadIdx.x & 31; s <= n; s += 32) {
-      const int a = cu[s], b = s < n ? cu[s + 1] : a;
-      bad |= a < 0 || a > tokens || b < a || b > tokens;
-      if (!bad) {
-        const int c = (b - a + rows - 1) / rows;
-        most = max(most, c);
-        sum += c;
-      }
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      const int s = 32 * k + lane;
+      start[k] = s < n ? cu[s] : 0;
+      len[k] = s < n ? cu[s + 1] : 0;  // the end, for now
     }
-    bad = __any_sync(~0u, bad);
-    if (bad) {
-      if (blockIdx.x == 0 && (threadIdx.x & 31) == 0) record_error(p.err_word, kErrIndex);
-      n = 0;
+    lead = cu[0];
+    tail_start = cu[n];
+    int bad = lead < 0 || tail_start > tokens, most = 0, sum = 0;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      len[k] -= start[k];
+      bad |= len[k] < 0 || start[k] < 0 || start[k] > tokens;
+      most = max(most, cut(len[k]));
+      sum += cut(len[k]);
     }
-    longest = bad ? 0 : warp_max(most);
-    units = bad ? 0 : warp_add(sum);
-    lead = bad ? 0 : cu[0];
-    const int tail = bad ? tokens : tokens - cu[n];
-    gaps = (lead + rows - 1) / rows + (tail + rows - 1) / rows;
+    for (int k = kHeld; 32 * k < n; ++k) {
+      const int s = 32 * k + lane, a = s < n ? cu[s] : 0, b = s < n ? cu[s + 1] : a;
+      bad |= b < a || a < 0 || a > tokens;
+      most = max(most, cut(b - a));
+      sum += cut(b - a);
+    }
+    longest = warp_max(most);
+    units = warp_add(sum);
+    if (__any_sync(~0u, bad)) {
+      if (blockIdx.x == 0 && lane == 0) record_error(p.err_word, kErrIndex);
+      n = longest = units = lead = tail_start = 0;
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) len[k] = 0;
+    }
+    gaps = cut(lead) + cut(tokens - tail_start);
   }
   __device__ __forceinline__ int total() const { return units + gaps; }
 
@@ -95,10 +117,9 @@ struct UnitWalk {
   __device__ __forceinline__ AttnUnit at(int rank) const {
     AttnUnit u{};
     if (rank >= units) {
-      const int g = rank - units, lead_units = (lead + rows - 1) / rows;
-      const int first = n > 0 || lead > 0 ? cu[n] : 0;
-      u.start = g < lead_units ? g * rows : first + (g - lead_units) * rows;
-      u.rows = min(rows, (g < lead_units ? lead : tokens) - u.start);
+      const int g = rank - units, first = cut(lead);
+      u.start = g < first ? g * ROWS : tail_start + (g - first) * ROWS;
+      u.rows = min(ROWS, (g < first ? lead : tokens) - u.start);
       return u;
     }
     int lo = 0, hi = longest;  // from(lo) > rank >= from(hi)
@@ -107,21 +128,30 @@ struct UnitWalk {
       const int m = (lo + hi) >> 1, f = from(m);
       if (f > rank) lo = m; else hi = m, after = f;
     }
+    u.q0 = lo * ROWS;
     int nth = rank - after;  // among the sequences with more than lo units
-    for (int s0 = 0; s0 < n; s0 += 32) {
-      const int s = s0 + (threadIdx.x & 31);
-      const unsigned has = __ballot_sync(~0u, count(s) > lo);
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      const unsigned has = __ballot_sync(~0u, cut(len[k]) > lo);
       const int c = __popc(has);
-      if (nth < c) {
-        const int q = s0 + (int)__fns(has, 0, nth + 1);
-        u.start = cu[q];
-        u.len = cu[q + 1] - u.start;
-        u.q0 = lo * rows;
-        return u;
+      if (nth >= 0 && nth < c) {
+        const int src = (int)__fns(has, 0, nth + 1);
+        u.start = __shfl_sync(~0u, start[k], src);
+        u.len = __shfl_sync(~0u, len[k], src);
       }
       nth -= c;
     }
-    return u;  // not reached
+    for (int k = kHeld; 32 * k < n && u.len == 0; ++k) {
+      const unsigned has = __ballot_sync(~0u, count(k) > lo);
+      const int c = __popc(has);
+      if (nth < c) {
+        const int q = 32 * k + (int)__fns(has, 0, nth + 1);
+        u.start = cu[q];
+        u.len = cu[q + 1] - u.start;
+      }
+      nth -= c;
+    }
+    return u;
   }
 };
 
@@ -131,10 +161,30 @@ __device__ __forceinline__ int64_t dealt_unit(uint32_t r, int c, int g) {
   return (int64_t)r * g + ((r & 1) ? g - 1 - c : c);
 }
 
-// mbar_wait by a whole warp: all its lanes get the same answer, so that they
-// leave a loop together.
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const WaitCtx& ctx) {
-  return __all_sync(~0u, mbar_wait(bar, parity, ctx));
+// Bounded waits like mbar_wait, with the time limit in a function of its own:
+// these kernels wait in some thirty places, and what a warp does between two
+// waits is short enough for fetching its instructions to count.
+// Returns ~0 to give up, else the time of the first call for this wait.
+__device__ __noinline__ uint64_t wait_limit(uint64_t since, const WaitCtx ctx) {
+  if (*ctx.abort) return ~0ull;
+  const uint64_t now = global_timer_ns();
+  if (since == 0) return now;
+  if (now - since <= ctx.timeout_ns) return since;
+  *ctx.abort = 1;
+  record_error(ctx.err_word, kErrTimeout);
+  return ~0ull;
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const WaitCtx& ctx) {
+  const uint32_t a = smem_u32(bar);
+  uint64_t since = 0;
+  for (uint32_t n = 1; !mbar_try_wait(a, parity); ++n)
+    if ((n & 63u) == 0u && (since = wait_limit(since, ctx)) == ~0ull) return false;
+  return true;
+}
+// By a whole warp: all its lanes get the same answer, so that they leave a loop
+// together.
+__device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, const WaitCtx& ctx) {
+  return __all_sync(~0u, wait_bar(bar, parity, ctx));
 }
 
 // Products of whole tiles, issued by the elected lane of a converged warp.  The
@@ -144,26 +194,27 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, c
 //
 // d (+)= A B^T over DP head values; A and B are 128-row tiles in shared memory.
 template <int DP>
-__device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t a_tile, uint32_t b_tile) {
+__device__ __forceinline__ void mma_tiles(uint32_t el, uint32_t d, uint32_t a_tile, uint32_t b_tile) {
   constexpr uint32_t idesc = make_idesc(false, false, kTile, kTile);
   const uint32_t a = desc_lo(a_tile, 16), b = desc_lo(b_tile, 16);
 #pragma unroll
   for (int kk = 0; kk < DP / 16; ++kk) {
     const uint32_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
-    mma_issue_lo(d, a + off, b + off, idesc, kk != 0);
+    mma_issue_lo(el, d, a + off, b + off, idesc, kk != 0);
   }
 }
 // d (+)= A B over 128 rows of the tile B (128 x DP); A is packed bf16 in TMEM,
 // `gap` columns from one run of 64 k to the next (32 when they are adjacent).
-template <int DP>
-__device__ __forceinline__ void mma_tmem_tile(uint32_t d, uint32_t a, int gap, uint32_t b_tile,
-                                              bool accumulate) {
+// R0, R1: which runs.
+template <int DP, int R0 = 0, int R1 = 2>
+__device__ __forceinline__ void mma_tmem_tile(uint32_t el, uint32_t d, uint32_t a, int gap,
+                                              uint32_t b_tile, bool accumulate) {
   constexpr uint32_t idesc = make_idesc(false, true, kTile, DP);
   const uint32_t b = desc_lo(b_tile, kBoxBytes);
 #pragma unroll
-  for (int kk = 0; kk < kTile / 16; ++kk)
-    mma_issue_ts(d, a + (kk >> 2) * gap + (kk & 3) * 8, b + ((kk * 2048) >> 4), idesc,
-                 kk != 0 || accumulate);
+  for (int kk = 4 * R0; kk < 4 * R1; ++kk)
+    mma_issue_ts(el, d, a + (kk >> 2) * gap + (kk & 3) * 8, b + ((kk * 2048) >> 4), idesc,
+                 kk != 4 * R0 || accumulate);
 }
 
 // A unit read from shared memory by a whole warp, the same in all its lanes.

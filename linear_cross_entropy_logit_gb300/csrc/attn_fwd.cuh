@@ -24,7 +24,9 @@
 //
 // The maximum is only moved when it grows by more than kMoveLog2 (2^8): until
 // then exponentials are relative to the old one, at most 2^8 in size, and O is
-// left alone.  l and m are fp32; P is rounded to bf16 (2^-9 each, the type of
+// left alone.  So half of a tile's exponentials are made before its maximum is
+// known, and made again in the rare case that it moves; P is handed over in
+// halves, the first to be multiplied while the second is made.  l and m are fp32; P is rounded to bf16 (2^-9 each, the type of
 // V), and l sums it before that rounding.
 #pragma once
 #include "attn_common.cuh"
@@ -46,6 +48,12 @@ struct FwdCfg {
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
   static constexpr int kSlots = DP == 128 ? 4 : 8;  // K and V tiles in flight
   static constexpr int kRing = 2 * kTileBytes;      // after the two Q tiles
+  // Whether the next K tile is waited for at a step's start, or behind its first
+  // product.  A wait costs the issuing warp some 150 cycles beside the softmax even
+  // when there is nothing to wait for, and with 8 slots there rarely is; with 4 the
+  // tile can still be on its way.  At the start / behind: 408 / 405 us at 8192 tokens,
+  // 32 / 8 heads of 128; 1005 / 1095 us at 32768 tokens, 8 / 2 heads of 64.
+  static constexpr bool kEarlyK = DP == 64;
   static constexpr int kBars = kRing + kSlots * kTileBytes;
   static constexpr int kSmem = kBars + 512;
 };
@@ -53,7 +61,7 @@ struct FwdCfg {
 struct FwdShared {
   uint64_t full[8], empty[8];  // ring of K and V tiles
   uint64_t qfull, qempty;
-  uint64_t sfull[2], pfull[2], ofull[2];
+  uint64_t sfull[2], phalf[2], pfull[2], ofull[2];
   uint64_t clean[2][2];        // by unit parity and query tile: its diagonal value tile is fit for use
   uint64_t ufull[2], uempty[2];
   uint64_t mma_done;
@@ -89,6 +97,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
     mbar_init(&sh.qempty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.sfull[i], 1);
+      mbar_init(&sh.phalf[i], 4);
       mbar_init(&sh.pfull[i], 4);
       mbar_init(&sh.ofull[i], 1);
       mbar_init(&sh.ufull[i], 1);
@@ -120,7 +129,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
     const float c = p.scale * kLog2e;
     uint32_t ns = 0, no = 0;  // tiles and units of this query tile so far
     for (uint32_t it = 0;; ++it) {
-      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      if (!wait_bar_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
       const AttnUnit u = sh.unit[it & 1];
       if (u.head < 0) break;
       int n0, n1;
@@ -143,73 +152,87 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
       float m = 0.f, l = 0.f;
       bool ok = true;
       for (int j = n - 1; j >= 0; --j, ++ns) {
-        if (!(ok = mbar_wait_warp(&sh.sfull[x], ns & 1, ctx))) break;
+        if (!(ok = wait_bar_warp(&sh.sfull[x], ns & 1, ctx))) break;
         tc_fence_after();
         uint32_t s[4][32];
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, s[i]);
         tmem_ld_wait();
+        auto row_max = [&] {
+          float mx[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            mx[i] = __uint_as_float(s[i][0]);
+#pragma unroll
+            for (int e = 1; e < 31; e += 2)
+              mx[i] = fmax3(mx[i], __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
+            mx[i] = fmaxf(mx[i], __uint_as_float(s[i][31]));
+          }
+          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        };
+        uint64_t sum[4];
+        // P of half of the row's keys, relative to the maximum m
+        auto half = [&](int i0) {
+          const float b = m == -INFINITY ? 0.f : -m * c;  // no key so far: all p are 0
+          const uint64_t c2 = pack_f32x2(c, c), b2 = pack_f32x2(b, b);
+#pragma unroll
+          for (int i = i0; i < i0 + 2; ++i) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float p0, p1;
+              unpack_f32x2(fma_f32x2(pack_u32x2(s[i][e], s[i][e + 1]), c2, b2), p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              const uint64_t both = pack_f32x2(p0, p1);
+              sum[(e >> 1) & 3] = i == 0 && e < 8 ? both : add_f32x2(sum[(e >> 1) & 3], both);
+              pk[e >> 1] = pack_bf16x2(p0, p1);
+            }
+            tmem_st_32x32b_x16(ts + 16 * i, pk);
+          }
+        };
+        auto ready = [&](uint64_t* bar) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar);
+        };
         if (j == n - 1) {  // the diagonal
           asm volatile("");  // a branch: as selects it would cost every tile 128 of them
 #pragma unroll
           for (int i = 0; i < 128; ++i)
             if (i > row) s[i >> 5][i & 31] = 0xff800000u;  // -infinity
+          m = row_max();
         }
-        float mx[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mx[i] = __uint_as_float(s[i][0]);
-#pragma unroll
-          for (int e = 1; e < 31; e += 2)
-            mx[i] = fmax3(mx[i], __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
-          mx[i] = fmaxf(mx[i], __uint_as_float(s[i][31]));
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (j == n - 1) {
-          m = top;
-        } else {
+        // The first half goes by the maximum so far, while this tile's is found: the
+        // exponentials need not wait for it.
+        for (;;) {
+          half(0);
+          const float top = row_max();
           const bool move = (top - m) * c > kMoveLog2;
-          if (__any_sync(~0u, move)) {
-            const float f = move ? ex2_approx((m - top) * c) : 1.f;
-            if (move) m = top;
-            l *= f;
+          if (!__any_sync(~0u, move)) break;
+          // O is rescaled and the first half done again
+          const float f = move ? ex2_approx((m - top) * c) : 1.f;
+          if (move) m = top;
+          l *= f;
+#pragma unroll 1
+          for (int d = 0; d < DP; d += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(to + d, o);
+            tmem_ld_wait();
 #pragma unroll
-            for (int d = 0; d < DP; d += 32) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(to + d, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st_32x32b_x32(to + d, o);
-            }
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st_32x32b_x32(to + d, o);
           }
         }
-        const float b = m == -INFINITY ? 0.f : -m * c;  // no key so far: all p are 0
-        const uint64_t c2 = pack_f32x2(c, c), b2 = pack_f32x2(b, b);
-        uint64_t sum[4] = {};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float p0, p1;
-            unpack_f32x2(fma_f32x2(pack_u32x2(s[i][e], s[i][e + 1]), c2, b2), p0, p1);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-            sum[(e >> 1) & 3] = add_f32x2(sum[(e >> 1) & 3], pack_f32x2(p0, p1));
-            pk[e >> 1] = pack_bf16x2(p0, p1);
-          }
-          tmem_st_32x32b_x16(ts + 16 * i, pk);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.pfull[x]);
+        ready(&sh.phalf[x]);
+        half(2);
+        ready(&sh.pfull[x]);
         float l0, l1;
         unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), l0, l1);
         l += l0 + l1;
       }
-      if (!ok || !mbar_wait_warp(&sh.ofull[x], no & 1, ctx)) break;
+      if (!ok || !wait_bar_warp(&sh.ofull[x], no & 1, ctx)) break;
       ++no;
       tc_fence_after();
       const uint32_t(&flags)[2][2][4] = sh.flags[it & 1];
@@ -220,7 +243,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
       const int r = u.q0 + x * kTile + row;  // row within the sequence
       const int64_t t = u.start + r;
       const float inv = 1.f / l;
-#pragma unroll
+#pragma unroll 1
       for (int d = 0; d < DP; d += 32) {
         uint32_t o[32];
         tmem_ld_32x32b_x32(to + d, o);
@@ -265,76 +288,70 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMA issuer
-    const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+    const uint32_t tm = __shfl_sync(~0u, tmem, 0), el = elect_one();
     const uint32_t q0 = smem_u32(smem);
     uint32_t base = 0;  // ring position of the unit's first tile
     uint32_t np[2] = {0, 0}, nq = 0, nclean = 0;  // bit 2 parity + tile of nclean: next phase
     bool ok = true;
     auto slot = [&](uint32_t pos) { return smem_u32(ring) + (pos % C::kSlots) * C::kTileBytes; };
     auto wait_tile = [&](uint32_t pos) {
-      ok = ok && mbar_wait_warp(&sh.full[pos % C::kSlots], (pos / C::kSlots) & 1, ctx);
-      tc_fence_after();
-      return ok;
+      return ok = ok && wait_bar_warp(&sh.full[pos % C::kSlots], (pos / C::kSlots) & 1, ctx);
     };
     for (uint32_t it = 0; ok; ++it) {
-      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      if (!wait_bar_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
       const AttnUnit u = uniform(sh.unit[it & 1]);
       if (u.head < 0) break;
       if (u.len > 0) {
         int n0, n1;
         unit_tiles(u, n0, n1);
         const int last = max(n0, n1) - 1;  // key tile j sits at ring position base + 2 (last - j)
-        if (!mbar_wait_warp(&sh.qfull, nq & 1, ctx)) break;
+        if (!wait_bar_warp(&sh.qfull, nq & 1, ctx)) break;
         ++nq;
         if (!wait_tile(base)) break;
-        if (elect_one()) {
-          const int x = n1 ? 1 : 0;
-          mma_tiles<DP>(tm + x * kTile, q0 + x * C::kTileBytes, slot(base));
-          mma_commit(&sh.sfull[x]);
-          mma_commit(&sh.empty[base % C::kSlots]);
-          if (last == 0) mma_commit(&sh.qempty);
-        }
-        __syncwarp();
+        const int x = n1 ? 1 : 0;
+        mma_tiles<DP>(el, tm + x * kTile, q0 + x * C::kTileBytes, slot(base));
+        mma_commit_if(el, &sh.sfull[x]);
+        mma_commit_if(el, &sh.empty[base % C::kSlots]);
+        if (last == 0) mma_commit_if(el, &sh.qempty);
         if (n1) {
           if (!wait_tile(base + 2)) break;
-          if (elect_one()) {
-            mma_tiles<DP>(tm, q0, slot(base + 2));
-            mma_commit(&sh.sfull[0]);
-          }
-          __syncwarp();
+          mma_tiles<DP>(el, tm, q0, slot(base + 2));
+          mma_commit_if(el, &sh.sfull[0]);
         }
         for (int j = last; j >= 0 && ok; --j) {
-          const uint32_t kpos = base + 2 * (last - j), vpos = kpos + 1, knext = kpos + 2;
+          const uint32_t vpos = base + 2 * (last - j) + 1, knext = vpos + 1;
           if (!wait_tile(vpos)) break;
+          if (C::kEarlyK && j > 0 && !wait_tile(knext)) break;
           if (j >= n0 - 1) {
             const uint32_t f = j - (n0 - 1), bit = 2 * (it & 1) + f;
-            if (!(ok = mbar_wait_warp(&sh.clean[it & 1][f], (nclean >> bit) & 1, ctx))) break;
+            if (!(ok = wait_bar_warp(&sh.clean[it & 1][f], (nclean >> bit) & 1, ctx))) break;
             nclean ^= 1u << bit;
           }
-          if (j > 0 && !wait_tile(knext)) break;
 #pragma unroll
           for (int x = 1; x >= 0; --x) {
             const int n = x ? n1 : n0;
             if (j >= n) continue;
-            if (!(ok = mbar_wait_warp(&sh.pfull[x], np[x] & 1, ctx))) break;
+            // the product with the first half of P runs while the second is made
+            if (!(ok = wait_bar_warp(&sh.phalf[x], np[x] & 1, ctx))) break;
+            tc_fence_after();
+            mma_tmem_tile<DP, 0, 1>(el, tm + 2 * kTile + x * DP, tm + x * kTile, 32, slot(vpos), j < n - 1);
+            if (!(ok = wait_bar_warp(&sh.pfull[x], np[x] & 1, ctx))) break;
             ++np[x];
             tc_fence_after();
-            if (elect_one()) {
-              mma_tmem_tile<DP>(tm + 2 * kTile + x * DP, tm + x * kTile, 32, slot(vpos), j < n - 1);
-              // the key tile right below a pair's top one was multiplied with tile 0 at the start
-              const bool top = n1 && j == last;
-              if (j > 0) {
-                mma_tiles<DP>(tm + x * kTile, q0 + x * C::kTileBytes, slot(knext));
-                mma_commit(&sh.sfull[x]);
-              } else {
-                mma_commit(&sh.ofull[x]);
-              }
-              if (x == 0 || j >= n0) mma_commit(&sh.empty[vpos % C::kSlots]);
-              if (j > 0 && (x == 0 || top)) mma_commit(&sh.empty[knext % C::kSlots]);
-              // the last product that reads Q is issued
-              if (j == 1 && (x == 0 || n0 == 1)) mma_commit(&sh.qempty);
+            mma_tmem_tile<DP, 1, 2>(el, tm + 2 * kTile + x * DP, tm + x * kTile, 32, slot(vpos), true);
+            // the key tile right below a pair's top one was multiplied with tile 0 at the start
+            const bool top = n1 && j == last;
+            if (j > 0) {
+              if (!C::kEarlyK && (x == 1 || j >= n1) && !wait_tile(knext)) break;
+              mma_tiles<DP>(el, tm + x * kTile, q0 + x * C::kTileBytes, slot(knext));
+              mma_commit_if(el, &sh.sfull[x]);
+            } else {
+              mma_commit_if(el, &sh.ofull[x]);
             }
-            __syncwarp();
+            if (x == 0 || j >= n0) mma_commit_if(el, &sh.empty[vpos % C::kSlots]);
+            if (j > 0 && (x == 0 || top)) mma_commit_if(el, &sh.empty[knext % C::kSlots]);
+            // the last product that reads Q is issued
+            if (j == 1 && (x == 0 || n0 == 1)) mma_commit_if(el, &sh.qempty);
           }
         }
         if (!ok) break;
@@ -343,8 +360,8 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
       if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
       __syncwarp();
     }
-    if (elect_one()) {
-      mma_commit(&sh.mma_done);
+    mma_commit_if(el, &sh.mma_done);
+    if (el) {
       mbar_wait_drain(&sh.mma_done, 0, p.timeout_ns);
     }
     __syncwarp();
@@ -355,8 +372,8 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
       prefetch_tensormap(&tk);
       prefetch_tensormap(&tv);
     }
-    UnitWalk walk;
-    walk.init(p, kFwdRows);
+    UnitWalk<kFwdRows> walk;
+    walk.init(p);
     const int64_t total = (int64_t)walk.total() * p.q_heads;
     uint32_t pos = 0, nq = 0;
     bool ok = true;
@@ -369,7 +386,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
         u.head = (int)(id % p.q_heads);
       }
       if (lane == 0) {
-        ok = mbar_wait(&sh.uempty[it & 1], ((it >> 1) & 1) ^ 1, ctx);
+        ok = wait_bar(&sh.uempty[it & 1], ((it >> 1) & 1) ^ 1, ctx);
         if (ok) {
           sh.unit[it & 1] = u;
           mbar_arrive(&sh.ufull[it & 1]);
@@ -380,13 +397,13 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
           const int last = max(n0, n1) - 1, kvh = u.head / p.group;
           auto load = [&](const CUtensorMap* map, int head, int r) {
             const int s = pos % C::kSlots;
-            if (!(ok = mbar_wait(&sh.empty[s], ((pos / C::kSlots) & 1) ^ 1, ctx))) return;
+            if (!(ok = wait_bar(&sh.empty[s], ((pos / C::kSlots) & 1) ^ 1, ctx))) return;
             mbar_arrive_expect_tx(&sh.full[s], C::kTileBytes);
             for (int b = 0; b < C::kBoxes; ++b)
               tma_load_3d(ring + s * C::kTileBytes + b * kBoxBytes, map, &sh.full[s], b * 64, head, r);
             ++pos;
           };
-          if ((ok = mbar_wait(&sh.qempty, (nq & 1) ^ 1, ctx))) {
+          if ((ok = wait_bar(&sh.qempty, (nq & 1) ^ 1, ctx))) {
             mbar_arrive_expect_tx(&sh.qfull, (n1 ? 2 : 1) * C::kTileBytes);
             for (int x = 0; x <= (n1 ? 1 : 0); ++x)
               for (int b = 0; b < C::kBoxes; ++b)
@@ -414,7 +431,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
     const int w = warp - 10;
     uint32_t base = 0;
     for (uint32_t it = 0;; ++it) {
-      if (!mbar_wait_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
+      if (!wait_bar_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
       const AttnUnit u = sh.unit[it & 1];
       if (u.head < 0) break;
       bool ok = true;
@@ -425,7 +442,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
         for (int j = last; j >= 0; --j) {
           const uint32_t pos = base + 2 * (last - j) + 1;
           const int f = j - (n0 - 1);
-          if (!(ok = mbar_wait_warp(&sh.full[pos % C::kSlots], (pos / C::kSlots) & 1, ctx))) break;
+          if (!(ok = wait_bar_warp(&sh.full[pos % C::kSlots], (pos / C::kSlots) & 1, ctx))) break;
           if (f >= 0) {
             clean_tile(ring + (pos % C::kSlots) * C::kTileBytes, C::kBoxes, u.len - j * kTile, w, 2,
                        sh.flags[it & 1][f][w]);

@@ -148,6 +148,9 @@ flce_status launch_backward(const flce_attention_desc* d, const CUtensorMap (&m)
   FLCE_HOST_TRY(set_smem(setup[0][dev], attn_dq<DP>, DqCfg<DP>::kSmem));
   FLCE_HOST_TRY(set_smem(setup[1][dev], attn_dkdv<DP>, DkvCfg<DP>::kSmem));
   const int64_t units = most_units(d, kTile);
+  attn_delta<<<dim3((unsigned)host::ceil_div(d->tokens, kDeltaRows), (unsigned)d->q_heads), 256, 0, st>>>(p);
+  host::count_launch();
+  FLCE_HOST_CUDA(cudaGetLastError());
   attn_dq<DP><<<(int)std::min<int64_t>(units * d->q_heads, sms), kBwdThreads, DqCfg<DP>::kSmem, st>>>(
       m[0], m[1], m[2], m[3], p);
   host::count_launch();

@@ -377,25 +377,35 @@ __host__ __device__ constexpr uint32_t make_idesc(bool a_mn, bool b_mn, uint32_t
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
   return (saddr >> 4) | ((lbo_bytes >> 4) << 16);
 }
-__device__ __forceinline__ void mma_issue_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
-                                             uint32_t idesc, uint32_t accumulate) {
+// Executed by a converged warp; the lane with `elected` set issues.  Predicated
+// rather than in a branch, so that the operands stay in uniform registers.
+__device__ __forceinline__ void mma_issue_lo(uint32_t elected, uint32_t d_tmem, uint32_t a_lo,
+                                             uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
       "mov.b64 a, {%1, 0x40004040};\n\tmov.b64 b, {%2, 0x40004040};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate)
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] * B[smem]^T: A is M lanes of packed bf16 pairs, 8
 // columns for the 16 k of one instruction.
-__device__ __forceinline__ void mma_issue_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
-                                             uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_issue_ts(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem,
+                                             uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
       "mov.b64 b, {%2, 0x40004040};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate)
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
+}
+__device__ __forceinline__ void mma_commit_if(uint32_t elected, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(smem_u32(bar)), "r"(elected) : "memory");
 }
 
 // True in one lane of a converged warp.
