@@ -37,26 +37,7 @@ struct AttnBwdParams : AttnParams {
   int splits;          // CTAs that share the query heads of a key / value head
 };
 
-// One thread's 64 scores and gradients of scores.
-__device__ __forceinline__ void load64(uint32_t (&r)[2][32], uint32_t at) {
-  tmem_ld_32x32b_x32(at, r[0]);
-  tmem_ld_32x32b_x32(at + 32, r[1]);
-  tmem_ld_wait();
-}
 __device__ __forceinline__ float as_f(uint32_t x) { return __uint_as_float(x); }
-
-// Writes `n` (a multiple of 8) fp32 values of a row as bf16, up to `limit`.
-template <int N>
-__device__ __forceinline__ void store_row(bf16* to, const uint32_t (&v)[N], float scale, int limit) {
-#pragma unroll
-  for (int e = 0; e < N; e += 8) {
-    if (e >= limit) break;
-    uint32_t w[4];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) w[g] = pack_bf16x2(as_f(v[e + 2 * g]) * scale, as_f(v[e + 2 * g + 1]) * scale);
-    *reinterpret_cast<uint4*>(to + e) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
 
 // ----------------------------------------------------------------------------
 // delta
@@ -128,7 +109,7 @@ struct DqCfg {
 
 struct DqShared {
   uint64_t kfull[5], kempty[5], vfull[4], vempty[4];
-  uint64_t qfull, qempty;
+  uint64_t qfull, qempty, gfull, gempty;  // Q and dout tiles
   uint64_t sfull, sread, dpfull[2], dsfull, accfull;
   uint64_t clean[2];
   uint64_t ufull[2], uempty[2];
@@ -158,6 +139,8 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
     for (int i = 0; i < C::kV; ++i) mbar_init(&sh.vfull[i], 1), mbar_init(&sh.vempty[i], 1);
     mbar_init(&sh.qfull, 1);
     mbar_init(&sh.qempty, 1);
+    mbar_init(&sh.gfull, 1);
+    mbar_init(&sh.gempty, 9);  // the MMAs and the 8 compute warps, which store through it
     mbar_init(&sh.sfull, 1);
     mbar_init(&sh.sread, 8);
     mbar_init(&sh.dsfull, 8);
@@ -200,6 +183,7 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
         if (half == 0 && row < u.rows) {
           uint4* o = reinterpret_cast<uint4*>(
               p.dq + ((int64_t)(u.start + row) * p.q_heads + u.head) * p.head_dim);
+#pragma unroll 1
           for (int d = 0; d < p.head_dim / 8; ++d) o[d] = make_uint4(0, 0, 0, 0);
         }
       } else {
@@ -253,17 +237,15 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
         if (!ok || !wait_bar_warp(&sh.accfull, units & 1, ctx)) break;
         ++units;
         tc_fence_after();
-        const int r = u.q0 + row;
-#pragma unroll 1
-        for (int d = 0; d < DP / 2; d += 32) {
-          uint32_t o[32];
-          const int d0 = half * (DP / 2) + d;
-          tmem_ld_32x32b_x32(t_acc + lanes + d0, o);
-          tmem_ld_wait();
-          if (r < u.len)
-            store_row(p.dq + ((int64_t)(u.start + r) * p.q_heads + u.head) * p.head_dim + d0, o,
-                      p.scale, p.head_dim - d0);
-        }
+        // each half of the warps writes half of the columns, through dout's tile
+        const int first = u.q0 + (warp & 3) * 32;
+        if (DP == 128 || half == 0)
+          store_rows(smem + C::kTileBytes + warp * 4096, t_acc + lanes + half * 64, p.scale,
+                     p.dq + ((int64_t)(u.start + first) * p.q_heads + u.head) * p.head_dim + half * 64,
+                     (int64_t)p.q_heads * p.head_dim, u.len - first, min(64, p.head_dim - half * 64));
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.gempty);
         tc_fence_before();
       }
       __syncwarp();
@@ -299,6 +281,7 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
         // the diagonal key tile is cleaned before any product reads it
         if (!wait_bar_warp(&sh.clean[it & 1], (it >> 1) & 1, ctx)) break;
         issue_s(base);
+        if (!(ok = ok && wait_bar_warp(&sh.gfull, units & 1, ctx))) break;
         issue_dp(base);
         for (int i = 0; i < n && ok; ++i) {
           const uint32_t t = base + i;
@@ -311,6 +294,7 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
           // Q and dout are free once the last S and dP are done
           if (i + 2 == n || n == 1) {
             mma_commit_if(el, &sh.qempty);
+            mma_commit_if(el, &sh.gempty);
           }
           if (!(ok = ok && wait_bar_warp(&sh.dsfull, t & 1, ctx))) break;
           tc_fence_after();
@@ -341,7 +325,7 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
     UnitWalk<kTile> walk;
     walk.init(p);
     const int64_t total = (int64_t)walk.total() * p.q_heads;
-    uint32_t t = 0, units = 0;
+    uint32_t t = 0, units = 0, nq = 0;
     uint32_t loaded_k = 0, loaded_v = 0;
     bool ok = true;
     for (uint32_t it = 0; ok; ++it) {
@@ -360,14 +344,11 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
         }
         if (ok && u.len > 0) {
           const int kvh = u.head / p.group;
-          if ((ok = wait_bar(&sh.qempty, (units & 1) ^ 1, ctx))) {
-            mbar_arrive_expect_tx(&sh.qfull, 2 * C::kTileBytes);
-            for (int b = 0; b < C::kBoxes; ++b) {
+          if ((ok = wait_bar(&sh.qempty, (nq & 1) ^ 1, ctx))) {
+            ++nq;
+            mbar_arrive_expect_tx(&sh.qfull, C::kTileBytes);
+            for (int b = 0; b < C::kBoxes; ++b)
               tma_load_3d(smem + b * kBoxBytes, &tq, &sh.qfull, b * 64, u.head, u.start + u.q0);
-              tma_load_3d(smem + C::kTileBytes + b * kBoxBytes, &tdo, &sh.qfull, b * 64, u.head,
-                          u.start + u.q0);
-            }
-            ++units;
           }
           for (int j = u.q0 / kTile; j >= 0 && ok; --j, ++t) {
             const int ks = t % C::kK, vs = t % C::kV, r = u.start + j * kTile;
@@ -377,6 +358,14 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
               tma_load_3d(smem + C::kRingK + ks * C::kTileBytes + b * kBoxBytes, &tk, &sh.kfull[ks],
                           b * 64, kvh, r);
             ++loaded_k;
+            if (j == u.q0 / kTile) {  // dout only now: its tile is free after the last unit's store
+              if (!(ok = wait_bar(&sh.gempty, (units & 1) ^ 1, ctx))) break;
+              mbar_arrive_expect_tx(&sh.gfull, C::kTileBytes);
+              for (int b = 0; b < C::kBoxes; ++b)
+                tma_load_3d(smem + C::kTileBytes + b * kBoxBytes, &tdo, &sh.gfull, b * 64, u.head,
+                            u.start + u.q0);
+              ++units;
+            }
             if (!(ok = wait_bar(&sh.vempty[vs], ((t / C::kV) & 1) ^ 1, ctx))) break;
             mbar_arrive_expect_tx(&sh.vfull[vs], C::kTileBytes);
             for (int b = 0; b < C::kBoxes; ++b)
@@ -390,7 +379,8 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
       if (u.head < 0) break;
     }
     if (!ok && lane == 0) {
-      if (units) mbar_wait_drain(&sh.qfull, (units - 1) & 1, p.timeout_ns);
+      if (nq) mbar_wait_drain(&sh.qfull, (nq - 1) & 1, p.timeout_ns);
+      if (units) mbar_wait_drain(&sh.gfull, (units - 1) & 1, p.timeout_ns);
       for (uint32_t i = loaded_k > C::kK ? loaded_k - C::kK : 0; i < loaded_k; ++i)
         mbar_wait_drain(&sh.kfull[i % C::kK], (i / C::kK) & 1, p.timeout_ns);
       for (uint32_t i = loaded_v > C::kV ? loaded_v - C::kV : 0; i < loaded_v; ++i)
@@ -450,7 +440,9 @@ struct DkvCfg {
   static constexpr int kQ = DP == 128 ? 3 : 4, kG = DP == 128 ? 2 : 4;
   static constexpr int kRingQ = 2 * kTileBytes;      // after K and V
   static constexpr int kRingG = kRingQ + kQ * kTileBytes;
-  static constexpr int kBars = kRingG + kG * kTileBytes;
+  // 4 KB for each compute warp's stores: V's tile, where it is large enough
+  static constexpr int kStage = DP == 128 ? kTileBytes : kRingG + kG * kTileBytes;
+  static constexpr int kBars = kRingG + kG * kTileBytes + (DP == 128 ? 0 : 8 * 4096);
   static constexpr int kStatStages = 2;              // -lse and delta of 128 queries
   static constexpr int kSmem = kBars + kStatStages * 1024 + 1024;  // 227 KB at 128
 };
@@ -458,7 +450,7 @@ struct DkvCfg {
 struct DkvShared {
   uint64_t qfull[4], qempty[4], gfull[4], gempty[4];  // Q and dout tiles
   uint64_t tfull[4], tempty[4];                       // statistics
-  uint64_t kvfull, kvempty;
+  uint64_t kfull, kempty, vfull, vempty;
   uint64_t sfull, dpfull, pfull, dsfull, accfull;
   uint64_t clean[4];                                  // by stage
   uint64_t ufull[2], uempty[2];
@@ -499,8 +491,10 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
     }
     for (int i = 0; i < C::kG; ++i) mbar_init(&sh.gfull[i], 1), mbar_init(&sh.gempty[i], 5);
     for (int i = 0; i < C::kStatStages; ++i) mbar_init(&sh.tfull[i], 1), mbar_init(&sh.tempty[i], 8);
-    mbar_init(&sh.kvfull, 1);
-    mbar_init(&sh.kvempty, 1);
+    mbar_init(&sh.kfull, 1);
+    mbar_init(&sh.kempty, 1);
+    mbar_init(&sh.vfull, 1);
+    mbar_init(&sh.vempty, 9);  // the MMAs and the 8 compute warps, which store through it
     mbar_init(&sh.sfull, 1);
     mbar_init(&sh.dpfull, 1);
     mbar_init(&sh.pfull, 8);
@@ -547,6 +541,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
                          ? reinterpret_cast<uint4*>((half ? p.dk : p.dv) + at)
                          : reinterpret_cast<uint4*>(p.partial + (half ? 0 : p.splits) * size +
                                                     split * size + at);
+#pragma unroll 1
           for (int d = 0; d < p.head_dim / (p.splits == 1 ? 8 : 4); ++d) o[d] = make_uint4(0, 0, 0, 0);
         }
       } else {
@@ -627,47 +622,38 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
         if (!ok || !wait_bar_warp(&sh.accfull, units & 1, ctx)) break;
         ++units;
         tc_fence_after();
-        // warps 0-3 write dV, warps 4-7 dK
-        const int r = u.q0 + row;
-        const bool live = r < u.len;
-        const int64_t at = ((int64_t)(u.start + r) * p.kv_heads + kvh) * p.head_dim;
+        // warps 0-3 write dV, warps 4-7 dK, through V's tile
+        const int row0 = u.q0 + (warp & 3) * 32, r = row0 + lane;  // the warp's first; this lane's
+        const float scale = half ? p.scale : 1.f;
+        const int64_t stride = (int64_t)p.kv_heads * p.head_dim;
+        const int64_t at = (int64_t)(u.start + row0) * stride + kvh * p.head_dim;
         const uint32_t* dw = sh.dirty[it & 1];
         const bool dirty = half == 0 && (dw[0] | dw[1] | dw[2] | dw[3]);
+        uint8_t* stage = smem + C::kStage + warp * 4096;
+        const uint32_t from = (half ? t_dk : t_dv) + lanes;
+        if (p.splits == 1)
+          store_rows(stage, from, scale, (half ? p.dk : p.dv) + at, stride, u.len - row0, p.head_dim);
+        else
+          store_rows(stage, from, scale,
+                     p.partial + ((half ? 0 : p.splits) + split) * p.tokens * stride + at, stride,
+                     u.len - row0, p.head_dim);
+        if (dirty) {  // add back the non-finite values of dout that each key sees
+          __syncwarp();
 #pragma unroll 1
-        for (int d = 0; d < DP; d += 32) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32((half ? t_dk : t_dv) + lanes + d, o);
-          tmem_ld_wait();
-          if (!live) continue;
-          if (dirty) {  // add back the non-finite values of dout that this key sees
-            for (int h = 0; h < per_split; ++h)
-              for (int i = row; i < kTile && u.q0 + i < u.len; ++i) {
-                const bf16* g = p.dout + ((int64_t)(u.start + u.q0 + i) * p.q_heads + kvh * p.group +
-                                          split * per_split + h) * p.head_dim + d;
-                for (int e = 0; e < 32 && d + e < p.head_dim; ++e) {
-                  const float v = __bfloat162float(g[e]);
-                  if (!isfinite(v)) {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                      if (x == e) o[x] = __float_as_uint(as_f(o[x]) + v);
-                  }
-                }
-              }
+          for (int i = row; r < u.len && i < kTile * per_split; ++i) {
+            const int q = i % kTile;  // query of the diagonal tile
+            if (q < row || u.q0 + q >= u.len) continue;
+            const bf16* g = p.dout + ((int64_t)(u.start + u.q0 + q) * p.q_heads + kvh * p.group +
+                                      split * per_split + i / kTile) * p.head_dim;
+            if (p.splits == 1) add_nonfinite(p.dv + at + lane * stride, g, p.head_dim);
+            else add_nonfinite(p.partial + (p.splits + split) * p.tokens * stride + at + lane * stride, g,
+                               p.head_dim);
           }
-          const float scale = half ? p.scale : 1.f;
-          if (p.splits == 1) {
-            store_row((half ? p.dk : p.dv) + at + d, o, scale, p.head_dim - d);
-          } else {
-            const int64_t size = (int64_t)p.tokens * p.kv_heads * p.head_dim;
-            float* to = p.partial + ((half ? 0 : p.splits) + split) * size + at + d;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              if (d + e < p.head_dim)
-                *reinterpret_cast<float4*>(to + e) =
-                    make_float4(as_f(o[e]) * scale, as_f(o[e + 1]) * scale, as_f(o[e + 2]) * scale,
-                                as_f(o[e + 3]) * scale);
-          }
+          __syncwarp();
         }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.vempty);
         tc_fence_before();
       }
       __syncwarp();
@@ -706,8 +692,9 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
       if (u.len > 0) {
         const int first = u.q0 / kTile, tiles = (u.len + kTile - 1) / kTile - first;
         const int n = tiles * per_split;
-        if (!wait_bar_warp(&sh.kvfull, units & 1, ctx)) break;
+        if (!wait_bar_warp(&sh.kfull, units & 1, ctx)) break;
         issue_s(base, true);
+        if (!(ok = ok && wait_bar_warp(&sh.vfull, units & 1, ctx))) break;
         issue_dp(base);
         int i = 0;  // query tile of step x within its head
         for (int x = 0; x < n && ok; ++x) {
@@ -723,7 +710,10 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
           mma_tmem_tile<DP>(el, a_dk, a_dp, 64, q_tile(t), x != 0);
           mma_commit_if(el, &sh.qempty[t % C::kQ]);
           if (x + 1 < n) issue_dp(t + 1);
-          if (x + 2 == n || n == 1) mma_commit_if(el, &sh.kvempty);
+          if (x + 2 == n || n == 1) {
+            mma_commit_if(el, &sh.kempty);
+            mma_commit_if(el, &sh.vempty);
+          }
         }
         if (!ok) break;
         mma_commit_if(el, &sh.accfull);
@@ -749,7 +739,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
     UnitWalk<kTile> walk;
     walk.init(p);
     const int64_t total = (int64_t)walk.total() * heads;
-    uint32_t nq = 0, ng = 0, units = 0;
+    uint32_t nq = 0, ng = 0, nk = 0, nv = 0;
     bool ok = true;
     for (uint32_t it = 0; ok; ++it) {
       const int64_t id = dealt_unit(it, blockIdx.x, gridDim.x);
@@ -771,14 +761,11 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
         if (ok && u.len > 0) {
           const int kvh = u.head / p.splits;
           const int h0 = kvh * p.group + (u.head % p.splits) * per_split;
-          if ((ok = wait_bar(&sh.kvempty, (units & 1) ^ 1, ctx))) {
-            mbar_arrive_expect_tx(&sh.kvfull, 2 * C::kTileBytes);
-            for (int b = 0; b < C::kBoxes; ++b) {
-              tma_load_3d(smem + b * kBoxBytes, &tk, &sh.kvfull, b * 64, kvh, u.start + u.q0);
-              tma_load_3d(smem + C::kTileBytes + b * kBoxBytes, &tv, &sh.kvfull, b * 64, kvh,
-                          u.start + u.q0);
-            }
-            ++units;
+          if ((ok = wait_bar(&sh.kempty, (nk & 1) ^ 1, ctx))) {
+            mbar_arrive_expect_tx(&sh.kfull, C::kTileBytes);
+            for (int b = 0; b < C::kBoxes; ++b)
+              tma_load_3d(smem + b * kBoxBytes, &tk, &sh.kfull, b * 64, kvh, u.start + u.q0);
+            ++nk;
           }
           for (int h = h0; h < h0 + per_split && ok; ++h)
             for (int i = u.q0; i < u.len; i += kTile) {
@@ -789,6 +776,14 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
                 tma_load_3d(smem + C::kRingQ + qs * C::kTileBytes + b * kBoxBytes, &tq, &sh.qfull[qs],
                             b * 64, h, u.start + i);
               ++nq;
+              if (h == h0 && i == u.q0) {  // V only now: its tile is free after the last unit's store
+                if (!(ok = wait_bar(&sh.vempty, (nv & 1) ^ 1, ctx))) break;
+                mbar_arrive_expect_tx(&sh.vfull, C::kTileBytes);
+                for (int b = 0; b < C::kBoxes; ++b)
+                  tma_load_3d(smem + C::kTileBytes + b * kBoxBytes, &tv, &sh.vfull, b * 64, kvh,
+                              u.start + u.q0);
+                ++nv;
+              }
               if (!(ok = wait_bar(&sh.gempty[gs], ((ng / C::kG) & 1) ^ 1, ctx))) break;
               mbar_arrive_expect_tx(&sh.gfull[gs], C::kTileBytes);
               for (int b = 0; b < C::kBoxes; ++b)
@@ -802,7 +797,8 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
       if (u.head < 0) break;
     }
     if (!ok && lane == 0) {
-      if (units) mbar_wait_drain(&sh.kvfull, (units - 1) & 1, p.timeout_ns);
+      if (nk) mbar_wait_drain(&sh.kfull, (nk - 1) & 1, p.timeout_ns);
+      if (nv) mbar_wait_drain(&sh.vfull, (nv - 1) & 1, p.timeout_ns);
       for (uint32_t i = nq > C::kQ ? nq - C::kQ : 0; i < nq; ++i)
         mbar_wait_drain(&sh.qfull[i % C::kQ], (i / C::kQ) & 1, p.timeout_ns);
       for (uint32_t i = ng > C::kG ? ng - C::kG : 0; i < ng; ++i)

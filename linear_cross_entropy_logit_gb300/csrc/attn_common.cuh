@@ -69,6 +69,7 @@ struct UnitWalk {
     int t = 0;
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) t += max(0, cut(len[k]) - i);
+#pragma unroll 1
     for (int k = kHeld; 32 * k < n; ++k) t += max(0, count(k) - i);
     return warp_add(t);
   }
@@ -95,6 +96,7 @@ struct UnitWalk {
       most = max(most, cut(len[k]));
       sum += cut(len[k]);
     }
+#pragma unroll 1
     for (int k = kHeld; 32 * k < n; ++k) {
       const int s = 32 * k + lane, a = s < n ? cu[s] : 0, b = s < n ? cu[s + 1] : a;
       bad |= b < a || a < 0 || a > tokens;
@@ -124,33 +126,33 @@ struct UnitWalk {
     }
     int lo = 0, hi = longest;  // from(lo) > rank >= from(hi)
     int after = 0;             // from(lo + 1) once hi = lo + 1
+#pragma unroll 1
     while (hi - lo > 1) {
       const int m = (lo + hi) >> 1, f = from(m);
       if (f > rank) lo = m; else hi = m, after = f;
     }
     u.q0 = lo * ROWS;
-    int nth = rank - after;  // among the sequences with more than lo units
+    // the sequence is the nth among those with more than lo units; its lane is the
+    // only one to add to the sums
+    int nth = rank - after, its_start = 0, its_len = 0;
+    auto pick = [&](int start_k, int len_k) {
+      const bool has = cut(len_k) > lo;
+      const unsigned all = __ballot_sync(~0u, has);
+      if (has && __popc(all & ((1u << (threadIdx.x & 31)) - 1)) == nth) {
+        its_start = start_k;
+        its_len = len_k;
+      }
+      nth -= __popc(all);
+    };
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      const unsigned has = __ballot_sync(~0u, cut(len[k]) > lo);
-      const int c = __popc(has);
-      if (nth >= 0 && nth < c) {
-        const int src = (int)__fns(has, 0, nth + 1);
-        u.start = __shfl_sync(~0u, start[k], src);
-        u.len = __shfl_sync(~0u, len[k], src);
-      }
-      nth -= c;
+    for (int k = 0; k < kHeld; ++k) pick(start[k], len[k]);
+#pragma unroll 1
+    for (int k = kHeld; 32 * k < n && nth >= 0; ++k) {
+      const int s = 32 * k + (threadIdx.x & 31), a = s < n ? cu[s] : 0;
+      pick(a, s < n ? cu[s + 1] - a : 0);
     }
-    for (int k = kHeld; 32 * k < n && u.len == 0; ++k) {
-      const unsigned has = __ballot_sync(~0u, count(k) > lo);
-      const int c = __popc(has);
-      if (nth < c) {
-        const int q = 32 * k + (int)__fns(has, 0, nth + 1);
-        u.start = cu[q];
-        u.len = cu[q + 1] - u.start;
-      }
-      nth -= c;
-    }
+    u.start = warp_add(its_start);
+    u.len = warp_add(its_len);
     return u;
   }
 };
@@ -203,6 +205,13 @@ __device__ __forceinline__ void mma_tiles(uint32_t el, uint32_t d, uint32_t a_ti
     mma_issue_lo(el, d, a + off, b + off, idesc, kk != 0);
   }
 }
+// One thread's 64 columns.
+__device__ __forceinline__ void load64(uint32_t (&r)[2][32], uint32_t at) {
+  tmem_ld_32x32b_x32(at, r[0]);
+  tmem_ld_32x32b_x32(at + 32, r[1]);
+  tmem_ld_wait();
+}
+
 // d (+)= A B over 128 rows of the tile B (128 x DP); A is packed bf16 in TMEM,
 // `gap` columns from one run of 64 k to the next (32 when they are adjacent).
 // R0, R1: which runs.
@@ -215,6 +224,62 @@ __device__ __forceinline__ void mma_tmem_tile(uint32_t el, uint32_t d, uint32_t 
   for (int kk = 4 * R0; kk < 4 * R1; ++kk)
     mma_issue_ts(el, d, a + (kk >> 2) * gap + (kk & 3) * 8, b + ((kk * 2048) >> 4), idesc,
                  kk != 4 * R0 || accumulate);
+}
+
+// Stores `cols` columns of a warp's 32 TMEM lanes (one row each) times `scale`, in
+// bf16 or fp32, through 4 KB of shared memory: eight lanes then write 128 bytes of
+// one row.  (Written by each lane for itself, a warp's store touches 32 lines and
+// takes as many cycles.)  `to`: the first row's first column; `rows`, `cols`: how
+// many are written, cols a multiple of 8.  The pieces of a row are permuted by the
+// row number, so that both sides are free of bank conflicts.  Once per unit, so its
+// instructions come from L2, eight to a line: unrolled it took 4000 cycles, rolled
+// loops a quarter of that.
+template <typename T>
+__device__ __forceinline__ void store_rows(uint8_t* stage, uint32_t taddr, float scale, T* to,
+                                           int64_t row_stride, int rows, int cols) {
+  constexpr int kCols = 128 / sizeof(T);  // columns in 128 bytes
+  const int lane = threadIdx.x & 31, p = lane & 7;
+  const uint32_t mine = smem_u32(stage) + lane * 128;
+#pragma unroll 1
+  for (int c = 0; c < cols; c += kCols) {
+    __syncwarp();  // the last round's reads
+#pragma unroll 1
+    for (int i = 0; i < 8; i += 16 * sizeof(T) / 16) {  // 16 columns: two or four pieces
+      uint32_t r[16];
+      tmem_ld_32x32b_x16(taddr + c + i * (16 / sizeof(T)), r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < (int)sizeof(T); ++e) {
+        uint32_t w[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if constexpr (sizeof(T) == 2)
+            w[g] = pack_bf16x2(__uint_as_float(r[8 * e + 2 * g]) * scale,
+                               __uint_as_float(r[8 * e + 2 * g + 1]) * scale);
+          else
+            w[g] = __float_as_uint(__uint_as_float(r[4 * e + g]) * scale);
+        }
+        st_shared_v4(mine + (((i + e) ^ p) << 4), w[0], w[1], w[2], w[3]);
+      }
+    }
+    __syncwarp();
+    T* at = to + (lane >> 3) * row_stride + c + p * (16 / sizeof(T));
+    const bool in = c + p * (int)(16 / sizeof(T)) < cols;
+#pragma unroll 2
+    for (int r = lane >> 3; r < 32; r += 4, at += 4 * row_stride) {
+      const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 128 + ((p ^ (r & 7)) << 4));
+      if (in && r < rows) *reinterpret_cast<uint4*>(at) = x;
+    }
+  }
+}
+// Adds the non-finite ones among the `cols` values of x to a row just stored.
+template <typename T>
+__device__ __noinline__ void add_nonfinite(T* row, const bf16* x, int cols) {
+#pragma unroll 1
+  for (int d = 0; d < cols; ++d) {
+    const float v = __bfloat162float(x[d]);
+    if (!isfinite(v)) row[d] = static_cast<T>(static_cast<float>(row[d]) + v);
+  }
 }
 
 // A unit read from shared memory by a whole warp, the same in all its lanes.
@@ -242,6 +307,7 @@ __device__ __forceinline__ void clean_tile(uint8_t* tile, int boxes, int valid, 
   const int lane = threadIdx.x & 31;
   if (lane < 4) flags[lane] = 0;
   __syncwarp();
+#pragma unroll 2
   for (int i = w * 32 + lane; i < boxes * kTile * 8; i += warps * 32) {
     uint4* at = reinterpret_cast<uint4*>(tile) + i;
     const int row = (i >> 3) & (kTile - 1);
@@ -264,6 +330,7 @@ __device__ __forceinline__ void clean_tile(uint8_t* tile, int boxes, int valid, 
 
 // The part of clean_tile that zeroes the rows from `valid` on.
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int boxes, int valid, int w, int warps) {
+#pragma unroll 1
   for (int i = w * 32 + (threadIdx.x & 31); i < boxes * kTile * 8; i += warps * 32)
     if (((i >> 3) & (kTile - 1)) >= valid)
       reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);

@@ -54,7 +54,8 @@ struct FwdCfg {
   // tile can still be on its way.  At the start / behind: 408 / 405 us at 8192 tokens,
   // 32 / 8 heads of 128; 1005 / 1095 us at 32768 tokens, 8 / 2 heads of 64.
   static constexpr bool kEarlyK = DP == 64;
-  static constexpr int kBars = kRing + kSlots * kTileBytes;
+  static constexpr int kStage = kRing + kSlots * kTileBytes;  // 4 KB for each softmax warp
+  static constexpr int kBars = kStage + 8 * 4096;
   static constexpr int kSmem = kBars + 512;
 };
 
@@ -67,6 +68,7 @@ struct FwdShared {
   uint64_t mma_done;
   AttnUnit unit[2];
   uint32_t flags[2][2][2][4];  // by unit parity, diagonal tile and cleaning warp: non-finite rows
+  alignas(16) uint32_t any[2][4];  // by unit parity: whether flags[..][tile][warp] has any set
   uint32_t tmem;
   int abort;
 };
@@ -141,6 +143,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
           const int64_t t = u.start + r;
           p.lse[(int64_t)u.head * p.tokens + t] = -INFINITY;
           uint4* o = reinterpret_cast<uint4*>(p.out + (t * p.q_heads + u.head) * p.head_dim);
+#pragma unroll 1
           for (int d = 0; d < p.head_dim / 8; ++d) o[d] = make_uint4(0, 0, 0, 0);
         }
       }
@@ -235,54 +238,28 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
       if (!ok || !wait_bar_warp(&sh.ofull[x], no & 1, ctx)) break;
       ++no;
       tc_fence_after();
-      const uint32_t(&flags)[2][2][4] = sh.flags[it & 1];
-      uint32_t any = 0;  // non-finite rows of this and the tile before it
-      for (int f = 0; f <= x; ++f)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) any |= flags[f][i >> 2][i & 3];
+      const uint4 found = *reinterpret_cast<const uint4*>(sh.any[it & 1]);
+      const bool any = found.x | found.y | (x ? found.z | found.w : 0);
       const int r = u.q0 + x * kTile + row;  // row within the sequence
-      const int64_t t = u.start + r;
-      const float inv = 1.f / l;
+      const int first = u.q0 + x * kTile + (warp & 3) * 32;  // the warp's first
+      store_rows(smem + C::kStage + warp * 4096, to, rcp_approx(l),
+                 p.out + ((int64_t)(u.start + first) * p.q_heads + u.head) * p.head_dim,
+                 (int64_t)p.q_heads * p.head_dim, u.len - first, p.head_dim);
+      if (any) {  // add back the non-finite values each row sees
+        __syncwarp();
 #pragma unroll 1
-      for (int d = 0; d < DP; d += 32) {
-        uint32_t o[32];
-        tmem_ld_32x32b_x32(to + d, o);
-        tmem_ld_wait();
-        if (any && r < u.len) {  // add back the non-finite values this row sees
-          for (int f = 0; f <= x; ++f)
-            for (int w = 0; w < 4; ++w)
-              for (uint32_t b = flags[f][0][w] | flags[f][1][w]; b; b &= b - 1) {
-                const int key = u.q0 + f * kTile + w * 32 + __ffs(b) - 1;
-                if (key > r) continue;
-                const bf16* v = p.v + (int64_t)(u.start + key) * p.v_row +
-                                (u.head / p.group) * p.v_head + d;
-                for (int e = 0; e < 32; ++e) {
-                  if (d + e >= p.head_dim) break;
-                  const float val = __bfloat162float(v[e]);
-                  if (!isfinite(val)) {
-#pragma unroll
-                    for (int g = 0; g < 32; ++g)
-                      if (g == e) o[g] = __float_as_uint(__uint_as_float(o[g]) + val);
-                  }
-                }
-              }
+        for (int i = 0; i < kTile * (x + 1) && u.q0 + i <= r && r < u.len; ++i) {
+          const int f = i / kTile, w = (i / 32) & 3;
+          if (((sh.flags[it & 1][f][0][w] | sh.flags[it & 1][f][1][w]) >> (i & 31)) & 1)
+            add_nonfinite(p.out + ((int64_t)(u.start + r) * p.q_heads + u.head) * p.head_dim,
+                          p.v + (int64_t)(u.start + u.q0 + i) * p.v_row + (u.head / p.group) * p.v_head,
+                          p.head_dim);
         }
-        if (r < u.len) {
-          bf16* out = p.out + (t * p.q_heads + u.head) * p.head_dim + d;
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            if (d + e >= p.head_dim) break;
-            uint32_t w[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-              w[g] = pack_bf16x2(__uint_as_float(o[e + 2 * g]) * inv,
-                                 __uint_as_float(o[e + 2 * g + 1]) * inv);
-            *reinterpret_cast<uint4*>(out + e) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
+        __syncwarp();
       }
       tc_fence_before();  // O is read before the next unit's first product into it
-      if (r < u.len) p.lse[(int64_t)u.head * p.tokens + t] = m * p.scale + logf(l);
+      if (r < u.len)
+        p.lse[(int64_t)u.head * p.tokens + u.start + r] = m * p.scale + lg2_approx(l) * kLn2;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
     }
@@ -450,7 +427,11 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
           }
           __syncwarp();
           if (lane == 0) {
-            if (f >= 0) mbar_arrive(&sh.clean[it & 1][f]);
+            if (f >= 0) {
+              const uint32_t* fl = sh.flags[it & 1][f][w];
+              sh.any[it & 1][2 * f + w] = fl[0] | fl[1] | fl[2] | fl[3];
+              mbar_arrive(&sh.clean[it & 1][f]);
+            }
             mbar_arrive(&sh.empty[pos % C::kSlots]);
           }
         }
