@@ -6,7 +6,6 @@ library is missing, ``lib()`` raises instead of falling back to anything.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -89,6 +88,10 @@ class FlceAttentionDesc(ctypes.Structure):
                 ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64),
                 ("k_row", ctypes.c_int64), ("k_head", ctypes.c_int64),
                 ("v_row", ctypes.c_int64), ("v_head", ctypes.c_int64)]
+
+
+_QK_DESC_BYTES = ctypes.sizeof(FlceQkNormRopeDesc)
+_ATTENTION_DESC_BYTES = ctypes.sizeof(FlceAttentionDesc)
 
 
 class FlceError(RuntimeError):
@@ -606,74 +609,79 @@ def flce_forward_noalloc(X, W, labels, ignore_index: int = -100, smoothing: floa
     return loss, lse, valid_count, err_word
 
 
-def _on_stream(stream):
-    """Context in which new tensors belong to the stream the call runs on, so
-    the allocator does not hand their memory to another stream's work too early."""
-    if stream is None:
-        return contextlib.nullcontext()
+# The attention and head-norm calls below are made for single tokens too, where
+# the host's time is the call's: their checks are kept to a few attribute reads.
+def _current_stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _with_stream(stream, call, *args, **kwargs):
+    """``call`` with ``stream`` as the current one, so that the tensors it makes belong to
+    the stream it runs on and their memory does not reach another stream's work too early."""
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return call(*args, **kwargs)
 
 
-def _heads(name, t, like=None):
-    """(row stride, head stride) of a [tokens, heads, head_dim] CUDA tensor whose
-    heads are contiguous; any number of tokens or heads may be 1."""
-    if not t.is_cuda or t.dim() != 3:
-        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, head_dim], got "
-                         f"{tuple(t.shape)} on {t.device}")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise TypeError(f"{name} must have the dtype and device of q: {t.dtype} on {t.device}")
+def _cuda_device(q) -> int:
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError(f"q must be a CUDA tensor, got one on {q.device}")
+    return dev
+
+
+def _heads(name, t, dtype, dev):
+    """(tokens, heads, head_dim, row stride, head stride) of a [tokens, heads, head_dim]
+    tensor whose heads are contiguous."""
+    if t.get_device() != dev or t.dtype is not dtype:
+        raise TypeError(f"{name} must have the dtype and device of q ({dtype}, cuda:{dev}), "
+                        f"got {t.dtype} on {t.device}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
     T, H, D = t.shape
     row, head, one = t.stride()
-    if D > 1 and one != 1:
+    if one != 1 and D > 1:
         raise ValueError(f"{name}: the head_dim values of a head must be contiguous")
-    return (row if T > 1 else H * D), (head if H > 1 else D)
+    # the stride of a single token or head means nothing
+    return T, H, D, (row if T > 1 else H * D), (head if H > 1 else D)
 
 
-def _result(name, t, shape, dtype, device):
-    """An output buffer: the caller's (checked), or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if t.shape != torch.Size(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
-    return t
-
-
-def _operand(name, t, shape, dtype, device):
-    """A contiguous input of the given shape and type."""
-    if t.shape != torch.Size(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}, "
+def _array(name, t, shape, dtype, dev):
+    """Checks a contiguous operand or output of the given shape and type; its address."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on cuda:{dev}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t
+    return t.data_ptr()
 
 
-def _workspace_bytes(buf, need: int, device):
-    """The caller's workspace, or a new one of the required size."""
-    return torch.empty(max(need, 256), dtype=torch.uint8, device=device) if buf is None else buf
+def _new(t, like, shape, dtype):
+    """The caller's output, or a new contiguous one."""
+    return torch.empty(shape, dtype=dtype, device=like.device) if t is None else t
 
 
-def _qk_norm_rope_desc(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
-    q_row, q_head = _heads("q", q)
-    k_row, k_head = _heads("k", k, q)
-    T, HQ, D = q.shape
-    if k.shape[0] != T or k.shape[2] != D:
+def _qk_norm_rope_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+    """(desc, device, the inputs' addresses)."""
+    dev, dtype = _cuda_device(q), q.dtype
+    T, HQ, D, q_row, q_head = _heads("q", q, dtype, dev)
+    Tk, HK, Dk, k_row, k_head = _heads("k", k, dtype, dev)
+    if Tk != T or Dk != D:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _operand(name, w, (D,), q.dtype, q.device)
+    wq = None if q_weight is None else _array("q_weight", q_weight, (D,), dtype, dev)
+    wk = None if k_weight is None else _array("k_weight", k_weight, (D,), dtype, dev)
     rows = half = 0
+    pc = ps = pp = None
     if cos is not None or sin is not None:
         if cos is None or sin is None or cos.dim() != 2:
             raise ValueError("cos and sin must both be [positions, rot_dim / 2] tensors, or None")
-        rows, half = cos.shape
-        _operand("cos", cos, (rows, half), torch.float32, q.device)
-        _operand("sin", sin, (rows, half), torch.float32, q.device)
+        rows, half = shape = cos.shape
+        pc = _array("cos", cos, shape, torch.float32, dev)
+        ps = _array("sin", sin, shape, torch.float32, dev)
     if positions is not None:
-        _operand("positions", positions, (T,), torch.int64, q.device)
-    return FlceQkNormRopeDesc(ctypes.sizeof(FlceQkNormRopeDesc), T, HQ, k.shape[1], D, 2 * half,
-                              rows, _dtype_code(q), eps, int(bool(interleaved)), q_row, q_head,
-                              k_row, k_head)
+        pp = _array("positions", positions, (T,), torch.int64, dev)
+    d = FlceQkNormRopeDesc(_QK_DESC_BYTES, T, HQ, HK, D, 2 * half, rows, _dtype_code(q), eps,
+                           1 if interleaved else 0, q_row, q_head, k_row, k_head)
+    return d, dev, (q.data_ptr(), k.data_ptr(), wq, wk, pc, ps, pp)
 
 
 def flce_qk_norm_rope_forward(q, k, q_weight, k_weight, cos, sin, positions=None,
@@ -685,15 +693,20 @@ def flce_qk_norm_rope_forward(q, k, q_weight, k_weight, cos, sin, positions=None
     cos, sin: float32 [positions, rot_dim / 2], or None for no rotation; the
     first rot_dim values of a head are turned, in pairs (j, j + rot_dim / 2), or
     (2j, 2j + 1) when interleaved.  positions: int64 [T] or None (0, 1, 2, ...)."""
-    d = _qk_norm_rope_desc(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
-    with _on_stream(stream):
-        q_out = _result("q_out", q_out, q.shape, q.dtype, q.device)
-        k_out = _result("k_out", k_out, k.shape, q.dtype, q.device)
-        err_word = new_err_word(q.device) if err_word is None else err_word
-        st = lib().flce_qk_norm_rope_forward(
-            ctypes.byref(d), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(cos),
-            _ptr(sin), _ptr(positions), _ptr(q_out), _ptr(k_out), _ptr(err_word), _stream(stream))
-    _check(st, "flce_qk_norm_rope_forward")
+    if stream is not None:
+        return _with_stream(stream, flce_qk_norm_rope_forward, q, k, q_weight, k_weight, cos, sin,
+                            positions, eps, interleaved=interleaved, q_out=q_out, k_out=k_out,
+                            err_word=err_word)
+    d, dev, ptrs = _qk_norm_rope_args(q, k, q_weight, k_weight, cos, sin, positions, eps,
+                                      interleaved)
+    dtype = q.dtype
+    q_out, k_out = _new(q_out, q, q.shape, dtype), _new(k_out, q, k.shape, dtype)
+    err_word = new_err_word(q.device) if err_word is None else err_word
+    st = lib().flce_qk_norm_rope_forward(
+        d, *ptrs, _array("q_out", q_out, q.shape, dtype, dev),
+        _array("k_out", k_out, k.shape, dtype, dev), err_word.data_ptr(), _current_stream(dev))
+    if st:
+        _check(st, "flce_qk_norm_rope_forward")
     return q_out, k_out, err_word
 
 
@@ -703,43 +716,51 @@ def flce_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, si
                                stream=None):
     """Gradients of flce_qk_norm_rope_forward: (dq, dk in q's dtype, dq_weight,
     dk_weight float32 [D], err_word)."""
-    d = _qk_norm_rope_desc(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
-    dev = q.device
-    _operand("dq_out", dq_out, q.shape, q.dtype, dev)
-    _operand("dk_out", dk_out, k.shape, q.dtype, dev)
-    with _on_stream(stream):
-        dq = _result("dq", dq, q.shape, q.dtype, dev)
-        dk = _result("dk", dk, k.shape, q.dtype, dev)
-        dq_weight = _result("dq_weight", dq_weight, (q.shape[2],), torch.float32, dev)
-        dk_weight = _result("dk_weight", dk_weight, (q.shape[2],), torch.float32, dev)
-        ws = _workspace_bytes(workspace_buf,
-                              lib().flce_qk_norm_rope_workspace_size(ctypes.byref(d)), dev)
-        err_word = new_err_word(dev) if err_word is None else err_word
-        st = lib().flce_qk_norm_rope_backward(
-            ctypes.byref(d), _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight),
-            _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions), _ptr(dq), _ptr(dk),
-            _ptr(dq_weight), _ptr(dk_weight), _ptr(ws), ws.numel(), _ptr(err_word),
-            _stream(stream))
-    _check(st, "flce_qk_norm_rope_backward")
+    if stream is not None:
+        return _with_stream(stream, flce_qk_norm_rope_backward, dq_out, dk_out, q, k, q_weight,
+                            k_weight, cos, sin, positions, eps, interleaved=interleaved, dq=dq,
+                            dk=dk, dq_weight=dq_weight, dk_weight=dk_weight,
+                            workspace_buf=workspace_buf, err_word=err_word)
+    d, dev, ptrs = _qk_norm_rope_args(q, k, q_weight, k_weight, cos, sin, positions, eps,
+                                      interleaved)
+    dtype, f32, w_shape = q.dtype, torch.float32, (q.shape[2],)
+    dq, dk = _new(dq, q, q.shape, dtype), _new(dk, q, k.shape, dtype)
+    dq_weight, dk_weight = _new(dq_weight, q, w_shape, f32), _new(dk_weight, q, w_shape, f32)
+    L = lib()
+    ws = workspace_buf
+    if ws is None:
+        ws = torch.empty(max(L.flce_qk_norm_rope_workspace_size(d), 256), dtype=torch.uint8,
+                         device=q.device)
+    err_word = new_err_word(q.device) if err_word is None else err_word
+    st = L.flce_qk_norm_rope_backward(
+        d, _array("dq_out", dq_out, q.shape, dtype, dev), _array("dk_out", dk_out, k.shape, dtype, dev),
+        *ptrs, _array("dq", dq, q.shape, dtype, dev), _array("dk", dk, k.shape, dtype, dev),
+        _array("dq_weight", dq_weight, w_shape, f32, dev),
+        _array("dk_weight", dk_weight, w_shape, f32, dev), ws.data_ptr(), ws.numel(),
+        err_word.data_ptr(), _current_stream(dev))
+    if st:
+        _check(st, "flce_qk_norm_rope_backward")
     return dq, dk, dq_weight, dk_weight, err_word
 
 
-def _attention_desc(q, k, v, cu_seqlens, scale):
-    q_row, q_head = _heads("q", q)
-    k_row, k_head = _heads("k", k, q)
-    v_row, v_head = _heads("v", v, q)
-    if q.dtype != torch.bfloat16:
-        raise TypeError(f"attention takes bfloat16 q, k and v, got {q.dtype}")
-    T, HQ, D = q.shape
-    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D:
+def _attention_args(q, k, v, cu_seqlens, scale):
+    """(desc, device, lse's shape)."""
+    dev, dtype = _cuda_device(q), q.dtype
+    if dtype is not torch.bfloat16:
+        raise TypeError(f"attention takes bfloat16 q, k and v, got {dtype}")
+    T, HQ, D, q_row, q_head = _heads("q", q, dtype, dev)
+    Tk, HK, Dk, k_row, k_head = _heads("k", k, dtype, dev)
+    Tv, Hv, Dv, v_row, v_head = _heads("v", v, dtype, dev)
+    if Tk != T or Dk != D or Tv != T or Hv != HK or Dv != D:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-        raise ValueError("cu_seqlens must hold the sequences' offsets, one more than sequences")
-    _operand("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, q.device)
-    scale = D ** -0.5 if scale is None else scale
-    return FlceAttentionDesc(ctypes.sizeof(FlceAttentionDesc), T, cu_seqlens.numel() - 1, HQ,
-                             k.shape[1], D, FLCE_BF16, scale, q_row, q_head, k_row, k_head, v_row,
-                             v_head)
+    n = cu_seqlens.numel()
+    if (n < 1 or cu_seqlens.dim() != 1 or cu_seqlens.dtype is not torch.int32
+            or cu_seqlens.get_device() != dev or not cu_seqlens.is_contiguous()):
+        raise ValueError("cu_seqlens must be a contiguous int32 tensor of the sequences' offsets, "
+                         f"one more than sequences, on cuda:{dev}")
+    return FlceAttentionDesc(_ATTENTION_DESC_BYTES, T, n - 1, HQ, HK, D, FLCE_BF16,
+                             D ** -0.5 if scale is None else scale, q_row, q_head, k_row, k_head,
+                             v_row, v_head), dev, (HQ, T)
 
 
 def flce_attention_forward(q, k, v, cu_seqlens, scale: Optional[float] = None, *, out=None,
@@ -748,15 +769,19 @@ def flce_attention_forward(q, k, v, cu_seqlens, scale: Optional[float] = None, *
     [T, Hk, D] bf16 (views are fine), cu_seqlens int32 offsets.  Returns
     (out [T, Hq, D] bf16, lse [Hq, T] float32, err_word); scale defaults to
     D ** -0.5.  Rows outside the sequences get out 0 and lse -inf."""
-    d = _attention_desc(q, k, v, cu_seqlens, scale)
-    with _on_stream(stream):
-        out = _result("out", out, q.shape, q.dtype, q.device)
-        lse = _result("lse", lse, (q.shape[1], q.shape[0]), torch.float32, q.device)
-        err_word = new_err_word(q.device) if err_word is None else err_word
-        st = lib().flce_attention_forward(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v),
-                                          _ptr(cu_seqlens), _ptr(out), _ptr(lse), _ptr(err_word),
-                                          _stream(stream))
-    _check(st, "flce_attention_forward")
+    if stream is not None:
+        return _with_stream(stream, flce_attention_forward, q, k, v, cu_seqlens, scale, out=out,
+                            lse=lse, err_word=err_word)
+    d, dev, lse_shape = _attention_args(q, k, v, cu_seqlens, scale)
+    dtype, f32 = q.dtype, torch.float32
+    out, lse = _new(out, q, q.shape, dtype), _new(lse, q, lse_shape, f32)
+    err_word = new_err_word(q.device) if err_word is None else err_word
+    st = lib().flce_attention_forward(
+        d, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
+        _array("out", out, q.shape, dtype, dev), _array("lse", lse, lse_shape, f32, dev),
+        err_word.data_ptr(), _current_stream(dev))
+    if st:
+        _check(st, "flce_attention_forward")
     return out, lse, err_word
 
 
@@ -765,23 +790,27 @@ def flce_attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale: Optional
                             stream=None):
     """Gradients (dq, dk, dv, err_word) of flce_attention_forward, contiguous bf16;
     those of a key / value head are summed over the query heads that read it."""
-    d = _attention_desc(q, k, v, cu_seqlens, scale)
-    dev = q.device
-    _operand("dout", dout, q.shape, q.dtype, dev)
-    _operand("out", out, q.shape, q.dtype, dev)
-    _operand("lse", lse, (q.shape[1], q.shape[0]), torch.float32, dev)
-    with _on_stream(stream):
-        dq = _result("dq", dq, q.shape, q.dtype, dev)
-        dk = _result("dk", dk, k.shape, q.dtype, dev)
-        dv = _result("dv", dv, v.shape, q.dtype, dev)
-        ws = _workspace_bytes(workspace_buf,
-                              lib().flce_attention_workspace_size(ctypes.byref(d)), dev)
-        err_word = new_err_word(dev) if err_word is None else err_word
-        st = lib().flce_attention_backward(ctypes.byref(d), _ptr(dout), _ptr(q), _ptr(k), _ptr(v),
-                                           _ptr(out), _ptr(lse), _ptr(cu_seqlens), _ptr(dq),
-                                           _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(),
-                                           _ptr(err_word), _stream(stream))
-    _check(st, "flce_attention_backward")
+    if stream is not None:
+        return _with_stream(stream, flce_attention_backward, dout, q, k, v, out, lse, cu_seqlens,
+                            scale, dq=dq, dk=dk, dv=dv, workspace_buf=workspace_buf,
+                            err_word=err_word)
+    d, dev, lse_shape = _attention_args(q, k, v, cu_seqlens, scale)
+    dtype, shape, kv_shape = q.dtype, q.shape, k.shape
+    dq, dk, dv = _new(dq, q, shape, dtype), _new(dk, q, kv_shape, dtype), _new(dv, q, kv_shape, dtype)
+    L = lib()
+    ws = workspace_buf
+    if ws is None:
+        ws = torch.empty(max(L.flce_attention_workspace_size(d), 256), dtype=torch.uint8,
+                         device=q.device)
+    err_word = new_err_word(q.device) if err_word is None else err_word
+    st = L.flce_attention_backward(
+        d, _array("dout", dout, shape, dtype, dev), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        _array("out", out, shape, dtype, dev), _array("lse", lse, lse_shape, torch.float32, dev),
+        cu_seqlens.data_ptr(), _array("dq", dq, shape, dtype, dev),
+        _array("dk", dk, kv_shape, dtype, dev), _array("dv", dv, kv_shape, dtype, dev),
+        ws.data_ptr(), ws.numel(), err_word.data_ptr(), _current_stream(dev))
+    if st:
+        _check(st, "flce_attention_backward")
     return dq, dk, dv, err_word
 
 
