@@ -12,8 +12,6 @@ using host::aligned;
 
 namespace {
 
-constexpr int kBlocksPerSm = 4;  // blocks of the persistent backward on each SM
-
 bool shape_ok(const flce_qk_norm_rope_desc* d) {
   if (!d || d->struct_size != sizeof(flce_qk_norm_rope_desc)) return false;
   if (d->dtype != FLCE_BF16 && d->dtype != FLCE_FP32) return false;
@@ -29,16 +27,39 @@ bool stride_ok(int64_t row, int64_t head, int64_t head_dim) {
   return row % 8 == 0 && head % 8 == 0 && row > 0 && head >= head_dim;
 }
 
-// Groups of G lanes hold a head of up to 8 G values.
-int group_lanes(int64_t head_dim) { return head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32; }
+// How a head is spread over lanes: 2 P values each, P = 8 where that divides what
+// is turned and the whole head (each lane then loads 16 bytes at a time), else 4.
+struct Spread {
+  int p, log_lanes;
+};
+Spread spread(const flce_qk_norm_rope_desc* d) {
+  const int p = d->rot_dim % 16 == 0 && d->head_dim % 16 == 0 ? 8 : 4;
+  int log_lanes = 0;
+  while ((2 * p << log_lanes) < d->head_dim) ++log_lanes;
+  return {p, log_lanes};
+}
 
-// Blocks of the backward, each of which writes one partial row: as many as
-// there is work for, kBlocksPerSm for each of the device's SMs at most.
-int64_t backward_blocks(const flce_qk_norm_rope_desc* d, int sms) {
-  const int64_t items =
-      d->tokens * host::ceil_div(d->q_heads + d->kv_heads, (int64_t)kNormHeads);
-  return std::min<int64_t>(host::ceil_div(items, kNormThreads / group_lanes(d->head_dim)),
-                           (int64_t)kBlocksPerSm * sms);
+int heads_per_item(const flce_qk_norm_rope_desc* d, bool bwd) {
+  if (d->dtype == FLCE_BF16)
+    return bwd ? NormHeads<__nv_bfloat16>::kBwd : NormHeads<__nv_bfloat16>::kFwd;
+  return bwd ? NormHeads<float>::kBwd : NormHeads<float>::kFwd;
+}
+
+// Blocks for the items of q and of k: one lane group each forward; backward
+// as many as there is work for, kNormBwdBlocks for each SM at most, in proportion.
+struct Blocks {
+  int64_t q, k;
+};
+Blocks blocks(const flce_qk_norm_rope_desc* d, bool bwd, int sms) {
+  const int64_t per = kNormThreads >> spread(d).log_lanes, u = heads_per_item(d, bwd);
+  const int64_t q = d->tokens * host::ceil_div(d->q_heads, u), k = d->tokens * host::ceil_div(d->kv_heads, u);
+  Blocks b{host::ceil_div(q, per), host::ceil_div(k, per)};
+  const int64_t most = (int64_t)kNormBwdBlocks * sms;
+  if (bwd && b.q + b.k > most) {
+    b.q = std::min(std::max<int64_t>(1, most * q / (q + k)), most - 1);
+    b.k = most - b.q;
+  }
+  return b;
 }
 
 flce_status check(const flce_qk_norm_rope_desc* d, const void* const* ptrs, int n,
@@ -62,28 +83,30 @@ flce_status check(const flce_qk_norm_rope_desc* d, const void* const* ptrs, int 
   return FLCE_OK;
 }
 
-QkNormRopeParams params(const flce_qk_norm_rope_desc* d, const void* q, const void* k,
+QkNormRopeParams params(const flce_qk_norm_rope_desc* d, bool bwd, const void* q, const void* k,
                         const void* wq, const void* wk, const float* cos_t, const float* sin_t,
                         const int64_t* positions, void* q_out, void* k_out, int32_t* err_word) {
   QkNormRopeParams p{};
-  p.q = q;
-  p.k = k;
-  p.wq = wq;
-  p.wk = wk;
+  const int64_t u = heads_per_item(d, bwd);
+  auto side = [&](const void* x, const void* w, void* out, int64_t row, int64_t head, int64_t heads) {
+    NormSide s{};
+    s.x = x;
+    s.w = w;
+    s.out = out;
+    s.row = row;
+    s.head = head;
+    s.heads = (int)heads;
+    s.per_token = (int)host::ceil_div(heads, u);
+    s.items = d->tokens * s.per_token;
+    return s;
+  };
+  p.q = side(q, wq, q_out, d->q_row, d->q_head, d->q_heads);
+  p.k = side(k, wk, k_out, d->k_row, d->k_head, d->kv_heads);
   p.cos_t = cos_t;
   p.sin_t = sin_t;
   p.positions = positions;
-  p.q_out = q_out;
-  p.k_out = k_out;
-  p.q_row = d->q_row;
-  p.q_head = d->q_head;
-  p.k_row = d->k_row;
-  p.k_head = d->k_head;
   p.table_rows = d->table_rows;
-  p.blocks_per_token = (int)host::ceil_div(d->q_heads + d->kv_heads, (int64_t)kNormHeads);
-  p.items = d->tokens * p.blocks_per_token;
-  p.q_heads = (int)d->q_heads;
-  p.kv_heads = (int)d->kv_heads;
+  p.log_lanes = spread(d).log_lanes;
   p.head_dim = (int)d->head_dim;
   p.rot_dim = (int)d->rot_dim;
   p.eps = d->eps;
@@ -92,36 +115,30 @@ QkNormRopeParams params(const flce_qk_norm_rope_desc* d, const void* q, const vo
   return p;
 }
 
-template <bool BWD, typename T, int G, bool PAIRS>
-void launch(const QkNormRopeParams& p, unsigned blocks, cudaStream_t st) {
+template <bool BWD, typename T, int P, bool PAIRS>
+void launch(const QkNormRopeParams& p, unsigned n, cudaStream_t st) {
   if constexpr (BWD)
-    qk_norm_rope_bwd<T, G, PAIRS><<<blocks, kNormThreads, 0, st>>>(p);
+    qk_norm_rope_bwd<T, P, PAIRS><<<n, kNormThreads, 0, st>>>(p);
   else
-    qk_norm_rope_fwd<T, G, PAIRS><<<blocks, kNormThreads, 0, st>>>(p);
+    qk_norm_rope_fwd<T, P, PAIRS><<<n, kNormThreads, 0, st>>>(p);
 }
 
 template <bool BWD, typename T>
-void launch_g(const flce_qk_norm_rope_desc* d, const QkNormRopeParams& p, unsigned blocks,
-              cudaStream_t st) {
-  const int g = group_lanes(d->head_dim);
-  if (d->interleaved) {
-    if (g == 8) launch<BWD, T, 8, true>(p, blocks, st);
-    else if (g == 16) launch<BWD, T, 16, true>(p, blocks, st);
-    else launch<BWD, T, 32, true>(p, blocks, st);
-  } else {
-    if (g == 8) launch<BWD, T, 8, false>(p, blocks, st);
-    else if (g == 16) launch<BWD, T, 16, false>(p, blocks, st);
-    else launch<BWD, T, 32, false>(p, blocks, st);
-  }
+void launch_t(const flce_qk_norm_rope_desc* d, const QkNormRopeParams& p, unsigned n, cudaStream_t st) {
+  const bool wide = spread(d).p == 8;
+  if (d->interleaved)
+    wide ? launch<BWD, T, 8, true>(p, n, st) : launch<BWD, T, 4, true>(p, n, st);
+  else
+    wide ? launch<BWD, T, 8, false>(p, n, st) : launch<BWD, T, 4, false>(p, n, st);
 }
 
 template <bool BWD>
-flce_status launch_any(const flce_qk_norm_rope_desc* d, const QkNormRopeParams& p,
-                       int64_t blocks, cudaStream_t st) {
+flce_status launch_any(const flce_qk_norm_rope_desc* d, const QkNormRopeParams& p, int64_t n,
+                       cudaStream_t st) {
   if (d->dtype == FLCE_BF16)
-    launch_g<BWD, __nv_bfloat16>(d, p, (unsigned)blocks, st);
+    launch_t<BWD, __nv_bfloat16>(d, p, (unsigned)n, st);
   else
-    launch_g<BWD, float>(d, p, (unsigned)blocks, st);
+    launch_t<BWD, float>(d, p, (unsigned)n, st);
   host::count_launch();
   FLCE_HOST_CUDA(cudaGetLastError());
   return FLCE_OK;
@@ -139,7 +156,8 @@ size_t flce_qk_norm_rope_workspace_size(const flce_qk_norm_rope_desc* d) {
     (void)cudaGetLastError();
     sms = 152;
   }
-  return host::align_up(std::max<size_t>(1, backward_blocks(d, sms)) * 2 * d->head_dim * 4);
+  const Blocks b = blocks(d, true, sms);
+  return host::align_up(std::max<size_t>(1, b.q + b.k) * d->head_dim * 4);
 }
 
 flce_status flce_qk_norm_rope_forward(const flce_qk_norm_rope_desc* d, const void* q,
@@ -154,11 +172,13 @@ flce_status flce_qk_norm_rope_forward(const flce_qk_norm_rope_desc* d, const voi
   if (d->tokens == 0) return FLCE_OK;
   int dev, sms;
   FLCE_HOST_TRY(host::device(&dev, &sms));
-  const QkNormRopeParams p = params(d, q, k, q_weight, k_weight, cos_table, sin_table, positions,
-                                    q_out, k_out, err_word);
-  const int64_t blocks = host::ceil_div(p.items, kNormThreads / group_lanes(d->head_dim));
-  if (blocks > INT_MAX) return FLCE_ERR_UNSUPPORTED;
-  return launch_any<false>(d, p, blocks, static_cast<cudaStream_t>(stream));
+  QkNormRopeParams p = params(d, false, q, k, q_weight, k_weight, cos_table, sin_table, positions,
+                              q_out, k_out, err_word);
+  const Blocks n = blocks(d, false, sms);
+  // items are divided as 32-bit numbers on the device
+  if (n.q + n.k > INT_MAX || p.q.items > UINT_MAX || p.k.items > UINT_MAX) return FLCE_ERR_UNSUPPORTED;
+  p.q_blocks = n.q;
+  return launch_any<false>(d, p, n.q + n.k, static_cast<cudaStream_t>(stream));
 }
 
 flce_status flce_qk_norm_rope_backward(const flce_qk_norm_rope_desc* d, const void* dq_out,
@@ -176,21 +196,24 @@ flce_status flce_qk_norm_rope_backward(const flce_qk_norm_rope_desc* d, const vo
     return FLCE_ERR_ARG;
   int dev, sms;
   FLCE_HOST_TRY(host::device(&dev, &sms));
-  const int64_t blocks = backward_blocks(d, sms);
+  const Blocks n = blocks(d, true, sms);
   if (!workspace || !aligned(workspace, host::kAlign) ||
-      ws_bytes < (size_t)blocks * 2 * d->head_dim * 4)
+      ws_bytes < (size_t)(n.q + n.k) * d->head_dim * 4)
     return FLCE_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (d->tokens > 0) {
-    QkNormRopeParams p = params(d, q, k, q_weight, k_weight, cos_table, sin_table, positions, dq,
+    QkNormRopeParams p = params(d, true, q, k, q_weight, k_weight, cos_table, sin_table, positions, dq,
                                 dk, err_word);
-    p.dq_out = dq_out;
-    p.dk_out = dk_out;
+    if (p.q.items > UINT_MAX || p.k.items > UINT_MAX) return FLCE_ERR_UNSUPPORTED;
+    p.q.dy = dq_out;
+    p.k.dy = dk_out;
+    p.q_blocks = n.q;
     p.partial = static_cast<float*>(workspace);
-    FLCE_HOST_TRY(launch_any<true>(d, p, blocks, st));
+    FLCE_HOST_TRY(launch_any<true>(d, p, n.q + n.k, st));
   }
-  qk_norm_rope_dw<<<(unsigned)host::ceil_div(2 * d->head_dim, 32), 1024, 0, st>>>(
-      static_cast<const float*>(workspace), (int)blocks, (int)d->head_dim, dq_weight, dk_weight);
+  qk_norm_rope_dw<<<dim3((unsigned)host::ceil_div(d->head_dim, 32), 2), 1024, 0, st>>>(
+      static_cast<const float*>(workspace), (int)n.q, (int)(n.q + n.k), (int)d->head_dim, dq_weight,
+      dk_weight);
   host::count_launch();
   FLCE_HOST_CUDA(cudaGetLastError());
   return FLCE_OK;
