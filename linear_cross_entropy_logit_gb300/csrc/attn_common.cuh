@@ -298,6 +298,14 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t x) {
   return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
 
+// The part of clean_tile that zeroes the rows from `valid` on.
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int boxes, int valid, int w, int warps) {
+#pragma unroll 1
+  for (int i = w * 32 + (threadIdx.x & 31); i < boxes * kTile * 8; i += warps * 32)
+    if (((i >> 3) & (kTile - 1)) >= valid)
+      reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
+}
+
 // Makes a tile fit to be multiplied by zeros: rows from `valid` on (another
 // sequence's, or none's) become zero; non-finite values become zero and their
 // row's bit is set in flags[4], for the caller to add them back where they are
@@ -306,34 +314,38 @@ __device__ __forceinline__ void clean_tile(uint8_t* tile, int boxes, int valid, 
                                            uint32_t* flags) {
   const int lane = threadIdx.x & 31;
   if (lane < 4) flags[lane] = 0;
+  if (valid < kTile) zero_rows(tile, boxes, valid, w, warps);
   __syncwarp();
-#pragma unroll 2
-  for (int i = w * 32 + lane; i < boxes * kTile * 8; i += warps * 32) {
-    uint4* at = reinterpret_cast<uint4*>(tile) + i;
-    const int row = (i >> 3) & (kTile - 1);
-    if (row >= valid) {
-      *at = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    uint4 x = *at;
-    if ((nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w)) == 0) continue;
-    uint32_t* h = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t b = nonfinite2(h[e]);
-      h[e] &= (b & 0x8000u ? 0u : 0xffffu) | (b & 0x80000000u ? 0u : 0xffff0000u);
-    }
-    *at = x;
-    atomicOr(&flags[row >> 5], 1u << (row & 31));
-  }
-}
-
-// The part of clean_tile that zeroes the rows from `valid` on.
-__device__ __forceinline__ void zero_rows(uint8_t* tile, int boxes, int valid, int w, int warps) {
+  constexpr int kAhead = 8;  // loads in flight
 #pragma unroll 1
-  for (int i = w * 32 + (threadIdx.x & 31); i < boxes * kTile * 8; i += warps * 32)
-    if (((i >> 3) & (kTile - 1)) >= valid)
-      reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = w * 32 + lane; i < boxes * kTile * 8; i += kAhead * warps * 32) {
+    uint4 x[kAhead];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e)
+      x[e] = reinterpret_cast<const uint4*>(tile)[i + e * warps * 32];
+    // the largest magnitude, NaN above all; its sign says nothing
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e)
+      top = bf16x2_max_abs(bf16x2_max_abs(bf16x2_max_abs(bf16x2_max_abs(top, x[e].x), x[e].y), x[e].z), x[e].w);
+    if (nonfinite2(top) == 0) continue;
+#pragma unroll 1
+    for (int e = 0; e < kAhead; ++e) {
+      uint4* at = reinterpret_cast<uint4*>(tile) + i + e * warps * 32;
+      uint4 y = *at;
+      if ((nonfinite2(y.x) | nonfinite2(y.y) | nonfinite2(y.z) | nonfinite2(y.w)) == 0) continue;
+      uint32_t* h = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint32_t b = nonfinite2(h[g]);
+        h[g] &= (b & 0x8000u ? 0u : 0xffffu) | (b & 0x80000000u ? 0u : 0xffff0000u);
+      }
+      *at = y;
+      const int row = ((i + e * warps * 32) >> 3) & (kTile - 1);
+      atomicOr(&flags[row >> 5], 1u << (row & 31));
+    }
+  }
+  __syncwarp();
 }
 
 }  // namespace flce
