@@ -22,9 +22,9 @@
 // sequence that only some rows see are zeroed too and added back in the
 // epilogue to the rows that see them.
 //
-// The maximum is only moved when it grows by more than kMoveLog2 (2^8): until
-// then exponentials are relative to the old one, at most 2^8 in size, and O is
-// left alone.  So half of a tile's exponentials are made before its maximum is
+// The maximum is only moved when it grows by more than kMoveLog2: until then
+// exponentials are relative to the old one, at most 2^16 in size, and O is left
+// alone.  So half of a tile's exponentials are made before its maximum is
 // known, and made again in the rare case that it moves; P is handed over in
 // halves, the first to be multiplied while the second is made.  l and m are fp32; P is rounded to bf16 (2^-9 each, the type of
 // V), and l sums it before that rounding.
@@ -35,10 +35,10 @@ namespace flce {
 
 constexpr int kFwdThreads = 384;
 constexpr int kFwdRows = 2 * kTile;
-constexpr float kMoveLog2 = 8.f;
+constexpr float kMoveLog2 = 16.f;
 // Registers per thread of the two softmax warpgroups and of the third: a
 // softmax thread holds a row of 128 scores.
-constexpr int kFwdSoftmaxRegs = 200, kFwdOtherRegs = 104;
+constexpr int kFwdSoftmaxRegs = 216, kFwdOtherRegs = 72;
 static_assert(2 * kFwdSoftmaxRegs + kFwdOtherRegs == 3 * (65536 / kFwdThreads / 8 * 8),
               "shares add up to what the block is launched with");
 
@@ -51,8 +51,8 @@ struct FwdCfg {
   // Whether the next K tile is waited for at a step's start, or behind its first
   // product.  A wait costs the issuing warp some 150 cycles beside the softmax even
   // when there is nothing to wait for, and with 8 slots there rarely is; with 4 the
-  // tile can still be on its way.  At the start / behind: 408 / 405 us at 8192 tokens,
-  // 32 / 8 heads of 128; 1005 / 1095 us at 32768 tokens, 8 / 2 heads of 64.
+  // tile can still be on its way.  At the start / behind: 377 / 362 us at 8192 tokens,
+  // 32 / 8 heads of 128; 993 / 1038 us at 32768 tokens, 8 / 2 heads of 64.
   static constexpr bool kEarlyK = DP == 64;
   static constexpr int kStage = kRing + kSlots * kTileBytes;  // 4 KB for each softmax warp
   static constexpr int kBars = kStage + 8 * 4096;
