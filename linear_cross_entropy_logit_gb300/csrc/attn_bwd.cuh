@@ -103,7 +103,10 @@ struct DqCfg {
   static constexpr int kK = DP == 128 ? 3 : 5, kV = DP == 128 ? 2 : 4;  // ring sizes
   static constexpr int kRingK = 2 * kTileBytes;                        // after Q and dout
   static constexpr int kRingV = kRingK + kK * kTileBytes;
-  static constexpr int kBars = kRingV + kV * kTileBytes;
+  // 4 KB for each storing warp: dout's tile, or beside the rings where there is room
+  static constexpr bool kThroughG = DP == 128;
+  static constexpr int kStage = kThroughG ? kTileBytes : kRingV + kV * kTileBytes;
+  static constexpr int kBars = kRingV + kV * kTileBytes + (kThroughG ? 0 : 4 * 4096);
   static constexpr int kSmem = kBars + 512;
 };
 
@@ -140,7 +143,7 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
     mbar_init(&sh.qfull, 1);
     mbar_init(&sh.qempty, 1);
     mbar_init(&sh.gfull, 1);
-    mbar_init(&sh.gempty, 9);  // the MMAs and the 8 compute warps, which store through it
+    mbar_init(&sh.gempty, C::kThroughG ? 9 : 1);  // the MMAs; the 8 compute warps if they store through it
     mbar_init(&sh.sfull, 1);
     mbar_init(&sh.sread, 8);
     mbar_init(&sh.dsfull, 8);
@@ -237,15 +240,17 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
         if (!ok || !wait_bar_warp(&sh.accfull, units & 1, ctx)) break;
         ++units;
         tc_fence_after();
-        // each half of the warps writes half of the columns, through dout's tile
+        // each half of the warps writes half of the columns
         const int first = u.q0 + (warp & 3) * 32;
         if (DP == 128 || half == 0)
-          store_rows(smem + C::kTileBytes + warp * 4096, t_acc + lanes + half * 64, p.scale,
+          store_rows(smem + C::kStage + warp * 4096, t_acc + lanes + half * 64, p.scale,
                      p.dq + ((int64_t)(u.start + first) * p.q_heads + u.head) * p.head_dim + half * 64,
                      (int64_t)p.q_heads * p.head_dim, u.len - first, min(64, p.head_dim - half * 64));
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.gempty);
+        if (C::kThroughG) {
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.gempty);
+        }
         tc_fence_before();
       }
       __syncwarp();
@@ -334,7 +339,7 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
       u.head = -1;
       if (id < total) {
         u = walk.at((int)(id / p.q_heads));
-        u.head = (int)(id % p.q_heads);
+        u.head = unit_ok(u, p) ? (int)(id % p.q_heads) : -1;
       }
       if (lane == 0) {
         ok = wait_bar(&sh.uempty[it & 1], ((it >> 1) & 1) ^ 1, ctx);
@@ -440,9 +445,11 @@ struct DkvCfg {
   static constexpr int kQ = DP == 128 ? 3 : 4, kG = DP == 128 ? 2 : 4;
   static constexpr int kRingQ = 2 * kTileBytes;      // after K and V
   static constexpr int kRingG = kRingQ + kQ * kTileBytes;
-  // 4 KB for each compute warp's stores: V's tile, where it is large enough
-  static constexpr int kStage = DP == 128 ? kTileBytes : kRingG + kG * kTileBytes;
-  static constexpr int kBars = kRingG + kG * kTileBytes + (DP == 128 ? 0 : 8 * 4096);
+  // 4 KB for each compute warp's stores: V's tile, or beside the rings where there is
+  // room
+  static constexpr bool kThroughV = DP == 128;
+  static constexpr int kStage = kThroughV ? kTileBytes : kRingG + kG * kTileBytes;
+  static constexpr int kBars = kRingG + kG * kTileBytes + (kThroughV ? 0 : 8 * 4096);
   static constexpr int kStatStages = 2;              // -lse and delta of 128 queries
   static constexpr int kSmem = kBars + kStatStages * 1024 + 1024;  // 227 KB at 128
 };
@@ -494,7 +501,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
     mbar_init(&sh.kfull, 1);
     mbar_init(&sh.kempty, 1);
     mbar_init(&sh.vfull, 1);
-    mbar_init(&sh.vempty, 9);  // the MMAs and the 8 compute warps, which store through it
+    mbar_init(&sh.vempty, C::kThroughV ? 9 : 1);  // the MMAs; the 8 compute warps if they store through it
     mbar_init(&sh.sfull, 1);
     mbar_init(&sh.dpfull, 1);
     mbar_init(&sh.pfull, 8);
@@ -622,7 +629,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
         if (!ok || !wait_bar_warp(&sh.accfull, units & 1, ctx)) break;
         ++units;
         tc_fence_after();
-        // warps 0-3 write dV, warps 4-7 dK, through V's tile
+        // warps 0-3 write dV, warps 4-7 dK
         const int row0 = u.q0 + (warp & 3) * 32, r = row0 + lane;  // the warp's first; this lane's
         const float scale = half ? p.scale : 1.f;
         const int64_t stride = (int64_t)p.kv_heads * p.head_dim;
@@ -651,9 +658,11 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
           }
           __syncwarp();
         }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.vempty);
+        if (C::kThroughV) {
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.vempty);
+        }
         tc_fence_before();
       }
       __syncwarp();
@@ -747,7 +756,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
       u.head = -1;
       if (id < total) {
         u = walk.at((int)(id / heads));
-        u.head = (int)(id % heads);
+        u.head = unit_ok(u, p) ? (int)(id % heads) : -1;
         // the walk counts from the sequence's start, key tiles have the most
         // queries there: mirrored
         if (u.len > 0) u.q0 = ((u.len + kTile - 1) / kTile - 1) * kTile - u.q0;

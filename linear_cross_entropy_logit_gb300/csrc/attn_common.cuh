@@ -157,6 +157,15 @@ struct UnitWalk {
   }
 };
 
+// Debug build: a mapped unit lies within the tokens (else it is reported and ends the
+// CTA's walk).
+__device__ __forceinline__ bool unit_ok(const AttnUnit& u, const AttnParams& p) {
+  const int end = u.len > 0 ? u.len : u.rows;
+  return dbg_ok(u.start >= 0 && end > 0 && u.start + (int64_t)end <= p.tokens && u.q0 >= 0 &&
+                    (u.len == 0 || u.q0 < u.len),
+                p.err_word);
+}
+
 // Unit number of round r of CTA c of g: every other round runs backwards, so
 // that a CTA with a long unit in one round gets a short one in the next.
 __device__ __forceinline__ int64_t dealt_unit(uint32_t r, int c, int g) {

@@ -360,7 +360,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
       u.head = -1;
       if (id < total) {
         u = walk.at((int)(id / p.q_heads));
-        u.head = (int)(id % p.q_heads);
+        u.head = unit_ok(u, p) ? (int)(id % p.q_heads) : -1;
       }
       if (lane == 0) {
         ok = wait_bar(&sh.uempty[it & 1], ((it >> 1) & 1) ^ 1, ctx);

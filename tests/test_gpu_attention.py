@@ -279,3 +279,18 @@ def test_autograd_graph_and_streams():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want[0]) and all(torch.equal(a, b) for a, b in zip(grads, want[2:5]))
+
+
+def test_debug_build_gives_the_same_bits():
+    """The bounds-checked build finds no unit out of range and computes the same."""
+    import torch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    q, k, v, g = make(777, 4, 2, 128, seed=14)
+    cu = [3, 100, 100, 400, 770]
+    want = run(q, k, v, g, cu)
+    prev = B.use_library(B.load(B.DEBUG_LIB_PATH))
+    try:
+        got = run(q, k, v, g, cu)
+    finally:
+        B.use_library(prev)
+    assert got[5] == 0 and all(torch.equal(a, b) for a, b in zip(want[:5], got[:5]))
