@@ -39,6 +39,28 @@ struct AttnBwdParams : AttnParams {
 
 __device__ __forceinline__ float as_f(uint32_t x) { return __uint_as_float(x); }
 
+// Zeroes a diagonal tile's entries on the far side of the diagonal in this thread's 64
+// columns: those below (columns < row) or above it.  A warp's 32 rows meet the
+// diagonal in one run of 32 columns; other runs are kept or dropped whole.
+template <bool BELOW>
+__device__ __forceinline__ void mask_diagonal(uint32_t (&v)[2][32], int half) {
+  const int w = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int run = 2 * half + k;
+    if (run == w) {
+      asm volatile("");  // kept a branch, as selects it would cost every run
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (BELOW ? e < lane : e > lane) v[k][e] = 0;
+    } else if (BELOW ? run < w : run > w) {
+      asm volatile("");
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[k][e] = 0;
+    }
+  }
+}
+
 // ----------------------------------------------------------------------------
 // delta
 // ----------------------------------------------------------------------------
@@ -221,12 +243,7 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
             s[i >> 5][i & 31] = __float_as_uint(a * as_f(s[i >> 5][i & 31]));
             s[i >> 5][(i & 31) + 1] = __float_as_uint(b * as_f(s[i >> 5][(i & 31) + 1]));
           }
-          if (j == n - 1) {  // the diagonal: keys after the row
-            asm volatile("");  // kept a branch, as selects it would cost every tile
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (half * 64 + i > row) s[i >> 5][i & 31] = 0;
-          }
+          if (j == n - 1) mask_diagonal<false>(s, half);  // keys after the row
           uint32_t pk[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i)
@@ -288,6 +305,10 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
         issue_s(base);
         if (!(ok = ok && wait_bar_warp(&sh.gfull, units & 1, ctx))) break;
         issue_dp(base);
+        if (n == 1) {
+          mma_commit_if(el, &sh.qempty);
+          mma_commit_if(el, &sh.gempty);
+        }
         for (int i = 0; i < n && ok; ++i) {
           const uint32_t t = base + i;
           if (!(ok = wait_bar_warp(&sh.sread, t & 1, ctx))) break;
@@ -297,7 +318,7 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
             issue_dp(t + 1);
           }
           // Q and dout are free once the last S and dP are done
-          if (i + 2 == n || n == 1) {
+          if (i + 2 == n) {
             mma_commit_if(el, &sh.qempty);
             mma_commit_if(el, &sh.gempty);
           }
@@ -558,9 +579,6 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
             const uint32_t ts = step % C::kStatStages;
             if (!(ok = wait_bar_warp(&sh.tfull[ts], (step / C::kStatStages) & 1, ctx))) break;
             const float* nl = stat + ts * 256 + half * 64;
-            const bool diag = i == first, masked = dkv_cleaned(u, i, first);
-            const int limit = u.len - i * kTile - half * 64;  // queries of this sequence
-            const int from = diag ? row - half * 64 : 0;      // ... not before the key
             if (!(ok = wait_bar_warp(&sh.sfull, step & 1, ctx))) break;
             tc_fence_after();
             uint32_t s[2][32];
@@ -578,12 +596,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
               r[i0 + 2] = __float_as_uint(ex2_approx(x));
               r[i0 + 3] = __float_as_uint(ex2_approx(y));
             }
-            if (masked) {
-              asm volatile("");  // kept a branch, as selects it would cost every tile
-#pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (e < from || e >= limit) s[e >> 5][e & 31] = 0;
-            }
+            if (i == first) mask_diagonal<true>(s, half);  // queries before the key
             uint32_t pk[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -608,12 +621,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
               r[i0 + 2] = __float_as_uint((as_f(r[i0 + 2]) - b.z) * as_f(q[i0 + 2]));
               r[i0 + 3] = __float_as_uint((as_f(r[i0 + 3]) - b.w) * as_f(q[i0 + 3]));
             }
-            if (masked) {
-              asm volatile("");  // kept a branch, as selects it would cost every tile
-#pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (e < from || e >= limit) g[e >> 5][e & 31] = 0;
-            }
+            if (i == first) mask_diagonal<true>(g, half);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               pk[e] = pack_bf16x2(as_f(g[e >> 4][2 * (e & 15)]), as_f(g[e >> 4][2 * (e & 15) + 1]));
@@ -705,6 +713,10 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
         issue_s(base, true);
         if (!(ok = ok && wait_bar_warp(&sh.vfull, units & 1, ctx))) break;
         issue_dp(base);
+        if (n == 1) {
+          mma_commit_if(el, &sh.kempty);
+          mma_commit_if(el, &sh.vempty);
+        }
         int i = 0;  // query tile of step x within its head
         for (int x = 0; x < n && ok; ++x) {
           const uint32_t t = base + x;
@@ -719,7 +731,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
           mma_tmem_tile<DP>(el, a_dk, a_dp, 64, q_tile(t), x != 0);
           mma_commit_if(el, &sh.qempty[t % C::kQ]);
           if (x + 1 < n) issue_dp(t + 1);
-          if (x + 2 == n || n == 1) {
+          if (x + 2 == n) {
             mma_commit_if(el, &sh.kempty);
             mma_commit_if(el, &sh.vempty);
           }
@@ -833,7 +845,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
             for (int e = 0; e < 4; ++e) {
               const int r = e * 32 + lane;
               const bool in = i + r < u.len;
-              nl[e] = in ? p.nlse[at + r] : 0.f;
+              nl[e] = in ? p.nlse[at + r] : -INFINITY;  // beyond the sequence: p = 0
               dl[e] = in ? p.delta[at + r] : 0.f;
             }
             if (!(ok = wait_bar_warp(&sh.tempty[ts], ((step / C::kStatStages) & 1) ^ 1, ctx))) break;

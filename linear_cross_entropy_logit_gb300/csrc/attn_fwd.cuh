@@ -201,10 +201,21 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
           if (lane == 0) mbar_arrive(bar);
         };
         if (j == n - 1) {  // the diagonal
-          asm volatile("");  // a branch: as selects it would cost every tile 128 of them
+          // a warp's 32 rows meet the diagonal in one run of 32 keys; those after it are masked
+          // whole.  Branches: as selects these would cost every tile.
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i > row) s[i >> 5][i & 31] = 0xff800000u;  // -infinity
+          for (int i = 0; i < 4; ++i) {
+            if (i == (warp & 3)) {
+              asm volatile("");
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e > lane) s[i][e] = 0xff800000u;  // -infinity
+            } else if (i > (warp & 3)) {
+              asm volatile("");
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[i][e] = 0xff800000u;
+            }
+          }
           m = row_max();
         }
         // The first half goes by the maximum so far, while this tile's is found: the
