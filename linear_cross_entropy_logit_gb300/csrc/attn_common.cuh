@@ -45,20 +45,22 @@ __device__ __forceinline__ int warp_max(int x) { return __reduce_max_sync(~0u, x
 // (ROWS = 256) the last unit of a sequence may have rows in one only, which takes
 // about 5/8 of the time and stands in class 5/8 i (151 -> 145 us for 37 ragged
 // sequences).  Every unit number is mapped by one warp on its own from the offsets,
-// so no list of units is written and no launch goes before the attention.  Cost:
-// about log2(longest / ROWS) passes over the sequences, 32 at a time; the first
-// 32 * kHeld are held in the warp's registers, the offsets of more are read again
-// in every pass.
+// so no list of units is written and no launch goes before the attention.  A CTA's
+// numbers ascend, so that the search goes on from where the last one ended: one pass
+// over the offsets for all its units of a class, and log2(classes) passes to find
+// the next class.
 template <int ROWS>
 struct UnitWalk {
-  static constexpr int kHeld = 4;
   const int32_t* cu;
   int n, tokens;
   int classes;    // every unit's class is below this
   int units;      // units of all sequences
   int lead, gaps; // rows before the first sequence; units of all rows in none
   int tail_start;
-  int start[kHeld], len[kHeld];  // of sequences lane + 32 k
+  // The last unit's class, whose units are numbers [first, end); whether it was part of a
+  // unit; its block of 32 sequences, and the units of the class before that block.
+  int cls, first, end;
+  int part, block, seen;
 
   static __device__ __forceinline__ int cut(int rows) { return (rows + ROWS - 1) / ROWS; }
   // Whole units of a sequence: with rows in every query tile.
@@ -71,97 +73,81 @@ struct UnitWalk {
   static __device__ __forceinline__ int above(int len, int c) {
     return max(0, whole(len) - c) + (part_class(len) >= c);
   }
-  __device__ __forceinline__ int length(int k) const {
-    const int s = 32 * k + (threadIdx.x & 31);
-    return s < n ? cu[s + 1] - cu[s] : 0;
-  }
+  __device__ __forceinline__ int length(int s) const { return s < n ? cu[s + 1] - cu[s] : 0; }
   __device__ __forceinline__ int from(int c) const {
     int t = 0;
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) t += above(len[k], c);
-#pragma unroll 1
-    for (int k = kHeld; 32 * k < n; ++k) t += above(length(k), c);
+#pragma unroll 4
+    for (int s = threadIdx.x & 31; s < n; s += 32) t += above(length(s), c);
     return warp_add(t);
   }
   // Executed by one whole warp.  Offsets that do not ascend within [0,
   // tokens] leave every row in no sequence.
   __device__ __forceinline__ void init(const AttnParams& p) {
-    const int lane = threadIdx.x & 31;
     cu = p.cu;
     n = p.n_seqs;
     tokens = p.tokens;
     lead = cu[0];
     tail_start = cu[n];
     int bad = lead < 0 || tail_start > tokens, most = 0, sum = 0;
-    auto add = [&](int first, int rows) {
-      bad |= rows < 0 || first < 0 || first > tokens;
+#pragma unroll 4
+    for (int s = threadIdx.x & 31; s < n; s += 32) {
+      const int begin = cu[s], rows = cu[s + 1] - begin;
+      bad |= rows < 0 || begin < 0 || begin > tokens;
       most = max(most, max(whole(rows), part_class(rows) + 1));
       sum += cut(rows);
-    };
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      const int s = 32 * k + lane;
-      start[k] = s < n ? cu[s] : 0;
-      len[k] = s < n ? cu[s + 1] - start[k] : 0;
-      add(start[k], len[k]);
     }
-#pragma unroll 1
-    for (int k = kHeld; 32 * k < n; ++k) add(32 * k + lane < n ? cu[32 * k + lane] : 0, length(k));
     classes = warp_max(most);
     units = warp_add(sum);
     if (__any_sync(~0u, bad)) {
-      if (blockIdx.x == 0 && lane == 0) record_error(p.err_word, kErrIndex);
+      if (blockIdx.x == 0 && (threadIdx.x & 31) == 0) record_error(p.err_word, kErrIndex);
       n = classes = units = lead = tail_start = 0;
-#pragma unroll
-      for (int k = 0; k < kHeld; ++k) len[k] = 0;
     }
     gaps = cut(lead) + cut(tokens - tail_start);
+    first = end = 0;
   }
   __device__ __forceinline__ int total() const { return units + gaps; }
 
-  // Unit `rank` in [0, total()).  Executed by one whole warp.
-  __device__ __forceinline__ AttnUnit at(int rank) const {
+  // Unit `rank` in [0, total()).  Executed by one whole warp, for ascending ranks.
+  __device__ __forceinline__ AttnUnit at(int rank) {
     AttnUnit u{};
     if (rank >= units) {
-      const int g = rank - units, first = cut(lead);
-      u.start = g < first ? g * ROWS : tail_start + (g - first) * ROWS;
-      u.rows = min(ROWS, (g < first ? lead : tokens) - u.start);
+      const int g = rank - units, before = cut(lead);
+      u.start = g < before ? g * ROWS : tail_start + (g - before) * ROWS;
+      u.rows = min(ROWS, (g < before ? lead : tokens) - u.start);
       return u;
     }
-    int lo = 0, hi = classes;  // from(lo) > rank >= from(hi)
-    int after = 0;             // from(lo + 1) once hi = lo + 1
+    if (rank >= end) {  // another class: from(lo) > rank >= from(hi)
+      int lo = 0, hi = classes;
+      first = 0;
+      end = units;
 #pragma unroll 1
-    while (hi - lo > 1) {
-      const int m = (lo + hi) >> 1, f = from(m);
-      if (f > rank) lo = m; else hi = m, after = f;
-    }
-    // The sequence is the nth among those with a whole unit of class lo, then those with a
-    // part of one; its lane is the only one to add to the sums.
-    int nth = rank - after, its_start = 0, its_len = 0, its_q0 = 0;
-    auto pick = [&](int start_k, int len_k, bool part) {
-      const bool has = part ? part_class(len_k) == lo : whole(len_k) > lo;
-      const unsigned all = __ballot_sync(~0u, has);
-      if (has && __popc(all & ((1u << (threadIdx.x & 31)) - 1)) == nth) {
-        its_start = start_k;
-        its_len = len_k;
-        its_q0 = (part ? whole(len_k) : lo) * ROWS;
+      while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1, f = from(m);
+        if (f > rank) lo = m, end = f; else hi = m, first = f;
       }
-      nth -= __popc(all);
-    };
-#pragma unroll 1
-    for (int part = 0; part < (ROWS > kTile ? 2 : 1) && nth >= 0; ++part) {
-#pragma unroll
-      for (int k = 0; k < kHeld; ++k) pick(start[k], len[k], part);
-#pragma unroll 1
-      for (int k = kHeld; 32 * k < n && nth >= 0; ++k) {
-        const int s = 32 * k + (threadIdx.x & 31);
-        pick(s < n ? cu[s] : 0, length(k), part);
-      }
+      cls = lo;
+      part = block = seen = 0;
     }
-    u.start = warp_add(its_start);
-    u.len = warp_add(its_len);
-    u.q0 = warp_add(its_q0);
-    return u;
+    // The unit is the nth of its class: the whole units come first, then the parts.
+    const int nth = rank - first;
+#pragma unroll 1
+    for (; part < 2; ++part, block = 0)
+#pragma unroll 1
+      for (; 32 * block < n; ++block) {
+        const int s = 32 * block + (threadIdx.x & 31), len = length(s);
+        const unsigned has = __ballot_sync(~0u, part ? part_class(len) == cls : whole(len) > cls);
+        const int before = __popc(has & ((1u << (threadIdx.x & 31)) - 1));
+        const unsigned here = __ballot_sync(~0u, ((has >> (threadIdx.x & 31)) & 1) && seen + before == nth);
+        if (here) {
+          const int q = 32 * block + __ffs(here) - 1;
+          u.start = cu[q];
+          u.len = cu[q + 1] - u.start;
+          u.q0 = (part ? whole(u.len) : cls) * ROWS;
+          return u;
+        }
+        seen += __popc(has);
+      }
+    return u;  // not reached
   }
 };
 
