@@ -32,7 +32,7 @@ static_assert(2 * (kBwdComputeRegs + kBwdOtherRegs) == 4 * (65536 / kBwdThreads)
 struct AttnBwdParams : AttnParams {
   const bf16* dout;    // tokens x q_heads x head_dim
   bf16 *dq, *dk, *dv;  // contiguous
-  float *nlse, *delta; // q_heads x tokens: -lse log2 e, delta (written by attn_delta)
+  float *nlse, *delta; // q_heads x tokens: -lse log2 e, delta (by attn_delta, then attn_dq)
   float* partial;      // splits > 1: dk, dv partial sums, 2 x splits x tokens x kv_heads x head_dim
   int splits;          // CTAs that share the query heads of a key / value head
 };
@@ -129,13 +129,14 @@ struct DqCfg {
   static constexpr bool kThroughG = DP == 128;
   static constexpr int kStage = kThroughG ? kTileBytes : kRingV + kV * kTileBytes;
   static constexpr int kBars = kRingV + kV * kTileBytes + (kThroughG ? 0 : 4 * 4096);
-  static constexpr int kSmem = kBars + 512;
+  static constexpr int kSums = kBars + 512;  // by half and row: sums of p dP
+  static constexpr int kSmem = kSums + 2 * kTile * 4;
 };
 
 struct DqShared {
   uint64_t kfull[5], kempty[5], vfull[4], vempty[4];
   uint64_t qfull, qempty, gfull, gempty;  // Q and dout tiles
-  uint64_t sfull, sread, dpfull[2], dsfull, accfull;
+  uint64_t sfull, sread, dpfull[2], dsfull, accfull, exchange;
   uint64_t clean[2];
   uint64_t ufull[2], uempty[2];
   uint64_t mma_done;
@@ -170,6 +171,7 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
     mbar_init(&sh.sread, 8);
     mbar_init(&sh.dsfull, 8);
     mbar_init(&sh.accfull, 1);
+    mbar_init(&sh.exchange, 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.dpfull[i], 1);
       mbar_init(&sh.clean[i], 4);
@@ -198,7 +200,8 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const float c = p.scale * kLog2e;
     const uint64_t c2 = pack_f32x2(c, c);
-    uint32_t step = 0, units = 0;
+    float* sums = reinterpret_cast<float*>(smem + C::kSums);
+    uint32_t step = 0, units = 0, singles = 0;
     for (uint32_t it = 0;; ++it) {
       if (!wait_bar_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
       const AttnUnit u = sh.unit[it & 1];
@@ -215,7 +218,8 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
         const bool live = u.q0 + row < u.len;
         const int64_t at = (int64_t)u.head * p.tokens + u.start + u.q0 + row;
         const float nl = live ? p.nlse[at] : 0.f, dl = live ? -p.delta[at] : 0.f;
-        const uint64_t nl2 = pack_f32x2(nl, nl), dl2 = pack_f32x2(dl, dl);
+        const uint64_t nl2 = pack_f32x2(nl, nl);
+        uint64_t dl2 = pack_f32x2(dl, dl);
         const int n = u.q0 / kTile + 1;
         for (int j = n - 1; j >= 0; --j, ++step) {
           const uint32_t t_dp = tmem + (1 + (step & 1)) * kTile + lanes + half * 64;
@@ -236,6 +240,30 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
           if (!(ok = wait_bar_warp(&sh.dpfull[step & 1], (step >> 1) & 1, ctx))) break;
           tc_fence_after();
           load64(g, t_dp);
+          if (n == 1) {
+            // A sequence's first rows see few keys, each with a large p, so that the rounding
+            // of out in delta shows in their gradients.  All their keys are here: delta =
+            // sum_j p_ij dP_ij in fp32 (dq and dk 3.6e-3 -> 2.4e-3 off for short sequences).
+            mask_diagonal<false>(s, half);
+            uint64_t sum = 0;
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+              // a masked dP may be anything
+              const uint32_t x = half * 64 + i <= row ? g[i >> 5][i & 31] : 0;
+              const uint32_t y = half * 64 + i < row ? g[i >> 5][(i & 31) + 1] : 0;
+              sum = fma_f32x2(pack_u32x2(s[i >> 5][i & 31], s[i >> 5][(i & 31) + 1]), pack_u32x2(x, y), sum);
+            }
+            float a, b;
+            unpack_f32x2(sum, a, b);
+            sums[half * kTile + row] = a + b;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.exchange);
+            if (!(ok = wait_bar_warp(&sh.exchange, singles & 1, ctx))) break;
+            ++singles;
+            const float d = sums[row] + sums[kTile + row];
+            dl2 = pack_f32x2(-d, -d);
+            if (half == 0 && live) p.delta[at] = d;  // for attn_dkdv
+          }
 #pragma unroll
           for (int i = 0; i < 64; i += 2) {
             float a, b;
