@@ -46,21 +46,20 @@ template <int DP>
 struct FwdCfg {
   static constexpr int kBoxes = DP / 64;
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
-  static constexpr int kSlots = DP == 128 ? 4 : 8;  // K and V tiles in flight
+  // A stage of the ring holds what one step needs: V of a key tile and K of the next (the
+  // first of a unit only K, the last only V).  One wait and one release a step: each costs
+  // the issuing warp some 150 to 250 cycles beside the softmax.  A ring of single tiles /
+  // this: 355 / 340 us at 8192 tokens, 32 / 8 heads of 128; 1020 / 976 us at 32768 tokens,
+  // 8 / 2 heads of 64.
+  static constexpr int kStages = DP == 128 ? 2 : 4;
   static constexpr int kRing = 2 * kTileBytes;      // after the two Q tiles
-  // Whether the next K tile is waited for at a step's start, or behind its first
-  // product.  A wait costs the issuing warp some 150 cycles beside the softmax even
-  // when there is nothing to wait for, and with 8 slots there rarely is; with 4 the
-  // tile can still be on its way.  At the start / behind: 377 / 362 us at 8192 tokens,
-  // 32 / 8 heads of 128; 993 / 1038 us at 32768 tokens, 8 / 2 heads of 64.
-  static constexpr bool kEarlyK = DP == 64;
-  static constexpr int kStage = kRing + kSlots * kTileBytes;  // 4 KB for each softmax warp
+  static constexpr int kStage = kRing + kStages * 2 * kTileBytes;  // 4 KB for each softmax warp
   static constexpr int kBars = kStage + 8 * 4096;
   static constexpr int kSmem = kBars + 512;
 };
 
 struct FwdShared {
-  uint64_t full[8], empty[8];  // ring of K and V tiles
+  uint64_t full[4], empty[4];  // ring of K and V tiles
   uint64_t qfull, qempty;
   uint64_t sfull[2], phalf[2], pfull[2], ofull[2];
   uint64_t clean[2][2];        // by unit parity and query tile: its diagonal value tile is fit for use
@@ -92,9 +91,9 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
   const WaitCtx ctx{&sh.abort, p.err_word, p.timeout_ns};
 
   if (threadIdx.x == 0) {
-    // K tiles lie in the even slots, V tiles in the odd ones; a V slot is given back
-    // by the MMAs and by both cleaning warps, which so see every V tile pass
-    for (int i = 0; i < C::kSlots; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], i & 1 ? 3 : 1);
+    // a stage is given back by the MMAs and by both cleaning warps, which so see every
+    // stage pass
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 3);
     mbar_init(&sh.qfull, 1);
     mbar_init(&sh.qempty, 1);
     for (int i = 0; i < 2; ++i) {
@@ -278,12 +277,13 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
     // ------------------------------------------------------------ MMA issuer
     const uint32_t tm = __shfl_sync(~0u, tmem, 0), el = elect_one();
     const uint32_t q0 = smem_u32(smem);
-    uint32_t base = 0;  // ring position of the unit's first tile
+    uint32_t base = 0;  // the unit's first stage
     uint32_t np[2] = {0, 0}, nq = 0, nclean = 0;  // bit 2 parity + tile of nclean: next phase
     bool ok = true;
-    auto slot = [&](uint32_t pos) { return smem_u32(ring) + (pos % C::kSlots) * C::kTileBytes; };
-    auto wait_tile = [&](uint32_t pos) {
-      return ok = ok && wait_bar_warp(&sh.full[pos % C::kSlots], (pos / C::kSlots) & 1, ctx);
+    auto k_tile = [&](uint32_t t) { return smem_u32(ring) + (t % C::kStages) * 2 * C::kTileBytes; };
+    auto v_tile = [&](uint32_t t) { return k_tile(t) + C::kTileBytes; };
+    auto wait_stage = [&](uint32_t t) {
+      return ok = ok && wait_bar_warp(&sh.full[t % C::kStages], (t / C::kStages) & 1, ctx);
     };
     for (uint32_t it = 0; ok; ++it) {
       if (!wait_bar_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
@@ -292,24 +292,23 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
       if (u.len > 0) {
         int n0, n1;
         unit_tiles(u, n0, n1);
-        const int last = max(n0, n1) - 1;  // key tile j sits at ring position base + 2 (last - j)
+        const int last = max(n0, n1) - 1;  // step j takes V_j and K_j-1 from stage base + last - j + 1
         if (!wait_bar_warp(&sh.qfull, nq & 1, ctx)) break;
         ++nq;
-        if (!wait_tile(base)) break;
+        if (!wait_stage(base)) break;
         const int x = n1 ? 1 : 0;
-        mma_tiles<DP>(el, tm + x * kTile, q0 + x * C::kTileBytes, slot(base));
+        mma_tiles<DP>(el, tm + x * kTile, q0 + x * C::kTileBytes, k_tile(base));
         mma_commit_if(el, &sh.sfull[x]);
-        mma_commit_if(el, &sh.empty[base % C::kSlots]);
+        mma_commit_if(el, &sh.empty[base % C::kStages]);
         if (last == 0) mma_commit_if(el, &sh.qempty);
-        if (n1) {
-          if (!wait_tile(base + 2)) break;
-          mma_tiles<DP>(el, tm, q0, slot(base + 2));
+        if (n1) {  // tile 0 starts one key tile lower
+          if (!wait_stage(base + 1)) break;
+          mma_tiles<DP>(el, tm, q0, k_tile(base + 1));
           mma_commit_if(el, &sh.sfull[0]);
         }
         for (int j = last; j >= 0 && ok; --j) {
-          const uint32_t vpos = base + 2 * (last - j) + 1, knext = vpos + 1;
-          if (!wait_tile(vpos)) break;
-          if (C::kEarlyK && j > 0 && !wait_tile(knext)) break;
+          const uint32_t t = base + last - j + 1;
+          if (!wait_stage(t)) break;
           if (j >= n0 - 1) {
             const uint32_t f = j - (n0 - 1), bit = 2 * (it & 1) + f;
             if (!(ok = wait_bar_warp(&sh.clean[it & 1][f], (nclean >> bit) & 1, ctx))) break;
@@ -322,28 +321,24 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
             // the product with the first half of P runs while the second is made
             if (!(ok = wait_bar_warp(&sh.phalf[x], np[x] & 1, ctx))) break;
             tc_fence_after();
-            mma_tmem_tile<DP, 0, 1>(el, tm + 2 * kTile + x * DP, tm + x * kTile, 32, slot(vpos), j < n - 1);
+            mma_tmem_tile<DP, 0, 1>(el, tm + 2 * kTile + x * DP, tm + x * kTile, 32, v_tile(t), j < n - 1);
             if (!(ok = wait_bar_warp(&sh.pfull[x], np[x] & 1, ctx))) break;
             ++np[x];
             tc_fence_after();
-            mma_tmem_tile<DP, 1, 2>(el, tm + 2 * kTile + x * DP, tm + x * kTile, 32, slot(vpos), true);
-            // the key tile right below a pair's top one was multiplied with tile 0 at the start
-            const bool top = n1 && j == last;
+            mma_tmem_tile<DP, 1, 2>(el, tm + 2 * kTile + x * DP, tm + x * kTile, 32, v_tile(t), true);
             if (j > 0) {
-              if (!C::kEarlyK && (x == 1 || j >= n1) && !wait_tile(knext)) break;
-              mma_tiles<DP>(el, tm + x * kTile, q0 + x * C::kTileBytes, slot(knext));
+              mma_tiles<DP>(el, tm + x * kTile, q0 + x * C::kTileBytes, k_tile(t));
               mma_commit_if(el, &sh.sfull[x]);
             } else {
               mma_commit_if(el, &sh.ofull[x]);
             }
-            if (x == 0 || j >= n0) mma_commit_if(el, &sh.empty[vpos % C::kSlots]);
-            if (j > 0 && (x == 0 || top)) mma_commit_if(el, &sh.empty[knext % C::kSlots]);
+            if (x == 0 || j >= n0) mma_commit_if(el, &sh.empty[t % C::kStages]);
             // the last product that reads Q is issued
             if (j == 1 && (x == 0 || n0 == 1)) mma_commit_if(el, &sh.qempty);
           }
         }
         if (!ok) break;
-        base += 2 * (last + 1);
+        base += last + 2;
       }
       if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
       __syncwarp();
@@ -363,7 +358,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
     UnitWalk<kFwdRows> walk;
     walk.init(p);
     const int64_t total = (int64_t)walk.total() * p.q_heads;
-    uint32_t pos = 0, nq = 0;
+    uint32_t t = 0, nq = 0;
     bool ok = true;
     for (uint32_t it = 0; ok; ++it) {
       const int64_t id = dealt_unit(it, blockIdx.x, gridDim.x);
@@ -383,14 +378,6 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
           int n0, n1;
           unit_tiles(u, n0, n1);
           const int last = max(n0, n1) - 1, kvh = u.head / p.group;
-          auto load = [&](const CUtensorMap* map, int head, int r) {
-            const int s = pos % C::kSlots;
-            if (!(ok = wait_bar(&sh.empty[s], ((pos / C::kSlots) & 1) ^ 1, ctx))) return;
-            mbar_arrive_expect_tx(&sh.full[s], C::kTileBytes);
-            for (int b = 0; b < C::kBoxes; ++b)
-              tma_load_3d(ring + s * C::kTileBytes + b * kBoxBytes, map, &sh.full[s], b * 64, head, r);
-            ++pos;
-          };
           if ((ok = wait_bar(&sh.qempty, (nq & 1) ^ 1, ctx))) {
             mbar_arrive_expect_tx(&sh.qfull, (n1 ? 2 : 1) * C::kTileBytes);
             for (int x = 0; x <= (n1 ? 1 : 0); ++x)
@@ -399,9 +386,18 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
                             u.start + u.q0 + x * kTile);
             ++nq;
           }
-          for (int j = last; j >= 0 && ok; --j) {
-            load(&tk, kvh, u.start + j * kTile);
-            if (ok) load(&tv, kvh, u.start + j * kTile);
+          for (int j = last; j >= -1 && ok; --j, ++t) {  // K_j and V_j+1
+            const int st = t % C::kStages;
+            uint8_t* at = ring + st * 2 * C::kTileBytes;
+            if (!(ok = wait_bar(&sh.empty[st], ((t / C::kStages) & 1) ^ 1, ctx))) break;
+            mbar_arrive_expect_tx(&sh.full[st], (j == last || j < 0 ? 1 : 2) * C::kTileBytes);
+            for (int b = 0; b < C::kBoxes; ++b) {
+              if (j < last)
+                tma_load_3d(at + C::kTileBytes + b * kBoxBytes, &tv, &sh.full[st], b * 64, kvh,
+                            u.start + (j + 1) * kTile);
+              if (j >= 0)
+                tma_load_3d(at + b * kBoxBytes, &tk, &sh.full[st], b * 64, kvh, u.start + j * kTile);
+            }
           }
         }
       }
@@ -411,13 +407,13 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
     if (!ok && lane == 0) {
       // copies in flight must land before the CTA's shared memory is given up
       if (nq) mbar_wait_drain(&sh.qfull, (nq - 1) & 1, p.timeout_ns);
-      for (uint32_t i = pos > C::kSlots ? pos - C::kSlots : 0; i < pos; ++i)
-        mbar_wait_drain(&sh.full[i % C::kSlots], (i / C::kSlots) & 1, p.timeout_ns);
+      for (uint32_t i = t > C::kStages ? t - C::kStages : 0; i < t; ++i)
+        mbar_wait_drain(&sh.full[i % C::kStages], (i / C::kStages) & 1, p.timeout_ns);
     }
   } else {
     // ------------------------------------------------------------ diagonal value tiles
     const int w = warp - 10;
-    uint32_t base = 0;
+    uint32_t t = 0;
     for (uint32_t it = 0;; ++it) {
       if (!wait_bar_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
       const AttnUnit u = sh.unit[it & 1];
@@ -427,12 +423,11 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
         int n0, n1;
         unit_tiles(u, n0, n1);
         const int last = max(n0, n1) - 1;
-        for (int j = last; j >= 0; --j) {
-          const uint32_t pos = base + 2 * (last - j) + 1;
-          const int f = j - (n0 - 1);
-          if (!(ok = wait_bar_warp(&sh.full[pos % C::kSlots], (pos / C::kSlots) & 1, ctx))) break;
+        for (int j = last + 1; j >= 0; --j, ++t) {  // the stage of V_j, if there is one
+          const int f = j <= last ? j - (n0 - 1) : -1;
+          if (!(ok = wait_bar_warp(&sh.full[t % C::kStages], (t / C::kStages) & 1, ctx))) break;
           if (f >= 0) {
-            clean_tile(ring + (pos % C::kSlots) * C::kTileBytes, C::kBoxes, u.len - j * kTile, w, 2,
+            clean_tile(ring + (t % C::kStages * 2 + 1) * C::kTileBytes, C::kBoxes, u.len - j * kTile, w, 2,
                        sh.flags[it & 1][f][w]);
             fence_proxy_async_shared();
           }
@@ -443,10 +438,9 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
               sh.any[it & 1][2 * f + w] = fl[0] | fl[1] | fl[2] | fl[3];
               mbar_arrive(&sh.clean[it & 1][f]);
             }
-            mbar_arrive(&sh.empty[pos % C::kSlots]);
+            mbar_arrive(&sh.empty[t % C::kStages]);
           }
         }
-        base += 2 * (last + 1);
       }
       if (!ok) break;
       __syncwarp();
