@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(256) attn_delta(const AttnBwdParams p) {
   const int lane = threadIdx.x & 7, slot = threadIdx.x >> 3, h = blockIdx.y;
   const int64_t t0 = (int64_t)blockIdx.x * kDeltaRows + slot;
   uint4 a[4][2], b[4][2];
+  grid_wait();
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -190,6 +191,7 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  grid_wait();
   const uint32_t t_acc = tmem + 3 * kTile;
 
   if (warp >= 8) regs_down<kBwdOtherRegs>();
@@ -572,6 +574,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  grid_wait();
   const uint32_t t_s = tmem, t_dp = tmem + kTile, t_dv = tmem + 2 * kTile, t_dk = tmem + 3 * kTile;
 
   if (warp >= 8) regs_down<kBwdOtherRegs>();
@@ -945,6 +948,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
 __global__ void __launch_bounds__(256) attn_sum_splits(const AttnBwdParams p) {
   const int64_t size = (int64_t)p.tokens * p.kv_heads * p.head_dim;
   const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
+  grid_wait();
   if (i >= size) return;
   const float* from = p.partial + (int64_t)blockIdx.y * p.splits * size + i;
   float4 t = *reinterpret_cast<const float4*>(from);

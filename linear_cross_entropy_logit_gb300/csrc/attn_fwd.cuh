@@ -117,6 +117,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  grid_wait();
 
   if (warp >= 8) regs_down<kFwdOtherRegs>();
   if (warp < 8) {

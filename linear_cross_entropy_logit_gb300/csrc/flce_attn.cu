@@ -149,18 +149,12 @@ flce_status launch_backward(const flce_attention_desc* d, const CUtensorMap (&m)
   FLCE_HOST_TRY(set_smem(setup[0][dev], attn_dq<DP>, DqCfg<DP>::kSmem));
   FLCE_HOST_TRY(set_smem(setup[1][dev], attn_dkdv<DP>, DkvCfg<DP>::kSmem));
   const int64_t units = most_units(d, kTile);
-  attn_delta<<<dim3((unsigned)host::ceil_div(d->tokens, kDeltaRows), (unsigned)d->q_heads), 256, 0, st>>>(p);
-  host::count_launch();
-  FLCE_HOST_CUDA(cudaGetLastError());
-  attn_dq<DP><<<(int)std::min<int64_t>(units * d->q_heads, sms), kBwdThreads, DqCfg<DP>::kSmem, st>>>(
-      m[0], m[1], m[2], m[3], p);
-  host::count_launch();
-  FLCE_HOST_CUDA(cudaGetLastError());
-  attn_dkdv<DP><<<(int)std::min<int64_t>(units * d->kv_heads * p.splits, sms), kBwdThreads,
-                  DkvCfg<DP>::kSmem, st>>>(m[0], m[1], m[2], m[3], p);
-  host::count_launch();
-  FLCE_HOST_CUDA(cudaGetLastError());
-  return FLCE_OK;
+  FLCE_HOST_TRY(host::launch(
+      attn_delta, dim3((unsigned)host::ceil_div(d->tokens, kDeltaRows), (unsigned)d->q_heads), 256, 0, st, p));
+  FLCE_HOST_TRY(host::launch(attn_dq<DP>, dim3((unsigned)std::min<int64_t>(units * d->q_heads, sms)),
+                             kBwdThreads, DqCfg<DP>::kSmem, st, m[0], m[1], m[2], m[3], p));
+  return host::launch(attn_dkdv<DP>, dim3((unsigned)std::min<int64_t>(units * d->kv_heads * p.splits, sms)),
+                      kBwdThreads, DkvCfg<DP>::kSmem, st, m[0], m[1], m[2], m[3], p);
 }
 
 }  // namespace
@@ -195,14 +189,11 @@ flce_status flce_attention_forward(const flce_attention_desc* d, const void* q, 
   static Setup setup[2][host::kMaxDevices];
   if (d->head_dim <= 64) {
     FLCE_HOST_TRY(set_smem(setup[0][dev], attn_fwd<64>, FwdCfg<64>::kSmem));
-    attn_fwd<64><<<grid, kFwdThreads, FwdCfg<64>::kSmem, st>>>(tq, tk, tv, p);
+    return host::launch(attn_fwd<64>, grid, kFwdThreads, FwdCfg<64>::kSmem, st, tq, tk, tv, p);
   } else {
     FLCE_HOST_TRY(set_smem(setup[1][dev], attn_fwd<128>, FwdCfg<128>::kSmem));
-    attn_fwd<128><<<grid, kFwdThreads, FwdCfg<128>::kSmem, st>>>(tq, tk, tv, p);
+    return host::launch(attn_fwd<128>, grid, kFwdThreads, FwdCfg<128>::kSmem, st, tq, tk, tv, p);
   }
-  host::count_launch();
-  FLCE_HOST_CUDA(cudaGetLastError());
-  return FLCE_OK;
 }
 
 flce_status flce_attention_backward(const flce_attention_desc* d, const void* dout, const void* q,
@@ -243,9 +234,7 @@ flce_status flce_attention_backward(const flce_attention_desc* d, const void* do
                                   : launch_backward<128>(d, m, p, dev, sms, st));
   if (p.splits > 1) {
     const int64_t values = d->tokens * d->kv_heads * d->head_dim;
-    attn_sum_splits<<<dim3((unsigned)host::ceil_div(values, 1024), 2), 256, 0, st>>>(p);
-    host::count_launch();
-    FLCE_HOST_CUDA(cudaGetLastError());
+    return host::launch(attn_sum_splits, dim3((unsigned)host::ceil_div(values, 1024), 2), 256, 0, st, p);
   }
   return FLCE_OK;
 }

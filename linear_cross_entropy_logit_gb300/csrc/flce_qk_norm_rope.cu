@@ -116,32 +116,28 @@ QkNormRopeParams params(const flce_qk_norm_rope_desc* d, bool bwd, const void* q
 }
 
 template <bool BWD, typename T, int P, bool PAIRS>
-void launch(const QkNormRopeParams& p, unsigned n, cudaStream_t st) {
+flce_status launch(const QkNormRopeParams& p, unsigned n, cudaStream_t st) {
   if constexpr (BWD)
-    qk_norm_rope_bwd<T, P, PAIRS><<<n, kNormThreads, 0, st>>>(p);
+    return host::launch(qk_norm_rope_bwd<T, P, PAIRS>, n, kNormThreads, 0, st, p);
   else
-    qk_norm_rope_fwd<T, P, PAIRS><<<n, kNormThreads, 0, st>>>(p);
+    return host::launch(qk_norm_rope_fwd<T, P, PAIRS>, n, kNormThreads, 0, st, p);
 }
 
 template <bool BWD, typename T>
-void launch_t(const flce_qk_norm_rope_desc* d, const QkNormRopeParams& p, unsigned n, cudaStream_t st) {
+flce_status launch_t(const flce_qk_norm_rope_desc* d, const QkNormRopeParams& p, unsigned n,
+                     cudaStream_t st) {
   const bool wide = spread(d).p == 8;
   if (d->interleaved)
-    wide ? launch<BWD, T, 8, true>(p, n, st) : launch<BWD, T, 4, true>(p, n, st);
+    return wide ? launch<BWD, T, 8, true>(p, n, st) : launch<BWD, T, 4, true>(p, n, st);
   else
-    wide ? launch<BWD, T, 8, false>(p, n, st) : launch<BWD, T, 4, false>(p, n, st);
+    return wide ? launch<BWD, T, 8, false>(p, n, st) : launch<BWD, T, 4, false>(p, n, st);
 }
 
 template <bool BWD>
 flce_status launch_any(const flce_qk_norm_rope_desc* d, const QkNormRopeParams& p, int64_t n,
                        cudaStream_t st) {
-  if (d->dtype == FLCE_BF16)
-    launch_t<BWD, __nv_bfloat16>(d, p, (unsigned)n, st);
-  else
-    launch_t<BWD, float>(d, p, (unsigned)n, st);
-  host::count_launch();
-  FLCE_HOST_CUDA(cudaGetLastError());
-  return FLCE_OK;
+  return d->dtype == FLCE_BF16 ? launch_t<BWD, __nv_bfloat16>(d, p, (unsigned)n, st)
+                               : launch_t<BWD, float>(d, p, (unsigned)n, st);
 }
 
 }  // namespace
@@ -211,12 +207,9 @@ flce_status flce_qk_norm_rope_backward(const flce_qk_norm_rope_desc* d, const vo
     p.partial = static_cast<float*>(workspace);
     FLCE_HOST_TRY(launch_any<true>(d, p, n.q + n.k, st));
   }
-  qk_norm_rope_dw<<<dim3((unsigned)host::ceil_div(d->head_dim, 32), 2), 1024, 0, st>>>(
-      static_cast<const float*>(workspace), (int)n.q, (int)(n.q + n.k), (int)d->head_dim, dq_weight,
-      dk_weight);
-  host::count_launch();
-  FLCE_HOST_CUDA(cudaGetLastError());
-  return FLCE_OK;
+  return host::launch(qk_norm_rope_dw, dim3((unsigned)host::ceil_div(d->head_dim, 32), 2), 1024, 0, st,
+                      static_cast<const float*>(workspace), (int)n.q, (int)(n.q + n.k), (int)d->head_dim,
+                      dq_weight, dk_weight);
 }
 
 }  // extern "C"

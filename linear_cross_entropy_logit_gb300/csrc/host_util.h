@@ -33,6 +33,31 @@ inline bool aligned(const void* p, size_t a) {
 inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Launches a kernel that calls grid_wait: its launch and set-up overlap the end of the
+// kernel ahead of it in the stream (head norm and its backward over 16384 tokens, 28 / 4
+// heads of 128: 125 -> 116.5 us; attention backward of 61 ragged sequences of 9999 tokens,
+// 16 heads of 64: 131 -> 123.5).  It may start as blocks of that one end, not before:
+// with launch_dependents at the kernels' start the attention passes are up to 7% slower.
+template <typename... P, typename... A>
+flce_status launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                   const A&... args) {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = &a;
+  c.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args...);
+  count_launch();
+  if (e == cudaSuccess) return FLCE_OK;
+  (void)cudaGetLastError();
+  return fail(e, "cudaLaunchKernelEx");
+}
+
 }  // namespace host
 }  // namespace flce
 

@@ -436,6 +436,10 @@ __device__ __forceinline__ void mma_commit_if(uint32_t elected, uint64_t* bar) {
       ::"r"(smem_u32(bar)), "r"(elected) : "memory");
 }
 
+// Kernels launched by host::launch may start before the kernel ahead of them in the
+// stream has ended: this waits until it has and its writes are seen.  Every thread calls it
+// before it touches global memory.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;

@@ -201,6 +201,7 @@ qk_norm_rope_fwd(const __grid_constant__ QkNormRopeParams p) {
   const int h0 = ((uint32_t)item - token * side.per_token) * U;
   const int heads = live ? side.heads - h0 : 0;
   const T* in = static_cast<const T*>(side.x) + token * side.row + h0 * side.head;
+  grid_wait();
   // first, for the angles wait for the position (55.6 -> 48.5 us at 16384 tokens, 28 + 4
   // heads of 128)
   Angles<P> t;
@@ -264,6 +265,7 @@ qk_norm_rope_bwd(const __grid_constant__ QkNormRopeParams p) {
   const int lanes = 1 << p.log_lanes, l = threadIdx.x & (lanes - 1);
   const NormLane<P, PAIRS> n(p, l);
   const bool weighted = side.w != nullptr;
+  grid_wait();
   Raw<T, P> w[2];
   w[0].zero();
   w[1].zero();
@@ -395,6 +397,7 @@ __global__ void __launch_bounds__(1024) qk_norm_rope_dw(const float* partial, in
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
   const int end = blockIdx.y ? rows : q_rows;
   float t = 0.f;
+  grid_wait();
   if (c < head_dim)
 #pragma unroll 4
     for (int r = (blockIdx.y ? q_rows : 0) + w; r < end; r += 32) t += partial[(int64_t)r * head_dim + c];
