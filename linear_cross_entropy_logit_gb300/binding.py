@@ -659,7 +659,7 @@ def _output(name, t, like, shape, dtype, dev):
     """The caller's output, checked, or a new contiguous one; its address."""
     if t is not None:
         return t, _array(name, t, shape, dtype, dev)
-    t = like.new_empty(shape, dtype=dtype)  # 3 us less than torch.empty with a device
+    t = torch.empty(shape, dtype=dtype, device=like.device)
     return t, t.data_ptr()
 
 
@@ -734,7 +734,8 @@ def flce_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, si
     L = lib()
     ws = workspace_buf
     if ws is None:
-        ws = q.new_empty(max(L.flce_qk_norm_rope_workspace_size(d), 256), dtype=torch.uint8)
+        ws = torch.empty(max(L.flce_qk_norm_rope_workspace_size(d), 256), dtype=torch.uint8,
+                         device=q.device)
     err_word = new_err_word(q.device) if err_word is None else err_word
     st = L.flce_qk_norm_rope_backward(
         d, _array("dq_out", dq_out, q.shape, dtype, dev), _array("dk_out", dk_out, k.shape, dtype, dev),
@@ -803,7 +804,8 @@ def flce_attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale: Optional
     L = lib()
     ws = workspace_buf
     if ws is None:
-        ws = q.new_empty(max(L.flce_attention_workspace_size(d), 256), dtype=torch.uint8)
+        ws = torch.empty(max(L.flce_attention_workspace_size(d), 256), dtype=torch.uint8,
+                         device=q.device)
     err_word = new_err_word(q.device) if err_word is None else err_word
     st = L.flce_attention_backward(
         d, _array("dout", dout, shape, dtype, dev), q.data_ptr(), k.data_ptr(), v.data_ptr(),
