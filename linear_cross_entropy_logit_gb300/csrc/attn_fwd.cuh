@@ -26,8 +26,18 @@
 // exponentials are relative to the old one, at most 2^16 in size, and O is left
 // alone.  So half of a tile's exponentials are made before its maximum is
 // known, and made again in the rare case that it moves; P is handed over in
-// halves, the first to be multiplied while the second is made.  l and m are fp32; P is rounded to bf16 (2^-9 each, the type of
-// V), and l sums it before that rounding.
+// halves, the first to be multiplied while the second is made.  l and m are fp32; P
+// is rounded to bf16 (the type of V, at most 2^-8 of it), and l sums it before that
+// rounding.
+//
+// What bounds it.  Heads of 128: a tile's chain of S, softmax, P V and the next S, as TMEM
+// holds one S and one O a tile (all 512 columns): 341 us at 8192 tokens, 32 / 8 heads, 1612
+// TFLOP/s of the visible pairs, tensor pipe 68% active.  Heads of 64: the softmax,
+// with half the products to hide it behind: 979 us at 32768 tokens, 8 / 2 heads, 1123
+// TFLOP/s.  Short sequences: each unit's latency of some 6000 cycles and the empty
+// part of its tiles: 140 us for 37 ragged sequences of 16384 tokens, 28 / 4 heads of
+// 128, 603 TFLOP/s.  Tried and slower: a third or fourth softmax warpgroup, the
+// epilogue in warps of its own, S ahead of P in more buffers, two issuing warps.
 #pragma once
 #include "attn_common.cuh"
 
