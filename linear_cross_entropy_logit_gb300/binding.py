@@ -883,6 +883,7 @@ class _QkNormRope(torch.autograd.Function):
         return q_out, k_out
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, gq, gk):
         q, k, wq, wk, cos, sin, positions, err = ctx.saved_tensors
         eps, interleaved = ctx.cfg
@@ -908,6 +909,7 @@ class _PackedAttention(torch.autograd.Function):
         return out
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, g):
         q, k, v, out, lse, cu_seqlens, err = ctx.saved_tensors
         dq, dk, dv, _ = flce_attention_backward(g.contiguous(), q, k, v, out, lse, cu_seqlens,

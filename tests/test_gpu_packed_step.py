@@ -71,3 +71,65 @@ def test_example_runs():
     assert r.returncode == 0, r.stderr[-2000:]
     losses = [float(line.split("loss ")[1].split(",")[0]) for line in r.stdout.splitlines()]
     assert len(losses) == 3 and losses[-1] < losses[0]
+
+
+@pytest.mark.parametrize("T,HQ,HK,D,cuts", [(40, 4, 2, 64, [0, 13, 40]), (700, 6, 2, 128, [0, 5, 300, 690]),
+                                            (2600, 8, 2, 64, [0, 2600])])
+def test_calls_in_a_row_see_each_others_results(T, HQ, HK, D, cuts):
+    """Each launch may start while the one before it ends: a chain of calls that read
+    what the last ones wrote, into the same buffers, gives the bits of calls made one by one."""
+    import torch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    gen = torch.Generator().manual_seed(T)
+
+    def r(*shape, dtype=torch.bfloat16):
+        return torch.randn(*shape, generator=gen).to("cuda", dtype)
+
+    x = [r(T, HQ, D), r(T, HK, D)]
+    w = [r(D), r(D)]
+    angle = r(T, D // 2, dtype=torch.float32)
+    cos, sin = angle.cos(), angle.sin()
+    cu = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+
+    def chain(wait):
+        q, k = x[0].clone(), x[1].clone()
+        v = x[1].flip(0).contiguous()
+        a, b, out, dq, dk, dv = (torch.empty_like(t) for t in (q, k, q, q, k, k))
+        lse = torch.empty(HQ, T, device="cuda")
+        dw = [torch.empty(D, device="cuda") for _ in range(2)]
+        err = B.new_err_word("cuda")
+        kept = []
+        wait()
+        for i in range(12):
+            B.flce_qk_norm_rope_forward(q, k, *w, cos, sin, q_out=a, k_out=b, err_word=err)
+            wait()
+            B.flce_attention_forward(a, b, v, cu, out=out, lse=lse, err_word=err)
+            wait()
+            B.flce_attention_backward(a, a, b, v, out, lse, cu, dq=dq, dk=dk, dv=dv, err_word=err)
+            wait()
+            # the next step's inputs: q and k from their gradients
+            B.flce_qk_norm_rope_backward(dq, dk, a, b, *w, cos, sin, dq=q, dk=k, dq_weight=dw[0],
+                                         dk_weight=dw[1], err_word=err)
+            wait()
+            if i % 4 == 3:
+                kept += [t.clone() for t in (q, k, out, lse, dv, *dw)]
+                wait()
+        assert int(err.item()) == 0
+        return kept
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(4):
+        got = chain(lambda: None)
+        assert all(torch.equal(p.nan_to_num(), t.nan_to_num()) for p, t in zip(got, want))
+    assert all(t[..., :cuts[-1], :].isfinite().all() for t in want if t.dim() == 3)
+
+
+def test_second_derivatives_are_refused():
+    import torch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    q, k, v = (torch.randn(9, 2, 64, device="cuda").bfloat16().requires_grad_() for _ in range(3))
+    cu = torch.tensor([0, 9], dtype=torch.int32, device="cuda")
+    out = B.packed_attention(*B.qk_norm_rope(q, k, None, None, None, None), v, cu)
+    (g,) = torch.autograd.grad(out.float().pow(2).sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.float().sum().backward()
