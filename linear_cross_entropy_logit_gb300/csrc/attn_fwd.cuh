@@ -1,6 +1,6 @@
 // Forward of packed causal attention on the tensor cores.
 //
-//   s_ij = scale q_i . k_j,  m_i a running maximum,  p_ij = 2^((s_ij - m_i) log2 e)
+//   s_ij = scale q_i . k_j,  m_i a moving reference,  p_ij = 2^((s_ij - m_i) log2 e)
 //   l_i = sum_j p_ij,  out_i = sum_j p_ij v_j / l_i,  lse_i = m_i + log l_i
 //
 // A persistent CTA takes units of 256 query rows of one sequence and head: two
@@ -22,21 +22,23 @@
 // sequence that only some rows see are zeroed too and added back in the
 // epilogue to the rows that see them.
 //
-// The maximum is only moved when it grows by more than kMoveLog2: until then
-// exponentials are relative to the old one, at most 2^16 in size, and O is left
-// alone.  So half of a tile's exponentials are made before its maximum is
-// known, and made again in the rare case that it moves; P is handed over in
-// halves, the first to be multiplied while the second is made.  l and m are fp32; P
-// is rounded to bf16 (the type of V, at most 2^-8 of it), and l sums it before that
-// rounding.
+// Exponentials are relative to a reference, the diagonal tile's maximum at first.  It is
+// only moved when they would pass 2^kMoveLog2, and O and l with it: until then O is left alone. So
+// half of a tile's exponentials are made at once, and made again in the rare case that it
+// moves; their sum tells whether it has to for them, and the other half's maximum for those
+// (the maximum of both halves: 142 / 136 us for 37 ragged sequences of 16384 tokens, 985 / 954
+// at 32768 tokens, 8 / 2 heads of 64; both halves by their sums, the second's reference
+// moved by itself: 140 and 1013).  P is handed over in halves, the first to be multiplied
+// while the second is made.  l is fp32; P is rounded to bf16 (the type of V, at most 2^-8
+// of it), and l sums it before that rounding.
 //
 // What bounds it.  Heads of 128: a tile's chain of S, softmax, P V and the next S, as TMEM
 // holds one S and one O a tile (all 512 columns): 341 us at 8192 tokens, 32 / 8 heads, 1612
 // TFLOP/s of the visible pairs, tensor pipe 68% active.  Heads of 64: the softmax,
-// with half the products to hide it behind: 979 us at 32768 tokens, 8 / 2 heads, 1123
+// with half the products to hide it behind: 954 us at 32768 tokens, 8 / 2 heads, 1153
 // TFLOP/s.  Short sequences: each unit's latency of some 6000 cycles and the empty
-// part of its tiles: 140 us for 37 ragged sequences of 16384 tokens, 28 / 4 heads of
-// 128, 603 TFLOP/s.  Tried and slower: a third or fourth softmax warpgroup, the
+// part of its tiles: 136 us for 37 ragged sequences of 16384 tokens, 28 / 4 heads of
+// 128, 621 TFLOP/s.  Tried and slower: a third or fourth softmax warpgroup, the
 // epilogue in warps of its own, S ahead of P in more buffers, two issuing warps.
 #pragma once
 #include "attn_common.cuh"
@@ -162,7 +164,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
         if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
         continue;
       }
-      float m = 0.f, l = 0.f;
+      float b = 0.f, l = 0.f;  // p = 2^(s c + b), l their sum
       bool ok = true;
       for (int j = n - 1; j >= 0; --j, ++ns) {
         if (!(ok = wait_bar_warp(&sh.sfull[x], ns & 1, ctx))) break;
@@ -171,22 +173,21 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(ts + 32 * i, s[i]);
         tmem_ld_wait();
-        auto row_max = [&] {
+        auto row_max = [&](int i0) {  // of runs i0 to 3
           float mx[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = i0; i < 4; ++i) {
             mx[i] = __uint_as_float(s[i][0]);
 #pragma unroll
             for (int e = 1; e < 31; e += 2)
               mx[i] = fmax3(mx[i], __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
             mx[i] = fmaxf(mx[i], __uint_as_float(s[i][31]));
           }
-          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          return i0 ? fmaxf(mx[2], mx[3]) : fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         };
         uint64_t sum[4];
-        // P of half of the row's keys, relative to the maximum m
+        // P of half of the row's keys; returns its sum
         auto half = [&](int i0) {
-          const float b = m == -INFINITY ? 0.f : -m * c;  // no key so far: all p are 0
           const uint64_t c2 = pack_f32x2(c, c), b2 = pack_f32x2(b, b);
 #pragma unroll
           for (int i = i0; i < i0 + 2; ++i) {
@@ -198,11 +199,14 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
               p0 = ex2_approx(p0);
               p1 = ex2_approx(p1);
               const uint64_t both = pack_f32x2(p0, p1);
-              sum[(e >> 1) & 3] = i == 0 && e < 8 ? both : add_f32x2(sum[(e >> 1) & 3], both);
+              sum[(e >> 1) & 3] = i == i0 && e < 8 ? both : add_f32x2(sum[(e >> 1) & 3], both);
               pk[e >> 1] = pack_bf16x2(p0, p1);
             }
             tmem_st_32x32b_x16(ts + 16 * i, pk);
           }
+          float l0, l1;
+          unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), l0, l1);
+          return l0 + l1;
         };
         auto ready = [&](uint64_t* bar) {
           tmem_st_wait();
@@ -226,18 +230,24 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
               for (int e = 0; e < 32; ++e) s[i][e] = 0xff800000u;
             }
           }
-          m = row_max();
+          const float top = row_max(0);
+          b = top == -INFINITY ? 0.f : -top * c;  // no key so far: l stays 0
         }
-        // The first half goes by the maximum so far, while this tile's is found: the
-        // exponentials need not wait for it.
-        for (;;) {
-          half(0);
-          const float top = row_max();
-          const bool move = (top - m) * c > kMoveLog2;
-          if (!__any_sync(~0u, move)) break;
-          // O is rescaled and the first half done again
-          const float f = move ? ex2_approx((m - top) * c) : 1.f;
-          if (move) m = top;
+        // The first half goes by the reference so far: its sum, and the second half's
+        // maximum, tell whether it has to move.
+        float s0;
+        for (bool again = false;; again = true) {
+          s0 = half(0);
+          const bool empty = l == 0.f && j < n - 1;
+          const bool move = fmaxf(s0 * 0x1p-16f, fmaf(row_max(2), c, b) - (kMoveLog2 - 1.f)) > 1.f || empty;
+          if (again || !__any_sync(~0u, move)) break;
+          // b moves, O and l are rescaled, and the half is done again
+          float f = 1.f;
+          if (move) {
+            const float top = row_max(0), to_b = top == -INFINITY ? 0.f : -top * c;
+            if (!empty) f = ex2_approx(to_b - b);
+            b = to_b;
+          }
           l *= f;
 #pragma unroll 1
           for (int d = 0; d < DP; d += 32) {
@@ -250,11 +260,9 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
           }
         }
         ready(&sh.phalf[x]);
-        half(2);
+        const float s1 = half(2);
         ready(&sh.pfull[x]);
-        float l0, l1;
-        unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), l0, l1);
-        l += l0 + l1;
+        l += s0 + s1;
       }
       if (!ok || !wait_bar_warp(&sh.ofull[x], no & 1, ctx)) break;
       ++no;
@@ -280,7 +288,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
       }
       tc_fence_before();  // O is read before the next unit's first product into it
       if (r < u.len)
-        p.lse[(int64_t)u.head * p.tokens + u.start + r] = m * p.scale + lg2_approx(l) * kLn2;
+        p.lse[(int64_t)u.head * p.tokens + u.start + r] = (lg2_approx(l) - b) * kLn2;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
     }

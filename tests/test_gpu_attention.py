@@ -294,3 +294,47 @@ def test_debug_build_gives_the_same_bits():
     finally:
         B.use_library(prev)
     assert got[5] == 0 and all(torch.equal(a, b) for a, b in zip(want[:5], got[:5]))
+
+
+# what the scores of a lower key tile's halves add to the diagonal tile's
+JUMPS = [(0, 20), (20, 0), (300, 0), (0, 300), (100, 400), (400, 100), (-300, 60), (60, -300), (8, 8)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("first,second", JUMPS)
+def test_scores_that_jump_between_halves_of_a_tile(first, second, D):
+    """The softmax's reference moves with either half of a key tile, at either of two tiles."""
+    from linear_cross_entropy_logit_gb300 import binding as B
+    q, k, v, _ = make(400, 2, 1, D, seed=15)
+    q[:, :, 0] = 1
+    k[:, :, 0] = 0
+    k[128:192, :, 0], k[192:256, :, 0] = first, second  # exact in bf16
+    k[:64, :, 0], k[64:128, :, 0] = second, first
+    out, lse, err = B.flce_attention_forward(q, k, v, offsets([0, 400]), 1.0)
+    want, want_lse = A.attention_forward(*(tensor_f64(t) for t in (q, k, v)), [0, 400], 1.0)
+    assert int(err.item()) == 0
+    assert rel_fro(tensor_f64(out), want) <= OUT
+    # LSE holds for scores up to 50; beyond, fp32's step grows with them
+    bound = LSE * np.maximum(1.0, np.abs(want_lse) / 50)
+    assert (np.abs(tensor_f64(lse) - want_lse) <= bound).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_keys_of_minus_infinity_have_no_weight(D):
+    """Scores of -infinity: in the diagonal tile of rows that see finite ones below it, and
+    everywhere (those rows have no softmax)."""
+    import torch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    for lo, hi in ((128, 400), (0, 200), (140, 150)):
+        q, k, v, _ = make(400, 4, 2, D, seed=16)
+        q[:, :, 0] = 1
+        k[lo:hi, :, 0] = float("-inf")
+        out, lse, err = B.flce_attention_forward(q, k, v, offsets([0, 400]))
+        with np.errstate(invalid="ignore"):
+            want, want_lse = A.attention_forward(*(tensor_f64(t) for t in (q, k, v)), [0, 400], D**-0.5)
+        rows = np.arange(400)
+        live = (rows < lo) | (rows >= hi) | (lo > 0)
+        assert int(err.item()) == 0
+        assert rel_fro(tensor_f64(out)[live], want[live]) <= OUT
+        assert np.abs(tensor_f64(lse)[:, live] - want_lse[:, live]).max() <= LSE
+        assert torch.isneginf(lse[:, torch.from_numpy(~live).cuda()]).all()
