@@ -64,6 +64,14 @@ __device__ __forceinline__ void mask_diagonal(uint32_t (&v)[2][32], int half) {
   }
 }
 
+// dS of a sequence's first query and key, in its first diagonal tile.  That query sees one
+// key, its p is 1 and its dS nothing but the rounding of lse and delta (1e-7 of dP): with it
+// a sequence of one token would have gradients where there are none.  A dS that is not
+// finite stays so.
+__device__ __forceinline__ void zero_first(uint32_t (&v)[2][32]) {
+  if (threadIdx.x == 0) v[0][0] = __float_as_uint(as_f(v[0][0]) * 0.f);
+}
+
 // ----------------------------------------------------------------------------
 // delta
 // ----------------------------------------------------------------------------
@@ -276,7 +284,10 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
             s[i >> 5][i & 31] = __float_as_uint(a * as_f(s[i >> 5][i & 31]));
             s[i >> 5][(i & 31) + 1] = __float_as_uint(b * as_f(s[i >> 5][(i & 31) + 1]));
           }
-          if (j == n - 1) mask_diagonal<false>(s, half);  // keys after the row
+          if (j == n - 1) {
+            mask_diagonal<false>(s, half);  // keys after the row
+            if (u.q0 == 0) zero_first(s);
+          }
           uint32_t pk[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i)
@@ -655,7 +666,10 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
               r[i0 + 2] = __float_as_uint((as_f(r[i0 + 2]) - b.z) * as_f(q[i0 + 2]));
               r[i0 + 3] = __float_as_uint((as_f(r[i0 + 3]) - b.w) * as_f(q[i0 + 3]));
             }
-            if (i == first) mask_diagonal<true>(g, half);
+            if (i == first) {
+              mask_diagonal<true>(g, half);
+              if (u.q0 == 0) zero_first(g);
+            }
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               pk[e] = pack_bf16x2(as_f(g[e >> 4][2 * (e & 15)]), as_f(g[e >> 4][2 * (e & 15) + 1]));

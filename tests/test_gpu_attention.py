@@ -338,3 +338,23 @@ def test_keys_of_minus_infinity_have_no_weight(D):
         assert rel_fro(tensor_f64(out)[live], want[live]) <= OUT
         assert np.abs(tensor_f64(lse)[:, live] - want_lse[:, live]).max() <= LSE
         assert torch.isneginf(lse[:, torch.from_numpy(~live).cuda()]).all()
+
+
+@pytest.mark.parametrize("D", [64, 80, 128])
+def test_first_tokens_take_no_gradient_through_the_softmax(D):
+    """A row with one visible key: dq is 0, and dk gets nothing from it (sequences of one
+    token: all of dq and dk are 0, exactly; dv is dout, summed over the heads of a group)."""
+    import torch
+    q, k, v, g = make(190, 6, 2, D, seed=17, spread=4.0)
+    cu = [0, 1, 2, 2, 3, 130, 131, 131, 185]
+    _, _, dq, dk, dv, err = run(q, k, v, g, cu)
+    starts = [a for a, b in zip(cu, cu[1:]) if b > a]
+    ones = [a for a, b in zip(cu, cu[1:]) if b == a + 1]
+    assert err == 0
+    assert not dq[starts].any() and not dk[ones].any()
+    want = g.float().view(190, 2, 3, D).sum(2).bfloat16()
+    assert (dv[ones].float() - want[ones].float()).abs().max() <= 2.0**-7 * want.float().abs().max()
+    # what the gradient holds that is not finite is not hidden by it
+    g[0, 0, 0] = float("nan")
+    _, _, dq, dk, _, _ = run(q, k, v, g, cu)
+    assert torch.isnan(dq[0, 0]).all() and torch.isnan(dk[0, 0]).all() and not dq[1].any()
