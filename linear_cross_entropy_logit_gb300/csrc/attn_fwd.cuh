@@ -34,7 +34,7 @@
 //
 // What bounds it.  Heads of 128: a tile's chain of S, softmax, P V and the next S, as TMEM
 // holds one S and one O a tile (all 512 columns): 341 us at 8192 tokens, 32 / 8 heads, 1612
-// TFLOP/s of the visible pairs, tensor pipe 68% active.  Heads of 64: the softmax,
+// TFLOP/s of the visible pairs, tensor pipe 67% active.  Heads of 64: the softmax,
 // with half the products to hide it behind: 954 us at 32768 tokens, 8 / 2 heads, 1153
 // TFLOP/s.  Short sequences: each unit's latency of some 6000 cycles and the empty
 // part of its tiles: 136 us for 37 ragged sequences of 16384 tokens, 28 / 4 heads of
