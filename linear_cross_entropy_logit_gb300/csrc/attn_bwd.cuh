@@ -10,10 +10,10 @@
 // TMEM of the CTA that owns its rows: no fp32 gradient goes through memory, no
 // atomics, the same bits every run.  Seven products where one kernel for all
 // three gradients would take five, but that one has to add dq up in memory
-// across CTAs.  At 8192 tokens, 32 / 8 heads of 128: delta 27 us, dq 495 us and dkdv 640 us,
+// across CTAs.  At 8192 tokens, 32 / 8 heads of 128: delta 22 us, dq 492 us and dkdv 640 us,
 // the two at 1670 and 1720 TFLOP/s of their three and four products over the visible
 // pairs: bound by the tensor cores.  61 ragged sequences of 9999 tokens, 16 heads of 64:
-// 12, 48 and 66 us, bound by each unit's latency.
+// 10, 48 and 66 us, bound by each unit's latency.
 //
 // Both: warps 0-7 compute (a thread owns one TMEM lane and 64 of the 128
 // columns), warp 8 issues MMAs, warp 9 maps units and loads, warps 12-15 clean
@@ -75,22 +75,26 @@ __device__ __forceinline__ void zero_first(uint32_t (&v)[2][32]) {
 // ----------------------------------------------------------------------------
 // delta
 // ----------------------------------------------------------------------------
-// Bound by reading out and dout once.  Eight lanes hold a row, 16 values each
-// (two of the 8 x 16 byte pieces), four rows a lane: 16 loads in flight.  A
-// kernel of its own rather than attn_dq's work: there its loads stood
-// before every unit, 3-4 us each (145 us against 12 + 48 for 61 ragged sequences of 9999
-// tokens, 16 heads of 64).
-constexpr int kDeltaRows = 128;  // tokens of one head per block of 256 threads
-__global__ void __launch_bounds__(256) attn_delta(const AttnBwdParams p) {
-  const int lane = threadIdx.x & 7, slot = threadIdx.x >> 3, h = blockIdx.y;
-  const int64_t t0 = (int64_t)blockIdx.x * kDeltaRows + slot;
-  uint4 a[4][2], b[4][2];
+// Bound by reading out and dout once: 136 MB in 22 us at 8192 tokens, 32 heads of 128
+// (6.1 TB/s).  Eight lanes hold a row, 8 or 16 values each, and eight or four rows: 16
+// loads in flight a lane.  Blocks of all heads of the same tokens run together (one head's
+// tokens after another's: 27 us).  A kernel of its own rather than attn_dq's work:
+// there its loads stood before every unit, 3-4 us each (145 us against 10 + 48 for 61 ragged
+// sequences of 9999 tokens, 16 heads of 64).
+constexpr int kDeltaRows = 128;  // tokens of one head per block
+template <int DP>
+__global__ void __launch_bounds__(DP == 128 ? 256 : 128) attn_delta(const AttnBwdParams p) {
+  constexpr int kPieces = DP / 64, kRows = 8 / kPieces, kStep = kDeltaRows / kRows;
+  const int lane = threadIdx.x & 7, slot = threadIdx.x >> 3;
+  const int64_t h = blockIdx.x % p.q_heads, t0 = (int64_t)(blockIdx.x / p.q_heads) * kDeltaRows + slot;
+  uint4 a[kRows][kPieces], b[kRows][kPieces];
+  float lse = 0.f;  // of row `lane`
   grid_wait();
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kRows; ++i)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int64_t t = t0 + 32 * i;
+    for (int e = 0; e < kPieces; ++e) {
+      const int64_t t = t0 + kStep * i;
       const int d = lane * 8 + 64 * e;
       a[i][e] = b[i][e] = make_uint4(0, 0, 0, 0);
       if (t < p.tokens && d < p.head_dim) {
@@ -99,11 +103,15 @@ __global__ void __launch_bounds__(256) attn_delta(const AttnBwdParams p) {
         b[i][e] = *reinterpret_cast<const uint4*>(p.dout + at);
       }
     }
+  const int64_t t = t0 + kStep * lane, at = h * p.tokens + t;
+  const bool mine = lane < kRows && t < p.tokens;  // lane i writes row i
+  if (mine) lse = p.lse[at];
+  float delta = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kRows; ++i) {
     float sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < kPieces; ++e) {
       const uint32_t x[4] = {a[i][e].x, a[i][e].y, a[i][e].z, a[i][e].w};
       const uint32_t y[4] = {b[i][e].x, b[i][e].y, b[i][e].z, b[i][e].w};
 #pragma unroll
@@ -114,12 +122,11 @@ __global__ void __launch_bounds__(256) attn_delta(const AttnBwdParams p) {
     }
 #pragma unroll
     for (int o = 4; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    const int64_t t = t0 + 32 * i;
-    if (lane == 0 && t < p.tokens) {
-      const int64_t at = (int64_t)h * p.tokens + t;
-      p.nlse[at] = -p.lse[at] * kLog2e;
-      p.delta[at] = sum;
-    }
+    if (lane == i) delta = sum;
+  }
+  if (mine) {
+    p.nlse[at] = -lse * kLog2e;
+    p.delta[at] = delta;
   }
 }
 

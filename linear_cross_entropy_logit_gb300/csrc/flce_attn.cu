@@ -150,7 +150,8 @@ flce_status launch_backward(const flce_attention_desc* d, const CUtensorMap (&m)
   FLCE_HOST_TRY(set_smem(setup[1][dev], attn_dkdv<DP>, DkvCfg<DP>::kSmem));
   const int64_t units = most_units(d, kTile);
   FLCE_HOST_TRY(host::launch(
-      attn_delta, dim3((unsigned)host::ceil_div(d->tokens, kDeltaRows), (unsigned)d->q_heads), 256, 0, st, p));
+      attn_delta<DP>, dim3((unsigned)(host::ceil_div(d->tokens, kDeltaRows) * d->q_heads)),
+      DP == 128 ? 256 : 128, 0, st, p));
   FLCE_HOST_TRY(host::launch(attn_dq<DP>, dim3((unsigned)std::min<int64_t>(units * d->q_heads, sms)),
                              kBwdThreads, DqCfg<DP>::kSmem, st, m[0], m[1], m[2], m[3], p));
   return host::launch(attn_dkdv<DP>, dim3((unsigned)std::min<int64_t>(units * d->kv_heads * p.splits, sms)),
