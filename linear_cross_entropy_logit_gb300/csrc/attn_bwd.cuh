@@ -17,11 +17,11 @@
 //
 // Both: warps 0-7 compute (a thread owns one TMEM lane and 64 of the 128
 // columns), warp 8 issues MMAs, warp 9 maps units and loads, warps 12-15 clean
-// tiles (and attn_dq's compute delta).  P and dS are rounded to bf16 for the
-// products (their operands' type); everything else is fp32.  A masked entry is
-// set to zero after the multiplication, so that what it held does not matter;
-// its partner in the product (a row of another sequence, or a non-finite value)
-// is zeroed in shared memory, as in the forward.
+// tiles.  P and dS are rounded to bf16 for the products (their operands' type);
+// everything else is fp32.  A masked entry is set to zero after the
+// multiplication, so that what it held does not matter; its partner in the
+// product (a row of another sequence, or a non-finite value) is zeroed in shared
+// memory, as in the forward.
 #pragma once
 #include "attn_common.cuh"
 
@@ -137,6 +137,13 @@ __global__ void __launch_bounds__(DP == 128 ? 256 : 128) attn_delta(const AttnBw
 // follows as soon as this one's is in registers, and its dP goes to the other
 // buffer, so the tensor cores never wait for a dS other than dQ's own.  Three K
 // tiles are held: of this step (for dQ += dS K), the next (S) and one in flight.
+//
+// S is made of the keys as they are, also on the diagonal, whose tile, if it holds a
+// non-finite value, is cleaned between that product and dQ's: a key with an infinite value may have a score of -infinity, which
+// leaves the row's softmax to its other keys (of the cleaned key it would be some finite
+// score instead).  Its part of dq is then 0 x infinity, so that value of dq is NaN in every
+// row that sees the key; the tile's non-finite values are all made up for in this way, for
+// the rows where they give another score have a NaN lse.
 template <int DP>
 struct DqCfg {
   static constexpr int kBoxes = DP / 64;
@@ -156,11 +163,13 @@ struct DqShared {
   uint64_t kfull[5], kempty[5], vfull[4], vempty[4];
   uint64_t qfull, qempty, gfull, gempty;  // Q and dout tiles
   uint64_t sfull, sread, dpfull[2], dsfull, accfull, exchange;
+  uint64_t diagonal;                      // S of a unit's diagonal tile is made
   uint64_t clean[2];
   uint64_t ufull[2], uempty[2];
   uint64_t mma_done;
   AttnUnit unit[2];
-  uint32_t flags[4][4];
+  uint32_t flags[2][4][4];  // by unit parity and cleaning warp: keys that are not finite
+  uint32_t dirty[2][4];     // whether flags[..][warp] has any set
   uint32_t tmem;
   int abort;
 };
@@ -191,6 +200,7 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
     mbar_init(&sh.dsfull, 8);
     mbar_init(&sh.accfull, 1);
     mbar_init(&sh.exchange, 8);
+    mbar_init(&sh.diagonal, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.dpfull[i], 1);
       mbar_init(&sh.clean[i], 4);
@@ -314,6 +324,20 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
           store_rows(smem + C::kStage + warp * 4096, t_acc + lanes + half * 64, p.scale,
                      p.dq + ((int64_t)(u.start + first) * p.q_heads + u.head) * p.head_dim + half * 64,
                      (int64_t)p.q_heads * p.head_dim, u.len - first, min(64, p.head_dim - half * 64));
+        const uint32_t* dw = sh.dirty[it & 1];
+        if ((DP == 128 || half == 0) && (dw[0] | dw[1] | dw[2] | dw[3])) {
+          __syncwarp();
+#pragma unroll 1
+          for (int i = 0; i <= row && u.q0 + row < u.len; ++i) {
+            const uint32_t(&fl)[4][4] = sh.flags[it & 1];
+            const int w = i >> 5;
+            if (((fl[0][w] | fl[1][w] | fl[2][w] | fl[3][w]) >> (i & 31)) & 1)
+              add_nonfinite(p.dq + ((int64_t)(u.start + u.q0 + row) * p.q_heads + u.head) * p.head_dim + half * 64,
+                            p.k + (int64_t)(u.start + u.q0 + i) * p.k_row + (u.head / p.group) * p.k_head + half * 64,
+                            min(64, p.head_dim - half * 64), 0.f);
+          }
+          __syncwarp();
+        }
         if (C::kThroughG) {
           fence_proxy_async_shared();
           __syncwarp();
@@ -351,11 +375,12 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
       if (u.len > 0) {
         const int n = u.q0 / kTile + 1;
         if (!wait_bar_warp(&sh.qfull, units & 1, ctx)) break;
-        // the diagonal key tile is cleaned before any product reads it
-        if (!wait_bar_warp(&sh.clean[it & 1], (it >> 1) & 1, ctx)) break;
         issue_s(base);
+        mma_commit_if(el, &sh.diagonal);
         if (!(ok = ok && wait_bar_warp(&sh.gfull, units & 1, ctx))) break;
         issue_dp(base);
+        // the diagonal key tile is fit for dQ's product
+        if (!(ok = ok && wait_bar_warp(&sh.clean[it & 1], (it >> 1) & 1, ctx))) break;
         if (n == 1) {
           mma_commit_if(el, &sh.qempty);
           mma_commit_if(el, &sh.gempty);
@@ -466,7 +491,7 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
   } else if (warp >= 12) {
     // ------------------------------------------------------------ diagonal key tiles
     const int w = warp - 12;
-    uint32_t t = 0;
+    uint32_t t = 0, units = 0;
     for (uint32_t it = 0;; ++it) {
       if (!wait_bar_warp(&sh.ufull[it & 1], (it >> 1) & 1, ctx)) break;
       const AttnUnit u = sh.unit[it & 1];
@@ -477,10 +502,24 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
           const uint32_t s = t % C::kK;
           if (!(ok = wait_bar_warp(&sh.kfull[s], (t / C::kK) & 1, ctx))) break;
           if (j == u.q0 / kTile) {
-            clean_tile(smem + C::kRingK + s * C::kTileBytes, C::kBoxes, u.len - u.q0, w, 4, sh.flags[w]);
+            // rows of another sequence are masked in S, so they are zeroed at any time
+            uint8_t* tile = smem + C::kRingK + s * C::kTileBytes;
+            if (u.len - u.q0 < kTile) zero_rows(tile, C::kBoxes, u.len - u.q0, w, 4);
+            uint32_t* fl = sh.flags[it & 1][w];
+            const bool dirty = has_nonfinite(tile, C::kBoxes, w, 4);
+            if (dirty) {
+              if (!(ok = wait_bar_warp(&sh.diagonal, units & 1, ctx))) break;
+              clean_tile(tile, C::kBoxes, kTile, w, 4, fl);
+            } else if (lane < 4) {
+              fl[lane] = 0;
+            }
+            ++units;
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.clean[it & 1]);
+            if (lane == 0) {
+              sh.dirty[it & 1][w] = dirty;
+              mbar_arrive(&sh.clean[it & 1]);
+            }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.kempty[s]);
@@ -715,9 +754,9 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
             if (q < row || u.q0 + q >= u.len) continue;
             const bf16* g = p.dout + ((int64_t)(u.start + u.q0 + q) * p.q_heads + kvh * p.group +
                                       split * per_split + i / kTile) * p.head_dim;
-            if (p.splits == 1) add_nonfinite(p.dv + at + lane * stride, g, p.head_dim);
+            if (p.splits == 1) add_nonfinite(p.dv + at + lane * stride, g, p.head_dim, 1.f);
             else add_nonfinite(p.partial + (p.splits + split) * p.tokens * stride + at + lane * stride, g,
-                               p.head_dim);
+                               p.head_dim, 1.f);
           }
           __syncwarp();
         }

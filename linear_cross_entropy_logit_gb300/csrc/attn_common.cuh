@@ -23,8 +23,8 @@ struct AttnParams {
   float scale;
   bf16* out;           // tokens x q_heads x head_dim
   float* lse;          // q_heads x tokens
-  const bf16* v;       // read directly where it holds non-finite values
-  int64_t v_row, v_head;
+  const bf16 *k, *v;   // read directly where they hold non-finite values
+  int64_t k_row, k_head, v_row, v_head;
   int* err_word;
   unsigned long long timeout_ns;
 };
@@ -275,13 +275,14 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, uint32_t taddr, float
     }
   }
 }
-// Adds the non-finite ones among the `cols` values of x to a row just stored.
+// Adds the non-finite ones among the `cols` values of x, times `weight`, to a row just
+// stored.
 template <typename T>
-__device__ __noinline__ void add_nonfinite(T* row, const bf16* x, int cols) {
+__device__ __noinline__ void add_nonfinite(T* row, const bf16* x, int cols, float weight) {
 #pragma unroll 1
   for (int d = 0; d < cols; ++d) {
     const float v = __bfloat162float(x[d]);
-    if (!isfinite(v)) row[d] = static_cast<T>(static_cast<float>(row[d]) + v);
+    if (!isfinite(v)) row[d] = static_cast<T>(static_cast<float>(row[d]) + v * weight);
   }
 }
 
@@ -307,6 +308,23 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int boxes, int valid, i
   for (int i = w * 32 + (threadIdx.x & 31); i < boxes * kTile * 8; i += warps * 32)
     if (((i >> 3) & (kTile - 1)) >= valid)
       reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
+}
+
+// Whether a warp's share of a tile (the pieces that it cleans) holds a non-finite value.
+__device__ __forceinline__ bool has_nonfinite(const uint8_t* tile, int boxes, int w, int warps) {
+  constexpr int kAhead = 8;  // loads in flight
+  uint32_t top = 0;  // the largest magnitude, NaN above all; its sign says nothing
+#pragma unroll 1
+  for (int i = w * 32 + (threadIdx.x & 31); i < boxes * kTile * 8; i += kAhead * warps * 32) {
+    uint4 x[kAhead];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e)
+      x[e] = reinterpret_cast<const uint4*>(tile)[i + e * warps * 32];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e)
+      top = bf16x2_max_abs(bf16x2_max_abs(bf16x2_max_abs(bf16x2_max_abs(top, x[e].x), x[e].y), x[e].z), x[e].w);
+  }
+  return __any_sync(~0u, nonfinite2(top) != 0);
 }
 
 // Makes a tile fit to be multiplied by zeros: rows from `valid` on (another

@@ -282,7 +282,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
           if (((sh.flags[it & 1][f][0][w] | sh.flags[it & 1][f][1][w]) >> (i & 31)) & 1)
             add_nonfinite(p.out + ((int64_t)(u.start + r) * p.q_heads + u.head) * p.head_dim,
                           p.v + (int64_t)(u.start + u.q0 + i) * p.v_row + (u.head / p.group) * p.v_head,
-                          p.head_dim);
+                          p.head_dim, 1.f);
         }
         __syncwarp();
       }

@@ -56,6 +56,8 @@ void fill(AttnParams& p, const flce_attention_desc* d, const int32_t* cu, int32_
   p.group = p.q_heads / p.kv_heads;
   p.head_dim = (int)d->head_dim;
   p.scale = d->scale;
+  p.k_row = d->k_row;
+  p.k_head = d->k_head;
   p.v_row = d->v_row;
   p.v_head = d->v_head;
   p.err_word = err_word;
@@ -218,6 +220,7 @@ flce_status flce_attention_backward(const flce_attention_desc* d, const void* do
   p.out = const_cast<bf16*>(static_cast<const bf16*>(out));
   p.lse = const_cast<float*>(lse);
   p.dout = static_cast<const bf16*>(dout);
+  p.k = static_cast<const bf16*>(k);
   p.dq = static_cast<bf16*>(dq);
   p.dk = static_cast<bf16*>(dk);
   p.dv = static_cast<bf16*>(dv);

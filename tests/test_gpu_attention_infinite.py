@@ -1,0 +1,58 @@
+"""Packed attention with infinite and very large inputs against the fp64 oracle.
+
+Tolerances as for ordinary inputs, over the values that the oracle has finite: OUT and GRAD
+in relative Frobenius norm (two and up to four roundings to bf16).  Where the oracle has NaN
+the kernels have to have NaN."""
+import numpy as np
+import pytest
+
+from oracle import attn_oracle as A
+from tests.gpu_util import tensor_f64
+from tests.test_gpu_attention import GRAD, make, run
+
+pytestmark = pytest.mark.gpu
+
+
+def oracle(q, k, v, g, cu, scale=None):
+    """(out, dq, dk, dv) in 64 bits."""
+    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    q, k, v, g = (tensor_f64(t) for t in (q, k, v, g))
+    with np.errstate(invalid="ignore"):
+        return (A.attention_forward(q, k, v, cu, scale)[0], *A.attention_backward(g, q, k, v, cu, scale))
+
+
+def close(got, want, bound, name):
+    """NaN where the oracle has NaN; the other values within `bound` of its norm."""
+    got = tensor_f64(got)
+    assert (np.isnan(got) == np.isnan(want)).all(), name
+    live = np.isfinite(want)
+    assert np.linalg.norm(got[live] - want[live]) <= bound * np.linalg.norm(want[live]), name
+
+
+# tokens and the infinite keys: within a sequence's first 128 rows alone, in a later diagonal
+# tile, in both; a last tile that is full and one that is not
+WEIGHTLESS = [(100, [40]), (128, [1, 127]), (300, [200]), (300, [3, 130, 299]), (384, [150, 383]),
+              (700, [90, 300, 301, 650])]
+
+
+@pytest.mark.parametrize("D", [64, 80, 128])
+@pytest.mark.parametrize("tokens,bad", WEIGHTLESS, ids=lambda x: str(x))
+@pytest.mark.parametrize("value", [float("-inf"), float("inf")])
+def test_gradients_beside_keys_without_weight(tokens, bad, D, value):
+    """Keys whose scores are all -infinity: they have no weight, so that the other keys'
+    gradients and the finite components of dq are the oracle's; dq is NaN (0 x infinity) in the
+    infinite component of the rows that see one."""
+    q, k, v, g = make(tokens + 40, 4, 2, D, seed=tokens + D)
+    q[:, :, 0] = 1.0 if value < 0 else -1.0
+    k[bad, :, 0] = value
+    cu = [0, tokens, tokens + 40]
+    _, _, dq, dk, dv, err = run(q, k, v, g, cu)
+    _, want_q, want_k, want_v = oracle(q, k, v, g, cu)
+    # the oracle multiplies masked keys by zero: rows before the first infinite one by themselves
+    n = bad[0]
+    want_q[:n] = oracle(q[:n], k[:n], v[:n], g[:n], [0, n])[1]
+    assert err == 0
+    close(dq, want_q, GRAD, "dq")
+    others = np.setdiff1d(np.arange(tokens + 40), bad)
+    close(dk[others], want_k[others], GRAD, "dk")
+    close(dv[others], want_v[others], GRAD, "dv")
