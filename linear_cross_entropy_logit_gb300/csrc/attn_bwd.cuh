@@ -548,6 +548,12 @@ attn_dq(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensor
 // they overwrite S^T and dP^T.  While the threads make P of a step, the tensor
 // cores run the last step's dK and this one's dP; while they make dS, this
 // step's dV and the next S.
+//
+// A ragged last tile of queries is filled up with copies of the last query, whose lse counts
+// as +infinity: p is 0, and so are they in the sums.  (Of zeros a key with an infinite value
+// would make 0 x infinity.)  The last query sees every key, so where a copy's score is such that
+// its p is NaN, the query's own p and with it the key's dv and dk are NaN.  Its dout is zero:
+// dP of a copy is NaN only for a value that is not finite, whose key's dk is NaN anyhow.
 template <int DP>
 struct DkvCfg {
   static constexpr int kBoxes = DP / 64;
@@ -974,8 +980,8 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
             uint8_t* g = smem + C::kRingG + gs * C::kTileBytes;
             const int valid = u.len - i * kTile;
             if (!(ok = wait_bar_warp(&sh.qfull[qs], (step / C::kQ) & 1, ctx))) break;
-            if (i == first) clean_tile(q, C::kBoxes, valid, w, 4, sh.flags[w][0]);
-            else if (valid < kTile) zero_rows(q, C::kBoxes, valid, w, 4);
+            if (valid < kTile) repeat_row(q, C::kBoxes, valid, w, 4);
+            if (i == first) clean_tile(q, C::kBoxes, kTile, w, 4, sh.flags[w][0]);
             if (!(ok = wait_bar_warp(&sh.gfull[gs], (step / C::kG) & 1, ctx))) break;
             if (i == first) {
               uint32_t* fl = sh.flags[w][1];

@@ -310,6 +310,19 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int boxes, int valid, i
       reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
 }
 
+// Fills the rows from `valid` on with row valid - 1 (16-byte pieces are swizzled by the
+// row number).  Before clean_tile: whether another warp has cleaned that row by then does not
+// matter, as each cleans its copies.
+__device__ __forceinline__ void repeat_row(uint8_t* tile, int boxes, int valid, int w, int warps) {
+#pragma unroll 1
+  for (int i = w * 32 + (threadIdx.x & 31); i < boxes * kTile * 8; i += warps * 32) {
+    const int row = (i >> 3) & (kTile - 1), from = valid - 1;
+    if (row >= valid)
+      reinterpret_cast<uint4*>(tile)[i] =
+          reinterpret_cast<const uint4*>(tile)[(i & ~(kTile * 8 - 1)) + from * 8 + ((i ^ row ^ from) & 7)];
+  }
+}
+
 // Whether a warp's share of a tile (the pieces that it cleans) holds a non-finite value.
 __device__ __forceinline__ bool has_nonfinite(const uint8_t* tile, int boxes, int w, int warps) {
   constexpr int kAhead = 8;  // loads in flight

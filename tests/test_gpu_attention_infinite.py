@@ -56,3 +56,16 @@ def test_gradients_beside_keys_without_weight(tokens, bad, D, value):
     others = np.setdiff1d(np.arange(tokens + 40), bad)
     close(dk[others], want_k[others], GRAD, "dk")
     close(dv[others], want_v[others], GRAD, "dv")
+
+
+@pytest.mark.parametrize("D", [64, 80, 128])
+@pytest.mark.parametrize("tokens,bad", WEIGHTLESS, ids=lambda x: str(x))
+def test_keys_without_weight_get_no_gradient(tokens, bad, D):
+    """dk and dv of a key whose scores are all -infinity are 0, whatever the length leaves empty
+    in the last tile of queries."""
+    q, k, v, g = make(tokens, 4, 2, D, seed=tokens + D)
+    q[:, :, 0] = 1.0
+    k[bad, :, 0] = float("-inf")
+    _, _, _, dk, dv, err = run(q, k, v, g, [0, tokens])
+    assert err == 0
+    assert (dk[bad] == 0).all() and (dv[bad] == 0).all()
