@@ -385,7 +385,9 @@ flce_status flce_qk_norm_rope_backward(const flce_qk_norm_rope_desc* desc, const
  * [cu_seqlens[0], cu_seqlens[sequences]) belong to none: their out is 0, their
  * lse -infinity, their gradients 0, and what they hold is not used.  Offsets
  * that do not ascend are reported as FLCE_ERR_INDEX and every row then counts
- * as belonging to none. */
+ * as belonging to none.  Finite values whose scores are finite in float give a
+ * finite out in sequences of up to 65536 tokens; longer ones for |v| up to
+ * 2^144 / tokens. */
 typedef struct {
   size_t struct_size;            /* sizeof(flce_attention_desc) */
   int64_t tokens, sequences;

@@ -29,8 +29,10 @@
 // (the maximum of both halves: 142 / 136 us for 37 ragged sequences of 16384 tokens, 985 / 954
 // at 32768 tokens, 8 / 2 heads of 64; both halves by their sums, the second's reference
 // moved by itself: 140 and 1013).  P is handed over in halves, the first to be multiplied
-// while the second is made.  l is fp32; P is rounded to bf16 (the type of V, at most 2^-8
-// of it), and l sums it before that rounding.
+// while the second is made.  An exponential is 2^-kShiftLog2 at the reference, so that none
+// passes 2^-16 and no sum over 65536 keys of them times finite values leaves fp32's range (at
+// 1, values above 5e33 did); l carries the same factor.  l is fp32; P is rounded to bf16
+// (the type of V, at most 2^-8 of it), and l sums it before that rounding.
 //
 // What bounds it.  Heads of 128: a tile's chain of S, softmax, P V and the next S, as TMEM
 // holds one S and one O a tile (all 512 columns): 341 us at 8192 tokens, 32 / 8 heads, 1612
@@ -47,7 +49,8 @@ namespace flce {
 
 constexpr int kFwdThreads = 384;
 constexpr int kFwdRows = 2 * kTile;
-constexpr float kMoveLog2 = 16.f;
+constexpr float kMoveLog2 = 16.f, kShiftLog2 = 32.f;
+static_assert(kShiftLog2 - kMoveLog2 == 16.f, "0x1p16f where the reference moves");
 // Registers per thread of the two softmax warpgroups and of the third: a
 // softmax thread holds a row of 128 scores.
 constexpr int kFwdSoftmaxRegs = 216, kFwdOtherRegs = 72;
@@ -164,7 +167,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
         if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
         continue;
       }
-      float b = 0.f, l = 0.f;  // p = 2^(s c + b), l their sum
+      float b = 0.f, l = 0.f;  // p = 2^(s c + b), l their sum; 2^-kShiftLog2 of what they stand for
       bool ok = true;
       for (int j = n - 1; j >= 0; --j, ++ns) {
         if (!(ok = wait_bar_warp(&sh.sfull[x], ns & 1, ctx))) break;
@@ -231,7 +234,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
             }
           }
           const float top = row_max(0);
-          b = top == -INFINITY ? 0.f : -top * c;  // no key so far: l stays 0
+          b = top == -INFINITY ? 0.f : fmaf(-top, c, -kShiftLog2);  // no key so far: l stays 0
         }
         // The first half goes by the reference so far: its sum, and the second half's
         // maximum, tell whether it has to move.
@@ -239,12 +242,13 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
         for (bool again = false;; again = true) {
           s0 = half(0);
           const bool empty = l == 0.f && j < n - 1;
-          const bool move = fmaxf(s0 * 0x1p-16f, fmaf(row_max(2), c, b) - (kMoveLog2 - 1.f)) > 1.f || empty;
+          const bool move =
+              fmaxf(s0 * 0x1p16f, fmaf(row_max(2), c, b) + (kShiftLog2 - kMoveLog2 + 1.f)) > 1.f || empty;
           if (again || !__any_sync(~0u, move)) break;
           // b moves, O and l are rescaled, and the half is done again
           float f = 1.f;
           if (move) {
-            const float top = row_max(0), to_b = top == -INFINITY ? 0.f : -top * c;
+            const float top = row_max(0), to_b = top == -INFINITY ? 0.f : fmaf(-top, c, -kShiftLog2);
             if (!empty) f = ex2_approx(to_b - b);
             b = to_b;
           }
@@ -288,7 +292,7 @@ attn_fwd(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtenso
       }
       tc_fence_before();  // O is read before the next unit's first product into it
       if (r < u.len)
-        p.lse[(int64_t)u.head * p.tokens + u.start + r] = (lg2_approx(l) - b) * kLn2;
+        p.lse[(int64_t)u.head * p.tokens + u.start + r] = (lg2_approx(l * 0x1p32f) - (b + kShiftLog2)) * kLn2;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.uempty[it & 1]);
     }

@@ -8,7 +8,7 @@ import pytest
 
 from oracle import attn_oracle as A
 from tests.gpu_util import tensor_f64
-from tests.test_gpu_attention import GRAD, make, run
+from tests.test_gpu_attention import GRAD, LSE, OUT, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +69,43 @@ def test_keys_without_weight_get_no_gradient(tokens, bad, D):
     _, _, _, dk, dv, err = run(q, k, v, g, [0, tokens])
     assert err == 0
     assert (dk[bad] == 0).all() and (dv[bad] == 0).all()
+
+
+BF16_MAX = 3.3895313892515355e38
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("tokens", [1, 70, 300, 1100])
+@pytest.mark.parametrize("size", [1e30, 5e36, 0.99 * BF16_MAX])
+def test_large_values_stay_finite(size, tokens, D):
+    """Finite values give finite results: neither the number of keys nor scores that rise above
+    the softmax's reference by less than what moves it take a sum past fp32."""
+    import torch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    q, k, v, _ = make(tokens, 2, 1, D, seed=18)
+    v = (torch.rand(tokens, 1, D, generator=torch.Generator().manual_seed(19)) * 0.5 + 0.49).cuda()
+    v = (v * size).bfloat16()
+    cu = [0, tokens]
+    for rise in (0.0, 10.0):  # of the scores from the diagonal tile to the first key: 10 < 16 ln 2
+        q, k = q * 0, k * 0
+        q[:, :, 0] = 1.0
+        k[:, 0, 0] = torch.linspace(rise, 0, tokens)
+        out, lse, err = B.flce_attention_forward(q, k, v, torch.tensor(cu, dtype=torch.int32, device="cuda"), 1.0)
+        want, want_lse = A.attention_forward(*(tensor_f64(t) for t in (q, k, v)), cu, 1.0)
+        assert int(err.item()) == 0
+        close(out, want, OUT, "out")
+        assert np.abs(tensor_f64(lse) - want_lse).max() <= LSE
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_values_keep_their_accuracy(D):
+    """The same at the other end: values of 1e-30 are not lost."""
+    import torch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    q, k, v, _ = make(500, 2, 1, D, seed=20)
+    v = (v.float() * 1e-30).bfloat16()
+    cu = torch.tensor([0, 500], dtype=torch.int32, device="cuda")
+    out, _, err = B.flce_attention_forward(q, k, v, cu)
+    want, _ = A.attention_forward(*(tensor_f64(t) for t in (q, k, v)), [0, 500], D ** -0.5)
+    assert int(err.item()) == 0
+    close(out, want, OUT, "out")
