@@ -109,3 +109,19 @@ def test_small_values_keep_their_accuracy(D):
     want, _ = A.attention_forward(*(tensor_f64(t) for t in (q, k, v)), [0, 500], D ** -0.5)
     assert int(err.item()) == 0
     close(out, want, OUT, "out")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("at", [7, 200])
+def test_a_query_without_softmax_reaches_the_keys_it_sees(at, D):
+    """A row whose scores are all -infinity has no softmax: its dq, and dk and dv of the keys it
+    sees, are NaN, in the diagonal tile as in the others."""
+    import torch
+    q, k, v, g = make(300, 2, 2, D, seed=21)
+    q[at, :, 0] = float("-inf")
+    k[:, :, 0] = 1.0
+    _, lse, dq, dk, dv, err = run(q, k, v, g, [0, 300])
+    assert err == 0 and torch.isneginf(lse[:, at]).all()
+    assert torch.isnan(dq[at]).all()
+    for t in (dk, dv):
+        assert torch.isnan(t[:at + 1]).all() and torch.isfinite(t[at + 1:]).all()
