@@ -39,6 +39,12 @@ struct AttnUnit {
 __device__ __forceinline__ int warp_add(int x) { return __reduce_add_sync(~0u, x); }
 __device__ __forceinline__ int warp_max(int x) { return __reduce_max_sync(~0u, x); }
 
+// Whether [begin, end) may be a sequence among `tokens` rows.  By comparisons alone: the
+// difference of offsets that may be anything passes 32 bits.
+__host__ __device__ constexpr bool sequence_ok(int begin, int end, int tokens) {
+  return 0 <= begin && begin <= end && end <= tokens;
+}
+
 // The sequences of a pack cut into units of ROWS rows, numbered so that the
 // longest come first: dealt out in this order, the CTAs end together.  Unit i of a
 // sequence sees i + 1 units' worth of keys and stands in class i; of two query tiles
@@ -88,11 +94,13 @@ struct UnitWalk {
     tokens = p.tokens;
     lead = cu[0];
     tail_start = cu[n];
-    int bad = lead < 0 || tail_start > tokens, most = 0, sum = 0;
+    int bad = !sequence_ok(lead, tail_start, tokens), most = 0, sum = 0;
 #pragma unroll 4
     for (int s = threadIdx.x & 31; s < n; s += 32) {
-      const int begin = cu[s], rows = cu[s + 1] - begin;
-      bad |= rows < 0 || begin < 0 || begin > tokens;
+      const int begin = cu[s], end = cu[s + 1];
+      const bool ok = sequence_ok(begin, end, tokens);
+      const int rows = ok ? end - begin : 0;
+      bad |= !ok;
       most = max(most, max(whole(rows), part_class(rows) + 1));
       sum += cut(rows);
     }
