@@ -38,6 +38,10 @@ struct AttnBwdParams : AttnParams {
   float *nlse, *delta; // q_heads x tokens: -lse log2 e, delta (by attn_delta, then attn_dq)
   float* partial;      // splits > 1: dk, dv partial sums, 2 x splits x tokens x kv_heads x head_dim
   int splits;          // CTAs that share the query heads of a key / value head
+  // Where the partial sums of dk, or dv, of a split begin.
+  __host__ __device__ int64_t partial_at(bool dv_sum, int split) const {
+    return (int64_t)((dv_sum ? splits : 0) + split) * tokens * kv_heads * head_dim;
+  }
 };
 
 __device__ __forceinline__ float as_f(uint32_t x) { return __uint_as_float(x); }
@@ -663,11 +667,8 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
       if (u.len == 0) {  // rows of no sequence
         if (row < u.rows) {
           const int64_t at = ((int64_t)(u.start + row) * p.kv_heads + kvh) * p.head_dim;
-          const int64_t size = (int64_t)p.tokens * p.kv_heads * p.head_dim;
-          uint4* o = p.splits == 1
-                         ? reinterpret_cast<uint4*>((half ? p.dk : p.dv) + at)
-                         : reinterpret_cast<uint4*>(p.partial + (half ? 0 : p.splits) * size +
-                                                    split * size + at);
+          uint4* o = p.splits == 1 ? reinterpret_cast<uint4*>((half ? p.dk : p.dv) + at)
+                                   : reinterpret_cast<uint4*>(p.partial + p.partial_at(!half, split) + at);
 #pragma unroll 1
           for (int d = 0; d < p.head_dim / (p.splits == 1 ? 8 : 4); ++d) o[d] = make_uint4(0, 0, 0, 0);
         }
@@ -751,8 +752,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
         if (p.splits == 1)
           store_rows(stage, from, scale, (half ? p.dk : p.dv) + at, stride, u.len - row0, p.head_dim);
         else
-          store_rows(stage, from, scale,
-                     p.partial + ((half ? 0 : p.splits) + split) * p.tokens * stride + at, stride,
+          store_rows(stage, from, scale, p.partial + p.partial_at(!half, split) + at, stride,
                      u.len - row0, p.head_dim);
         if (dirty) {  // add back the non-finite values of dout that each key sees
           __syncwarp();
@@ -763,8 +763,7 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
             const bf16* g = p.dout + ((int64_t)(u.start + u.q0 + q) * p.q_heads + kvh * p.group +
                                       split * per_split + i / kTile) * p.head_dim;
             if (p.splits == 1) add_nonfinite(p.dv + at + lane * stride, g, p.head_dim, 1.f);
-            else add_nonfinite(p.partial + (p.splits + split) * p.tokens * stride + at + lane * stride, g,
-                               p.head_dim, 1.f);
+            else add_nonfinite(p.partial + p.partial_at(true, split) + at + lane * stride, g, p.head_dim, 1.f);
           }
           __syncwarp();
         }

@@ -47,3 +47,18 @@ def test_offsets_that_no_sequence_has(cu):
     out, lse, dq, dk, dv, err = run(q, k, v, g, cu)
     assert err == B.FLCE_ERR_INDEX
     assert torch.isneginf(lse).all() and not any(t.any() for t in (out, dq, dk, dv))
+
+
+# splits, tokens, key / value heads, head size: the second and third pass 32 bits in the product
+# of splits and tokens alone
+PARTIALS = [(2, 100, 8, 128), (65521, 17000, 1, 8), (4096, 2**20, 2, 128)]
+
+
+def test_partial_sums_lie_where_the_workspace_has_them(tmp_path):
+    """Offsets of the backward's partial sums of dk and dv of each split, in 64 bits."""
+    body = "".join(
+        f'{{ flce::AttnBwdParams p{{}}; p.splits = {s}; p.tokens = {t}; p.kv_heads = {h}; p.head_dim = {d};\n'
+        f'  printf("%lld %lld %lld\\n", (long long)p.partial_at(false, 0), (long long)p.partial_at(false, {s - 1}),\n'
+        f'         (long long)p.partial_at(true, {s - 1})); }}\n' for s, t, h, d in PARTIALS)
+    got = [int(x) for x in host_program(tmp_path, "attn_bwd.cuh", body)]
+    assert got == [part * t * h * d for s, t, h, d in PARTIALS for part in (0, s - 1, 2 * s - 1)]
