@@ -615,6 +615,10 @@ def _current_stream(dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
 def _with_stream(stream, call, *args, **kwargs):
     """``call`` with ``stream`` as the current one, so that the tensors it makes belong to
     the stream it runs on and their memory does not reach another stream's work too early."""
@@ -628,6 +632,8 @@ def _cuda_device(q) -> int:
     dev = q.get_device()
     if dev < 0:
         raise ValueError(f"q must be a CUDA tensor, got one on {q.device}")
+    if dev != _current_device():  # the library launches on that one
+        raise ValueError(f"q is on {q.device}, the current device is cuda:{_current_device()}")
     return dev
 
 
