@@ -252,10 +252,21 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _check_device(name, t):
+    """Refuses a CUDA tensor of another GPU than the one that the library launches on."""
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
+
+
 def _check_inputs(X, W, labels):
     for name, t in (("X", X), ("W", W), ("labels", labels)):
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA tensor")
+        _check_device(name, t)
     if X.dtype != W.dtype:
         raise TypeError("X and W must have the same dtype")
     if labels.dtype != torch.int64:
@@ -540,6 +551,7 @@ def flce_forward_vocab_shard(X, W_shard, labels, vocab_offset: int, vocab_total:
 def flce_combine_vocab_shards(partials, labels, vocab_total: int, options: FlceOptions = None, *,
                               loss=None, lse=None, valid_count=None, err_word=None, stream=None):
     """LSE-combine of P shards' partials (float32 [P, N, 4]) -> (loss, lse, valid_count, err)."""
+    _check_device("partials", partials)
     n_shards, N = partials.shape[0], partials.shape[1]
     dev = partials.device
     options = make_options() if options is None else options
@@ -615,10 +627,6 @@ def _current_stream(dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _current_device() -> int:
-    return torch._C._cuda_getDevice()
-
-
 def _with_stream(stream, call, *args, **kwargs):
     """``call`` with ``stream`` as the current one, so that the tensors it makes belong to
     the stream it runs on and their memory does not reach another stream's work too early."""
@@ -632,8 +640,7 @@ def _cuda_device(q) -> int:
     dev = q.get_device()
     if dev < 0:
         raise ValueError(f"q must be a CUDA tensor, got one on {q.device}")
-    if dev != _current_device():  # the library launches on that one
-        raise ValueError(f"q is on {q.device}, the current device is cuda:{_current_device()}")
+    _check_device("q", q)
     return dev
 
 

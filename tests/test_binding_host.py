@@ -35,3 +35,15 @@ def test_attention_and_norm_refuse_tensors_of_another_gpu(B, monkeypatch):
                  lambda: B.qk_norm_rope(t, t, None, None, None, None)):
         with pytest.raises(ValueError, match="current device"):
             call()
+
+
+def test_loss_refuses_tensors_of_another_gpu(B, monkeypatch):
+    monkeypatch.setattr(B, "_current_device", lambda: 0)
+    t = Elsewhere()
+    for call in (lambda: B.flce_forward(t, t, t), lambda: B.flce_forward_ex(t, t, t, B.make_options()),
+                 lambda: B.flce_backward(t, t, t, t, t), lambda: B.flce_fwd_bwd(t, t, t),
+                 lambda: B.flce_forward_vocab_shard(t, t, t, 0, 10), lambda: B.flce_combine_vocab_shards(t, t, 10),
+                 lambda: B.flce_backward_vocab_shard(t, t, t, 0, 10, t, t),
+                 lambda: B.flce_forward_noalloc(t, t, t, loss=t, lse=t, valid_count=t, err_word=t)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
