@@ -676,6 +676,25 @@ def _output(name, t, like, shape, dtype, dev):
     return t, t.data_ptr()
 
 
+def _error_word(t, like, dev):
+    """The caller's error word, checked, or a new one; its address."""
+    if t is None:
+        t = new_err_word(like.device)
+    elif t.dtype is not torch.int32 or t.get_device() != dev or not t.numel():
+        raise ValueError(f"err_word must be an int32 tensor on cuda:{dev}, got {t.numel()} {t.dtype} on {t.device}")
+    return t, t.data_ptr()
+
+
+def _scratch(t, need, like, dev):
+    """The caller's workspace, checked, or a new one; its address and size."""
+    if t is None:
+        t = torch.empty(max(need, 256), dtype=torch.uint8, device=like.device)
+    elif t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace_buf must be a contiguous tensor on cuda:{dev}, "
+                         f"got {tuple(t.shape)} on {t.device}")
+    return t, t.data_ptr(), t.numel()
+
+
 def _qk_norm_rope_args(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
     """(desc, device, the inputs' addresses)."""
     dev, dtype = _cuda_device(q), q.dtype
@@ -718,9 +737,9 @@ def flce_qk_norm_rope_forward(q, k, q_weight, k_weight, cos, sin, positions=None
     dtype = q.dtype
     q_out, p_q = _output("q_out", q_out, q, q.shape, dtype, dev)
     k_out, p_k = _output("k_out", k_out, q, k.shape, dtype, dev)
-    err_word = new_err_word(q.device) if err_word is None else err_word
+    err_word, p_err = _error_word(err_word, q, dev)
     st = lib().flce_qk_norm_rope_forward(
-        d, *ptrs, p_q, p_k, err_word.data_ptr(), _current_stream(dev))
+        d, *ptrs, p_q, p_k, p_err, _current_stream(dev))
     if st:
         _check(st, "flce_qk_norm_rope_forward")
     return q_out, k_out, err_word
@@ -745,14 +764,12 @@ def flce_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, si
     dq_weight, p_dwq = _output("dq_weight", dq_weight, q, w_shape, f32, dev)
     dk_weight, p_dwk = _output("dk_weight", dk_weight, q, w_shape, f32, dev)
     L = lib()
-    ws = workspace_buf
-    if ws is None:
-        ws = torch.empty(max(L.flce_qk_norm_rope_workspace_size(d), 256), dtype=torch.uint8,
-                         device=q.device)
-    err_word = new_err_word(q.device) if err_word is None else err_word
+    need = L.flce_qk_norm_rope_workspace_size(d) if workspace_buf is None else 0
+    ws, p_ws, ws_bytes = _scratch(workspace_buf, need, q, dev)
+    err_word, p_err = _error_word(err_word, q, dev)
     st = L.flce_qk_norm_rope_backward(
         d, _array("dq_out", dq_out, q.shape, dtype, dev), _array("dk_out", dk_out, k.shape, dtype, dev),
-        *ptrs, p_dq, p_dk, p_dwq, p_dwk, ws.data_ptr(), ws.numel(), err_word.data_ptr(),
+        *ptrs, p_dq, p_dk, p_dwq, p_dwk, p_ws, ws_bytes, p_err,
         _current_stream(dev))
     if st:
         _check(st, "flce_qk_norm_rope_backward")
@@ -791,10 +808,10 @@ def flce_attention_forward(q, k, v, cu_seqlens, scale: Optional[float] = None, *
     d, dev, lse_shape = _attention_args(q, k, v, cu_seqlens, scale)
     out, p_out = _output("out", out, q, q.shape, q.dtype, dev)
     lse, p_lse = _output("lse", lse, q, lse_shape, torch.float32, dev)
-    err_word = new_err_word(q.device) if err_word is None else err_word
+    err_word, p_err = _error_word(err_word, q, dev)
     st = lib().flce_attention_forward(
         d, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), p_out, p_lse,
-        err_word.data_ptr(), _current_stream(dev))
+        p_err, _current_stream(dev))
     if st:
         _check(st, "flce_attention_forward")
     return out, lse, err_word
@@ -815,15 +832,13 @@ def flce_attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale: Optional
     dk, p_dk = _output("dk", dk, q, kv_shape, dtype, dev)
     dv, p_dv = _output("dv", dv, q, kv_shape, dtype, dev)
     L = lib()
-    ws = workspace_buf
-    if ws is None:
-        ws = torch.empty(max(L.flce_attention_workspace_size(d), 256), dtype=torch.uint8,
-                         device=q.device)
-    err_word = new_err_word(q.device) if err_word is None else err_word
+    need = L.flce_attention_workspace_size(d) if workspace_buf is None else 0
+    ws, p_ws, ws_bytes = _scratch(workspace_buf, need, q, dev)
+    err_word, p_err = _error_word(err_word, q, dev)
     st = L.flce_attention_backward(
         d, _array("dout", dout, shape, dtype, dev), q.data_ptr(), k.data_ptr(), v.data_ptr(),
         _array("out", out, shape, dtype, dev), _array("lse", lse, lse_shape, torch.float32, dev),
-        cu_seqlens.data_ptr(), p_dq, p_dk, p_dv, ws.data_ptr(), ws.numel(), err_word.data_ptr(),
+        cu_seqlens.data_ptr(), p_dq, p_dk, p_dv, p_ws, ws_bytes, p_err,
         _current_stream(dev))
     if st:
         _check(st, "flce_attention_backward")

@@ -47,3 +47,39 @@ def test_loss_refuses_tensors_of_another_gpu(B, monkeypatch):
                  lambda: B.flce_forward_noalloc(t, t, t, loss=t, lse=t, valid_count=t, err_word=t)):
         with pytest.raises(ValueError, match="current device"):
             call()
+
+
+def test_error_words_and_workspaces_are_checked(B):
+    import torch
+    for bad in (torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int64, device="meta"),
+                torch.zeros(0, dtype=torch.int32, device="meta")):
+        with pytest.raises(ValueError, match="err_word"):
+            B._error_word(bad, None, bad.get_device() if bad.is_meta else 0)
+    host = torch.zeros(4096, dtype=torch.uint8)
+    for bad, dev in ((host, 0), (host.expand(2, 4096), -1), (host[::2], -1)):
+        with pytest.raises(ValueError, match="workspace_buf"):
+            B._scratch(bad, 256, None, dev)
+
+
+@pytest.mark.gpu
+def test_error_words_and_workspaces_on_the_host_are_refused(B):
+    import torch
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    lse = torch.zeros(2, 4, device="cuda")
+    err, ws = torch.zeros(1, dtype=torch.int32), torch.zeros(1 << 20, dtype=torch.uint8)
+    forward = (lambda **kw: B.flce_attention_forward(q, q, q, cu, **kw),
+               lambda **kw: B.flce_qk_norm_rope_forward(q, q, None, None, None, None, **kw))
+    backward = (lambda **kw: B.flce_attention_backward(q, q, q, q, q, lse, cu, **kw),
+                lambda **kw: B.flce_qk_norm_rope_backward(q, q, q, q, None, None, None, None, **kw))
+    for call in forward + backward:
+        with pytest.raises(ValueError, match="err_word"):
+            call(err_word=err)
+    one = torch.zeros(1, dtype=torch.uint8, device="cuda")
+    for call in backward:
+        for bad in (ws, one.expand(1 << 20)):
+            with pytest.raises(ValueError, match="workspace_buf"):
+                call(workspace_buf=bad)
+        with pytest.raises(B.FlceError):  # too small
+            call(workspace_buf=one)
+        call(workspace_buf=ws.cuda(), err_word=err.cuda())
