@@ -44,12 +44,13 @@ class Block(torch.nn.Module):
         self.register_buffer("cos", angle.cos().float())
         self.register_buffer("sin", angle.sin().float())
 
-    def forward(self, x, cu_seqlens, positions, labels):
+    def forward(self, x, cu_seqlens, positions, labels, err_word=None):
         q_heads, kv_heads, dim = self.shape
         # q, k and v are views of the projection's output
         q, k, v = (x @ self.qkv.T).view(x.shape[0], -1, dim).split([q_heads, kv_heads, kv_heads], 1)
-        q, k = B.qk_norm_rope(q, k, self.q_norm, self.k_norm, self.cos, self.sin, positions)
-        a = B.packed_attention(q, k, v, cu_seqlens)
+        q, k = B.qk_norm_rope(q, k, self.q_norm, self.k_norm, self.cos, self.sin, positions,
+                              err_word=err_word)
+        a = B.packed_attention(q, k, v, cu_seqlens, err_word=err_word)
         h = x + a.reshape(x.shape[0], -1) @ self.out.T
         return B.linear_cross_entropy(h, self.vocab, labels, ignore_index=-100)
 
@@ -77,14 +78,17 @@ def main():
     block = Block(a.hidden, a.q_heads, a.kv_heads, a.head_dim, a.vocab, a.tokens)
     opt = torch.optim.SGD(block.parameters(), lr=0.1)
     batch = packed_batch(a.tokens, a.sequences, a.hidden, a.vocab)
+    err = B.new_err_word("cuda")
     for step in range(a.steps):
         torch.cuda.synchronize()
         t = time.perf_counter()
         opt.zero_grad(set_to_none=True)
-        loss = block(*batch)
+        loss = block(*batch, err)
         loss.backward()
         opt.step()
         torch.cuda.synchronize()
+        if err.item():
+            raise B.FlceError(err.item(), "packed training step")
         print(f"step {step}: loss {loss.item():.4f}, {1e3 * (time.perf_counter() - t):.2f} ms", flush=True)
 
 

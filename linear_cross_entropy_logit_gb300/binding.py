@@ -903,48 +903,53 @@ def linear_cross_entropy(h, W, labels, ignore_index: int = -100, smoothing: floa
 
 class _QkNormRope(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
-        q_out, k_out, err = flce_qk_norm_rope_forward(q, k, q_weight, k_weight, cos, sin,
-                                                      positions, eps, interleaved=interleaved)
-        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions, err)
-        ctx.cfg = (eps, interleaved)
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, err):
+        q_out, k_out, err = flce_qk_norm_rope_forward(q, k, q_weight, k_weight, cos, sin, positions,
+                                                      eps, interleaved=interleaved, err_word=err)
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
+        # not saved: the caller may read and clear it before the backward
+        ctx.cfg = (eps, interleaved, err)
         return q_out, k_out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, gq, gk):
-        q, k, wq, wk, cos, sin, positions, err = ctx.saved_tensors
-        eps, interleaved = ctx.cfg
+        q, k, wq, wk, cos, sin, positions = ctx.saved_tensors
+        eps, interleaved, err = ctx.cfg
         dq, dk, dwq, dwk, _ = flce_qk_norm_rope_backward(
             gq.contiguous(), gk.contiguous(), q, k, wq, wk, cos, sin, positions, eps,
             interleaved=interleaved, err_word=err)
         return (dq, dk, None if wq is None else dwq.to(wq.dtype),
-                None if wk is None else dwk.to(wk.dtype), None, None, None, None, None)
+                None if wk is None else dwk.to(wk.dtype), None, None, None, None, None, None)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions=None, eps: float = 1e-6,
-                 interleaved: bool = False):
-    """Autograd entry of flce_qk_norm_rope_forward: (q_out, k_out)."""
-    return _QkNormRope.apply(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+                 interleaved: bool = False, *, err_word=None):
+    """Autograd entry of flce_qk_norm_rope_forward: (q_out, k_out).  The forward and the
+    backward report into err_word; without one what goes wrong on the device is not seen."""
+    return _QkNormRope.apply(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, err_word)
 
 
 class _PackedAttention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, cu_seqlens, scale):
-        out, lse, err = flce_attention_forward(q, k, v, cu_seqlens, scale)
-        ctx.save_for_backward(q, k, v, out, lse, cu_seqlens, err)
-        ctx.scale = scale
+    def forward(ctx, q, k, v, cu_seqlens, scale, err):
+        out, lse, err = flce_attention_forward(q, k, v, cu_seqlens, scale, err_word=err)
+        ctx.save_for_backward(q, k, v, out, lse, cu_seqlens)
+        # err is not saved: the caller may read and clear it before the backward
+        ctx.cfg = (scale, err)
         return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, g):
-        q, k, v, out, lse, cu_seqlens, err = ctx.saved_tensors
+        q, k, v, out, lse, cu_seqlens = ctx.saved_tensors
+        scale, err = ctx.cfg
         dq, dk, dv, _ = flce_attention_backward(g.contiguous(), q, k, v, out, lse, cu_seqlens,
-                                                ctx.scale, err_word=err)
-        return dq, dk, dv, None, None
+                                                scale, err_word=err)
+        return dq, dk, dv, None, None, None
 
 
-def packed_attention(q, k, v, cu_seqlens, scale: Optional[float] = None):
-    """Autograd entry of flce_attention_forward: out [T, Hq, D]."""
-    return _PackedAttention.apply(q, k, v, cu_seqlens, scale)
+def packed_attention(q, k, v, cu_seqlens, scale: Optional[float] = None, *, err_word=None):
+    """Autograd entry of flce_attention_forward: out [T, Hq, D].  The forward and the
+    backward report into err_word; without one what goes wrong on the device is not seen."""
+    return _PackedAttention.apply(q, k, v, cu_seqlens, scale, err_word)
