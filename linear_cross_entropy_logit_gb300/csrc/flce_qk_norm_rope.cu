@@ -75,8 +75,8 @@ flce_status check(const flce_qk_norm_rope_desc* d, const void* const* ptrs, int 
   if (d->rot_dim > 0) {
     if (!cos_t || !sin_t || !aligned(cos_t, 16) || !aligned(sin_t, 16) || d->table_rows <= 0)
       return FLCE_ERR_ARG;
-    if (!aligned(positions, 8)) return FLCE_ERR_ARG;
   }
+  if (!aligned(positions, 8)) return FLCE_ERR_ARG;
   if (d->tokens == 0) return FLCE_OK;
   for (int i = 0; i < n; ++i)
     if (!ptrs[i] || !aligned(ptrs[i], 16)) return FLCE_ERR_ARG;
