@@ -586,7 +586,7 @@ struct DkvShared {
   uint64_t ufull[2], uempty[2];
   uint64_t mma_done;
   AttnUnit unit[2];
-  uint32_t flags[4][2][4];
+  uint32_t flags[4][4];  // by cleaning warp: non-finite rows of the tile it is at
   uint32_t dirty[2][4];  // by unit parity and cleaning warp: non-finite dout on the diagonal
   uint32_t tmem;
   int abort;
@@ -982,10 +982,11 @@ attn_dkdv(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtens
             const int valid = u.len - i * kTile;
             if (!(ok = wait_bar_warp(&sh.qfull[qs], (step / C::kQ) & 1, ctx))) break;
             if (valid < kTile) repeat_row(q, C::kBoxes, valid, w, 4);
-            if (i == first) clean_tile(q, C::kBoxes, kTile, w, 4, sh.flags[w][0]);
+            // a query that is not finite has no finite lse: nothing to add back
+            if (i == first) clean_tile(q, C::kBoxes, kTile, w, 4, sh.flags[w]);
             if (!(ok = wait_bar_warp(&sh.gfull[gs], (step / C::kG) & 1, ctx))) break;
             if (i == first) {
-              uint32_t* fl = sh.flags[w][1];
+              uint32_t* fl = sh.flags[w];
               clean_tile(g, C::kBoxes, valid, w, 4, fl);
               __syncwarp();
               if (lane == 0 && (fl[0] | fl[1] | fl[2] | fl[3])) sh.dirty[it & 1][w] = 1;

@@ -104,16 +104,16 @@ flce_status set_smem(Setup& s, Kern kern, int smem) {
 }
 
 // CTAs that share the query heads of one key / value head in attn_dkdv, each
-// summing its own (a divisor of their number): the fewest that give every SM a unit.
+// summing its own (a divisor of their number): the fewest that give every SM a unit, counted
+// as if the tokens filled whole tiles (short sequences have more units than that).
 // Without (backward, us): 8192 tokens, 8 / 1 heads of 128 792, with 329; 2048 tokens,
 // 32 / 8 heads 152, with 123.  More splits cost the partial sums' traffic: 2 units a
 // SM 135, 8192 tokens, 32 / 8 heads 1170 unsplit and 1297 fully split.
-constexpr int64_t kDealt = 1;
 int choose_splits(const flce_attention_desc* d, int sms) {
   const int group = (int)(d->q_heads / d->kv_heads);
   const int64_t units = std::max<int64_t>(1, d->tokens / kTile) * d->kv_heads;
   for (int s = 1; s < group; ++s)
-    if (group % s == 0 && units * s >= kDealt * sms) return s;
+    if (group % s == 0 && units * s >= sms) return s;
   return group;
 }
 

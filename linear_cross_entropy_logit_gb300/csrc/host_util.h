@@ -61,11 +61,6 @@ flce_status launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cu
 }  // namespace host
 }  // namespace flce
 
-#define FLCE_HOST_CUDA(call)                                          \
-  do {                                                                \
-    cudaError_t e_ = (call);                                          \
-    if (e_ != cudaSuccess) return ::flce::host::fail(e_, #call);      \
-  } while (0)
 #define FLCE_HOST_TRY(expr)              \
   do {                                   \
     flce_status s_ = (expr);             \
