@@ -129,9 +129,10 @@ __global__ void __launch_bounds__(DP == 128 ? 256 : 128) attn_delta(const AttnBw
     if (lane == i) delta = sum;
   }
   if (mine) {
-    // A row whose scores are all -infinity has no softmax: NaN, not the +infinity that would make
-    // p infinite where the score is made of a cleaned query.
-    p.nlse[at] = lse == -INFINITY ? __int_as_float(0x7fffffff) : -lse * kLog2e;
+    // A row whose scores are all -infinity has no softmax: + nl 0 makes its +infinity NaN, which
+    // would make p infinite where the score is made of a cleaned query.
+    const float nl = -lse * kLog2e;
+    p.nlse[at] = fmaf(nl, 0.f, nl);
     p.delta[at] = delta;
   }
 }
