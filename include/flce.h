@@ -385,9 +385,11 @@ flce_status flce_qk_norm_rope_backward(const flce_qk_norm_rope_desc* desc, const
  * [cu_seqlens[0], cu_seqlens[sequences]) belong to none: their out is 0, their
  * lse -infinity, their gradients 0, and what they hold is not used.  Offsets
  * that do not ascend are reported as FLCE_ERR_INDEX and every row then counts
- * as belonging to none.  Finite values whose scores are finite in float give a
- * finite out in sequences of up to 65536 tokens; longer ones for |v| up to
- * 2^144 / tokens. */
+ * as belonging to none.  Scores are float: their rounding, 2^-24 of their size,
+ * is the weights' relative error.  With scores of up to 2^24 in size, finite
+ * values give a finite out in sequences of up to 65536 tokens, and in longer
+ * ones for |v| up to 2^144 / tokens.  What is not finite reaches the rows and
+ * gradients that it enters by the formulas, masked places never. */
 typedef struct {
   size_t struct_size;            /* sizeof(flce_attention_desc) */
   int64_t tokens, sequences;

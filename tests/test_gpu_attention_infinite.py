@@ -125,3 +125,24 @@ def test_a_query_without_softmax_reaches_the_keys_it_sees(at, D):
     assert torch.isnan(dq[at]).all()
     for t in (dk, dv):
         assert torch.isnan(t[:at + 1]).all() and torch.isfinite(t[at + 1:]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_far_from_zero(sign, D):
+    """Scores of 2^24 in size and one step nearer to zero (both exact in fp32): every row, the first
+    as well, has a finite softmax."""
+    import torch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    q, k, v, _ = make(300, 2, 1, D, seed=23)
+    q, k = q * 0, k * 0
+    q[:, :, 0], q[:, :, 1] = 4096, 1
+    k[:, :, 0] = 4096 * sign
+    k[::3, :, 1] = -sign
+    cu = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
+    out, lse, err = B.flce_attention_forward(q, k, v, cu, 1.0)
+    want, want_lse = A.attention_forward(*(tensor_f64(t) for t in (q, k, v)), [0, 300], 1.0)
+    assert int(err.item()) == 0
+    # a score times log2 e is rounded in fp32 once (the fused multiply-add's own result is small)
+    close(out, want, OUT, "out")
+    assert np.abs(tensor_f64(lse) - want_lse).max() <= 2.0**-22 * 2.0**24
