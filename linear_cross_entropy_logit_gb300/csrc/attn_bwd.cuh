@@ -10,10 +10,10 @@
 // TMEM of the CTA that owns its rows: no fp32 gradient goes through memory, no
 // atomics, the same bits every run.  Seven products where one kernel for all
 // three gradients would take five, but that one has to add dq up in memory
-// across CTAs.  At 8192 tokens, 32 / 8 heads of 128: delta 22 us, dq 492 us and dkdv 640 us,
-// the two at 1670 and 1720 TFLOP/s of their three and four products over the visible
-// pairs: bound by the tensor cores.  61 ragged sequences of 9999 tokens, 16 heads of 64:
-// 10, 48 and 66 us, bound by each unit's latency.
+// across CTAs.  At 8192 tokens, 32 / 8 heads of 128, each launch by itself: delta 25 us, dq
+// 498 us and dkdv 643 us, the two at 1660 and 1710 TFLOP/s of their three and four products
+// over the visible pairs: bound by the tensor cores.  61 ragged sequences of 9999 tokens, 16
+// heads of 64: 11, 50 and 67 us, bound by each unit's latency.
 //
 // Both: warps 0-7 compute (a thread owns one TMEM lane and 64 of the 128
 // columns), warp 8 issues MMAs, warp 9 maps units and loads, warps 12-15 clean
@@ -79,8 +79,8 @@ __device__ __forceinline__ void zero_first(uint32_t (&v)[2][32]) {
 // ----------------------------------------------------------------------------
 // delta
 // ----------------------------------------------------------------------------
-// Bound by reading out and dout once: 136 MB in 22 us at 8192 tokens, 32 heads of 128
-// (6.1 TB/s).  Eight lanes hold a row, 8 or 16 values each, and eight or four rows: 16
+// Bound by reading out and dout once: 136 MB in 22 to 25 us at 8192 tokens, 32 heads of 128
+// (5.4 to 6.1 TB/s).  Eight lanes hold a row, 8 or 16 values each, and eight or four rows: 16
 // loads in flight a lane.  Blocks of all heads of the same tokens run together (one head's
 // tokens after another's: 27 us).  A kernel of its own rather than attn_dq's work:
 // there its loads stood before every unit, 3-4 us each (145 us against 10 + 48 for 61 ragged

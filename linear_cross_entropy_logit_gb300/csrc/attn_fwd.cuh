@@ -34,13 +34,13 @@
 // 1, values above 5e33 did); l carries the same factor.  l is fp32; P is rounded to bf16
 // (the type of V, at most 2^-8 of it), and l sums it before that rounding.
 //
-// What bounds it.  Heads of 128: a tile's chain of S, softmax, P V and the next S, as TMEM
-// holds one S and one O a tile (all 512 columns): 341 us at 8192 tokens, 32 / 8 heads, 1612
-// TFLOP/s of the visible pairs, tensor pipe 67% active.  Heads of 64: the softmax,
-// with half the products to hide it behind: 954 us at 32768 tokens, 8 / 2 heads, 1153
-// TFLOP/s.  Short sequences: each unit's latency of some 6000 cycles and the empty
-// part of its tiles: 136 us for 37 ragged sequences of 16384 tokens, 28 / 4 heads of
-// 128, 621 TFLOP/s.  Tried and slower: a third or fourth softmax warpgroup, the
+// What bounds it (times of calls one after the other).  Heads of 128: a tile's chain of S,
+// softmax, P V and the next S, as TMEM holds one S and one O a tile (all 512 columns): 361 us
+// at 8192 tokens, 32 / 8 heads, 1520 TFLOP/s of the visible pairs, tensor pipe 67% active
+// (a launch by itself takes 339 to 348).  Heads of 64: the same chain with half the products
+// in it, no pipe above 50%: 953 us at 32768 tokens, 8 / 2 heads, 1154 TFLOP/s.  Short
+// sequences: each unit's latency of some 6000 cycles and the empty part of its tiles: 136 us
+// for 37 ragged sequences of 16384 tokens, 28 / 4 heads of 128, 620 TFLOP/s.  Tried and slower: a third or fourth softmax warpgroup, the
 // epilogue in warps of its own, S ahead of P in more buffers, two issuing warps.
 #pragma once
 #include "attn_common.cuh"
