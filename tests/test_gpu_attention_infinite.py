@@ -146,3 +146,51 @@ def test_scores_far_from_zero(sign, D):
     # a score times log2 e is rounded in fp32 once (the fused multiply-add's own result is small)
     close(out, want, OUT, "out")
     assert np.abs(tensor_f64(lse) - want_lse).max() <= 2.0**-22 * 2.0**24
+
+
+def by_pairs(q, k, v, g, cu, scale):
+    """(out, dq, dk, dv) in 64 bits from the visible pairs alone, row by row: a masked pair is not
+    even multiplied by zero."""
+    group = q.shape[1] // k.shape[1]
+    out, dq, dk, dv = (np.zeros_like(t) for t in (q, q, k, v))
+    for lo, hi in zip(cu, cu[1:]):
+        for h in range(q.shape[1]):
+            kh = h // group
+            for i in range(lo, hi):
+                seen = slice(lo, i + 1)
+                s = scale * (k[seen, kh] @ q[i, h])
+                e = np.exp(s - s.max())
+                p = e / e.sum()
+                dp = v[seen, kh] @ g[i, h]
+                ds = p * (dp - (p * dp).sum())
+                out[i, h] = p @ v[seen, kh]
+                dq[i, h] = scale * (ds @ k[seen, kh])
+                dk[seen, kh] += scale * np.outer(ds, q[i, h])
+                dv[seen, kh] += np.outer(p, g[i, h])
+    return out, dq, dk, dv
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_places_that_are_not_finite(seed):
+    """Infinities and NaN anywhere in one of q, k, v and dout: the results are finite exactly where
+    the formulas' are, and right there."""
+    rng = np.random.default_rng(seed)
+    D, HK = int(rng.choice([8, 64, 72, 128])), int(rng.choice([1, 2]))
+    HQ = HK * int(rng.choice([1, 2, 3]))
+    cu = np.cumsum([0, *rng.choice([1, 5, 64, 100, 128, 129, 200, 257], int(rng.integers(1, 4)))]).tolist()
+    x = list(make(cu[-1], HQ, HK, D, seed=seed))
+    if rng.integers(2):  # infinite keys then have scores of one sign
+        x[0] = x[0].abs()
+    t = x[seed % 4]
+    for _ in range(int(rng.integers(1, 4))):
+        t[tuple(int(rng.integers(n)) for n in t.shape)] = float(rng.choice([np.inf, -np.inf, -np.inf, np.nan]))
+    out, _, dq, dk, dv, err = run(*x, cu)
+    assert err == 0
+    with np.errstate(all="ignore"):
+        want = by_pairs(*(tensor_f64(t) for t in x), cu, D ** -0.5)
+    for name, a, b, bound in zip(("out", "dq", "dk", "dv"), (out, dq, dk, dv), want, (OUT, GRAD, GRAD, GRAD)):
+        a, live = tensor_f64(a), np.isfinite(b)
+        assert (np.isfinite(a) == live).all(), name
+        # short sequences alone have next to no gradient of q and k: what is left is rounding of dout's size
+        size = max(np.linalg.norm(b[live]), 0.1)
+        assert np.linalg.norm(a[live] - b[live]) <= bound * size, name
