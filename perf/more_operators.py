@@ -140,13 +140,13 @@ def prepare_distill(s, c, gen):
     order = rand(N, K).argsort(-1)
     ids = token_of[rank.gather(1, order)]
     t = (12.0 - 1.5 * torch.log1p(torch.arange(K, device="cuda")) + 0.5 * randn(N, K)).sort(-1, descending=True).values
-    # hidden states of a student that has learned part of it: its logits at the teacher's first
-    # token are about 9, at the second about 6; the others have a spread of 0.02 sqrt(H)
+    # hidden states of a student early in its training: its logits at the teacher's first token
+    # are about 6, at the second about 4; the others have a spread of 0.02 sqrt(H)
     X = randn(N, H)
     X /= X.square().mean(-1, keepdim=True).sqrt()
-    X.addcmul_(W[ids[:, 0]].float(), torch.tensor(9.0 / (0.0004 * H), device="cuda"))
+    X.addcmul_(W[ids[:, 0]].float(), torch.tensor(6.0 / (0.0004 * H), device="cuda"))
     if K > 1:
-        X.addcmul_(W[ids[:, 1]].float(), torch.tensor(6.0 / (0.0004 * H), device="cuda"))
+        X.addcmul_(W[ids[:, 1]].float(), torch.tensor(4.0 / (0.0004 * H), device="cuda"))
     # prompt tokens have no entries, some rows fewer than K
     if c["short"]:
         ids.masked_fill_(torch.arange(K, device="cuda") >= (K * (0.3 + rand(N, 1))).ceil().clamp_(max=K), -1)
