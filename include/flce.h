@@ -416,14 +416,76 @@ flce_status flce_attention_backward(const flce_attention_desc* desc, const void*
                                     void* dk, void* dv, void* workspace, size_t ws_bytes,
                                     int32_t* err_word, void* stream);
 
+/* Layer norm of rows, or RMS norm, with the residual sum in front of it:
+ *   s = x + residual, rounded to dtype and stored (x itself without a residual),
+ *   n = (s - mu) / sqrt(mean((s - mu)^2) + eps), mu = mean(s), or 0 for rms,
+ *   y = weight * n + bias
+ * No error word: nothing that the inputs hold is an error. */
+typedef struct {
+  size_t struct_size;            /* sizeof(flce_layer_norm_desc) */
+  int64_t rows;
+  int64_t cols;                  /* a multiple of 8, at most 16384 */
+  flce_dtype dtype;              /* of x, residual, weight, bias, y and sum */
+  float eps;
+  int rms;                       /* 1: no mean is taken off */
+  int64_t x_row, residual_row;   /* strides of their rows in elements, multiples of 8, at least cols */
+} flce_layer_norm_desc;
+
+/* y and sum are contiguous; sum is written if a residual is given, and may then be x
+ * or residual itself where that is contiguous.  A weight of NULL counts as ones, a
+ * bias of NULL as zeros.  mean (not for rms) and rstd: float, rows, for the backward. */
+flce_status flce_layer_norm_forward(const flce_layer_norm_desc* desc, const void* x, const void* residual,
+                                    const void* weight, const void* bias, void* y, void* sum, float* mean,
+                                    float* rstd, void* stream);
+
+/* Gradients of the sum (and so of x and of residual; contiguous, dtype), of the weight
+ * and, unless dbias is NULL, of the bias (float, cols, summed over the rows in a fixed
+ * order; zero when rows = 0).  x is the sum that was normed, with desc's x_row; dy and
+ * dsum are contiguous; dsum, a gradient that reached the stored sum by itself, is added
+ * to dx and may be NULL.  dx may be dy or dsum.  workspace: 256-byte aligned,
+ * flce_layer_norm_workspace_size bytes (0 on an invalid desc), sized for the current
+ * device. */
+size_t flce_layer_norm_workspace_size(const flce_layer_norm_desc* desc);
+flce_status flce_layer_norm_backward(const flce_layer_norm_desc* desc, const void* dy, const void* x,
+                                     const void* weight, const float* mean, const float* rstd, const void* dsum,
+                                     void* dx, float* dweight, float* dbias, void* workspace, size_t ws_bytes,
+                                     void* stream);
+
+/* Rotary positions of query and key heads, without a norm:
+ *   y = magnitude * R(position) x  on the first rot_dim values of a head,
+ * the others as they are.  R turns pair j, (j, j + rot_dim/2) or (2j, 2j + 1) when
+ * interleaved, by position * inv_freq[j] (device double, rot_dim/2): any frequencies,
+ * so also those of a context scaled past the trained length.  The angle is taken modulo
+ * one turn in 64-bit integers: any position, a negative one too, is as exact as 0. */
+typedef struct {
+  size_t struct_size;            /* sizeof(flce_rope_desc) */
+  int64_t tokens, q_heads, kv_heads;
+  int64_t head_dim;              /* a multiple of 8, at most 256 */
+  int64_t rot_dim;               /* a multiple of 8, 8 to head_dim */
+  flce_dtype dtype;
+  float magnitude;               /* 1, or what a scaling puts on cosine and sine */
+  int interleaved;
+  int64_t q_row, q_head, k_row, k_head;  /* strides of the inputs in elements */
+} flce_rope_desc;
+
+/* q_out and k_out are contiguous (tokens x heads x head_dim), and may be q and k
+ * themselves where those are.  positions (int64, one per token) of NULL count as
+ * 0, 1, 2... */
+flce_status flce_rope_forward(const flce_rope_desc* desc, const void* q, const void* k, const double* inv_freq,
+                              const int64_t* positions, void* q_out, void* k_out, void* stream);
+
+/* Gradients of q and k (contiguous) from those of the outputs, whose strides desc holds. */
+flce_status flce_rope_backward(const flce_rope_desc* desc, const void* dq_out, const void* dk_out,
+                               const double* inv_freq, const int64_t* positions, void* dq, void* dk, void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* flce_status_string(flce_status s);
 
 /* Text of the last CUDA error this thread saw inside the library ("" if none). */
 const char* flce_last_cuda_error(void);
 
-/* Number of kernels the last forward or backward call on this thread (of the
- * loss, the attention or the head norm) enqueued. */
+/* Number of kernels the last forward or backward call on this thread (of any of
+ * the operators above) enqueued. */
 int flce_last_launch_count(void);
 
 /* Optional per-kernel timing.  While enabled (per host thread), every GEMM

@@ -7,6 +7,7 @@ library is missing, ``lib()`` raises instead of falling back to anything.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -49,6 +50,8 @@ EXPORTED = (
     "flce_cluster_multicast", "flce_debug_last_multicast_launches",
     "flce_qk_norm_rope_forward", "flce_qk_norm_rope_workspace_size", "flce_qk_norm_rope_backward",
     "flce_attention_forward", "flce_attention_workspace_size", "flce_attention_backward",
+    "flce_layer_norm_forward", "flce_layer_norm_workspace_size", "flce_layer_norm_backward",
+    "flce_rope_forward", "flce_rope_backward",
 )
 
 PROFILE_KINDS = ("fwd_logits_lse", "bwd_dz_recompute", "bwd_dw_gemm", "bwd_dx_gemm",
@@ -90,6 +93,27 @@ class FlceAttentionDesc(ctypes.Structure):
                 ("v_row", ctypes.c_int64), ("v_head", ctypes.c_int64)]
 
 
+class FlceLayerNormDesc(ctypes.Structure):
+    """Mirror of ``flce_layer_norm_desc`` in include/flce.h."""
+    _fields_ = [("struct_size", ctypes.c_size_t), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("rms", ctypes.c_int), ("x_row", ctypes.c_int64),
+                ("residual_row", ctypes.c_int64)]
+
+
+class FlceRopeDesc(ctypes.Structure):
+    """Mirror of ``flce_rope_desc`` in include/flce.h."""
+    _fields_ = [("struct_size", ctypes.c_size_t), ("tokens", ctypes.c_int64),
+                ("q_heads", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("rot_dim", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("magnitude", ctypes.c_float),
+                ("interleaved", ctypes.c_int), ("q_row", ctypes.c_int64),
+                ("q_head", ctypes.c_int64), ("k_row", ctypes.c_int64),
+                ("k_head", ctypes.c_int64)]
+
+
+_LAYER_NORM_DESC_BYTES = ctypes.sizeof(FlceLayerNormDesc)
+_ROPE_DESC_BYTES = ctypes.sizeof(FlceRopeDesc)
 _QK_DESC_BYTES = ctypes.sizeof(FlceQkNormRopeDesc)
 _ATTENTION_DESC_BYTES = ctypes.sizeof(FlceAttentionDesc)
 
@@ -218,6 +242,17 @@ def load(path: str) -> ctypes.CDLL:
     L.flce_attention_workspace_size.restype = SZ
     L.flce_attention_backward.argtypes = [AD, P, P, P, P, P, P, P, P, P, P, P, SZ, P, P]
     L.flce_attention_backward.restype = I32
+    ND, RD = ctypes.POINTER(FlceLayerNormDesc), ctypes.POINTER(FlceRopeDesc)
+    L.flce_layer_norm_forward.argtypes = [ND, P, P, P, P, P, P, P, P, P]
+    L.flce_layer_norm_forward.restype = I32
+    L.flce_layer_norm_workspace_size.argtypes = [ND]
+    L.flce_layer_norm_workspace_size.restype = SZ
+    L.flce_layer_norm_backward.argtypes = [ND, P, P, P, P, P, P, P, P, P, P, SZ, P]
+    L.flce_layer_norm_backward.restype = I32
+    L.flce_rope_forward.argtypes = [RD, P, P, P, P, P, P, P]
+    L.flce_rope_forward.restype = I32
+    L.flce_rope_backward.argtypes = [RD, P, P, P, P, P, P, P]
+    L.flce_rope_backward.restype = I32
     return L
 
 
@@ -845,6 +880,180 @@ def flce_attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale: Optional
     return dq, dk, dv, err_word
 
 
+def _cuda_rows(name, x) -> int:
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor, got one on {x.device}")
+    _check_device(name, x)
+    return dev
+
+
+def _rows(name, t, shape, dtype, dev):
+    """The row stride of a [rows, cols] tensor whose rows are contiguous."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} tensor {tuple(shape)} on cuda:{dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.stride(1) != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: the values of a row must be contiguous")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _layer_norm_args(x, weight, eps, rms):
+    """(desc, device, shape, dtype, the weight's address)."""
+    dev, dtype = _cuda_rows("x", x), x.dtype
+    if x.dim() != 2:
+        raise ValueError(f"x must be [rows, cols], got {tuple(x.shape)}")
+    shape = x.shape
+    row = _rows("x", x, shape, dtype, dev)
+    w = None if weight is None else _array("weight", weight, (shape[1],), dtype, dev)
+    d = FlceLayerNormDesc(_LAYER_NORM_DESC_BYTES, shape[0], shape[1], _dtype_code(x, "x"), eps,
+                          1 if rms else 0, row, shape[1])
+    return d, dev, shape, dtype, w
+
+
+def flce_layer_norm_forward(x, weight, bias=None, eps: float = 1e-5, *, residual=None,
+                            rms: bool = False, out=None, sum_out=None, mean=None, rstd=None,
+                            stream=None):
+    """Layer norm (or RMS norm) of the rows of x [rows, cols], or of x + residual.
+    Returns (y, sum, mean, rstd): sum is x + residual as it was normed, or x itself
+    without a residual; mean is None for rms.  The backward takes the last three."""
+    if stream is not None:
+        return _with_stream(stream, flce_layer_norm_forward, x, weight, bias, eps,
+                            residual=residual, rms=rms, out=out, sum_out=sum_out, mean=mean,
+                            rstd=rstd)
+    d, dev, shape, dtype, w = _layer_norm_args(x, weight, eps, rms)
+    b = None if bias is None else _array("bias", bias, (shape[1],), dtype, dev)
+    p_res = p_sum = p_mean = None
+    if residual is not None:
+        d.residual_row = _rows("residual", residual, shape, dtype, dev)
+        p_res = residual.data_ptr()
+        sum_out, p_sum = _output("sum_out", sum_out, x, shape, dtype, dev)
+    f32, rows = torch.float32, shape[:1]
+    out, p_out = _output("out", out, x, shape, dtype, dev)
+    if not rms:
+        mean, p_mean = _output("mean", mean, x, rows, f32, dev)
+    rstd, p_rstd = _output("rstd", rstd, x, rows, f32, dev)
+    st = lib().flce_layer_norm_forward(d, x.data_ptr(), p_res, w, b, p_out, p_sum, p_mean, p_rstd,
+                                       _current_stream(dev))
+    if st:
+        _check(st, "flce_layer_norm_forward")
+    return out, x if residual is None else sum_out, None if rms else mean, rstd
+
+
+def flce_layer_norm_backward(dy, x, weight, mean, rstd, *, dsum=None, rms: bool = False,
+                             bias: bool = True, dx=None, dweight=None, dbias=None,
+                             workspace_buf=None, stream=None):
+    """Gradients of flce_layer_norm_forward, whose sum is x here: (dx in x's dtype, of the
+    sum and so of x and residual alike; dweight, dbias float32 [cols]).  dsum, the gradient
+    that reached the stored sum itself, is added to dx.  dbias is None if not bias."""
+    if stream is not None:
+        return _with_stream(stream, flce_layer_norm_backward, dy, x, weight, mean, rstd, dsum=dsum,
+                            rms=rms, bias=bias, dx=dx, dweight=dweight, dbias=dbias,
+                            workspace_buf=workspace_buf)
+    d, dev, shape, dtype, w = _layer_norm_args(x, weight, 0.0, rms)
+    f32, rows, cols = torch.float32, shape[:1], shape[1:]
+    p_db = None
+    dx, p_dx = _output("dx", dx, x, shape, dtype, dev)
+    dweight, p_dw = _output("dweight", dweight, x, cols, f32, dev)
+    if bias:
+        dbias, p_db = _output("dbias", dbias, x, cols, f32, dev)
+    L = lib()
+    need = L.flce_layer_norm_workspace_size(d) if workspace_buf is None else 0
+    ws, p_ws, ws_bytes = _scratch(workspace_buf, need, x, dev)
+    st = L.flce_layer_norm_backward(
+        d, _array("dy", dy, shape, dtype, dev), x.data_ptr(), w,
+        None if rms else _array("mean", mean, rows, f32, dev), _array("rstd", rstd, rows, f32, dev),
+        None if dsum is None else _array("dsum", dsum, shape, dtype, dev), p_dx, p_dw, p_db, p_ws,
+        ws_bytes, _current_stream(dev))
+    if st:
+        _check(st, "flce_layer_norm_backward")
+    return dx, dweight, dbias if bias else None
+
+
+def rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: str = "none", *,
+                     factor: float = 1.0, trained_length: int = 8192, low: float = 1.0,
+                     high: Optional[float] = None, device="cuda"):
+    """(inv_freq float64 [rot_dim / 2], magnitude) for ``rope``: theta^(-2j / rot_dim), for
+    contexts of factor times the trained length changed by ``scaling``:
+
+      "linear"  every frequency divided by factor
+      "ntk"     theta grown so that the lowest frequency is divided by factor
+      "llama3"  frequencies with fewer than ``low`` turns in the trained length divided by
+                factor, those with more than ``high`` (4) kept, linear in turns between
+      "yarn"    the same, with ``high`` 32 and linear in the index between, and magnitude
+                1 + 0.1 ln(factor)"""
+    if rot_dim <= 0 or rot_dim % 2 or not theta > 1.0 or not factor >= 1.0:
+        raise ValueError(f"rot_dim must be even, theta above 1 and factor at least 1: got {rot_dim}, {theta}, {factor}")
+    half, magnitude = rot_dim // 2, 1.0
+    if scaling == "ntk" and half > 1:
+        theta *= factor ** (half / (half - 1.0))
+    j = torch.arange(half, dtype=torch.float64)
+    inv = theta ** (-j / half)
+    if scaling == "linear":
+        inv = inv / factor
+    elif scaling in ("llama3", "yarn"):
+        high = (4.0 if scaling == "llama3" else 32.0) if high is None else high
+        if not 0.0 < low < high:
+            raise ValueError(f"0 < low < high is needed, got {low}, {high}")
+        if scaling == "llama3":
+            kept = (trained_length * inv / (2.0 * math.pi) - low) / (high - low)
+        else:
+            def index_of(turns):
+                return half * math.log(trained_length / (2.0 * math.pi * turns)) / math.log(theta)
+
+            first = max(math.floor(index_of(high)), 0)
+            last = min(math.ceil(index_of(low)), rot_dim - 1)
+            kept = 1.0 - (j - first) / max(last - first, 1e-3)
+            magnitude = 1.0 + 0.1 * math.log(factor)
+        kept = kept.clamp(0.0, 1.0)
+        inv = inv * kept + inv / factor * (1.0 - kept)
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f"scaling must be none, linear, ntk, llama3 or yarn, got {scaling!r}")
+    return inv.to(device), magnitude
+
+
+def _rope(name, backward, q, k, inv_freq, positions, magnitude, interleaved, q_out, k_out):
+    dev, dtype = _cuda_device(q), q.dtype
+    T, HQ, D, q_row, q_head = _heads("q", q, dtype, dev)
+    Tk, HK, Dk, k_row, k_head = _heads("k", k, dtype, dev)
+    if Tk != T or Dk != D:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}")
+    p_f = _array("inv_freq", inv_freq, inv_freq.shape[:1], torch.float64, dev)
+    p_p = None if positions is None else _array("positions", positions, (T,), torch.int64, dev)
+    d = FlceRopeDesc(_ROPE_DESC_BYTES, T, HQ, HK, D, 2 * inv_freq.numel(), _dtype_code(q, "q and k"), magnitude,
+                     1 if interleaved else 0, q_row, q_head, k_row, k_head)
+    q_out, p_q = _output("q_out", q_out, q, q.shape, dtype, dev)
+    k_out, p_k = _output("k_out", k_out, q, k.shape, dtype, dev)
+    L = lib()
+    st = (L.flce_rope_backward if backward else L.flce_rope_forward)(
+        d, q.data_ptr(), k.data_ptr(), p_f, p_p, p_q, p_k, _current_stream(dev))
+    if st:
+        _check(st, name)
+    return q_out, k_out
+
+
+def flce_rope_forward(q, k, inv_freq, positions=None, *, magnitude: float = 1.0,
+                      interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary positions of q [T, Hq, D] and k [T, Hk, D] (views are fine): the first
+    2 * len(inv_freq) values of each head turned by positions * inv_freq and multiplied by
+    magnitude, in pairs (j, j + rot_dim / 2), or (2j, 2j + 1) when interleaved.  Returns
+    (q_out, k_out), contiguous.  inv_freq: float64, any (see rope_frequencies); positions:
+    int64 [T] or None (0, 1, 2, ...), any."""
+    if stream is not None:
+        return _with_stream(stream, flce_rope_forward, q, k, inv_freq, positions, magnitude=magnitude,
+                            interleaved=interleaved, q_out=q_out, k_out=k_out)
+    return _rope("flce_rope_forward", False, q, k, inv_freq, positions, magnitude, interleaved, q_out, k_out)
+
+
+def flce_rope_backward(dq_out, dk_out, inv_freq, positions=None, *, magnitude: float = 1.0,
+                       interleaved: bool = False, dq=None, dk=None, stream=None):
+    """Gradients (dq, dk) of flce_rope_forward: the heads turned back."""
+    if stream is not None:
+        return _with_stream(stream, flce_rope_backward, dq_out, dk_out, inv_freq, positions,
+                            magnitude=magnitude, interleaved=interleaved, dq=dq, dk=dk)
+    return _rope("flce_rope_backward", True, dq_out, dk_out, inv_freq, positions, magnitude, interleaved, dq, dk)
+
+
 def last_launch_count() -> int:
     return int(lib().flce_last_launch_count())
 
@@ -953,3 +1162,65 @@ def packed_attention(q, k, v, cu_seqlens, scale: Optional[float] = None, *, err_
     """Autograd entry of flce_attention_forward: out [T, Hq, D].  The forward and the
     backward report into err_word; without one what goes wrong on the device is not seen."""
     return _PackedAttention.apply(q, k, v, cu_seqlens, scale, err_word)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, bias, eps, rms):
+        y, s, mean, rstd = flce_layer_norm_forward(x, weight, bias, eps, residual=residual, rms=rms)
+        ctx.save_for_backward(s, weight, mean, rstd)
+        ctx.cfg = (residual is not None, None if bias is None else bias.dtype, rms)
+        ctx.set_materialize_grads(False)
+        return y if residual is None else (y, s)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, ds=None):
+        s, weight, mean, rstd = ctx.saved_tensors
+        summed, bias_dtype, rms = ctx.cfg
+        dx = dw = db = None
+        if dy is None:  # only the sum was used
+            dx = ds
+        else:
+            dx, dw, db = flce_layer_norm_backward(dy.contiguous(), s, weight, mean, rstd,
+                                                  dsum=None if ds is None else ds.contiguous(), rms=rms,
+                                                  bias=bias_dtype is not None)
+        return (dx, dx if summed else None, None if weight is None or dw is None else dw.to(weight.dtype),
+                None if db is None else db.to(bias_dtype), None, None)
+
+
+def layer_norm(x, weight, bias=None, eps: float = 1e-5, *, residual=None, rms: bool = False):
+    """Autograd entry of flce_layer_norm_forward for x [..., cols]: y, or with a residual
+    (y, x + residual)."""
+    shape = x.shape
+    rows = x.reshape(-1, shape[-1])
+    if residual is None:
+        return _LayerNorm.apply(rows, None, weight, bias, eps, rms).view(shape)
+    y, s = _LayerNorm.apply(rows, residual.reshape(-1, shape[-1]), weight, bias, eps, rms)
+    return y.view(shape), s.view(shape)
+
+
+class _Rope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, inv_freq, positions, magnitude, interleaved):
+        ctx.save_for_backward(inv_freq, positions)
+        ctx.cfg = {"magnitude": magnitude, "interleaved": interleaved}
+        return flce_rope_forward(q, k, inv_freq, positions, **ctx.cfg)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gq, gk):
+        inv_freq, positions = ctx.saved_tensors
+        return (*flce_rope_backward(_dense_heads(gq), _dense_heads(gk), inv_freq, positions, **ctx.cfg),
+                None, None, None, None)
+
+
+def _dense_heads(g):
+    """g, or a contiguous copy where its strides are not those of heads (a broadcast gradient)."""
+    row, head, one = g.stride()
+    return g if one == 1 and head >= g.shape[2] and row % 8 == 0 and head % 8 == 0 and row > 0 else g.contiguous()
+
+
+def rope(q, k, inv_freq, positions=None, *, magnitude: float = 1.0, interleaved: bool = False):
+    """Autograd entry of flce_rope_forward: (q_out, k_out)."""
+    return _Rope.apply(q, k, inv_freq, positions, magnitude, interleaved)
