@@ -324,6 +324,54 @@ flce_status flce_backward_vocab_shard(const void* X, const void* W_shard, const 
                                       size_t ws_bytes, int32_t* err_word, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Linear distillation from a teacher's top logits: the student's Z = X W^T as
+ * above, never stored, at a temperature T; the teacher's K entries of each token,
+ * ids and logits t.
+ *   q_ik = exp(t_ik / T - tl_i),  tl_i = log sum_k exp(t_ik / T) over the entries, or
+ *          teacher_lse[i], the teacher's over its whole vocabulary (at T)
+ *   l_i  = sum_k q_ik (log q_ik - log p_i,id_ik),  p = softmax(z / T) over all V
+ *   loss = sum_i l_i / N_valid (mean) or sum_i l_i (sum)
+ *   dZ_ij = c / T (p_ij sum_k q_ik - sum of q_ik with id_ik = j)
+ * A negative id, or a logit of -infinity, is no entry; entries of the same id add up.
+ * A token without entries does not count (a prompt's, padding): no loss, zero dX, not in
+ * N_valid; nor does one with an id of V or more, which is reported as FLCE_ERR_LABEL.
+ * The hidden states of tokens that do not count must be finite all the same (0 times
+ * infinity is NaN in dW, as it is in linear cross-entropy).  The loss is not multiplied
+ * by T^2.  Results do not change from run to run.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  size_t struct_size;        /* sizeof(flce_distill_desc) */
+  int64_t N, H, V;           /* as for the loss */
+  int64_t K;                 /* entries of a token, 1 to 1024 */
+  flce_dtype dtype;          /* of X, W and dX: FLCE_BF16 */
+  flce_dtype teacher_dtype;  /* of the teacher's logits */
+  flce_dtype dw_dtype;       /* of dW: FLCE_BF16, or FLCE_FP32, which can accumulate */
+  float temperature;         /* T, 1e-30 to 1e30 */
+  flce_reduction reduction;
+} flce_distill_desc;
+
+/* Bytes of the workspace of a forward or a backward (FLCE_MODE_FWD, _BWD; _FWD_BWD for one
+ * that serves both); 0 on an invalid desc. */
+size_t flce_distill_workspace_size(const flce_distill_desc* desc, int mode);
+
+/* ids: int64, N x K; teacher: N x K logits; teacher_lse: float N, or NULL.  Writes the loss,
+ * the rows' losses (row_loss, NULL to leave out), lse_i = log sum_j exp(z_ij / T) of every
+ * row, the student's logits z at the ids (float, N x K; 0 where there is no entry) and
+ * N_valid. */
+flce_status flce_distill_forward(const flce_distill_desc* desc, const void* X, const void* W, const int64_t* ids,
+                                 const void* teacher, const float* teacher_lse, float* loss, float* row_loss,
+                                 float* lse, float* logits, int32_t* valid_count, void* workspace, size_t ws_bytes,
+                                 int32_t* err_word, void* stream);
+
+/* dX (dtype) and dW (dw_dtype; += when accumulating) from the forward's inputs and its lse,
+ * logits and valid_count. */
+flce_status flce_distill_backward(const flce_distill_desc* desc, const void* X, const void* W, const int64_t* ids,
+                                  const void* teacher, const float* teacher_lse, const float* lse,
+                                  const float* logits, const int32_t* valid_count, const float* grad_loss, void* dX,
+                                  void* dW, int accumulate_dW, void* workspace, size_t ws_bytes, int32_t* err_word,
+                                  void* stream);
+
+/* ---------------------------------------------------------------------------
  * Attention of the packed batch whose loss the calls above compute.  The
  * conventions at the top hold here too: device pointers, the caller's memory,
  * asynchronous on `stream`, argument errors returned, data errors in

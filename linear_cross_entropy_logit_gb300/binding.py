@@ -52,6 +52,7 @@ EXPORTED = (
     "flce_attention_forward", "flce_attention_workspace_size", "flce_attention_backward",
     "flce_layer_norm_forward", "flce_layer_norm_workspace_size", "flce_layer_norm_backward",
     "flce_rope_forward", "flce_rope_backward",
+    "flce_distill_workspace_size", "flce_distill_forward", "flce_distill_backward",
 )
 
 PROFILE_KINDS = ("fwd_logits_lse", "bwd_dz_recompute", "bwd_dw_gemm", "bwd_dx_gemm",
@@ -112,6 +113,15 @@ class FlceRopeDesc(ctypes.Structure):
                 ("k_head", ctypes.c_int64)]
 
 
+class FlceDistillDesc(ctypes.Structure):
+    """Mirror of ``flce_distill_desc`` in include/flce.h."""
+    _fields_ = [("struct_size", ctypes.c_size_t), ("N", ctypes.c_int64), ("H", ctypes.c_int64),
+                ("V", ctypes.c_int64), ("K", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("teacher_dtype", ctypes.c_int), ("dw_dtype", ctypes.c_int),
+                ("temperature", ctypes.c_float), ("reduction", ctypes.c_int)]
+
+
+_DISTILL_DESC_BYTES = ctypes.sizeof(FlceDistillDesc)
 _LAYER_NORM_DESC_BYTES = ctypes.sizeof(FlceLayerNormDesc)
 _ROPE_DESC_BYTES = ctypes.sizeof(FlceRopeDesc)
 _QK_DESC_BYTES = ctypes.sizeof(FlceQkNormRopeDesc)
@@ -242,6 +252,13 @@ def load(path: str) -> ctypes.CDLL:
     L.flce_attention_workspace_size.restype = SZ
     L.flce_attention_backward.argtypes = [AD, P, P, P, P, P, P, P, P, P, P, P, SZ, P, P]
     L.flce_attention_backward.restype = I32
+    DD = ctypes.POINTER(FlceDistillDesc)
+    L.flce_distill_workspace_size.argtypes = [DD, I32]
+    L.flce_distill_workspace_size.restype = SZ
+    L.flce_distill_forward.argtypes = [DD, P, P, P, P, P, P, P, P, P, P, P, SZ, P, P]
+    L.flce_distill_forward.restype = I32
+    L.flce_distill_backward.argtypes = [DD, P, P, P, P, P, P, P, P, P, P, P, I32, P, SZ, P, P]
+    L.flce_distill_backward.restype = I32
     ND, RD = ctypes.POINTER(FlceLayerNormDesc), ctypes.POINTER(FlceRopeDesc)
     L.flce_layer_norm_forward.argtypes = [ND, P, P, P, P, P, P, P, P, P]
     L.flce_layer_norm_forward.restype = I32
@@ -1054,6 +1071,92 @@ def flce_rope_backward(dq_out, dk_out, inv_freq, positions=None, *, magnitude: f
     return _rope("flce_rope_backward", True, dq_out, dk_out, inv_freq, positions, magnitude, interleaved, dq, dk)
 
 
+def _distill_args(X, W, ids, teacher_logits, temperature, reduction, teacher_lse, dw_dtype):
+    """(desc, device, the teacher's addresses)."""
+    dev = _cuda_rows("X", X)
+    if X.dtype is not torch.bfloat16:
+        raise TypeError(f"distillation takes bfloat16 X and W, got {X.dtype}")
+    if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1] or ids.dim() != 2 or ids.shape[0] != X.shape[0]:
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}, ids {tuple(ids.shape)}")
+    (N, H), V = X.shape, W.shape[0]
+    _array("X", X, X.shape, torch.bfloat16, dev)
+    _array("W", W, W.shape, torch.bfloat16, dev)
+    p_ids = _array("ids", ids, ids.shape, torch.int64, dev)
+    t_code = _dtype_code(teacher_logits, "the teacher's logits")
+    p_t = _array("teacher_logits", teacher_logits, ids.shape, teacher_logits.dtype, dev)
+    p_tl = None if teacher_lse is None else _array("teacher_lse", teacher_lse, (N,), torch.float32, dev)
+    d = FlceDistillDesc(_DISTILL_DESC_BYTES, N, H, V, ids.shape[1], FLCE_BF16, t_code,
+                        FLCE_FP32 if dw_dtype is torch.float32 else FLCE_BF16, temperature, _red_code(reduction))
+    return d, dev, (p_ids, p_t, p_tl)
+
+
+def flce_distill_workspace_size(N: int, H: int, V: int, K: int, mode: int = MODE_FWD_BWD) -> int:
+    """Workspace bytes of a distillation of N tokens with K entries each."""
+    return int(lib().flce_distill_workspace_size(
+        FlceDistillDesc(_DISTILL_DESC_BYTES, N, H, V, K, FLCE_BF16, FLCE_FP32, FLCE_BF16, 1.0, FLCE_MEAN), mode))
+
+
+def flce_distill_forward(X, W, ids, teacher_logits, temperature: float = 1.0, reduction: str = "mean", *,
+                         teacher_lse=None, loss=None, lse=None, logits=None, valid_count=None, row_loss=None,
+                         workspace_buf=None, err_word=None, stream=None):
+    """Divergence of the student's softmax (X [N, H] W [V, H]^T / temperature, bf16, logits never
+    stored) from the teacher's top logits: ids int64 [N, K], negative for no entry, and
+    teacher_logits [N, K] bf16 or float32.  Without teacher_lse (float32 [N], the teacher's
+    log-sum-exp over its whole vocabulary at the same temperature) the entries' probabilities
+    are normed to one.  Returns (loss[1], lse[N], logits[N, K] of the student at the ids,
+    valid_count[1], err_word); the backward takes the middle three."""
+    if stream is not None:
+        return _with_stream(stream, flce_distill_forward, X, W, ids, teacher_logits, temperature, reduction,
+                            teacher_lse=teacher_lse, loss=loss, lse=lse, logits=logits, valid_count=valid_count,
+                            row_loss=row_loss, workspace_buf=workspace_buf, err_word=err_word)
+    d, dev, teacher = _distill_args(X, W, ids, teacher_logits, temperature, reduction, teacher_lse, torch.bfloat16)
+    f32, N = torch.float32, X.shape[0]
+    loss, p_loss = _output("loss", loss, X, (1,), f32, dev)
+    lse, p_lse = _output("lse", lse, X, (N,), f32, dev)
+    logits, p_logits = _output("logits", logits, X, ids.shape, f32, dev)
+    valid_count, p_valid = _output("valid_count", valid_count, X, (1,), torch.int32, dev)
+    p_rows = None if row_loss is None else _array("row_loss", row_loss, (N,), f32, dev)
+    L = lib()
+    need = L.flce_distill_workspace_size(d, MODE_FWD) if workspace_buf is None else 0
+    ws, p_ws, ws_bytes = _scratch(workspace_buf, need, X, dev)
+    err_word, p_err = _error_word(err_word, X, dev)
+    st = L.flce_distill_forward(d, X.data_ptr(), W.data_ptr(), *teacher, p_loss, p_rows, p_lse, p_logits, p_valid,
+                                p_ws, ws_bytes, p_err, _current_stream(dev))
+    if st:
+        _check(st, "flce_distill_forward")
+    return loss, lse, logits, valid_count, err_word
+
+
+def flce_distill_backward(X, W, ids, teacher_logits, lse, logits, valid_count, temperature: float = 1.0,
+                          reduction: str = "mean", *, teacher_lse=None, grad_loss=None, dX=None, dW=None,
+                          accumulate_dW: bool = False, workspace_buf=None, err_word=None, stream=None):
+    """Gradients (dX [N, H] bf16, dW [V, H], err_word) of flce_distill_forward.  dW is bf16, or
+    the caller's float32 tensor, which alone can be accumulated into."""
+    if stream is not None:
+        return _with_stream(stream, flce_distill_backward, X, W, ids, teacher_logits, lse, logits, valid_count,
+                            temperature, reduction, teacher_lse=teacher_lse, grad_loss=grad_loss, dX=dX, dW=dW,
+                            accumulate_dW=accumulate_dW, workspace_buf=workspace_buf, err_word=err_word)
+    f32 = torch.float32
+    dw_dtype = f32 if dW is not None and dW.dtype is f32 else torch.bfloat16
+    d, dev, teacher = _distill_args(X, W, ids, teacher_logits, temperature, reduction, teacher_lse, dw_dtype)
+    if accumulate_dW and (dW is None or dw_dtype is not f32):
+        raise ValueError("accumulate_dW needs an existing float32 dW")
+    dX, p_dx = _output("dX", dX, X, X.shape, torch.bfloat16, dev)
+    dW, p_dw = _output("dW", dW, X, W.shape, dw_dtype, dev)
+    p_grad = None if grad_loss is None else _array("grad_loss", grad_loss, (1,), f32, dev)
+    L = lib()
+    need = L.flce_distill_workspace_size(d, MODE_BWD) if workspace_buf is None else 0
+    ws, p_ws, ws_bytes = _scratch(workspace_buf, need, X, dev)
+    err_word, p_err = _error_word(err_word, X, dev)
+    st = L.flce_distill_backward(
+        d, X.data_ptr(), W.data_ptr(), *teacher, _array("lse", lse, X.shape[:1], f32, dev),
+        _array("logits", logits, ids.shape, f32, dev), _array("valid_count", valid_count, (1,), torch.int32, dev),
+        p_grad, p_dx, p_dw, int(bool(accumulate_dW)), p_ws, ws_bytes, p_err, _current_stream(dev))
+    if st:
+        _check(st, "flce_distill_backward")
+    return dX, dW, err_word
+
+
 def last_launch_count() -> int:
     return int(lib().flce_last_launch_count())
 
@@ -1224,3 +1327,37 @@ def _dense_heads(g):
 def rope(q, k, inv_freq, positions=None, *, magnitude: float = 1.0, interleaved: bool = False):
     """Autograd entry of flce_rope_forward: (q_out, k_out)."""
     return _Rope.apply(q, k, inv_freq, positions, magnitude, interleaved)
+
+
+class _LinearDistillation(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, W, ids, teacher_logits, temperature, reduction, teacher_lse, err):
+        loss, lse, logits, valid, err = flce_distill_forward(X, W, ids, teacher_logits, temperature, reduction,
+                                                             teacher_lse=teacher_lse, err_word=err)
+        ctx.save_for_backward(X, W, ids, teacher_logits, teacher_lse, lse, logits, valid)
+        # err is not saved: the caller may read and clear it before the backward
+        ctx.cfg = (temperature, reduction, err)
+        return loss[0]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g):
+        X, W, ids, teacher_logits, teacher_lse, lse, logits, valid = ctx.saved_tensors
+        temperature, reduction, err = ctx.cfg
+        dX, dW, _ = flce_distill_backward(X, W, ids, teacher_logits, lse, logits, valid, temperature, reduction,
+                                          teacher_lse=teacher_lse,
+                                          grad_loss=g.reshape(1).to(torch.float32).contiguous(), err_word=err)
+        return dX, dW, None, None, None, None, None, None
+
+
+def linear_distillation(h, W, ids, teacher_logits, temperature: float = 1.0, reduction: str = "mean", *,
+                        teacher_lse=None, err_word=None):
+    """Autograd entry of flce_distill_forward, in the shape of linear_cross_entropy: the loss.
+    h may be [..., H]; ids and teacher_logits [..., K] and teacher_lse [...] of the same leading
+    shape.  The teacher's side gets no gradient.  The forward and the backward report into
+    err_word; without one what goes wrong on the device is not seen."""
+    H, K = h.shape[-1], ids.shape[-1]
+    return _LinearDistillation.apply(
+        h.reshape(-1, H).contiguous(), W.contiguous(), ids.reshape(-1, K).contiguous(),
+        teacher_logits.detach().reshape(-1, K).contiguous(), temperature, reduction,
+        None if teacher_lse is None else teacher_lse.detach().reshape(-1).contiguous(), err_word)

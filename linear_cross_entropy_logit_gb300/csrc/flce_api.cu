@@ -35,6 +35,7 @@
 #include "flce.h"
 #include "aux_kernels.cuh"
 #include "bwd_fused.cuh"
+#include "distill.cuh"
 #include "gemm_core.cuh"
 #include "host_util.h"
 #include "ptx.cuh"
@@ -580,6 +581,16 @@ flce_status launch_quad(int dev, int num_sms, const CUtensorMap& a, const CUtens
   return FLCE_OK;
 }
 
+// Run-time choice between the CTA-pair and QUAD kernels.
+template <Epi EPI, bool A_MN, bool B_MN>
+flce_status launch_pair(const Walk& w, int dev, int num_sms, const CUtensorMap& a, const CUtensorMap& b,
+                        const CUtensorMap& out, const GemmParams& p, cudaStream_t st, int prof_kind) {
+  if (w.quad)
+    return w.share_b ? launch_quad<EPI, A_MN, B_MN, true>(dev, num_sms, a, b, out, p, st, prof_kind)
+                     : launch_quad<EPI, A_MN, B_MN, false>(dev, num_sms, a, b, out, p, st, prof_kind);
+  return launch_gemm<EPI, A_MN, B_MN, true, false>(dev, num_sms, a, b, out, p, st, prof_kind);
+}
+
 // Run-time choice between the 1-CTA (128 x 256), CTA-pair (256 x 256) and
 // QUAD kernels.
 template <Epi EPI, bool A_MN, bool B_MN>
@@ -658,6 +669,19 @@ uint32_t b_box_rows(bool pair) { return pair ? BN / 2 : BN; }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// What a distillation call adds to the loss's: the loss of a row comes from the teacher's
+// entries, and dZ is patched at them.
+struct DistillCall {
+  const flce_distill_desc* desc;
+  DistillParams p;
+  // backward: per row and per entry, in the workspace
+  int64_t* marks;
+  float* lse_q;
+  int* ids32;
+  uint16_t* dz;
+  bool dw_bf16;
+};
+
 struct Common {
   const void* X;
   const void* W;
@@ -680,6 +704,8 @@ struct Common {
   int64_t vocab_total = 0;
   bool dx_partial_f32 = false;
   Tuning tun{};
+  // linear distillation: the teacher's entries take the place of the labels
+  const DistillCall* distill = nullptr;
 };
 
 flce_status validate_common(const Common& c, int mode, Plan* pl) {
@@ -768,6 +794,36 @@ flce_status cast_inputs(const Common& c, const Plan& pl, int sms, const void** X
   return FLCE_OK;
 }
 
+flce_status loss_finalize(const Common& c, const Plan& pl, const double* block_loss, const int* block_valid,
+                          float* loss, int32_t* valid_count) {
+  loss_finalize_kernel<<<1, MERGE_THREADS, 0, c.st>>>(block_loss, block_valid,
+                                                       c.N > 0 ? pl.merge_blocks : 0,
+                                                       c.reduction == FLCE_SUM, loss, valid_count);
+  ++g_launches;
+  FLCE_CUDA(cudaGetLastError());
+  return FLCE_OK;
+}
+
+// A distillation's forward after the softmax's partials: the student's logits at the entries
+// and the rows' losses.
+flce_status distill_rows(const Common& c, const Plan& pl, const void* Xb, const void* Wb, const float4* partials,
+                         float* lse, double* block_loss, int* block_valid) {
+  const DistillCall& d = *c.distill;
+  distill_gather<<<(unsigned)c.N, kGatherThreads, 0, c.st>>>(
+      static_cast<const __nv_bfloat16*>(Xb), static_cast<const __nv_bfloat16*>(Wb), d.p);
+  ++g_launches;
+  FLCE_CUDA(cudaGetLastError());
+  if (d.desc->teacher_dtype == FLCE_BF16)
+    distill_merge<__nv_bfloat16><<<pl.merge_blocks, MERGE_THREADS, 0, c.st>>>(
+        partials, pl.n_groups, pl.m_pad, d.p, lse, c.row_loss, block_loss, block_valid);
+  else
+    distill_merge<float><<<pl.merge_blocks, MERGE_THREADS, 0, c.st>>>(
+        partials, pl.n_groups, pl.m_pad, d.p, lse, c.row_loss, block_loss, block_valid);
+  ++g_launches;
+  FLCE_CUDA(cudaGetLastError());
+  return FLCE_OK;
+}
+
 flce_status run_forward(const Common& c, const Plan& pl, int dev, int sms, const void* Xb,
                         const void* Wb, float* loss, float* lse, int32_t* valid_count,
                         float4* shard_out = nullptr) {
@@ -795,6 +851,7 @@ flce_status run_forward(const Common& c, const Plan& pl, int dev, int sms, const
     p.col_base = (int)c.vocab_offset;
     p.col_limit = (int)c.V;
     p.smoothing = c.smoothing;
+    if (c.distill) p.z_log2e = LOG2E * c.distill->p.inv_t;
     p.partials = reinterpret_cast<float4*>(ws + pl.off_partials);
     p.m_pad = pl.m_pad;
     p.l2_keep_b = 0;
@@ -811,6 +868,10 @@ flce_status run_forward(const Common& c, const Plan& pl, int dev, int sms, const
     FLCE_TRY(map_kmajor(&tmW, Wb, c.H, c.V, c.H, b_box_rows(pair, walk)));
     FLCE_TRY((launch_tile<Epi::kLse, false, false>(pair, ext, walk, dev, sms, tmX, tmW, tmX, p,
                                                   c.st, 0)));
+    if (c.distill) {
+      FLCE_TRY(distill_rows(c, pl, Xb, Wb, p.partials, lse, block_loss, block_valid));
+      return loss_finalize(c, pl, block_loss, block_valid, loss, valid_count);
+    }
     if (shard_out) {
       // vocabulary shard: one merged partial per row, no loss yet
       shard_partial_kernel<<<pl.merge_blocks, MERGE_THREADS, 0, c.st>>>(
@@ -826,9 +887,34 @@ flce_status run_forward(const Common& c, const Plan& pl, int dev, int sms, const
     ++g_launches;
     FLCE_CUDA(cudaGetLastError());
   }
-  loss_finalize_kernel<<<1, MERGE_THREADS, 0, c.st>>>(block_loss, block_valid,
-                                                       c.N > 0 ? pl.merge_blocks : 0,
-                                                       c.reduction == FLCE_SUM, loss, valid_count);
+  return loss_finalize(c, pl, block_loss, block_valid, loss, valid_count);
+}
+
+// Per row of a distillation's backward: marks for the GEMM core, dZ at the entries, and c.
+flce_status distill_rows_backward(const Common& c, const float* lse, const int32_t* valid_count,
+                                  const float* grad_loss, float* scale) {
+  const DistillCall& d = *c.distill;
+  const unsigned blocks = (unsigned)ceil_div(std::max<int64_t>(c.N, 1), kPrepareThreads / 32);
+  const size_t smem = (size_t)kPrepareThreads / 32 * 2 * d.p.K * 4;
+  const int sum = c.reduction == FLCE_SUM;
+  if (d.desc->teacher_dtype == FLCE_BF16)
+    distill_prepare<__nv_bfloat16><<<blocks, kPrepareThreads, smem, c.st>>>(
+        d.p, lse, valid_count, grad_loss, sum, scale, d.marks, d.lse_q, d.ids32, d.dz);
+  else
+    distill_prepare<float><<<blocks, kPrepareThreads, smem, c.st>>>(
+        d.p, lse, valid_count, grad_loss, sum, scale, d.marks, d.lse_q, d.ids32, d.dz);
+  ++g_launches;
+  FLCE_CUDA(cudaGetLastError());
+  return FLCE_OK;
+}
+
+// The entries of a chunk put into its dZ.
+flce_status distill_chunk(const Common& c, int sms, int64_t v0, int64_t w, int64_t pitch, void* dz) {
+  const DistillCall& d = *c.distill;
+  const int64_t entries = c.N * d.p.K;
+  const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(entries, 256), 8 * sms);
+  distill_scatter<<<blocks, 256, 0, c.st>>>(d.ids32, d.dz, entries, d.p.K, (int)v0, (int)w, pitch,
+                                            static_cast<uint16_t*>(dz));
   ++g_launches;
   FLCE_CUDA(cudaGetLastError());
   return FLCE_OK;
@@ -836,14 +922,22 @@ flce_status run_forward(const Common& c, const Plan& pl, int dev, int sms, const
 
 flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, const void* Xb,
                          const void* Wb, const float* lse, const int32_t* valid_count,
-                         const float* grad_loss, void* dX, float* dW, int accumulate) {
+                         const float* grad_loss, void* dX, void* dW_out, int accumulate) {
   uint8_t* ws = static_cast<uint8_t*>(c.ws);
   float* scale = reinterpret_cast<float*>(ws + pl.off_scalars);
-  grad_scale_kernel<<<1, 1, 0, c.st>>>(valid_count, grad_loss, c.reduction == FLCE_SUM, scale);
-  ++g_launches;
-  FLCE_CUDA(cudaGetLastError());
+  float* dW = static_cast<float*>(dW_out);
+  const bool dw_bf16 = c.distill && c.distill->dw_bf16;
+  if (c.distill) {
+    FLCE_TRY(distill_rows_backward(c, lse, valid_count, grad_loss, scale));
+    lse = c.distill->lse_q;
+  } else {
+    grad_scale_kernel<<<1, 1, 0, c.st>>>(valid_count, grad_loss, c.reduction == FLCE_SUM, scale);
+    ++g_launches;
+    FLCE_CUDA(cudaGetLastError());
+  }
   if (c.N == 0) {
-    if (!accumulate) FLCE_CUDA(cudaMemsetAsync(dW, 0, (size_t)c.V * c.H * 4, c.st));
+    if (!accumulate)
+      FLCE_CUDA(cudaMemsetAsync(dW_out, 0, (size_t)c.V * c.H * (dw_bf16 ? 2 : 4), c.st));
     return FLCE_OK;
   }
   const int64_t N = c.N, H = c.H, V = c.V, Cv = pl.chunk;
@@ -901,6 +995,7 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
     p3.col_limit = (int)w;
     p3.smoothing = c.smoothing;
     p3.z_loss = c.z_loss;
+    if (c.distill) p3.z_log2e = LOG2E * c.distill->p.inv_t;
     p3.row_list = sk.list;
     p3.row_count = sk.count;
     p3.list_cap = pl.n_blocks128;
@@ -1041,12 +1136,16 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
       FLCE_TRY(map_mnmajor(&tmWc_mn, Wc, H, w, H));
       FLCE_TRY(map_dz_store(&tmDzSt, dz, w, N, Cv));
       FLCE_TRY(map_mnmajor(&tmDz_mn, dz, w, N, Cv));
-      FLCE_TRY(map_f32_out(&tmDw, dW + v0 * H, H, w, H));
+      if (dw_bf16)
+        FLCE_TRY(map_dz_store(&tmDw, static_cast<uint16_t*>(dW_out) + v0 * H, H, w, H));
+      else
+        FLCE_TRY(map_f32_out(&tmDw, dW + v0 * H, H, w, H));
 
       // K3: recompute Z[:, v0:v0+w] and write dZ (bf16) into the chunk scratch.
       FLCE_TRY((launch_tile<Epi::kDz, false, false>(pair, ext, w3, dev, sms,
                                                     w3.quad ? tmX_k64 : tmX_k, tmWc_k, tmDzSt,
                                                     p3, c.st, 1)));
+      if (c.distill) FLCE_TRY(distill_chunk(c, sms, v0, w, Cv, dz));
 
       // K4: dW[v0:v0+w, :] = dZ_chunk^T X   (K = N tokens)
       GemmParams p4{};
@@ -1073,9 +1172,12 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
       p4.l2_keep_frac = l2_keep_fraction(c.tun, (double)N * H * 2);
       p4.err_word = c.err_word;
       p4.timeout_ns = kTimeoutNs;
-      FLCE_TRY((launch_tile<Epi::kStore, true, true>(pair, ext, pick_walk(c.tun, pair, ext, p4),
-                                                     dev, sms, tmDz_mn, tmX_mn, tmDw, p4, c.st,
-                                                     2)));
+      const Walk w4 = pick_walk(c.tun, pair, ext, p4);
+      if (dw_bf16)
+        FLCE_TRY((launch_pair<Epi::kStoreBf16, true, true>(w4, dev, sms, tmDz_mn, tmX_mn, tmDw, p4, c.st, 2)));
+      else
+        FLCE_TRY((launch_tile<Epi::kStore, true, true>(pair, ext, w4, dev, sms, tmDz_mn, tmX_mn, tmDw, p4, c.st,
+                                                       2)));
 
       // K5: dX_acc (+)= dZ_chunk W[v0:v0+w, :]   (K = w vocabulary columns)
       GemmParams p5{};
@@ -1565,6 +1667,139 @@ flce_status flce_backward_vocab_shard(const void* X, const void* W_shard, const 
   FLCE_TRY(cast_inputs(c, pl, sms, &Xb, &Wb));
   return run_backward(c, pl, dev, sms, Xb, Wb, lse, valid_count, grad_loss, dX_partial, dW_shard,
                       accumulate_dW);
+}
+
+// ---------------------------------------------------------------------------
+// Linear distillation
+// ---------------------------------------------------------------------------
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kMaxTop = 1024;
+
+bool distill_ok(const flce_distill_desc* d) {
+  if (!d || d->struct_size != sizeof(flce_distill_desc)) return false;
+  if (!shape_ok(d->N, d->H, d->V) || d->K <= 0 || d->K > kMaxTop || d->N > INT64_MAX / kMaxTop) return false;
+  if (d->dtype != FLCE_BF16 && d->dtype != FLCE_FP32) return false;
+  if (d->teacher_dtype != FLCE_BF16 && d->teacher_dtype != FLCE_FP32) return false;
+  if (d->dw_dtype != FLCE_BF16 && d->dw_dtype != FLCE_FP32) return false;
+  if (d->reduction != FLCE_MEAN && d->reduction != FLCE_SUM) return false;
+  // T and 1 / T are normal numbers
+  return d->temperature >= 1e-30f && d->temperature <= 1e30f;
+}
+
+// CTA-pair tiles, three launches a chunk (the entries are put in between them).
+Tuning distill_tuning() {
+  Tuning t = default_tuning();
+  t.pair = true;
+  t.merge = 0;
+  t.l2_hints = false;
+  return t;
+}
+
+// The loss's plan, and behind it the backward's rows and entries.
+struct DistillPlan {
+  Plan pl;
+  size_t off_marks, off_lse_q, off_ids, off_dz, total;
+};
+bool distill_plan(const flce_distill_desc* d, int mode, DistillPlan* out) {
+  if (!distill_ok(d) || !make_plan(d->N, d->H, d->V, FLCE_BF16, mode, distill_tuning(), &out->pl)) return false;
+  size_t off = out->pl.total;
+  auto region = [&](size_t* at, size_t bytes) {
+    *at = off;
+    off = align_up(off + bytes, kAlign);
+  };
+  const size_t n = (mode & FLCE_MODE_BWD) ? (size_t)d->N : 0;
+  region(&out->off_marks, n * sizeof(int64_t));
+  region(&out->off_lse_q, n * sizeof(float));
+  region(&out->off_ids, n * d->K * sizeof(int));
+  region(&out->off_dz, n * d->K * sizeof(uint16_t));
+  out->total = off;
+  return true;
+}
+
+// Checks what both directions share and fills the call.
+flce_status distill_call(const flce_distill_desc* d, int mode, const void* X, const void* W, const int64_t* ids,
+                         const void* teacher, const float* teacher_lse, float* logits, float* row_loss,
+                         void* ws, size_t ws_bytes, int32_t* err_word, void* stream, Common* c, DistillCall* dc,
+                         DistillPlan* pl) {
+  g_launches = 0;
+  g_quad_launches = 0;
+  if (!distill_ok(d)) return FLCE_ERR_ARG;
+  if (d->dtype != FLCE_BF16) return FLCE_ERR_UNSUPPORTED;
+  if (!err_word || !aligned(err_word, 4) || !W || !aligned(W, 16)) return FLCE_ERR_ARG;
+  if (!aligned(X, 16) || !aligned(ids, 8) || !aligned(teacher, d->teacher_dtype == FLCE_BF16 ? 2 : 4) || !aligned(teacher_lse, 4) ||
+      !aligned(logits, 4) || !aligned(row_loss, 4))
+    return FLCE_ERR_ARG;
+  if (d->N > 0 && (!X || !ids || !teacher || !logits)) return FLCE_ERR_ARG;
+  if (!distill_plan(d, mode, pl)) return FLCE_ERR_ARG;
+  if (!ws || !aligned(ws, kAlign) || ws_bytes < pl->total) return FLCE_ERR_WORKSPACE;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  *dc = DistillCall{d,
+                    DistillParams{ids, teacher, teacher_lse, logits, (int)d->N, (int)d->K, (int)d->H, (int)d->V,
+                                  1.f / d->temperature, err_word},
+                    reinterpret_cast<int64_t*>(base + pl->off_marks),
+                    reinterpret_cast<float*>(base + pl->off_lse_q),
+                    reinterpret_cast<int*>(base + pl->off_ids),
+                    reinterpret_cast<uint16_t*>(base + pl->off_dz),
+                    d->dw_dtype == FLCE_BF16};
+  // The GEMM core's labels: none forward; backward the rows' marks, V for one that counts
+  // (a column that does not exist, so that no target is taken off) and -1 for one that
+  // does not.
+  const flce_options o = defaults(-1, 0.f, d->reduction);
+  *c = make_common(X, W, (mode & FLCE_MODE_BWD) ? dc->marks : nullptr, d->N, d->H, d->V, FLCE_BF16, &o, ws,
+                   ws_bytes, err_word, stream);
+  c->row_loss = row_loss;
+  c->vocab_total = d->V + 1;
+  c->tun = distill_tuning();
+  c->distill = dc;
+  return FLCE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t flce_distill_workspace_size(const flce_distill_desc* d, int mode) {
+  DistillPlan pl;
+  return distill_plan(d, mode, &pl) ? pl.total : 0;
+}
+
+flce_status flce_distill_forward(const flce_distill_desc* d, const void* X, const void* W, const int64_t* ids,
+                                 const void* teacher, const float* teacher_lse, float* loss, float* row_loss,
+                                 float* lse, float* logits, int32_t* valid_count, void* workspace, size_t ws_bytes,
+                                 int32_t* err_word, void* stream) {
+  Common c;
+  DistillCall dc;
+  DistillPlan pl;
+  FLCE_TRY(distill_call(d, FLCE_MODE_FWD, X, W, ids, teacher, teacher_lse, logits, row_loss, workspace, ws_bytes,
+                        err_word, stream, &c, &dc, &pl));
+  if (!loss || !aligned(loss, 4) || !valid_count || !aligned(valid_count, 4) || !aligned(lse, 4))
+    return FLCE_ERR_ARG;
+  if (d->N > 0 && !lse) return FLCE_ERR_ARG;
+  int dev, sms;
+  FLCE_TRY(host::device(&dev, &sms));
+  return run_forward(c, pl.pl, dev, sms, X, W, loss, lse, valid_count);
+}
+
+flce_status flce_distill_backward(const flce_distill_desc* d, const void* X, const void* W, const int64_t* ids,
+                                  const void* teacher, const float* teacher_lse, const float* lse,
+                                  const float* logits, const int32_t* valid_count, const float* grad_loss, void* dX,
+                                  void* dW, int accumulate_dW, void* workspace, size_t ws_bytes, int32_t* err_word,
+                                  void* stream) {
+  Common c;
+  DistillCall dc;
+  DistillPlan pl;
+  FLCE_TRY(distill_call(d, FLCE_MODE_BWD, X, W, ids, teacher, teacher_lse, const_cast<float*>(logits), nullptr,
+                        workspace, ws_bytes, err_word, stream, &c, &dc, &pl));
+  if (!valid_count || !aligned(valid_count, 4) || !aligned(grad_loss, 4) || !aligned(lse, 4)) return FLCE_ERR_ARG;
+  if (!dW || !aligned(dW, 16) || !aligned(dX, 16)) return FLCE_ERR_ARG;
+  if (accumulate_dW && d->dw_dtype != FLCE_FP32) return FLCE_ERR_ARG;
+  if (d->N > 0 && (!lse || !dX)) return FLCE_ERR_ARG;
+  int dev, sms;
+  FLCE_TRY(host::device(&dev, &sms));
+  return run_backward(c, pl.pl, dev, sms, X, W, lse, valid_count, grad_loss, dX, dW, accumulate_dW);
 }
 
 flce_status flce_debug_wait_timeout(int32_t* err_word, uint64_t timeout_ns,

@@ -50,6 +50,9 @@
 //          TMA into the bounded N x Cv chunk scratch.
 //   kStore fp32 tile written (or reduce-added) by TMA: the dW and dX GEMMs of
 //          step 4 ("Backward Hidden and Weight Accumulation").
+//   kStoreBf16  the tile rounded to bf16 and written by TMA: a dW that is not
+//          accumulated over calls leaves in the weight's type.
+// kLse and kDz take exp(z / T) for any temperature T: z_log2e is log2(e) / T.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -81,7 +84,7 @@ struct TileCfg {
   static constexpr int STAGE = A_STAGE + B_STAGE;
 };
 
-enum class Epi : int { kLse = 0, kDz = 1, kStore = 2 };
+enum class Epi : int { kLse = 0, kDz = 1, kStore = 2, kStoreBf16 = 3 };
 
 struct GemmParams {
   int m_size;      // rows of D
@@ -96,12 +99,13 @@ struct GemmParams {
   int m_band;      // m_fastest: walk row blocks in bands of this many (0 = all at once)
   int n_band;      // !m_fastest: walk column groups in bands of this many (0 = all at once)
   // kLse / kDz
-  const int64_t* labels;  // per D row (token)
+  const int64_t* labels;  // per D row (token); null (kLse): no targets
   long long ignore_index;
   int vocab;              // V
   int col_base;           // vocabulary index of D column 0
   int col_limit;          // D columns >= col_limit do not exist
   float smoothing;        // eps
+  float z_log2e = LOG2E;  // exp(z / T) = exp2(z * z_log2e)
   float z_loss;           // kDz: z-loss weight alpha (softmax term scaled by 1 + 2 alpha lse)
   float4* partials;       // kLse: [n_groups][m_pad] of (max*log2e, sum, z_y, sum_z)
   int m_pad;              // m_blocks * TILE_M
@@ -329,15 +333,16 @@ struct DzRow {
   float eps_v;     // c * valid * eps / V
   float tgt;       // c * valid * (1 - eps)
   float arg0;      // neg_lse2 + log2(pcoef) (-inf when pcoef = 0): pcoef * p = exp2(z log2 e + arg0)
+  float z_log2e;   // log2(e) / T
 };
 
 __device__ __forceinline__ DzRow dz_row(bool valid, float lse_r, float c, float eps, float z_loss,
-                                        int vocab) {
+                                        int vocab, float z_log2e = LOG2E) {
   const float coef = valid ? c : 0.f;
   const float pcoef = coef * fmaf(2.f * z_loss, lse_r, 1.f);
   const float neg_lse2 = -lse_r * LOG2E;
   return {pcoef, neg_lse2, coef * eps / (float)vocab, coef * (1.f - eps),
-          neg_lse2 + __log2f(pcoef)};
+          neg_lse2 + __log2f(pcoef), z_log2e};
 }
 
 // dZ of one 64-column slice of this thread's row: TMEM columns taddr .. +63 in,
@@ -358,11 +363,11 @@ __device__ __forceinline__ float dz_slice(uint32_t taddr, const DzRow& d, long l
   if (!PMAX && __all_sync(0xffffffffu, d.eps_v == 0.f && d.pcoef >= 0.f)) {
 #pragma unroll
     for (int j = 0; j < 64; ++j)
-      r[j] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(r[j]), LOG2E, d.arg0)));
+      r[j] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(r[j]), d.z_log2e, d.arg0)));
   } else {
 #pragma unroll
     for (int j = 0; j < 64; ++j) {
-      const float pj = ex2_approx(fmaf(__uint_as_float(r[j]), LOG2E, d.neg_lse2));
+      const float pj = ex2_approx(fmaf(__uint_as_float(r[j]), d.z_log2e, d.neg_lse2));
       if constexpr (PMAX) pm[j & 1] = fmaxf(pm[j & 1], pj);
       r[j] = __float_as_uint(fmaf(d.pcoef, pj, -d.eps_v));
     }
@@ -798,8 +803,9 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
       // Per-row state for kLse (natural-log max is m2 / log2(e)).
       float m2 = -INFINITY, ssum = 0.f, zy = 0.f, zsum = 0.f;
       long long label = 0;
-      if constexpr (EPI != Epi::kStore)
-        label = row_ok ? (long long)p.labels[row] : (long long)p.ignore_index;
+      if constexpr (EPI == Epi::kLse || EPI == Epi::kDz)
+        label = row_ok && (EPI == Epi::kDz || p.labels) ? (long long)p.labels[row]
+                                                        : (long long)p.ignore_index;
       // A label outside [0, V) that is not ignore_index counts as ignored, as
       // in the forward's merge (which records FLCE_ERR_LABEL for it).
       const bool valid =
@@ -808,7 +814,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
 
       DzRow dzr{};
       if constexpr (EPI == Epi::kDz)
-        dzr = dz_row(valid, row_ok ? p.lse[row] : 0.f, c_scale, p.smoothing, p.z_loss, p.vocab);
+        dzr = dz_row(valid, row_ok ? p.lse[row] : 0.f, c_scale, p.smoothing, p.z_loss, p.vocab,
+                     p.z_log2e);
 
       for (int nb = nb0; nb < nb1; ++nb) {
         const uint32_t acc = tile & 1u;
@@ -864,7 +871,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
               mx[(j >> 1) & 3] =
                   fmax3(mx[(j >> 1) & 3], __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
             // running max in units of log2 (scaling by log2(e) > 0 keeps the order)
-            const float cm2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * LOG2E;
+            const float cm2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.z_log2e;
             if (cm2 > m2) {
               ssum *= ex2_approx(m2 - cm2);
               m2 = cm2;
@@ -872,7 +879,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
             // sum chains j mod 4, packed two per f32x2 register (each lane
             // rounds like the scalar FMA and add: same bits)
             uint64_t ps01 = 0ull, ps23 = 0ull;
-            const uint64_t l2e = pack_f32x2(LOG2E, LOG2E), nm2 = pack_f32x2(-m2, -m2);
+            const uint64_t l2e = pack_f32x2(p.z_log2e, p.z_log2e), nm2 = pack_f32x2(-m2, -m2);
 #pragma unroll
             for (int j = 0; j < 64; j += 2) {
               float a0, a1;
@@ -911,6 +918,20 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
             }
             staged_store(stag0 + (nstore++ & 1u) * STAGING_BUF_BYTES, staging, lane, w, &tmOut,
                          c0, store_row0, false);
+          }
+        } else if constexpr (EPI == Epi::kStoreBf16) {
+#pragma unroll 1
+          for (int sl = 0; sl < BN / 64; ++sl) {
+            const int c0 = nb * BN + sl * 64;
+            if (c0 >= p.n_size) break;  // warp-uniform
+            uint32_t r[64], w[32];
+            tmem_ld_32x32b_x64(taddr + sl * 64, r);
+            tmem_ld_wait_regs64(r);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              w[j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+            staged_store(stag0 + (nstore++ & 1u) * STAGING_BUF_BYTES, staging, lane, w, &tmOut, c0,
+                         store_row0, false);
           }
         } else {  // kStore
 #pragma unroll 1
