@@ -26,7 +26,7 @@ bool stride_ok(int64_t row, int64_t head, int64_t head_dim) {
 
 template <typename T, int P>
 flce_status launch(const flce_rope_desc* d, const RopeParams& p, dim3 grid, int threads, cudaStream_t st) {
-  const size_t smem = (size_t)p.tokens_per_block * (p.rot_dim / 2) * sizeof(float2);
+  const size_t smem = (size_t)p.tokens_per_block * p.rot_dim * sizeof(float);
   return d->interleaved ? host::launch(rope_kernel<T, P, true>, grid, threads, smem, st, p)
                         : host::launch(rope_kernel<T, P, false>, grid, threads, smem, st, p);
 }
@@ -63,10 +63,15 @@ flce_status run(const flce_rope_desc* d, const void* q, const void* k, const dou
   p.backward = backward;
   const bool wide = d->rot_dim % 16 == 0 && d->head_dim % 16 == 0;
   p.units = (int)d->head_dim / (wide ? 16 : 8);
-  const int threads = kRopeThreads / p.units * p.units;
-  p.tokens_per_block = 1;
-  p.heads_per_block = p.q_heads + p.kv_heads;
-  const dim3 grid((unsigned)host::ceil_div(d->tokens, p.tokens_per_block), 1);
+  // A thread takes kRopeHeads heads of its token, with fewer tokens a block where that would
+  // leave SMs idle; the heads of a single token are then shared by as many threads as
+  // there are.
+  const int groups = kRopeThreads / p.units, heads = p.q_heads + p.kv_heads;
+  const int fit = groups / std::min(groups, (int)host::ceil_div(heads, d->dtype == FLCE_BF16 ? kRopeHeads<__nv_bfloat16> : kRopeHeads<float>));
+  p.tokens_per_block = (int)std::max<int64_t>(1, std::min<int64_t>(fit, d->tokens / (2 * sms)));
+  p.slots = std::min(groups / p.tokens_per_block, heads);
+  const int threads = p.units * p.slots * p.tokens_per_block;
+  const dim3 grid((unsigned)host::ceil_div(d->tokens, p.tokens_per_block));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (d->dtype == FLCE_BF16)
     return wide ? launch<__nv_bfloat16, 8>(d, p, grid, threads, st) : launch<__nv_bfloat16, 4>(d, p, grid, threads, st);

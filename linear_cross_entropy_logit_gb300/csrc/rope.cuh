@@ -4,16 +4,19 @@
 // interleaved.  The backward is the same with the negative angle.
 //
 // Angles are taken in turns, as 64-bit fractions of one: position * round(2^64 f),
-// f = inv_freq / 2 pi, wraps around as the angle does, so that only f's own rounding
-// (2^-53) grows with the position, and a position of a million is as exact as one of
-// ten.  Its upper 24 bits go to cosine and sine of pi x.
+// f = inv_freq / 2 pi, wraps around as the angle does.  f has 64 bits itself, so that
+// a position of a million is as exact as one of ten; integers take it from inv_freq's
+// bits, the fp64 pipe is slow here.  Cosine and sine take the angle as a float of
+// half turns, off by 2^-25 at most.
 //
 // About 4 flops a value: bound by HBM.  A block computes the cosines and sines of its
-// tokens once, in shared memory, and turns all their heads with them; a thread holds
-// both halves of P pairs, so that every value is read once, 16 bytes at a time.
+// tokens once, in shared memory.  A thread holds both halves of P pairs of a head, so
+// that every value is read once, 16 bytes at a time, and turns the same pairs of several
+// heads of one token with angles that stay in its registers.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
+#include "heads.cuh"
 #include "ptx.cuh"
 
 namespace flce {
@@ -25,65 +28,124 @@ struct RopeParams {
   const int64_t* positions;  // one per token, or null (0, 1, 2, ...)
   int64_t tokens, q_row, q_head, k_row, k_head;
   int q_heads, kv_heads, head_dim, rot_dim;
-  int units;      // pieces of 2 P values of a head
-  int tokens_per_block, heads_per_block;
+  int units;             // threads that share a head, 2 P values each
+  int tokens_per_block;
+  int slots;             // groups of units threads that share a token's heads
   float magnitude;
   int backward;
 };
 
-constexpr int kRopeThreads = 256;  // at most; a multiple of the units
+constexpr int kRopeThreads = 256;  // at most: slots x tokens x units of them work
+// Heads whose loads a thread has in flight.
+template <typename T>
+constexpr int kRopeHeads = sizeof(T) == 2 ? 4 : 2;
 
-// The position's angle in turns, in [-1/2, 1/2), times two: the argument of sincospi.
-__device__ __forceinline__ float rope_half_turns(int64_t position, double inv_freq) {
-  const double f = inv_freq * 0.15915494309189533577;  // 1 / 2 pi
-  const uint64_t step = __double2ull_rn((f - floor(f)) * 18446744073709551616.0);
-  const int64_t phase = (int64_t)((uint64_t)position * step);
-  return __ll2float_rn(phase) * 1.0842021724855044e-19f;  // 2^-63
+// inv_freq / 2 pi in turns, modulo one, as a 64-bit fraction: its 53 bits times
+// 2^66 / 2 pi, shifted by its exponent.
+__device__ __forceinline__ uint64_t rope_step(double inv_freq) {
+  const uint64_t bits = (uint64_t)__double_as_longlong(inv_freq);
+  const int e = (int)(bits >> 52 & 2047);
+  const uint64_t mantissa = (bits << 11) | 0x8000000000000000ull;
+  const uint64_t f = e ? __umul64hi(mantissa, 0xa2f9836e4e44152aull) : 0;
+  const int left = e - 1024;
+  const uint64_t step = left >= 0 ? (left < 64 ? f << left : 0) : (left > -64 ? f >> -left : 0);
+  return bits >> 63 ? 0 - step : step;
+}
+// Cosine and sine of the position's angle; NaN for a frequency that is not finite.
+__device__ __forceinline__ float2 rope_angle(int64_t position, double inv_freq) {
+  const int64_t phase = (int64_t)((uint64_t)position * rope_step(inv_freq));
+  float s, c;
+  sincospif(__ll2float_rn(phase) * 1.0842021724855044e-19f, &s, &c);  // 2^-63
+  const float bad = isfinite(inv_freq) ? 0.f : __int_as_float(0x7fc00000);
+  return make_float2(c + bad, s + bad);
 }
 
+// Where the values of a unit lie in its head, and how they are paired.
 template <typename T, int P, bool PAIRS>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  extern __shared__ float2 angles[];  // tokens_per_block x rot / 2
+struct RopeHead {
+  Raw<T, P> r[2];
+  __device__ __forceinline__ void load(const T* in, int a0, int a1) {
+    r[0].load(in + a0);
+    r[1].load(in + a1);
+  }
+  __device__ __forceinline__ void turn_and_store(T* out, int a0, int a1, const uint64_t (&c)[P / 2],
+                                                 const uint64_t (&s)[P / 2], bool turns) const {
+    uint64_t v[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = r[i / (P / 2)].pair(i % (P / 2));
+    if (turns) {
+      if constexpr (PAIRS) {  // (a, b) (c, c) + (b, a) (-s, s)
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          float a, b, ci[2], si[2];
+          unpack_f32x2(v[i], a, b);
+          unpack_f32x2(c[i / 2], ci[0], ci[1]);
+          unpack_f32x2(s[i / 2], si[0], si[1]);
+          v[i] = fma_f32x2(pack_f32x2(b, a), pack_f32x2(-si[i & 1], si[i & 1]),
+                           mul_f32x2(v[i], pack_f32x2(ci[i & 1], ci[i & 1])));
+        }
+      } else {  // two pairs at a time
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i) {
+          const uint64_t a = v[i], b = v[i + P / 2], m = mul_f32x2(s[i], pack_f32x2(-1.f, -1.f));
+          v[i] = fma_f32x2(b, m, mul_f32x2(a, c[i]));
+          v[i + P / 2] = fma_f32x2(a, s[i], mul_f32x2(b, c[i]));
+        }
+      }
+    }
+    store_values<T, P>(out + a0, v);
+    store_values<T, P>(out + a1, v + P / 2);
+  }
+};
+
+template <typename T, int P, bool PAIRS>
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ float angles[];  // by token: rot / 2 cosines, rot / 2 sines
   const int64_t token0 = (int64_t)blockIdx.x * p.tokens_per_block;
   const int tokens = (int)min((int64_t)p.tokens_per_block, p.tokens - token0), half = p.rot_dim / 2;
-  const int head0 = blockIdx.y * p.heads_per_block;
-  const int heads = min(p.heads_per_block, p.q_heads + p.kv_heads - head0);
-  grid_wait();
-  for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
-    const int t = i / half;
-    const int64_t position = p.positions ? p.positions[token0 + t] : token0 + t;
-    float s, c;
-    sincospif(rope_half_turns(position, p.inv_freq[i - t * half]), &s, &c);
-    angles[i] = make_float2(c * p.magnitude, (p.backward ? -s : s) * p.magnitude);
-  }
-  __syncthreads();
-  const int u = threadIdx.x % p.units, groups = blockDim.x / p.units;
+  const int group = threadIdx.x / p.units, u = threadIdx.x - group * p.units;
+  const int t = group / p.slots, slot = group - t * p.slots, heads = p.q_heads + p.kv_heads;
   const bool turns = u * 2 * P < p.rot_dim;
   const int a0 = !PAIRS && turns ? P * u : 2 * P * u;
   const int a1 = !PAIRS && turns ? half + P * u : 2 * P * u + P;
-  for (int i = threadIdx.x / p.units; i < tokens * heads; i += groups) {
-    const int t = i / heads, h = head0 + i - t * heads;
-    const int64_t token = token0 + t;
-    const bool is_q = h < p.q_heads;
-    const T* in = is_q ? static_cast<const T*>(p.q) + token * p.q_row + h * p.q_head
-                       : static_cast<const T*>(p.k) + token * p.k_row + (h - p.q_heads) * p.k_head;
-    T* out = is_q ? static_cast<T*>(p.q_out) + (token * p.q_heads + h) * p.head_dim
-                  : static_cast<T*>(p.k_out) + (token * p.kv_heads + h - p.q_heads) * p.head_dim;
-    float x[2 * P];
+  const int64_t token = token0 + t;
+  const T* q = static_cast<const T*>(p.q) + token * p.q_row;
+  const T* k = static_cast<const T*>(p.k) + token * p.k_row;
+  T* q_out = static_cast<T*>(p.q_out) + token * p.q_heads * p.head_dim;
+  T* k_out = static_cast<T*>(p.k_out) + token * p.kv_heads * p.head_dim;
+  auto in = [&](int h) { return h < p.q_heads ? q + h * p.q_head : k + (h - p.q_heads) * p.k_head; };
+  grid_wait();
+  constexpr int U = kRopeHeads<T>;
+  for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
+    const int at = i / half, j = i - at * half;
+    const float2 w = rope_angle(p.positions ? p.positions[token0 + at] : token0 + at, p.inv_freq[j]);
+    angles[at * p.rot_dim + j] = w.x * p.magnitude;
+    angles[at * p.rot_dim + half + j] = (p.backward ? -w.y : w.y) * p.magnitude;
+  }
+  __syncthreads();
+  if (t >= tokens) return;
+  uint64_t c[P / 2] = {}, s[P / 2] = {};
+  if (turns) {
 #pragma unroll
-    for (int j = 0; j < P; ++j) x[j] = (float)in[a0 + j], x[P + j] = (float)in[a1 + j];
-    if (turns) {
-      const float2* w = angles + t * half + P * u;
-#pragma unroll
-      for (int j = 0; j < P; ++j) {
-        float &a = PAIRS ? x[2 * j] : x[j], &b = PAIRS ? x[2 * j + 1] : x[P + j];
-        const float c = w[j].x, s = w[j].y, y = a * c - b * s;
-        b = b * c + a * s;
-        a = y;
-      }
+    for (int i = 0; i < P; i += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(angles + t * p.rot_dim + P * u + i);
+      const float4 b = *reinterpret_cast<const float4*>(angles + t * p.rot_dim + half + P * u + i);
+      c[i / 2] = pack_f32x2(a.x, a.y), c[i / 2 + 1] = pack_f32x2(a.z, a.w);
+      s[i / 2] = pack_f32x2(b.x, b.y), s[i / 2 + 1] = pack_f32x2(b.z, b.w);
     }
+  }
+  for (int h0 = slot; h0 < heads; h0 += U * p.slots) {
+    RopeHead<T, P, PAIRS> x[U];
 #pragma unroll
-    for (int j = 0; j < P; ++j) out[a0 + j] = (T)x[j], out[a1 + j] = (T)x[P + j];
+    for (int i = 0; i < U; ++i)
+      if (h0 + i * p.slots < heads) x[i].load(in(h0 + i * p.slots), a0, a1);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int h = h0 + i * p.slots;
+      if (h < heads)
+        x[i].turn_and_store(h < p.q_heads ? q_out + h * p.head_dim : k_out + (h - p.q_heads) * p.head_dim, a0, a1,
+                            c, s, turns);
+    }
   }
 }
 
