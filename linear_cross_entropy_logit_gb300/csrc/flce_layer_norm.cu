@@ -2,6 +2,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <mutex>
 
 #include "host_util.h"
 #include "layer_norm.cuh"
@@ -12,6 +13,8 @@ using host::aligned;
 namespace {
 
 constexpr int64_t kMaxCols = 16384;
+constexpr int kSmemPerSm = 224 * 1024;
+constexpr int kFwdThreads = 1024, kBwdThreads = 512;  // of an SM
 
 bool shape_ok(const flce_layer_norm_desc* d) {
   if (!d || d->struct_size != sizeof(flce_layer_norm_desc)) return false;
@@ -23,20 +26,35 @@ bool shape_ok(const flce_layer_norm_desc* d) {
 int elem(const flce_layer_norm_desc* d) { return d->dtype == FLCE_BF16 ? 2 : 4; }
 int vectors(const flce_layer_norm_desc* d) { return (int)(d->cols * elem(d) / 16); }
 
-// Vectors of a row that a thread holds, and the threads that share it.
+// Vectors of a row that a thread holds, up to 32 values, and the threads that share it.
 struct Split {
   int c, threads;
 };
 Split split(const flce_layer_norm_desc* d) {
   const int v = vectors(d);
-  const int c = v <= 32 ? 1 : v <= 2048 ? 2 : 4;
+  const int c = v <= 32 ? 1 : v <= 512 ? 2 : v <= 2048 ? 4 : 8;
   return {c, (int)host::ceil_div(host::ceil_div(v, c), 32) * 32};
 }
 
-int64_t bwd_blocks(const flce_layer_norm_desc* d, int sms) {
-  const int64_t per_sm = std::max(1, std::min(16, 512 / split(d).threads));
-  return std::min<int64_t>(d->rows, per_sm * sms);
+// Rows in a block's ring: four, or what shared memory has room for (three arrays of
+// 16384 floats are 192 KB).
+int stages(const flce_layer_norm_desc* d) {
+  return vectors(d) <= 1024 ? 4 : vectors(d) <= 2048 ? 2 : 1;
 }
+
+int ring_bytes(const flce_layer_norm_desc* d, int arrays) {
+  const Split s = split(d);
+  return stages(d) * arrays * s.c * s.threads * 16;
+}
+
+// Blocks of a persistent launch: what an SM has room for, `most` threads at most.
+int64_t blocks(const flce_layer_norm_desc* d, int arrays, int most, int sms) {
+  const int per_sm = std::min(std::min(32, most / split(d).threads), kSmemPerSm / (ring_bytes(d, arrays) + 2048));
+  return std::min<int64_t>(d->rows, (int64_t)std::max(1, per_sm) * sms);
+}
+// Backward: the same number whether a gradient of the sum is given or not, for its partial
+// rows are the workspace.
+int64_t bwd_blocks(const flce_layer_norm_desc* d, int sms) { return blocks(d, 3, kBwdThreads, sms); }
 
 bool rows_ok(int64_t row, int64_t cols) { return row % 8 == 0 && row >= cols; }
 
@@ -63,37 +81,54 @@ LayerNormParams params(const flce_layer_norm_desc* d) {
   return p;
 }
 
-template <typename T, int C>
-flce_status launch_fwd(const flce_layer_norm_desc* d, const LayerNormParams& p, cudaStream_t st) {
-  const dim3 grid((unsigned)d->rows);
-  const int threads = split(d).threads;
-  return d->rms ? host::launch(layer_norm_fwd<T, C, false>, grid, threads, 0, st, p)
-                : host::launch(layer_norm_fwd<T, C, true>, grid, threads, 0, st, p);
+struct Setup {
+  std::once_flag once[host::kMaxDevices];
+  cudaError_t err[host::kMaxDevices] = {};
+};
+template <typename Kern>
+flce_status run(Setup& s, Kern kern, const flce_layer_norm_desc* d, int arrays, int64_t blocks,
+                const LayerNormParams& p, int dev, cudaStream_t st) {
+  std::call_once(s.once[dev], [&] {
+    s.err[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm);
+  });
+  if (s.err[dev] != cudaSuccess) return host::fail(s.err[dev], "cudaFuncSetAttribute");
+  return host::launch(kern, dim3((unsigned)blocks), split(d).threads, ring_bytes(d, arrays), st, p);
 }
 
-template <typename T, int C>
-flce_status launch_bwd(const flce_layer_norm_desc* d, const LayerNormParams& p, int64_t blocks, cudaStream_t st) {
-  const dim3 grid((unsigned)blocks);
-  const int threads = split(d).threads;
-  if (d->rms)
-    return p.db_partial ? host::launch(layer_norm_bwd<T, C, false, true>, grid, threads, 0, st, p)
-                        : host::launch(layer_norm_bwd<T, C, false, false>, grid, threads, 0, st, p);
-  return p.db_partial ? host::launch(layer_norm_bwd<T, C, true, true>, grid, threads, 0, st, p)
-                      : host::launch(layer_norm_bwd<T, C, true, false>, grid, threads, 0, st, p);
-}
+struct Launch {
+  const flce_layer_norm_desc* d;
+  const LayerNormParams& p;
+  int dev, sms;
+  cudaStream_t st;
+  bool bwd;
 
-template <typename T>
-flce_status run_fwd(const flce_layer_norm_desc* d, const LayerNormParams& p, cudaStream_t st) {
-  const int c = split(d).c;
-  return c == 1 ? launch_fwd<T, 1>(d, p, st) : c == 2 ? launch_fwd<T, 2>(d, p, st) : launch_fwd<T, 4>(d, p, st);
-}
-template <typename T>
-flce_status run_bwd(const flce_layer_norm_desc* d, const LayerNormParams& p, int64_t blocks, cudaStream_t st) {
-  const int c = split(d).c;
-  return c == 1   ? launch_bwd<T, 1>(d, p, blocks, st)
-         : c == 2 ? launch_bwd<T, 2>(d, p, blocks, st)
-                  : launch_bwd<T, 4>(d, p, blocks, st);
-}
+  template <typename T, int C, int STAGES, bool CENTER>
+  flce_status pick() const {
+    static Setup fwd, with, without;
+    if (!bwd) {
+      const int arrays = p.residual ? 2 : 1;
+      return run(fwd, layer_norm_fwd<T, C, STAGES, CENTER>, d, arrays, blocks(d, arrays, kFwdThreads, sms), p, dev, st);
+    }
+    const int arrays = p.ds ? 3 : 2;
+    const int64_t n = bwd_blocks(d, sms);
+    return p.db_partial ? run(with, layer_norm_bwd<T, C, STAGES, CENTER, true>, d, arrays, n, p, dev, st)
+                        : run(without, layer_norm_bwd<T, C, STAGES, CENTER, false>, d, arrays, n, p, dev, st);
+  }
+  template <typename T, int C, int STAGES>
+  flce_status pick() const {
+    return d->rms ? pick<T, C, STAGES, false>() : pick<T, C, STAGES, true>();
+  }
+  template <typename T>
+  flce_status pick() const {
+    const int c = split(d).c;
+    if (c == 1) return pick<T, 1, 4>();
+    if (c == 2) return pick<T, 2, 4>();
+    if (c == 4) return stages(d) == 4 ? pick<T, 4, 4>() : pick<T, 4, 2>();
+    if constexpr (sizeof(T) == 4) return pick<T, 8, 1>();
+    return FLCE_ERR_UNSUPPORTED;
+  }
+  flce_status operator()() const { return d->dtype == FLCE_BF16 ? pick<__nv_bfloat16>() : pick<float>(); }
+};
 
 }  // namespace
 
@@ -133,7 +168,7 @@ flce_status flce_layer_norm_forward(const flce_layer_norm_desc* d, const void* x
   p.mean = mean;
   p.rstd = rstd;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d->dtype == FLCE_BF16 ? run_fwd<__nv_bfloat16>(d, p, st) : run_fwd<float>(d, p, st);
+  return Launch{d, p, dev, sms, st, false}();
 }
 
 flce_status flce_layer_norm_backward(const flce_layer_norm_desc* d, const void* dy, const void* x, const void* weight,
@@ -148,9 +183,9 @@ flce_status flce_layer_norm_backward(const flce_layer_norm_desc* d, const void* 
   if (d->rows > 0 && (!rstd || (!d->rms && !mean))) return FLCE_ERR_ARG;
   int dev, sms;
   FLCE_HOST_TRY(host::device(&dev, &sms));
-  const int64_t blocks = bwd_blocks(d, sms);
+  const int64_t partial_rows = bwd_blocks(d, sms);
   if (!workspace || !aligned(workspace, host::kAlign) ||
-      ws_bytes < 2 * (size_t)std::max<int64_t>(1, blocks) * d->cols * 4)
+      ws_bytes < 2 * (size_t)std::max<int64_t>(1, partial_rows) * d->cols * 4)
     return FLCE_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   LayerNormParams p = params(d);
@@ -162,11 +197,10 @@ flce_status flce_layer_norm_backward(const flce_layer_norm_desc* d, const void* 
   p.mean = const_cast<float*>(mean);
   p.rstd = const_cast<float*>(rstd);
   p.dw_partial = static_cast<float*>(workspace);
-  p.db_partial = dbias ? p.dw_partial + blocks * d->cols : nullptr;
-  if (d->rows > 0)
-    FLCE_HOST_TRY(d->dtype == FLCE_BF16 ? run_bwd<__nv_bfloat16>(d, p, blocks, st) : run_bwd<float>(d, p, blocks, st));
+  p.db_partial = dbias ? p.dw_partial + partial_rows * d->cols : nullptr;
+  if (d->rows > 0) FLCE_HOST_TRY((Launch{d, p, dev, sms, st, true}()));
   return host::launch(layer_norm_dw, dim3((unsigned)host::ceil_div(d->cols, 32), dbias ? 2 : 1), 1024, 0, st,
-                      static_cast<const float*>(p.dw_partial), static_cast<const float*>(p.db_partial), (int)blocks,
+                      static_cast<const float*>(p.dw_partial), static_cast<const float*>(p.db_partial), (int)partial_rows,
                       (int)d->cols, dweight, dbias);
 }
 

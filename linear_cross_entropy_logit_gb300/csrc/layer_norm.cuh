@@ -6,8 +6,8 @@
 //   backward  dx = r (g w - mean(g w) - n mean(g w n)) + ds   (RMS: without mean(g w)),
 //             dw = sum over rows of g n,  db = sum over rows of g
 //
-// A few flops per value: bound by HBM.  A row is held in the registers of the
-// threads that share it, so that it is read once and the variance is summed from
+// A few flops per value: bound by HBM.  Persistent blocks, a row at a time shared by a
+// block's threads, the next rows on their way to shared memory.  The variance is summed from
 // differences to the mean.  All arithmetic is fp32; outputs are rounded once.
 #pragma once
 #include <cuda_bf16.h>
@@ -27,6 +27,8 @@ struct LayerNormParams {
   int vectors;               // 16-byte vectors of a row
   float eps, inv_cols;
 };
+
+constexpr int kLayerNormThreads = 512;  // at most
 
 // 16 bytes as floats.
 template <typename T>
@@ -58,165 +60,212 @@ struct Vec {
     return make_uint4(u[0], u[1], u[2], u[3]);
   }
   __device__ __forceinline__ void store(void* p, int64_t i) const { static_cast<uint4*>(p)[i] = packed(); }
-  // To the type and back.
-  __device__ __forceinline__ void round() {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 v = packed();
-      load(&v, 0);
+};
+
+// Sums over the block of K values, the same in every thread.  `shared` holds 32 K floats
+// that no thread still reads.
+template <int K>
+__device__ __forceinline__ void block_sum(float (&x)[K], float (*shared)[K]) {
+  auto warp = [&] {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < K; ++k) x[k] += __shfl_xor_sync(~0u, x[k], o);
+  };
+  warp();
+  if (blockDim.x == 32) return;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (lane == 0) shared[threadIdx.x >> 5][k] = x[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) x[k] = lane < blockDim.x >> 5 ? shared[lane][k] : 0.f;
+  warp();
+}
+
+// The rows of a persistent block that are on their way, each of `arrays` arrays, in shared
+// memory.  A thread copies the vectors that it reads itself, so that nothing waits for
+// another thread, and no registers are held for them.
+template <int C>
+struct RowRing {
+  uint4* mine;
+  int vectors, arrays;
+  __device__ __forceinline__ RowRing(uint4* ring, int vectors, int arrays)
+      : mine(ring + threadIdx.x), vectors(vectors), arrays(arrays) {}
+  __device__ __forceinline__ uint4* at(int s, int array, int c) const {
+    return mine + ((s * arrays + array) * C + c) * blockDim.x;
+  }
+  __device__ __forceinline__ void fetch(int s, int array, const void* row) const {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int i = c * blockDim.x + threadIdx.x;
+      if (i < vectors) cp_async<16>(at(s, array, c), static_cast<const uint4*>(row) + i);
     }
   }
 };
 
-// Sum over the block, the same in every thread.  `shared` holds 32 floats that no
-// thread still reads.
-__device__ __forceinline__ float block_sum(float x, float* shared) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-  if (blockDim.x == 32) return x;
-  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = (threadIdx.x & 31) < blockDim.x >> 5 ? shared[threadIdx.x & 31] : 0.f;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-  return x;
-}
-
-// A block a row, C vectors a thread.
-template <typename T, int C, bool CENTER>
-__global__ void __launch_bounds__(1024) layer_norm_fwd(const __grid_constant__ LayerNormParams p) {
-  __shared__ float shared[2][32];
-  const int64_t row = blockIdx.x;
-  const T* x = static_cast<const T*>(p.x) + row * p.x_row;
-  grid_wait();
-  Vec<T> v[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int i = c * blockDim.x + threadIdx.x;
-    if (i < p.vectors)
-      v[c].load(x, i);
-    else
-      v[c].fill(0.f);
-  }
-  if (p.residual) {
-    const T* r = static_cast<const T*>(p.residual) + row * p.residual_row;
-    Vec<T> e[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int i = c * blockDim.x + threadIdx.x;
-      if (i < p.vectors) e[c].load(r, i);
+// Persistent over rows, C vectors of a row a thread, STAGES rows in the ring.
+template <typename T, int C, int STAGES, bool CENTER>
+__global__ void __launch_bounds__(kLayerNormThreads) layer_norm_fwd(const __grid_constant__ LayerNormParams p) {
+  extern __shared__ uint4 ring_space[];
+  __shared__ float shared[2][2][32][1];
+  constexpr int N = Vec<T>::N;
+  RowRing<C> ring(ring_space, p.vectors, p.residual ? 2 : 1);
+  auto fetch = [&](int s, int64_t row) {
+    if (row < p.rows) {
+      ring.fetch(s, 0, static_cast<const T*>(p.x) + row * p.x_row);
+      if (p.residual) ring.fetch(s, 1, static_cast<const T*>(p.residual) + row * p.residual_row);
     }
+    cp_async_commit();
+  };
+  grid_wait();
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) fetch(s, blockIdx.x + (int64_t)s * gridDim.x);
+  int stage = 0, parity = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    fetch((stage + STAGES - 1) % STAGES, row + (STAGES - 1) * (int64_t)gridDim.x);
+    cp_async_wait<STAGES - 1>();
+    Vec<T> v[C];
+    float sum[1] = {0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = c * blockDim.x + threadIdx.x;
-      if (i < p.vectors) {
+      if (i >= p.vectors) {
+        v[c].fill(0.f);
+        continue;
+      }
+      v[c].load(ring.at(stage, 0, c), 0);
+      if (p.residual) {
+        Vec<T> e;
+        e.load(ring.at(stage, 1, c), 0);
 #pragma unroll
-        for (int j = 0; j < Vec<T>::N; ++j) v[c].f[j] += e[c].f[j];
-        v[c].round();
-        v[c].store(p.sum, row * p.vectors + i);
+        for (int j = 0; j < N; ++j) v[c].f[j] += e.f[j];
+        const uint4 stored = v[c].packed();
+        static_cast<uint4*>(p.sum)[row * p.vectors + i] = stored;
+        v[c].load(&stored, 0);
+      }
+      if (CENTER)
+#pragma unroll
+        for (int j = 0; j < N; ++j) sum[0] += v[c].f[j];
+    }
+    float mean = 0.f;
+    if constexpr (CENTER) {
+      block_sum(sum, shared[parity][0]);
+      mean = sum[0] * p.inv_cols;
+    }
+    float square[1] = {0.f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const bool in = c * blockDim.x + threadIdx.x < p.vectors;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        v[c].f[j] -= mean;
+        if (in) square[0] = fmaf(v[c].f[j], v[c].f[j], square[0]);
       }
     }
-  }
-  float mean = 0.f;
-  if constexpr (CENTER) {
-    float t = 0.f;
+    block_sum(square, shared[parity][1]);
+    const float r = rsqrtf(square[0] * p.inv_cols + p.eps);
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int c = 0; c < C; ++c) {
+      const int i = c * blockDim.x + threadIdx.x;
+      if (i >= p.vectors) continue;
+      Vec<T> w, b;
+      if (p.w)
+        w.load(p.w, i);
+      else
+        w.fill(1.f);
+      if (p.b)
+        b.load(p.b, i);
+      else
+        b.fill(0.f);
 #pragma unroll
-      for (int j = 0; j < Vec<T>::N; ++j) t += v[c].f[j];
-    mean = block_sum(t, shared[0]) * p.inv_cols;
-  }
-  float t = 0.f;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const bool in = c * blockDim.x + threadIdx.x < p.vectors;
-#pragma unroll
-    for (int j = 0; j < Vec<T>::N; ++j) {
-      v[c].f[j] -= mean;
-      if (in) t = fmaf(v[c].f[j], v[c].f[j], t);
+      for (int j = 0; j < N; ++j) v[c].f[j] = fmaf(v[c].f[j] * r, w.f[j], b.f[j]);
+      v[c].store(p.out, row * p.vectors + i);
     }
-  }
-  const float r = rsqrtf(block_sum(t, shared[1]) * p.inv_cols + p.eps);
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int i = c * blockDim.x + threadIdx.x;
-    if (i >= p.vectors) continue;
-    Vec<T> w, b;
-    if (p.w)
-      w.load(p.w, i);
-    else
-      w.fill(1.f);
-    if (p.b)
-      b.load(p.b, i);
-    else
-      b.fill(0.f);
-#pragma unroll
-    for (int j = 0; j < Vec<T>::N; ++j) v[c].f[j] = fmaf(v[c].f[j] * r, w.f[j], b.f[j]);
-    v[c].store(p.out, row * p.vectors + i);
-  }
-  if (threadIdx.x == 0) {
-    if (CENTER) p.mean[row] = mean;
-    p.rstd[row] = r;
+    if (threadIdx.x == 0) {
+      if (CENTER) p.mean[row] = mean;
+      p.rstd[row] = r;
+    }
+    stage = (stage + 1) % STAGES;
+    parity ^= 1;
   }
 }
 
 // Persistent over rows: a thread has the same columns of each, so that the weights'
 // gradients are summed in its registers, in the order of the rows; one partial row per
-// block goes to the workspace.  No atomics: results do not change run to run.
-template <typename T, int C, bool CENTER, bool BIAS>
-__global__ void __launch_bounds__(1024) layer_norm_bwd(const __grid_constant__ LayerNormParams p) {
-  __shared__ float shared[2][2][32];
-  constexpr int N = Vec<T>::N;
+// block goes to the workspace.  No atomics: results do not change run to run.  The row is
+// read from the ring twice, before and after its sums, instead of being held.
+template <typename T, int C, int STAGES, bool CENTER, bool BIAS>
+__global__ void __launch_bounds__(kLayerNormThreads) layer_norm_bwd(const __grid_constant__ LayerNormParams p) {
+  extern __shared__ uint4 ring_space[];
+  constexpr int K = CENTER ? 2 : 1, N = Vec<T>::N;
+  __shared__ float shared[2][32][K];
+  RowRing<C> ring(ring_space, p.vectors, p.ds ? 3 : 2);
+  auto fetch = [&](int s, int64_t row) {
+    if (row < p.rows) {
+      ring.fetch(s, 0, static_cast<const T*>(p.x) + row * p.x_row);
+      ring.fetch(s, 1, static_cast<const uint4*>(p.dy) + row * p.vectors);
+      if (p.ds) ring.fetch(s, 2, static_cast<const uint4*>(p.ds) + row * p.vectors);
+    }
+    cp_async_commit();
+  };
   float dw[C][N] = {}, db[BIAS ? C : 1][N] = {};
   grid_wait();
-  int turn = 0;
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) fetch(s, blockIdx.x + (int64_t)s * gridDim.x);
+  int stage = 0, parity = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const T* x = static_cast<const T*>(p.x) + row * p.x_row;
+    fetch((stage + STAGES - 1) % STAGES, row + (STAGES - 1) * (int64_t)gridDim.x);
     const float mean = CENTER ? p.mean[row] : 0.f, r = p.rstd[row];
-    Vec<T> v[C], g[C];
-    float gw = 0.f, gwn = 0.f;
+    cp_async_wait<STAGES - 1>();
+    float sum[K] = {};  // of g w n, and of g w
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = c * blockDim.x + threadIdx.x;
       if (i >= p.vectors) continue;
-      v[c].load(x, i);
-      g[c].load(p.dy, row * p.vectors + i);
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int i = c * blockDim.x + threadIdx.x;
-      if (i >= p.vectors) continue;
-      Vec<T> w;
+      Vec<T> x, g, w;
+      x.load(ring.at(stage, 0, c), 0);
+      g.load(ring.at(stage, 1, c), 0);
       if (p.w)
         w.load(p.w, i);
       else
         w.fill(1.f);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const float n = (v[c].f[j] - mean) * r;
-        dw[c][j] = fmaf(g[c].f[j], n, dw[c][j]);
-        if (BIAS) db[c][j] += g[c].f[j];
-        v[c].f[j] = n;
-        g[c].f[j] *= w.f[j];
-        if (CENTER) gw += g[c].f[j];
-        gwn = fmaf(g[c].f[j], n, gwn);
+        const float n = (x.f[j] - mean) * r, gw = g.f[j] * w.f[j];
+        dw[c][j] = fmaf(g.f[j], n, dw[c][j]);
+        if (BIAS) db[c][j] += g.f[j];
+        sum[0] = fmaf(gw, n, sum[0]);
+        if (CENTER) sum[K - 1] += gw;
       }
     }
-    gwn = block_sum(gwn, shared[turn][0]) * p.inv_cols;
-    if (CENTER) gw = block_sum(gw, shared[turn][1]) * p.inv_cols;
-    turn ^= 1;
+    block_sum(sum, shared[parity]);
+    const float along = sum[0] * p.inv_cols, level = CENTER ? sum[K - 1] * p.inv_cols : 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = c * blockDim.x + threadIdx.x;
       if (i >= p.vectors) continue;
-      Vec<T> d;
+      Vec<T> x, g, w, d;
+      x.load(ring.at(stage, 0, c), 0);
+      g.load(ring.at(stage, 1, c), 0);
+      if (p.w)
+        w.load(p.w, i);
+      else
+        w.fill(1.f);
       if (p.ds)
-        d.load(p.ds, row * p.vectors + i);
+        d.load(ring.at(stage, 2, c), 0);
       else
         d.fill(0.f);
 #pragma unroll
-      for (int j = 0; j < N; ++j) d.f[j] = fmaf(r, g[c].f[j] - gw * (CENTER ? 1.f : 0.f) - v[c].f[j] * gwn, d.f[j]);
+      for (int j = 0; j < N; ++j) {
+        const float n = (x.f[j] - mean) * r;
+        d.f[j] = fmaf(r, fmaf(g.f[j], w.f[j], -level) - n * along, d.f[j]);
+      }
       d.store(p.out, row * p.vectors + i);
     }
+    stage = (stage + 1) % STAGES;
+    parity ^= 1;
   }
 #pragma unroll
   for (int c = 0; c < C; ++c) {
