@@ -14,7 +14,8 @@ namespace {
 
 constexpr int64_t kMaxCols = 16384;
 constexpr int kSmemPerSm = 224 * 1024;
-constexpr int kFwdThreads = 1024, kBwdThreads = 512;  // of an SM
+// Threads of an SM, as many as have room for their registers (80 and 128).
+constexpr int kFwdThreads = 768, kBwdThreads = 512;
 
 bool shape_ok(const flce_layer_norm_desc* d) {
   if (!d || d->struct_size != sizeof(flce_layer_norm_desc)) return false;
@@ -31,8 +32,8 @@ struct Split {
   int c, threads;
 };
 Split split(const flce_layer_norm_desc* d) {
-  const int v = vectors(d);
-  const int c = v <= 32 ? 1 : v <= 512 ? 2 : v <= 2048 ? 4 : 8;
+  const int v = vectors(d), sixteen = elem(d);  // vectors of 16 values
+  const int c = v <= 32 ? 1 : v <= sixteen * kLayerNormThreads ? sixteen : 2 * sixteen;
   return {c, (int)host::ceil_div(host::ceil_div(v, c), 32) * 32};
 }
 
@@ -106,10 +107,10 @@ struct Launch {
   flce_status pick() const {
     static Setup fwd, with, without;
     if (!bwd) {
-      const int arrays = p.residual ? 2 : 1;
+      const int arrays = 2;
       return run(fwd, layer_norm_fwd<T, C, STAGES, CENTER>, d, arrays, blocks(d, arrays, kFwdThreads, sms), p, dev, st);
     }
-    const int arrays = p.ds ? 3 : 2;
+    const int arrays = 3;
     const int64_t n = bwd_blocks(d, sms);
     return p.db_partial ? run(with, layer_norm_bwd<T, C, STAGES, CENTER, true>, d, arrays, n, p, dev, st)
                         : run(without, layer_norm_bwd<T, C, STAGES, CENTER, false>, d, arrays, n, p, dev, st);
@@ -121,11 +122,12 @@ struct Launch {
   template <typename T>
   flce_status pick() const {
     const int c = split(d).c;
+    constexpr int kSixteen = sizeof(T);
     if (c == 1) return pick<T, 1, 4>();
-    if (c == 2) return pick<T, 2, 4>();
-    if (c == 4) return stages(d) == 4 ? pick<T, 4, 4>() : pick<T, 4, 2>();
-    if constexpr (sizeof(T) == 4) return pick<T, 8, 1>();
-    return FLCE_ERR_UNSUPPORTED;
+    if (c == 2 * kSixteen) return pick<T, 2 * kSixteen, sizeof(T) == 2 ? 2 : 1>();
+    if constexpr (sizeof(T) == 4)
+      if (stages(d) == 2) return pick<T, kSixteen, 2>();
+    return pick<T, kSixteen, 4>();
   }
   flce_status operator()() const { return d->dtype == FLCE_BF16 ? pick<__nv_bfloat16>() : pick<float>(); }
 };

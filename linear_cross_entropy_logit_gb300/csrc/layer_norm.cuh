@@ -30,104 +30,176 @@ struct LayerNormParams {
 
 constexpr int kLayerNormThreads = 512;  // at most
 
-// 16 bytes as floats.
+// 16 bytes as floats, packed in twos.
 template <typename T>
 struct Vec {
-  static constexpr int N = 16 / sizeof(T);
-  float f[N];
-  __device__ __forceinline__ void load(const void* p, int64_t i) {
-    const uint4 v = static_cast<const uint4*>(p)[i];
+  static constexpr int N = 16 / sizeof(T), H = N / 2;
+  uint64_t f[H];
+  __device__ __forceinline__ void unpack(const uint4& v) {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (sizeof(T) == 4) {
-        f[j] = __uint_as_float(u[j]);
-      } else {
-        f[2 * j] = __uint_as_float(u[j] << 16);
-        f[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-      }
-    }
+    for (int j = 0; j < H; ++j)
+      f[j] = sizeof(T) == 4 ? pack_u32x2(u[2 * j], u[2 * j + 1]) : pack_u32x2(u[j] << 16, u[j] & 0xffff0000u);
   }
+  __device__ __forceinline__ void load(const void* p, int64_t i) { unpack(static_cast<const uint4*>(p)[i]); }
   __device__ __forceinline__ void fill(float x) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) f[j] = x;
+    for (int j = 0; j < H; ++j) f[j] = pack_f32x2(x, x);
   }
   __device__ __forceinline__ uint4 packed() const {
     uint32_t u[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      u[j] = sizeof(T) == 4 ? __float_as_uint(f[j]) : pack_bf16x2(f[2 * j], f[2 * j + 1]);
+    for (int j = 0; j < H; ++j) {
+      float a, b;
+      unpack_f32x2(f[j], a, b);
+      if constexpr (sizeof(T) == 4)
+        u[2 * j] = __float_as_uint(a), u[2 * j + 1] = __float_as_uint(b);
+      else
+        u[j] = pack_bf16x2(a, b);
+    }
     return make_uint4(u[0], u[1], u[2], u[3]);
   }
-  __device__ __forceinline__ void store(void* p, int64_t i) const { static_cast<uint4*>(p)[i] = packed(); }
 };
-
-// Sums over the block of K values, the same in every thread.  `shared` holds 32 K floats
-// that no thread still reads.
-template <int K>
-__device__ __forceinline__ void block_sum(float (&x)[K], float (*shared)[K]) {
-  auto warp = [&] {
+__device__ __forceinline__ float halves(uint64_t x) {
+  float a, b;
+  unpack_f32x2(x, a, b);
+  return a + b;
+}
+__device__ __forceinline__ float lanes(float x) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-#pragma unroll
-      for (int k = 0; k < K; ++k) x[k] += __shfl_xor_sync(~0u, x[k], o);
-  };
-  warp();
-  if (blockDim.x == 32) return;
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-    if (lane == 0) shared[threadIdx.x >> 5][k] = x[k];
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < K; ++k) x[k] = lane < blockDim.x >> 5 ? shared[lane][k] : 0.f;
-  warp();
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+  return x;
 }
 
-// The rows of a persistent block that are on their way, each of `arrays` arrays, in shared
-// memory.  A thread copies the vectors that it reads itself, so that nothing waits for
-// another thread, and no registers are held for them.
-template <int C>
+// Two values of each warp, those of warp i in lane i of every warp, zeros in the other
+// lanes.  Two calls in a row use different `shared`; the barrier of the second tells that
+// the first has been read.
+constexpr int kLayerNormWarps = kLayerNormThreads / 32;
+__device__ __forceinline__ float2 warp_pairs(float a, float b, float2* shared) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (warps == 1) return lane ? make_float2(0.f, 0.f) : make_float2(a, b);
+  if (lane == 0) shared[threadIdx.x >> 5] = make_float2(a, b);
+  __syncthreads();
+  return lane < warps ? shared[lane] : make_float2(0.f, 0.f);
+}
+// Their sums.  Read by every lane, two warps at a time, and added: shorter than a tree of
+// shuffles, which the forward's weighted sums take (backward of 8192 rows of 4096, bf16:
+// 48 -> 38 us).  `shared` has zeros behind the last warp.
+__device__ __forceinline__ float2 warp_pairs_sum(float a, float b, float2* shared) {
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return make_float2(a, b);
+  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = make_float2(a, b);
+  __syncthreads();
+  float2 t = make_float2(0.f, 0.f);
+  for (int i = 0; i < warps; i += 2) {
+    const float4 q = *reinterpret_cast<const float4*>(shared + i);
+    t.x += q.x + q.z;
+    t.y += q.y + q.w;
+  }
+  return t;
+}
+
+// The rows of a persistent block that are on their way, A arrays of each (the last if it is
+// there), in shared memory.  A thread copies the vectors that it reads itself, so that
+// nothing waits for another thread, and no registers are held for them.
+template <int C, int STAGES, int A>
 struct RowRing {
   uint4* mine;
-  int vectors, arrays;
-  __device__ __forceinline__ RowRing(uint4* ring, int vectors, int arrays)
-      : mine(ring + threadIdx.x), vectors(vectors), arrays(arrays) {}
-  __device__ __forceinline__ uint4* at(int s, int array, int c) const {
-    return mine + ((s * arrays + array) * C + c) * blockDim.x;
+  const uint4* from[A];
+  int64_t step[A];  // from a row of this block to the next
+  int64_t left;     // rows not yet fetched
+  int vectors, arrays, in = 0, out = 0;  // stages to fill and to read next
+  __device__ __forceinline__ RowRing(uint4* ring, const LayerNormParams& p, int arrays)
+      : mine(ring + threadIdx.x), left(p.rows > blockIdx.x ? (p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x : 0),
+        vectors(p.vectors), arrays(arrays) {}
+  // row_vectors: from a row of the array to the next, in vectors
+  __device__ __forceinline__ void source(int a, const void* p, int64_t row_vectors) {
+    from[a] = static_cast<const uint4*>(p) + blockIdx.x * row_vectors + threadIdx.x;
+    step[a] = gridDim.x * row_vectors;
   }
-  __device__ __forceinline__ void fetch(int s, int array, const void* row) const {
+  __device__ __forceinline__ void fetch() {
+    if (left > 0) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int i = c * blockDim.x + threadIdx.x;
-      if (i < vectors) cp_async<16>(at(s, array, c), static_cast<const uint4*>(row) + i);
+      for (int a = 0; a < A; ++a) {
+        if (a + 1 == A && arrays < A) continue;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (c * blockDim.x + threadIdx.x < vectors)
+            cp_async<16>(mine + ((in * A + a) * C + c) * blockDim.x, from[a] + c * blockDim.x);
+        from[a] += step[a];
+      }
+      --left;
     }
+    cp_async_commit();
+    in = in + 1 == STAGES ? 0 : in + 1;
+  }
+  __device__ __forceinline__ const uint4& at(int a, int c) const { return mine[((out * A + a) * C + c) * blockDim.x]; }
+  __device__ __forceinline__ void next() { out = out + 1 == STAGES ? 0 : out + 1; }
+};
+
+// A thread's columns of the weight or the bias: held in registers where there are few, else
+// read again for each row.
+template <typename T, int C>
+struct Columns {
+  static constexpr bool kHeld = C * Vec<T>::N <= 16;
+  const void* p;
+  float missing;
+  Vec<T> held[kHeld ? C : 1];
+  __device__ __forceinline__ void take(Vec<T>& v, int c, int vectors) const {
+    const int i = c * blockDim.x + threadIdx.x;
+    if (p && i < vectors)
+      v.load(p, i);
+    else
+      v.fill(missing);
+  }
+  __device__ __forceinline__ Columns(const void* p, float missing, int vectors) : p(p), missing(missing) {
+    if constexpr (kHeld) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) take(held[c], c, vectors);
+    }
+  }
+  __device__ __forceinline__ Vec<T> at(int c, int vectors) const {
+    if constexpr (kHeld) return held[c];
+    Vec<T> v;
+    take(v, c, vectors);
+    return v;
   }
 };
 
-// Persistent over rows, C vectors of a row a thread, STAGES rows in the ring.
+// Persistent over rows, C vectors of a row a thread, STAGES rows in the ring.  Each warp takes
+// its own part's mean m_w and sum of squares s_w around it; the row's are
+//   mean = sum n_w m_w / n,   sum s_w + sum n_w (m_w - mean)^2:
+// one barrier a row, and nothing cancels.
 template <typename T, int C, int STAGES, bool CENTER>
-__global__ void __launch_bounds__(kLayerNormThreads) layer_norm_fwd(const __grid_constant__ LayerNormParams p) {
+__global__ void __maxnreg__(80) layer_norm_fwd(const __grid_constant__ LayerNormParams p) {
   extern __shared__ uint4 ring_space[];
-  __shared__ float shared[2][2][32][1];
-  constexpr int N = Vec<T>::N;
-  RowRing<C> ring(ring_space, p.vectors, p.residual ? 2 : 1);
-  auto fetch = [&](int s, int64_t row) {
-    if (row < p.rows) {
-      ring.fetch(s, 0, static_cast<const T*>(p.x) + row * p.x_row);
-      if (p.residual) ring.fetch(s, 1, static_cast<const T*>(p.residual) + row * p.residual_row);
-    }
-    cp_async_commit();
-  };
+  __shared__ float2 shared[2][kLayerNormWarps];
+  __shared__ float share[kLayerNormWarps];  // n_w / n
+  constexpr int H = Vec<T>::H;
+  RowRing<C, STAGES, 2> ring(ring_space, p, p.residual ? 2 : 1);
+  ring.source(0, p.x, p.x_row / Vec<T>::N);
+  ring.source(1, p.residual, p.residual_row / Vec<T>::N);
+  float count = 0.f;  // values of this warp
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    count += Vec<T>::N * min(32, max(0, p.vectors - (c * (int)blockDim.x + ((int)threadIdx.x & ~31))));
+  const float inv_count = count > 0.f ? 1.f / count : 0.f;
+  if ((threadIdx.x & 31) == 0) share[threadIdx.x >> 5] = count * p.inv_cols;
+  __syncthreads();
+  const float share_of_lane = (threadIdx.x & 31) < blockDim.x >> 5 ? share[threadIdx.x & 31] : 0.f;
   grid_wait();
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) fetch(s, blockIdx.x + (int64_t)s * gridDim.x);
-  int stage = 0, parity = 0;
+  for (int s = 0; s < STAGES - 1; ++s) ring.fetch();
+  const Columns<T, C> weight(p.w, 1.f, p.vectors), bias(p.b, 0.f, p.vectors);
+  const int64_t out_step = (int64_t)gridDim.x * p.vectors;
+  uint4* out = static_cast<uint4*>(p.out) + (int64_t)blockIdx.x * p.vectors + threadIdx.x;
+  uint4* sum_out = static_cast<uint4*>(p.sum) + (int64_t)blockIdx.x * p.vectors + threadIdx.x;
+  int parity = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    fetch((stage + STAGES - 1) % STAGES, row + (STAGES - 1) * (int64_t)gridDim.x);
+    ring.fetch();
     cp_async_wait<STAGES - 1>();
     Vec<T> v[C];
-    float sum[1] = {0.f};
+    uint64_t sum = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = c * blockDim.x + threadIdx.x;
@@ -135,149 +207,154 @@ __global__ void __launch_bounds__(kLayerNormThreads) layer_norm_fwd(const __grid
         v[c].fill(0.f);
         continue;
       }
-      v[c].load(ring.at(stage, 0, c), 0);
+      v[c].unpack(ring.at(0, c));
       if (p.residual) {
         Vec<T> e;
-        e.load(ring.at(stage, 1, c), 0);
+        e.unpack(ring.at(1, c));
 #pragma unroll
-        for (int j = 0; j < N; ++j) v[c].f[j] += e.f[j];
+        for (int j = 0; j < H; ++j) v[c].f[j] = add_f32x2(v[c].f[j], e.f[j]);
         const uint4 stored = v[c].packed();
-        static_cast<uint4*>(p.sum)[row * p.vectors + i] = stored;
-        v[c].load(&stored, 0);
+        sum_out[c * blockDim.x] = stored;
+        v[c].unpack(stored);
       }
       if (CENTER)
 #pragma unroll
-        for (int j = 0; j < N; ++j) sum[0] += v[c].f[j];
+        for (int j = 0; j < H; ++j) sum = add_f32x2(sum, v[c].f[j]);
     }
-    float mean = 0.f;
-    if constexpr (CENTER) {
-      block_sum(sum, shared[parity][0]);
-      mean = sum[0] * p.inv_cols;
-    }
-    float square[1] = {0.f};
+    const float part = CENTER ? lanes(halves(sum)) * inv_count : 0.f;
+    const uint64_t minus = pack_f32x2(-part, -part);
+    uint64_t square = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const bool in = c * blockDim.x + threadIdx.x < p.vectors;
+      if (c * blockDim.x + threadIdx.x >= p.vectors) continue;
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        v[c].f[j] -= mean;
-        if (in) square[0] = fmaf(v[c].f[j], v[c].f[j], square[0]);
+      for (int j = 0; j < H; ++j) {
+        const uint64_t d = CENTER ? add_f32x2(v[c].f[j], minus) : v[c].f[j];
+        square = fma_f32x2(d, d, square);
       }
     }
-    block_sum(square, shared[parity][1]);
-    const float r = rsqrtf(square[0] * p.inv_cols + p.eps);
+    const float2 w = warp_pairs(part, lanes(halves(square)), shared[parity]);
+    const float mean = CENTER ? lanes(share_of_lane * w.x) : 0.f, off = w.x - mean;
+    const float total = lanes(CENTER ? fmaf(share_of_lane * off, off, w.y * p.inv_cols) : w.y * p.inv_cols);
+    const float r = rsqrtf(total + p.eps);
+    const uint64_t r2 = pack_f32x2(r, r), m2 = pack_f32x2(-mean, -mean);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = c * blockDim.x + threadIdx.x;
       if (i >= p.vectors) continue;
-      Vec<T> w, b;
-      if (p.w)
-        w.load(p.w, i);
-      else
-        w.fill(1.f);
-      if (p.b)
-        b.load(p.b, i);
-      else
-        b.fill(0.f);
+      const Vec<T> wc = weight.at(c, p.vectors), bc = bias.at(c, p.vectors);
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[c].f[j] = fmaf(v[c].f[j] * r, w.f[j], b.f[j]);
-      v[c].store(p.out, row * p.vectors + i);
+      for (int j = 0; j < H; ++j) {
+        const uint64_t d = CENTER ? add_f32x2(v[c].f[j], m2) : v[c].f[j];
+        v[c].f[j] = fma_f32x2(mul_f32x2(d, r2), wc.f[j], bc.f[j]);
+      }
+      out[c * blockDim.x] = v[c].packed();
     }
     if (threadIdx.x == 0) {
       if (CENTER) p.mean[row] = mean;
       p.rstd[row] = r;
     }
-    stage = (stage + 1) % STAGES;
+    ring.next();
+    out += out_step;
+    sum_out += out_step;
     parity ^= 1;
   }
 }
 
 // Persistent over rows: a thread has the same columns of each, so that the weights'
 // gradients are summed in its registers, in the order of the rows; one partial row per
-// block goes to the workspace.  No atomics: results do not change run to run.  The row is
-// read from the ring twice, before and after its sums, instead of being held.
+// block goes to the workspace.  No atomics: results do not change run to run.  n and g w
+// are held over the row's sums where a thread has few, else made again from the ring.
 template <typename T, int C, int STAGES, bool CENTER, bool BIAS>
 __global__ void __launch_bounds__(kLayerNormThreads) layer_norm_bwd(const __grid_constant__ LayerNormParams p) {
   extern __shared__ uint4 ring_space[];
-  constexpr int K = CENTER ? 2 : 1, N = Vec<T>::N;
-  __shared__ float shared[2][32][K];
-  RowRing<C> ring(ring_space, p.vectors, p.ds ? 3 : 2);
-  auto fetch = [&](int s, int64_t row) {
-    if (row < p.rows) {
-      ring.fetch(s, 0, static_cast<const T*>(p.x) + row * p.x_row);
-      ring.fetch(s, 1, static_cast<const uint4*>(p.dy) + row * p.vectors);
-      if (p.ds) ring.fetch(s, 2, static_cast<const uint4*>(p.ds) + row * p.vectors);
-    }
-    cp_async_commit();
-  };
-  float dw[C][N] = {}, db[BIAS ? C : 1][N] = {};
+  __shared__ __align__(16) float2 shared[2][kLayerNormWarps];
+  constexpr int H = Vec<T>::H;
+  constexpr bool kHeld = Columns<T, C>::kHeld;
+  RowRing<C, STAGES, 3> ring(ring_space, p, p.ds ? 3 : 2);
+  ring.source(0, p.x, p.x_row / Vec<T>::N);
+  ring.source(1, p.dy, p.vectors);
+  ring.source(2, p.ds, p.vectors);
+  uint64_t dw[C][H] = {}, db[BIAS ? C : 1][H] = {};
+  if (threadIdx.x < 2) shared[threadIdx.x][(blockDim.x >> 5) & (kLayerNormWarps - 1)] = make_float2(0.f, 0.f);
   grid_wait();
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) fetch(s, blockIdx.x + (int64_t)s * gridDim.x);
-  int stage = 0, parity = 0;
+  for (int s = 0; s < STAGES - 1; ++s) ring.fetch();
+  const Columns<T, C> weight(p.w, 1.f, p.vectors);
+  uint4* out = static_cast<uint4*>(p.out) + (int64_t)blockIdx.x * p.vectors + threadIdx.x;
+  int parity = 0;
+  // of the row after this one, on their way
+  float mean_next = CENTER && blockIdx.x < p.rows ? p.mean[blockIdx.x] : 0.f;
+  float r_next = blockIdx.x < p.rows ? p.rstd[blockIdx.x] : 0.f;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    fetch((stage + STAGES - 1) % STAGES, row + (STAGES - 1) * (int64_t)gridDim.x);
-    const float mean = CENTER ? p.mean[row] : 0.f, r = p.rstd[row];
+    ring.fetch();
+    const float r = r_next;
+    const uint64_t r2 = pack_f32x2(r, r), m2 = pack_f32x2(-mean_next, -mean_next);
+    if (row + gridDim.x < p.rows) {
+      if (CENTER) mean_next = p.mean[row + gridDim.x];
+      r_next = p.rstd[row + gridDim.x];
+    }
     cp_async_wait<STAGES - 1>();
-    float sum[K] = {};  // of g w n, and of g w
+    Vec<T> n[kHeld ? C : 1], gw[kHeld ? C : 1];
+    uint64_t sn = 0, sg = 0;  // sums of g w n, and of g w
+    auto read = [&](int c, Vec<T>& n, Vec<T>& g) {
+      n.unpack(ring.at(0, c));
+      g.unpack(ring.at(1, c));
+#pragma unroll
+      for (int j = 0; j < H; ++j) n.f[j] = mul_f32x2(CENTER ? add_f32x2(n.f[j], m2) : n.f[j], r2);
+    };
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int i = c * blockDim.x + threadIdx.x;
-      if (i >= p.vectors) continue;
-      Vec<T> x, g, w;
-      x.load(ring.at(stage, 0, c), 0);
-      g.load(ring.at(stage, 1, c), 0);
-      if (p.w)
-        w.load(p.w, i);
-      else
-        w.fill(1.f);
+      if (c * blockDim.x + threadIdx.x >= p.vectors) continue;
+      Vec<T>&nc = n[kHeld ? c : 0], &gc = gw[kHeld ? c : 0];
+      read(c, nc, gc);
+      const Vec<T> w = weight.at(c, p.vectors);
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float n = (x.f[j] - mean) * r, gw = g.f[j] * w.f[j];
-        dw[c][j] = fmaf(g.f[j], n, dw[c][j]);
-        if (BIAS) db[c][j] += g.f[j];
-        sum[0] = fmaf(gw, n, sum[0]);
-        if (CENTER) sum[K - 1] += gw;
+      for (int j = 0; j < H; ++j) {
+        dw[c][j] = fma_f32x2(gc.f[j], nc.f[j], dw[c][j]);
+        if (BIAS) db[c][j] = add_f32x2(db[c][j], gc.f[j]);
+        gc.f[j] = mul_f32x2(gc.f[j], w.f[j]);
+        sn = fma_f32x2(gc.f[j], nc.f[j], sn);
+        if (CENTER) sg = add_f32x2(sg, gc.f[j]);
       }
     }
-    block_sum(sum, shared[parity]);
-    const float along = sum[0] * p.inv_cols, level = CENTER ? sum[K - 1] * p.inv_cols : 0.f;
+    const float2 w = warp_pairs_sum(lanes(halves(sn)), CENTER ? lanes(halves(sg)) : 0.f, shared[parity]);
+    const float along = -w.x * p.inv_cols, level = -w.y * p.inv_cols;
+    const uint64_t a2 = pack_f32x2(along, along), l2 = pack_f32x2(level, level);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = c * blockDim.x + threadIdx.x;
       if (i >= p.vectors) continue;
-      Vec<T> x, g, w, d;
-      x.load(ring.at(stage, 0, c), 0);
-      g.load(ring.at(stage, 1, c), 0);
-      if (p.w)
-        w.load(p.w, i);
-      else
-        w.fill(1.f);
+      Vec<T>&nc = n[kHeld ? c : 0], &gc = gw[kHeld ? c : 0];
+      if constexpr (!kHeld) {
+        read(c, nc, gc);
+        const Vec<T> w = weight.at(c, p.vectors);
+#pragma unroll
+        for (int j = 0; j < H; ++j) gc.f[j] = mul_f32x2(gc.f[j], w.f[j]);
+      }
+      Vec<T> d;
       if (p.ds)
-        d.load(ring.at(stage, 2, c), 0);
+        d.unpack(ring.at(2, c));
       else
         d.fill(0.f);
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float n = (x.f[j] - mean) * r;
-        d.f[j] = fmaf(r, fmaf(g.f[j], w.f[j], -level) - n * along, d.f[j]);
-      }
-      d.store(p.out, row * p.vectors + i);
+      for (int j = 0; j < H; ++j)
+        d.f[j] = fma_f32x2(r2, fma_f32x2(nc.f[j], a2, CENTER ? add_f32x2(gc.f[j], l2) : gc.f[j]), d.f[j]);
+      out[c * blockDim.x] = d.packed();
     }
-    stage = (stage + 1) % STAGES;
+    ring.next();
+    out += (int64_t)gridDim.x * p.vectors;
     parity ^= 1;
   }
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int i = c * blockDim.x + threadIdx.x;
     if (i >= p.vectors) continue;
-    const int64_t at = ((int64_t)blockIdx.x * p.vectors + i) * N;
+    const int64_t at = ((int64_t)blockIdx.x * p.vectors + i) * H;
 #pragma unroll
-    for (int j = 0; j < N; j += 4) {
-      *reinterpret_cast<float4*>(p.dw_partial + at + j) = make_float4(dw[c][j], dw[c][j + 1], dw[c][j + 2], dw[c][j + 3]);
-      if (BIAS)
-        *reinterpret_cast<float4*>(p.db_partial + at + j) =
-            make_float4(db[c][j], db[c][j + 1], db[c][j + 2], db[c][j + 3]);
+    for (int j = 0; j < H; j += 2) {
+      reinterpret_cast<ulonglong2*>(p.dw_partial)[(at + j) / 2] = make_ulonglong2(dw[c][j], dw[c][j + 1]);
+      if (BIAS) reinterpret_cast<ulonglong2*>(p.db_partial)[(at + j) / 2] = make_ulonglong2(db[c][j], db[c][j + 1]);
     }
   }
 }
