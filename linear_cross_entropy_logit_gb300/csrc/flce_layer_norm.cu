@@ -107,10 +107,10 @@ struct Launch {
   flce_status pick() const {
     static Setup fwd, with, without;
     if (!bwd) {
-      const int arrays = 2;
+      const int arrays = p.residual ? 2 : 1;
       return run(fwd, layer_norm_fwd<T, C, STAGES, CENTER>, d, arrays, blocks(d, arrays, kFwdThreads, sms), p, dev, st);
     }
-    const int arrays = 3;
+    const int arrays = p.ds ? 3 : 2;
     const int64_t n = bwd_blocks(d, sms);
     return p.db_partial ? run(with, layer_norm_bwd<T, C, STAGES, CENTER, true>, d, arrays, n, p, dev, st)
                         : run(without, layer_norm_bwd<T, C, STAGES, CENTER, false>, d, arrays, n, p, dev, st);
