@@ -88,101 +88,119 @@ __device__ __forceinline__ TeacherRow teacher_row(const DistillParams& p, int64_
   return r;
 }
 
-// The student's logits at the teacher's ids: a block a row of X, a warp four entries at a
-// time, in fp32 (an exact product of two bf16 each).  Bound by the reads of the rows of W.
-constexpr int kGatherThreads = 256;
-__global__ void __launch_bounds__(kGatherThreads) distill_gather(const __nv_bfloat16* X, const __nv_bfloat16* W,
-                                                                 const __grid_constant__ DistillParams p) {
-  const int64_t row = blockIdx.x;
-  const int lane = threadIdx.x & 31, vectors = p.H / 8;
-  const uint4* x_row = reinterpret_cast<const uint4*>(X + row * p.H);  // in L1 after the first warp
-  constexpr int U = 4;
-  for (int k0 = (threadIdx.x >> 5) * U; k0 < p.K; k0 += kGatherThreads / 32 * U) {
-    const uint4* w[U];
-    bool live[U];
-    float sum[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t id = k0 + u < p.K ? p.ids[row * p.K + k0 + u] : -1;
-      live[u] = id >= 0 && id < p.V;
-      w[u] = reinterpret_cast<const uint4*>(W + (live[u] ? id : 0) * p.H);
-      sum[u] = 0.f;
-    }
-    for (int i = lane; i < vectors; i += 32) {
-      const uint4 x = x_row[i];
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+// What a row's loss needs beside lse: l = rest + Q (lse - tl) for a row that counts.
+struct DistillRow {
+  float rest;  // sum of q (t - z) / T
+  float tl, Q;
+  int valid;
+};
+
+// Forward, a block a row at a time: the student's logits at the teacher's ids, in fp32 (products
+// of two bf16 are exact; the tensor cores' sums are off by up to 4e-6 at H = 4096, these by
+// 1e-7), and the row's part of the loss.  A warp takes four entries at a time, so that eight
+// loads of 512 bytes are in flight; the row of X stays in L1.
+// Bound by the reads of the rows of W, 4.3 GB for 8192 tokens of 64 entries at H = 4096: 563 us
+// alone.  So it is launched ahead of the forward GEMM, which does not read its results, and
+// lets it start at once: two small blocks a SM find room beside the GEMM's and read
+// while that computes.
+constexpr int kRowsThreads = 256, kRowsBlocks = 2;  // blocks of an SM
+template <typename T>
+__global__ void __launch_bounds__(kRowsThreads, 4) distill_rows(const __nv_bfloat16* X, const __nv_bfloat16* W,
+                                                             const __grid_constant__ DistillParams p,
+                                                             DistillRow* rows) {
+  extern __shared__ float z_of[];  // two rows of K logits
+  launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vectors = p.H / 8;
+  constexpr int U = 4, kWarps = kRowsThreads / 32;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x, ++turn) {
+    const uint4* x_row = reinterpret_cast<const uint4*>(X + row * p.H);
+    float* z = z_of + (turn & 1) * p.K;
+    for (int k0 = warp * U; k0 < p.K; k0 += kWarps * U) {
+      const uint4* w[U];
+      bool live[U];
+      uint64_t sum[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (!live[u]) continue;
-        const uint4 v = w[u][i];
-        const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
+        const int64_t id = k0 + u < p.K ? p.ids[row * p.K + k0 + u] : -1;
+        live[u] = id >= 0 && id < p.V;
+        w[u] = reinterpret_cast<const uint4*>(W + (live[u] ? id : 0) * p.H);
+        sum[u] = 0;
+      }
+      // entries that are none read row 0 too: loads without branches between them
+      auto step = [&](int i) {
+        const uint4 x = x_row[i];
+        uint4 v[U];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sum[u] = fmaf(__uint_as_float(xs[j] << 16), __uint_as_float(vs[j] << 16), sum[u]);
-          sum[u] = fmaf(__uint_as_float(xs[j] & 0xffff0000u), __uint_as_float(vs[j] & 0xffff0000u), sum[u]);
+        for (int u = 0; u < U; ++u) v[u] = ld_stream_v4(w[u] + i);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const uint32_t vs[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            sum[u] = fma_f32x2(pack_u32x2(xs[j] << 16, xs[j] & 0xffff0000u),
+                               pack_u32x2(vs[j] << 16, vs[j] & 0xffff0000u), sum[u]);
+        }
+      };
+#pragma unroll 2
+      for (int i = lane; i < vectors; i += 32) step(i);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float a, b;
+        unpack_f32x2(sum[u], a, b);
+        const float s = live[u] ? warp_sum(a + b) : 0.f;
+        if (lane == 0 && k0 + u < p.K) {
+          p.logits[row * p.K + k0 + u] = s;
+          z[k0 + u] = s;
         }
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float s = warp_sum(sum[u]);
-      if (lane == 0 && k0 + u < p.K) p.logits[row * p.K + k0 + u] = live[u] ? s : 0.f;
+    __syncthreads();
+    // one warp has the rest of the row; the others go on to the next, whose logits lie elsewhere
+    if (turn % kWarps != warp) continue;
+    const TeacherRow tr = teacher_row<T>(p, row, lane);
+    if (tr.error && lane == 0) record_error(p.err_word, kErrLabel);
+    float rest = 0.f;
+    for (int k = lane; k < p.K; k += 32) {
+      const float t = teacher_logit(p, row * p.K + k, (const T*)nullptr) * p.inv_t;
+      if (tr.valid && entry(p.ids[row * p.K + k], t)) {
+        const float q = expf(t - tr.tl);
+        if (!(q == 0.f)) rest = fmaf(q, t - z[k] * p.inv_t, rest);
+      }
     }
+    rest = warp_sum(rest);
+    if (lane == 0) rows[row] = DistillRow{rest, tr.tl, tr.Q, tr.valid};
   }
 }
 
-// lse of each row from the vocabulary groups' partials (as lse_merge_kernel), then its loss
-// by the entries: a block MERGE_ROWS rows, each warp four of them.  All orders are fixed.
-template <typename T>
+// lse of each row from the vocabulary groups' partials (as lse_merge_kernel) and its loss: a
+// block MERGE_ROWS rows.  All orders are fixed.
 __global__ void __launch_bounds__(MERGE_THREADS)
-    distill_merge(const float4* __restrict__ partials, int n_groups, int m_pad,
-                  const __grid_constant__ DistillParams p, float* __restrict__ lse_out,
-                  float* __restrict__ row_loss, double* __restrict__ block_loss, int* __restrict__ block_valid) {
+    distill_merge(const float4* __restrict__ partials, int n_groups, int m_pad, int N,
+                  const DistillRow* __restrict__ rows, float* __restrict__ lse_out, float* __restrict__ row_loss,
+                  double* __restrict__ block_loss, int* __restrict__ block_valid) {
   __shared__ float4 s_part[MERGE_SLICES][MERGE_ROWS];
-  __shared__ float s_lse[MERGE_ROWS];
-  __shared__ double s_loss[MERGE_ROWS];
-  __shared__ int s_valid[MERGE_ROWS];
   const int r = threadIdx.x % MERGE_ROWS, slice = threadIdx.x / MERGE_ROWS;
-  const int row0 = blockIdx.x * MERGE_ROWS;
-  if (row0 + r < p.N) s_part[slice][r] = merge_slice(partials, n_groups, m_pad, row0 + r, slice);
-  __syncthreads();
-  if (slice == 0) {
-    s_loss[r] = 0.0;
-    s_valid[r] = 0;
-    if (row0 + r < p.N) {
-      const float4 t = combine_slices(s_part, r);
-      s_lse[r] = (t.x + log2f(t.y)) * LN2;
-      lse_out[row0 + r] = s_lse[r];
-    }
-  }
-  __syncthreads();
-  for (int i = slice; i < MERGE_ROWS && row0 + i < p.N; i += MERGE_SLICES) {
-    const int64_t row = row0 + i;
-    const TeacherRow tr = teacher_row<T>(p, row, r);
-    if (tr.error && r == 0) record_error(p.err_word, kErrLabel);
-    double l = 0.0;
-    if (tr.valid) {
-      for (int k = r; k < p.K; k += 32) {
-        const float t = teacher_logit(p, row * p.K + k, (const T*)nullptr) * p.inv_t;
-        if (entry(p.ids[row * p.K + k], t)) {
-          const float q = expf(t - tr.tl);
-          if (!(q == 0.f)) l += (double)q * (double)(t - p.logits[row * p.K + k] * p.inv_t);
-        }
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-      if (!(tr.Q == 0.f)) l += (double)tr.Q * (double)(s_lse[i] - tr.tl);
-    }
-    if (r == 0) {
-      s_loss[i] = l;
-      s_valid[i] = tr.valid;
-      if (row_loss) row_loss[row] = (float)l;
-    }
-  }
+  const int row = blockIdx.x * MERGE_ROWS + r;
+  grid_wait();
+  if (row < N) s_part[slice][r] = merge_slice(partials, n_groups, m_pad, row, slice);
   __syncthreads();
   if (slice) return;
-  double loss = s_loss[r];
-  int valid = s_valid[r];
+  double loss = 0.0;
+  int valid = 0;
+  if (row < N) {
+    const float4 t = combine_slices(s_part, r);
+    const float lse = (t.x + log2f(t.y)) * LN2;
+    lse_out[row] = lse;
+    const DistillRow d = rows[row];
+    valid = d.valid;
+    if (valid) {
+      loss = d.rest;
+      if (!(d.Q == 0.f)) loss += (double)d.Q * (double)(lse - d.tl);
+    }
+    if (row_loss) row_loss[row] = (float)loss;
+  }
 #pragma unroll
   for (int o = MERGE_ROWS / 2; o > 0; o >>= 1) {
     loss += __shfl_xor_sync(~0u, loss, o);
@@ -209,6 +227,7 @@ __global__ void __launch_bounds__(kPrepareThreads)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int* id_of = shared + warp * 2 * p.K;
   float* q_of = reinterpret_cast<float*>(id_of + p.K);
+  grid_wait();
   const float g = grad_loss ? *grad_loss : 1.f;
   const int nv = reduction_sum ? 1 : *valid_count;
   const float c = nv > 0 ? (float)((double)g * (double)p.inv_t / (double)nv) : 0.f;
@@ -243,6 +262,7 @@ __global__ void __launch_bounds__(kPrepareThreads)
 __global__ void __launch_bounds__(256) distill_scatter(const int* __restrict__ ids32, const uint16_t* __restrict__ dz,
                                                        int64_t entries, int K, int v0, int width, int64_t pitch,
                                                        uint16_t* __restrict__ chunk) {
+  grid_wait();
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < entries; i += (int64_t)gridDim.x * 256) {
     const int at = ids32[i] - v0;
     if (ids32[i] >= 0 && at >= 0 && at < width) chunk[i / K * pitch + at] = dz[i];

@@ -74,6 +74,7 @@ struct Tuning {
   bool l2_hints;       // evict_last policy on the re-read operand
   int64_t chunk_set;   // requested vocabulary chunk width (0 = automatic)
   bool mcast;          // pair launches may take 4-CTA clusters with operand multicast
+  bool overlap = false;  // GEMM launches may start while the kernel ahead of them ends
 };
 
 Tuning default_tuning() {
@@ -468,7 +469,7 @@ int fewest_workers(int units, int max_workers, int step) {
 template <Epi EPI, bool A_MN, bool B_MN, bool PAIR, bool EXT>
 flce_status launch_gemm(int dev, int num_sms, const CUtensorMap& a, const CUtensorMap& b,
                         const CUtensorMap& out, const GemmParams& p, cudaStream_t st,
-                        int prof_kind = -1) {
+                        int prof_kind = -1, bool overlap = false) {
   constexpr int stages = PAIR ? kPairStages : kStages;
   auto kern = [] {
     if constexpr (PAIR)
@@ -492,9 +493,13 @@ flce_status launch_gemm(int dev, int num_sms, const CUtensorMap& a, const CUtens
     rec.stop = prof_event();
     if (rec.start && rec.stop) FLCE_CUDA(cudaEventRecord(rec.start, st));
   }
-  kern<<<grid, NUM_THREADS, smem, st>>>(a, b, out, p);
-  ++g_launches;
-  FLCE_CUDA(cudaGetLastError());
+  if (overlap) {
+    FLCE_HOST_TRY(host::launch(kern, dim3(grid), NUM_THREADS, smem, st, a, b, out, p));
+  } else {
+    kern<<<grid, NUM_THREADS, smem, st>>>(a, b, out, p);
+    ++g_launches;
+    FLCE_CUDA(cudaGetLastError());
+  }
   if (rec.start && rec.stop) {
     FLCE_CUDA(cudaEventRecord(rec.stop, st));
     g_prof_pending.push_back(rec);
@@ -508,6 +513,7 @@ flce_status launch_gemm(int dev, int num_sms, const CUtensorMap& a, const CUtens
 struct Walk {
   bool quad = false;
   bool share_b = false;  // QUAD: the pairs share B (differ in row block), else A
+  bool overlap = false;  // may start while the kernel ahead of it ends (GemmParams::late_wait)
 };
 
 // QUAD needs whole groups of two pairs whose units pair up exactly: units
@@ -515,6 +521,7 @@ struct Walk {
 // column group (share A, group length 1), and every unit needs its partner.
 Walk pick_walk(const Tuning& t, bool pair, bool ext, const GemmParams& p) {
   Walk w;
+  w.overlap = t.overlap;
   if (!pair || ext || !t.mcast || p.num_units < 4 || p.num_units % 2 != 0) return w;
   if (p.m_fastest) {
     const bool banded = p.m_band > 0 && p.m_band < p.m_blocks;
@@ -537,7 +544,7 @@ uint32_t b_box_rows(bool pair, const Walk& w) { return w.quad ? 64 : (pair ? BN 
 template <Epi EPI, bool A_MN, bool B_MN, bool SHARE_B>
 flce_status launch_quad(int dev, int num_sms, const CUtensorMap& a, const CUtensorMap& b,
                         const CUtensorMap& out, const GemmParams& p, cudaStream_t st,
-                        int prof_kind) {
+                        int prof_kind, bool overlap) {
   auto kern = gemm_quad_kernel<EPI, A_MN, B_MN, kPairStages, SHARE_B>;
   constexpr int smem = gemm_smem_bytes<EPI, kPairStages, true, false>();
   static KernelSetup setup[kMaxDevices];
@@ -554,7 +561,7 @@ flce_status launch_quad(int dev, int num_sms, const CUtensorMap& a, const CUtens
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[2];
+  cudaLaunchAttribute at[3];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = 2;
   at[0].val.clusterDim.y = 1;
@@ -563,8 +570,10 @@ flce_status launch_quad(int dev, int num_sms, const CUtensorMap& a, const CUtens
   at[1].val.preferredClusterDim.x = 4;
   at[1].val.preferredClusterDim.y = 1;
   at[1].val.preferredClusterDim.z = 1;
+  at[2].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[2].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = overlap ? 3 : 2;
   ProfRec rec{prof_kind, nullptr, nullptr};
   if (g_prof_on && prof_kind >= 0) {
     rec.start = prof_event();
@@ -586,9 +595,10 @@ template <Epi EPI, bool A_MN, bool B_MN>
 flce_status launch_pair(const Walk& w, int dev, int num_sms, const CUtensorMap& a, const CUtensorMap& b,
                         const CUtensorMap& out, const GemmParams& p, cudaStream_t st, int prof_kind) {
   if (w.quad)
-    return w.share_b ? launch_quad<EPI, A_MN, B_MN, true>(dev, num_sms, a, b, out, p, st, prof_kind)
-                     : launch_quad<EPI, A_MN, B_MN, false>(dev, num_sms, a, b, out, p, st, prof_kind);
-  return launch_gemm<EPI, A_MN, B_MN, true, false>(dev, num_sms, a, b, out, p, st, prof_kind);
+    return w.share_b
+               ? launch_quad<EPI, A_MN, B_MN, true>(dev, num_sms, a, b, out, p, st, prof_kind, w.overlap)
+               : launch_quad<EPI, A_MN, B_MN, false>(dev, num_sms, a, b, out, p, st, prof_kind, w.overlap);
+  return launch_gemm<EPI, A_MN, B_MN, true, false>(dev, num_sms, a, b, out, p, st, prof_kind, w.overlap);
 }
 
 // Run-time choice between the 1-CTA (128 x 256), CTA-pair (256 x 256) and
@@ -598,12 +608,13 @@ flce_status launch_tile(bool pair, bool ext, const Walk& w, int dev, int num_sms
                         const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out,
                         const GemmParams& p, cudaStream_t st, int prof_kind = -1) {
   if (w.quad)
-    return w.share_b ? launch_quad<EPI, A_MN, B_MN, true>(dev, num_sms, a, b, out, p, st, prof_kind)
-                     : launch_quad<EPI, A_MN, B_MN, false>(dev, num_sms, a, b, out, p, st, prof_kind);
+    return w.share_b
+               ? launch_quad<EPI, A_MN, B_MN, true>(dev, num_sms, a, b, out, p, st, prof_kind, w.overlap)
+               : launch_quad<EPI, A_MN, B_MN, false>(dev, num_sms, a, b, out, p, st, prof_kind, w.overlap);
   if (ext)
     return pair ? launch_gemm<EPI, A_MN, B_MN, true, true>(dev, num_sms, a, b, out, p, st, prof_kind)
                 : launch_gemm<EPI, A_MN, B_MN, false, true>(dev, num_sms, a, b, out, p, st, prof_kind);
-  return pair ? launch_gemm<EPI, A_MN, B_MN, true, false>(dev, num_sms, a, b, out, p, st, prof_kind)
+  return pair ? launch_gemm<EPI, A_MN, B_MN, true, false>(dev, num_sms, a, b, out, p, st, prof_kind, w.overlap)
               : launch_gemm<EPI, A_MN, B_MN, false, false>(dev, num_sms, a, b, out, p, st, prof_kind);
 }
 
@@ -674,7 +685,8 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 struct DistillCall {
   const flce_distill_desc* desc;
   DistillParams p;
-  // backward: per row and per entry, in the workspace
+  // in the workspace: forward, per row; backward, per row and per entry
+  DistillRow* rows;
   int64_t* marks;
   float* lse_q;
   int* ids32;
@@ -804,21 +816,22 @@ flce_status loss_finalize(const Common& c, const Plan& pl, const double* block_l
   return FLCE_OK;
 }
 
-// A distillation's forward after the softmax's partials: the student's logits at the entries
-// and the rows' losses.
-flce_status distill_rows(const Common& c, const Plan& pl, const void* Xb, const void* Wb, const float4* partials,
-                         float* lse, double* block_loss, int* block_valid) {
+// The student's logits at a distillation's entries and what the rows' losses take from them.
+template <typename T>
+flce_status launch_rows(const Common& c, int dev, int sms, const void* Xb, const void* Wb) {
   const DistillCall& d = *c.distill;
-  distill_gather<<<(unsigned)c.N, kGatherThreads, 0, c.st>>>(
-      static_cast<const __nv_bfloat16*>(Xb), static_cast<const __nv_bfloat16*>(Wb), d.p);
-  ++g_launches;
-  FLCE_CUDA(cudaGetLastError());
-  if (d.desc->teacher_dtype == FLCE_BF16)
-    distill_merge<__nv_bfloat16><<<pl.merge_blocks, MERGE_THREADS, 0, c.st>>>(
-        partials, pl.n_groups, pl.m_pad, d.p, lse, c.row_loss, block_loss, block_valid);
-  else
-    distill_merge<float><<<pl.merge_blocks, MERGE_THREADS, 0, c.st>>>(
-        partials, pl.n_groups, pl.m_pad, d.p, lse, c.row_loss, block_loss, block_valid);
+  // A SM divides its memory into L1 and shared memory when it starts a block while empty: all
+  // shared memory, or the GEMM's blocks would not fit beside.
+  static KernelSetup setup[kMaxDevices];
+  KernelSetup& ks = setup[dev];
+  std::call_once(ks.once, [&] {
+    ks.err = cudaFuncSetAttribute(distill_rows<T>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                  cudaSharedmemCarveoutMaxShared);
+  });
+  if (ks.err != cudaSuccess) return cuda_fail(ks.err, "cudaFuncSetAttribute");
+  const unsigned blocks = (unsigned)std::min<int64_t>(c.N, kRowsBlocks * sms);
+  distill_rows<T><<<blocks, kRowsThreads, 2 * (size_t)d.p.K * sizeof(float), c.st>>>(
+      static_cast<const __nv_bfloat16*>(Xb), static_cast<const __nv_bfloat16*>(Wb), d.p, d.rows);
   ++g_launches;
   FLCE_CUDA(cudaGetLastError());
   return FLCE_OK;
@@ -866,10 +879,18 @@ flce_status run_forward(const Common& c, const Plan& pl, int dev, int sms, const
     CUtensorMap tmX, tmW;
     FLCE_TRY(map_kmajor(&tmX, Xb, c.H, c.N, c.H, a_box_rows(walk)));
     FLCE_TRY(map_kmajor(&tmW, Wb, c.H, c.V, c.H, b_box_rows(pair, walk)));
+    if (c.distill) {
+      FLCE_TRY(c.distill->desc->teacher_dtype == FLCE_BF16 ? launch_rows<__nv_bfloat16>(c, dev, sms, Xb, Wb)
+                                                           : launch_rows<float>(c, dev, sms, Xb, Wb));
+      p.late_wait = 1;
+    }
     FLCE_TRY((launch_tile<Epi::kLse, false, false>(pair, ext, walk, dev, sms, tmX, tmW, tmX, p,
                                                   c.st, 0)));
     if (c.distill) {
-      FLCE_TRY(distill_rows(c, pl, Xb, Wb, p.partials, lse, block_loss, block_valid));
+      FLCE_TRY(host::launch(distill_merge, dim3(pl.merge_blocks), MERGE_THREADS, 0, c.st,
+                            static_cast<const float4*>(p.partials), pl.n_groups, pl.m_pad, (int)c.N,
+                            static_cast<const DistillRow*>(c.distill->rows), lse, c.row_loss, block_loss,
+                            block_valid));
       return loss_finalize(c, pl, block_loss, block_valid, loss, valid_count);
     }
     if (shard_out) {
@@ -897,15 +918,9 @@ flce_status distill_rows_backward(const Common& c, const float* lse, const int32
   const unsigned blocks = (unsigned)ceil_div(std::max<int64_t>(c.N, 1), kPrepareThreads / 32);
   const size_t smem = (size_t)kPrepareThreads / 32 * 2 * d.p.K * 4;
   const int sum = c.reduction == FLCE_SUM;
-  if (d.desc->teacher_dtype == FLCE_BF16)
-    distill_prepare<__nv_bfloat16><<<blocks, kPrepareThreads, smem, c.st>>>(
-        d.p, lse, valid_count, grad_loss, sum, scale, d.marks, d.lse_q, d.ids32, d.dz);
-  else
-    distill_prepare<float><<<blocks, kPrepareThreads, smem, c.st>>>(
-        d.p, lse, valid_count, grad_loss, sum, scale, d.marks, d.lse_q, d.ids32, d.dz);
-  ++g_launches;
-  FLCE_CUDA(cudaGetLastError());
-  return FLCE_OK;
+  return host::launch(d.desc->teacher_dtype == FLCE_BF16 ? distill_prepare<__nv_bfloat16> : distill_prepare<float>,
+                      dim3(blocks), kPrepareThreads, smem, c.st, d.p, lse, valid_count, grad_loss, sum, scale,
+                      d.marks, d.lse_q, d.ids32, d.dz);
 }
 
 // The entries of a chunk put into its dZ.
@@ -913,11 +928,9 @@ flce_status distill_chunk(const Common& c, int sms, int64_t v0, int64_t w, int64
   const DistillCall& d = *c.distill;
   const int64_t entries = c.N * d.p.K;
   const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(entries, 256), 8 * sms);
-  distill_scatter<<<blocks, 256, 0, c.st>>>(d.ids32, d.dz, entries, d.p.K, (int)v0, (int)w, pitch,
-                                            static_cast<uint16_t*>(dz));
-  ++g_launches;
-  FLCE_CUDA(cudaGetLastError());
-  return FLCE_OK;
+  return host::launch(distill_scatter, dim3(blocks), 256, 0, c.st, static_cast<const int*>(d.ids32),
+                      static_cast<const uint16_t*>(d.dz), entries, d.p.K, (int)v0, (int)w, pitch,
+                      static_cast<uint16_t*>(dz));
 }
 
 flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, const void* Xb,
@@ -1695,13 +1708,14 @@ Tuning distill_tuning() {
   t.pair = true;
   t.merge = 0;
   t.l2_hints = false;
+  t.overlap = true;
   return t;
 }
 
 // The loss's plan, and behind it the backward's rows and entries.
 struct DistillPlan {
   Plan pl;
-  size_t off_marks, off_lse_q, off_ids, off_dz, total;
+  size_t off_rows, off_marks, off_lse_q, off_ids, off_dz, total;
 };
 bool distill_plan(const flce_distill_desc* d, int mode, DistillPlan* out) {
   if (!distill_ok(d) || !make_plan(d->N, d->H, d->V, FLCE_BF16, mode, distill_tuning(), &out->pl)) return false;
@@ -1710,6 +1724,7 @@ bool distill_plan(const flce_distill_desc* d, int mode, DistillPlan* out) {
     *at = off;
     off = align_up(off + bytes, kAlign);
   };
+  region(&out->off_rows, (mode & FLCE_MODE_FWD) ? d->N * sizeof(DistillRow) : 0);
   const size_t n = (mode & FLCE_MODE_BWD) ? (size_t)d->N : 0;
   region(&out->off_marks, n * sizeof(int64_t));
   region(&out->off_lse_q, n * sizeof(float));
@@ -1739,6 +1754,7 @@ flce_status distill_call(const flce_distill_desc* d, int mode, const void* X, co
   *dc = DistillCall{d,
                     DistillParams{ids, teacher, teacher_lse, logits, (int)d->N, (int)d->K, (int)d->H, (int)d->V,
                                   1.f / d->temperature, err_word},
+                    reinterpret_cast<DistillRow*>(base + pl->off_rows),
                     reinterpret_cast<int64_t*>(base + pl->off_marks),
                     reinterpret_cast<float*>(base + pl->off_lse_q),
                     reinterpret_cast<int*>(base + pl->off_ids),

@@ -148,6 +148,10 @@ struct GemmParams {
   // control
   int* err_word;
   unsigned long long timeout_ns;
+  // Launched to overlap the end of the kernel ahead of it: 0 waits for that kernel before it
+  // reads memory; 1 (a kernel that it does not depend on) before it ends, so that what
+  // follows this launch follows both.  Without the launch attribute neither waits.
+  int late_wait;
 };
 
 // EXT = the optional features (token-block skip lists, gradient filtering,
@@ -556,6 +560,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
     __syncthreads();
   }
   tc_fence_after();
+  if (!p.late_wait) grid_wait();
   const uint32_t tmem_base = *tmem_slot;
   const WaitCtx ctx{abort_flag, p.err_word, p.timeout_ns};
   const int num_kb_all = (p.k_size + BK - 1) / BK;
@@ -973,6 +978,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
     }
   }
 
+  if (p.late_wait && threadIdx.x == 0) grid_wait();
   __syncthreads();
   if constexpr (PAIR) {
     if (*abort_flag) {

@@ -439,6 +439,7 @@ __device__ __forceinline__ void mma_commit_if(uint32_t elected, uint64_t* bar) {
 // Kernels launched by host::launch may start before the kernel ahead of them in the
 // stream has ended: this waits until it has and its writes are seen.  Every thread calls it
 // before it touches global memory.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -643,6 +644,14 @@ __device__ __forceinline__ uint32_t bf16x2_max_abs(uint32_t a, uint32_t b) {
   return d;
 }
 
+// Read-only data that is used once: not kept in L1.
+__device__ __forceinline__ uint4 ld_stream_v4(const uint4* p) {
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "l"(p));
+  return v;
+}
 // Two floats -> packed bf16x2 (round to nearest even); `lo` in the low half.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
