@@ -258,6 +258,21 @@ __global__ void __launch_bounds__(kPrepareThreads)
   }
 }
 
+// dX of few tokens: the sum of the parts' rows, `pitch` values apart, in their order.
+__global__ void __launch_bounds__(256) distill_dx(const float4* __restrict__ parts, int k_parts, int64_t pitch4,
+                                                  uint2* __restrict__ dX, int64_t n4) {
+  grid_wait();
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+    float4 t = parts[i];
+#pragma unroll 4
+    for (int k = 1; k < k_parts; ++k) {
+      const float4 v = parts[k * pitch4 + i];
+      t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+    }
+    dX[i] = make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+  }
+}
+
 // The entries of a vocabulary chunk put into its dZ, which holds the softmax term there.
 __global__ void __launch_bounds__(256) distill_scatter(const int* __restrict__ ids32, const uint16_t* __restrict__ dz,
                                                        int64_t entries, int K, int v0, int width, int64_t pitch,

@@ -692,6 +692,9 @@ struct DistillCall {
   int* ids32;
   uint16_t* dz;
   bool dw_bf16;
+  // dX in parts of the contraction, where its tiles are few: rows of the parts in dx_parts
+  int k_parts;
+  float* dx_parts;
 };
 
 struct Common {
@@ -962,11 +965,15 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
 
   // X as the K-major A operand of the dZ recompute: 128-row boxes (pairs, the
   // merged launches) or 64-row boxes (QUAD walks)
+  const int k_parts = c.distill ? c.distill->k_parts : 1;
   CUtensorMap tmX_k, tmX_k64, tmX_mn, tmDxAcc;
   FLCE_TRY(map_kmajor(&tmX_k, Xb, H, N, H, BM));
   FLCE_TRY(map_kmajor(&tmX_k64, Xb, H, N, H, 64));
   FLCE_TRY(map_mnmajor(&tmX_mn, Xb, H, N, H));
-  FLCE_TRY(map_f32_out(&tmDxAcc, dx_acc, H, N, H));
+  if (k_parts > 1)
+    FLCE_TRY(map_f32_out(&tmDxAcc, c.distill->dx_parts, H, (uint64_t)k_parts * pl.m_pad, H));
+  else
+    FLCE_TRY(map_f32_out(&tmDxAcc, dx_acc, H, N, H));
 
   const bool pair = c.tun.pair;
   const bool ext = ext_features(c);
@@ -1216,11 +1223,30 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
       p5.l2_keep_frac = l2_keep_fraction(c.tun, (double)w * H * 2);
       p5.err_word = c.err_word;
       p5.timeout_ns = kTimeoutNs;
+      if (k_parts > 1) {  // CTA pairs, no multicast
+        const int num_kb = (int)ceil_div(w, BK);
+        p5.part_kb = (int)ceil_div(num_kb, k_parts);
+        p5.k_parts = (int)ceil_div(num_kb, p5.part_kb);
+        p5.part_rows = pl.m_pad;
+        p5.num_units *= p5.k_parts;
+        Walk wp;
+        wp.overlap = c.tun.overlap;
+        FLCE_TRY(map_kmajor(&tmDz_k, dz, w, N, Cv, a_box_rows(wp)));
+        FLCE_TRY((launch_gemm<Epi::kStorePart, false, true, true, false>(dev, sms, tmDz_k, tmWc_mn, tmDxAcc, p5,
+                                                                         c.st, 3, wp.overlap)));
+        continue;
+      }
       const Walk w5 = pick_walk(c.tun, pair, ext, p5);
       FLCE_TRY(map_kmajor(&tmDz_k, dz, w, N, Cv, a_box_rows(w5)));
       FLCE_TRY((launch_tile<Epi::kStore, false, true>(pair, ext, w5, dev, sms, tmDz_k, tmWc_mn,
                                                       tmDxAcc, p5, c.st, 3)));
     }
+  }
+  if (k_parts > 1) {
+    const int64_t n4 = N * H / 4;
+    return host::launch(distill_dx, dim3((unsigned)std::min<int64_t>(ceil_div(n4, 256), 8 * sms)), 256, 0, c.st,
+                        reinterpret_cast<const float4*>(c.distill->dx_parts), k_parts, (int64_t)pl.m_pad * H / 4,
+                        static_cast<uint2*>(dX), n4);
   }
   if (c.dtype == FLCE_BF16 && !c.dx_partial_f32) {
     const size_t n4 = (size_t)N * H / 4;
@@ -1715,8 +1741,15 @@ Tuning distill_tuning() {
 // The loss's plan, and behind it the backward's rows and entries.
 struct DistillPlan {
   Plan pl;
-  size_t off_rows, off_marks, off_lse_q, off_ids, off_dz, total;
+  size_t off_rows, off_marks, off_lse_q, off_ids, off_dz, off_dx_parts, total;
+  int k_parts;
 };
+// Parts of dX's contraction: as many as give each CTA pair a unit, of eight k-blocks at least.
+int dx_parts(const Plan& p) {
+  const int64_t tiles = ceil_div(std::max<int64_t>(p.N, 1), 2 * BM) * ceil_div(p.H, BN);
+  const int64_t most = std::min<int64_t>({device_pairs() / tiles, ceil_div(std::min(p.chunk, p.V), BK) / 8, 32});
+  return (int)std::max<int64_t>(1, most);
+}
 bool distill_plan(const flce_distill_desc* d, int mode, DistillPlan* out) {
   if (!distill_ok(d) || !make_plan(d->N, d->H, d->V, FLCE_BF16, mode, distill_tuning(), &out->pl)) return false;
   size_t off = out->pl.total;
@@ -1730,6 +1763,8 @@ bool distill_plan(const flce_distill_desc* d, int mode, DistillPlan* out) {
   region(&out->off_lse_q, n * sizeof(float));
   region(&out->off_ids, n * d->K * sizeof(int));
   region(&out->off_dz, n * d->K * sizeof(uint16_t));
+  out->k_parts = n ? dx_parts(out->pl) : 1;
+  region(&out->off_dx_parts, out->k_parts > 1 ? (size_t)out->k_parts * out->pl.m_pad * d->H * sizeof(float) : 0);
   out->total = off;
   return true;
 }
@@ -1759,7 +1794,9 @@ flce_status distill_call(const flce_distill_desc* d, int mode, const void* X, co
                     reinterpret_cast<float*>(base + pl->off_lse_q),
                     reinterpret_cast<int*>(base + pl->off_ids),
                     reinterpret_cast<uint16_t*>(base + pl->off_dz),
-                    d->dw_dtype == FLCE_BF16};
+                    d->dw_dtype == FLCE_BF16,
+                    pl->k_parts,
+                    reinterpret_cast<float*>(base + pl->off_dx_parts)};
   // The GEMM core's labels: none forward; backward the rows' marks, V for one that counts
   // (a column that does not exist, so that no target is taken off) and -1 for one that
   // does not.

@@ -52,6 +52,9 @@
 //          step 4 ("Backward Hidden and Weight Accumulation").
 //   kStoreBf16  the tile rounded to bf16 and written by TMA: a dW that is not
 //          accumulated over calls leaves in the weight's type.
+//   kStorePart  kStore of a part of the contraction: a launch of few tiles and a long
+//          contraction (dX of few tokens) splits it over the CTAs, each part into rows of
+//          its own, which are added in a fixed order afterwards.
 // kLse and kDz take exp(z / T) for any temperature T: z_log2e is log2(e) / T.
 #pragma once
 #include <cstdint>
@@ -84,7 +87,7 @@ struct TileCfg {
   static constexpr int STAGE = A_STAGE + B_STAGE;
 };
 
-enum class Epi : int { kLse = 0, kDz = 1, kStore = 2, kStoreBf16 = 3 };
+enum class Epi : int { kLse = 0, kDz = 1, kStore = 2, kStoreBf16 = 3, kStorePart = 4 };
 
 struct GemmParams {
   int m_size;      // rows of D
@@ -113,6 +116,11 @@ struct GemmParams {
   const float* scale;     // kDz: device scalar c = grad / N_valid
   // kStore
   int reduce_add;         // 1: TMA reduce-add onto the output, 0: overwrite
+  // kStorePart: k_parts units for each tile, part i the k-blocks from i * part_kb on, into
+  // the rows from i * part_rows on
+  int k_parts;
+  int part_kb;
+  int part_rows;
   // Skipping fully ignored token blocks (SFT-style masking).  When row_list is
   // set, units walk only the row blocks it lists (device count *row_count, in
   // units of TILE_M rows).  When k_list is set, the contraction walks only the
@@ -487,6 +495,19 @@ __device__ __forceinline__ void load_half_quad(uint8_t* dst, const CUtensorMap* 
   }
 }
 
+// The k-blocks of a unit: all of them, or those of its part.
+struct KRange {
+  int first, count;
+};
+template <Epi EPI>
+__device__ __forceinline__ KRange k_range(const GemmParams& p, int u, int num_kb) {
+  if constexpr (EPI == Epi::kStorePart) {
+    const int first = u % p.k_parts * p.part_kb;
+    return {first, min(p.part_kb, num_kb - first)};
+  }
+  return {0, num_kb};
+}
+
 // CL: 1 single-CTA tiles, 2 CTA pairs, 4 CTA pairs with 4-CTA clusters
 // preferred (QUAD; EXT must be false).
 template <Epi EPI, bool A_MN, bool B_MN, int STAGES, int CL, bool EXT, bool SHARE_B = false>
@@ -567,6 +588,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
   const int num_kb = EXT ? kblock_count(p, num_kb_all) : num_kb_all;
   const UnitSpace us = EXT ? unit_space(p) : UnitSpace{p.m_blocks, p.num_units};
 
+  const int parts = EPI == Epi::kStorePart ? p.k_parts : 1;  // units of a tile
+
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -584,7 +607,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
         if constexpr (QUAD)
           unit_coords_quad<SHARE_B>(p, u, mb, nb0, nb1, g);
         else
-          unit_coords<EXT>(p, us, u, mb, nb0, nb1, g);
+          unit_coords<EXT>(p, us, u / parts, mb, nb0, nb1, g);
+        const KRange kr = k_range<EPI>(p, u, num_kb);
         const int a_row = mb * Cfg::TILE_M + (int)rank * BM;
         for (int nb = nb0; nb < nb1 && ok; ++nb) {
           const int b_row = nb * BN + (int)rank * Cfg::B_ROWS;
@@ -593,8 +617,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
           if constexpr (EXT) {
             if (p.fmask) last_kept = load_tile_keep(p, mb, num_kb, tile_keep);
           }
-          for (int ki = 0; ki < num_kb; ++ki) {
-            int kb = ki;
+          for (int ki = 0; ki < kr.count; ++ki) {
+            int kb = kr.first + ki;
             if constexpr (EXT) {
               kb = kblock_at(p, ki);
               if (p.fmask && ki > last_kept) break;
@@ -727,7 +751,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
         if constexpr (QUAD)
           unit_coords_quad<SHARE_B>(p, u, mb, nb0, nb1, g);
         else
-          unit_coords<EXT>(p, us, u, mb, nb0, nb1, g);
+          unit_coords<EXT>(p, us, u / parts, mb, nb0, nb1, g);
+        const KRange kr = k_range<EPI>(p, u, num_kb);
         for (int nb = nb0; nb < nb1 && ok; ++nb) {
           const uint32_t acc = tile & 1u;
           const uint32_t ra = tile >> 1;
@@ -737,7 +762,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
           }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + acc * BN;
-          for (int ki = 0; ki < num_kb; ++ki) {
+          for (int ki = 0; ki < kr.count; ++ki) {
             const int s = it % STAGES;
             const uint32_t r = it / STAGES;
             if (!mbar_wait(&full[s], r & 1u, ctx)) {
@@ -800,9 +825,10 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
       if constexpr (QUAD)
         unit_coords_quad<SHARE_B>(p, u, mb, nb0, nb1, g);
       else
-        unit_coords<EXT>(p, us, u, mb, nb0, nb1, g);
+        unit_coords<EXT>(p, us, u / parts, mb, nb0, nb1, g);
       const int row = mb * Cfg::TILE_M + row_in_tile;
-      const int store_row0 = mb * Cfg::TILE_M + (int)rank * BM + q * 32;
+      int store_row0 = mb * Cfg::TILE_M + (int)rank * BM + q * 32;
+      if constexpr (EPI == Epi::kStorePart) store_row0 += u % p.k_parts * p.part_rows;
       const bool row_ok = row < p.m_size;
 
       // Per-row state for kLse (natural-log max is m2 / log2(e)).
@@ -938,7 +964,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
             staged_store(stag0 + (nstore++ & 1u) * STAGING_BUF_BYTES, staging, lane, w, &tmOut, c0,
                          store_row0, false);
           }
-        } else {  // kStore
+        } else {  // kStore, kStorePart
 #pragma unroll 1
           for (int sl = 0; sl < BN / 32; ++sl) {
             const int c0 = nb * BN + sl * 32;
