@@ -1267,40 +1267,64 @@ def packed_attention(q, k, v, cu_seqlens, scale: Optional[float] = None, *, err_
     return _PackedAttention.apply(q, k, v, cu_seqlens, scale, err_word)
 
 
+def _aligned(t):
+    """t contiguous from a 16-byte boundary on: itself, or a copy."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _dense_rows(t):
+    """t, or a contiguous copy where its rows are not what the kernels read (a broadcast row,
+    a stride or a start off their alignment)."""
+    row, one = t.stride()
+    return t if one == 1 and row >= t.shape[1] and row % 8 == 0 and t.data_ptr() % 16 == 0 else _aligned(t)
+
+
+def _dense_heads(t):
+    """The same of [tokens, heads, head_dim]."""
+    row, head, one = t.stride()
+    ok = one == 1 and head >= t.shape[2] and row > 0 and row % 8 == 0 and head % 8 == 0 and t.data_ptr() % 16 == 0
+    return t if ok else _aligned(t)
+
+
 class _LayerNorm(torch.autograd.Function):
+    # Shapes are changed in here, not by views around it: x and the residual then get one
+    # gradient tensor, which autograd copies where both are leaves; through views they would
+    # come to share its memory unseen.
     @staticmethod
     def forward(ctx, x, residual, weight, bias, eps, rms):
-        y, s, mean, rstd = flce_layer_norm_forward(x, weight, bias, eps, residual=residual, rms=rms)
+        shape = x.shape
+        rows = _dense_rows(x.reshape(-1, shape[-1]))
+        r = None if residual is None else _dense_rows(residual.reshape(-1, shape[-1]))
+        y, s, mean, rstd = flce_layer_norm_forward(rows, weight, bias, eps, residual=r, rms=rms)
         ctx.save_for_backward(s, weight, mean, rstd)
-        ctx.cfg = (residual is not None, None if bias is None else bias.dtype, rms)
+        ctx.cfg = (shape, residual is not None, None if bias is None else bias.dtype, rms)
         ctx.set_materialize_grads(False)
-        return y if residual is None else (y, s)
+        return y.view(shape) if residual is None else (y.view(shape), s.view(shape))
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy, ds=None):
         s, weight, mean, rstd = ctx.saved_tensors
-        summed, bias_dtype, rms = ctx.cfg
+        shape, summed, bias_dtype, rms = ctx.cfg
         dx = dw = db = None
         if dy is None:  # only the sum was used
             dx = ds
         else:
-            dx, dw, db = flce_layer_norm_backward(dy.contiguous(), s, weight, mean, rstd,
-                                                  dsum=None if ds is None else ds.contiguous(), rms=rms,
+            dx, dw, db = flce_layer_norm_backward(_aligned(dy).view(s.shape), s, weight, mean, rstd,
+                                                  dsum=None if ds is None else _aligned(ds).view(s.shape), rms=rms,
                                                   bias=bias_dtype is not None)
+            dx = dx.view(shape)
         return (dx, dx if summed else None, None if weight is None or dw is None else dw.to(weight.dtype),
                 None if db is None else db.to(bias_dtype), None, None)
 
 
 def layer_norm(x, weight, bias=None, eps: float = 1e-5, *, residual=None, rms: bool = False):
-    """Autograd entry of flce_layer_norm_forward for x [..., cols]: y, or with a residual
-    (y, x + residual)."""
-    shape = x.shape
-    rows = x.reshape(-1, shape[-1])
-    if residual is None:
-        return _LayerNorm.apply(rows, None, weight, bias, eps, rms).view(shape)
-    y, s = _LayerNorm.apply(rows, residual.reshape(-1, shape[-1]), weight, bias, eps, rms)
-    return y.view(shape), s.view(shape)
+    """Autograd entry of flce_layer_norm_forward for x [..., cols]: y, or with a residual of x's
+    shape (y, x + residual)."""
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError(f"residual {tuple(residual.shape)} must have the shape of x {tuple(x.shape)}")
+    return _LayerNorm.apply(x, residual, weight, bias, eps, rms)
 
 
 class _Rope(torch.autograd.Function):
@@ -1318,15 +1342,9 @@ class _Rope(torch.autograd.Function):
                 None, None, None, None)
 
 
-def _dense_heads(g):
-    """g, or a contiguous copy where its strides are not those of heads (a broadcast gradient)."""
-    row, head, one = g.stride()
-    return g if one == 1 and head >= g.shape[2] and row % 8 == 0 and head % 8 == 0 and row > 0 else g.contiguous()
-
-
 def rope(q, k, inv_freq, positions=None, *, magnitude: float = 1.0, interleaved: bool = False):
     """Autograd entry of flce_rope_forward: (q_out, k_out)."""
-    return _Rope.apply(q, k, inv_freq, positions, magnitude, interleaved)
+    return _Rope.apply(_dense_heads(q), _dense_heads(k), inv_freq, positions, magnitude, interleaved)
 
 
 class _LinearDistillation(torch.autograd.Function):
@@ -1358,6 +1376,6 @@ def linear_distillation(h, W, ids, teacher_logits, temperature: float = 1.0, red
     err_word; without one what goes wrong on the device is not seen."""
     H, K = h.shape[-1], ids.shape[-1]
     return _LinearDistillation.apply(
-        h.reshape(-1, H).contiguous(), W.contiguous(), ids.reshape(-1, K).contiguous(),
+        _aligned(h.reshape(-1, H)), _aligned(W), ids.reshape(-1, K).contiguous(),
         teacher_logits.detach().reshape(-1, K).contiguous(), temperature, reduction,
         None if teacher_lse is None else teacher_lse.detach().reshape(-1).contiguous(), err_word)

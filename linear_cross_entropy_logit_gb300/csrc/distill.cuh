@@ -174,24 +174,42 @@ __global__ void __launch_bounds__(kRowsThreads, 4) distill_rows(const __nv_bfloa
   }
 }
 
-// lse of each row from the vocabulary groups' partials (as lse_merge_kernel) and its loss: a
-// block MERGE_ROWS rows.  All orders are fixed.
-__global__ void __launch_bounds__(MERGE_THREADS)
+// lse of each row from the vocabulary groups' partials, and its loss: a block MERGE_ROWS rows,
+// as lse_merge_kernel, but a warp for every 32nd group: with few tokens there are few
+// blocks, and each waits for its reads (64 tokens, 501 groups: 30 -> 10 us).  All orders are
+// fixed.
+constexpr int kMergeWarps = 32;
+__global__ void __launch_bounds__(32 * kMergeWarps)
     distill_merge(const float4* __restrict__ partials, int n_groups, int m_pad, int N,
                   const DistillRow* __restrict__ rows, float* __restrict__ lse_out, float* __restrict__ row_loss,
                   double* __restrict__ block_loss, int* __restrict__ block_valid) {
-  __shared__ float4 s_part[MERGE_SLICES][MERGE_ROWS];
-  const int r = threadIdx.x % MERGE_ROWS, slice = threadIdx.x / MERGE_ROWS;
+  __shared__ float2 part[kMergeWarps][MERGE_ROWS];
+  const int r = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int row = blockIdx.x * MERGE_ROWS + r;
   grid_wait();
-  if (row < N) s_part[slice][r] = merge_slice(partials, n_groups, m_pad, row, slice);
+  float m = -INFINITY, sum = 0.f;
+  if (row < N)
+#pragma unroll 4
+    for (int g = warp; g < n_groups; g += kMergeWarps) {
+      const float4 q = partials[(size_t)g * m_pad + row];
+      const float top = fmaxf(m, q.x);
+      // a group without a column (maximum -infinity) adds nothing
+      sum = sum * (m > -INFINITY ? ex2_approx(m - top) : 0.f) + (q.x > -INFINITY ? q.y * ex2_approx(q.x - top) : 0.f);
+      m = top;
+    }
+  part[warp][r] = make_float2(m, sum);
   __syncthreads();
-  if (slice) return;
+  if (warp) return;
   double loss = 0.0;
   int valid = 0;
   if (row < N) {
-    const float4 t = combine_slices(s_part, r);
-    const float lse = (t.x + log2f(t.y)) * LN2;
+    float top = -INFINITY, total = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMergeWarps; ++k) top = fmaxf(top, part[k][r].x);
+#pragma unroll
+    for (int k = 0; k < kMergeWarps; ++k)
+      if (part[k][r].x > -INFINITY) total += part[k][r].y * ex2_approx(part[k][r].x - top);
+    const float lse = (top + log2f(total)) * LN2;
     lse_out[row] = lse;
     const DistillRow d = rows[row];
     valid = d.valid;
@@ -202,7 +220,7 @@ __global__ void __launch_bounds__(MERGE_THREADS)
     if (row_loss) row_loss[row] = (float)loss;
   }
 #pragma unroll
-  for (int o = MERGE_ROWS / 2; o > 0; o >>= 1) {
+  for (int o = 16; o > 0; o >>= 1) {
     loss += __shfl_xor_sync(~0u, loss, o);
     valid += __shfl_xor_sync(~0u, valid, o);
   }

@@ -890,7 +890,7 @@ flce_status run_forward(const Common& c, const Plan& pl, int dev, int sms, const
     FLCE_TRY((launch_tile<Epi::kLse, false, false>(pair, ext, walk, dev, sms, tmX, tmW, tmX, p,
                                                   c.st, 0)));
     if (c.distill) {
-      FLCE_TRY(host::launch(distill_merge, dim3(pl.merge_blocks), MERGE_THREADS, 0, c.st,
+      FLCE_TRY(host::launch(distill_merge, dim3(pl.merge_blocks), 32 * kMergeWarps, 0, c.st,
                             static_cast<const float4*>(p.partials), pl.n_groups, pl.m_pad, (int)c.N,
                             static_cast<const DistillRow*>(c.distill->rows), lse, c.row_loss, block_loss,
                             block_valid));

@@ -163,7 +163,6 @@ def test_tensors_of_another_gpu_or_the_host_are_refused(B, monkeypatch):  # noqa
     for t, match in ((Elsewhere(), "current device"), (torch.zeros(8, 8), "CUDA tensor")):
         for call in (lambda: B.flce_distill_forward(t, t, t, t), lambda: B.flce_distill_backward(t, t, t, t, t, t, t),
                      lambda: B.flce_layer_norm_forward(t, t), lambda: B.flce_layer_norm_backward(t, t, t, t, t),
-                     lambda: B.flce_rope_forward(t, t, t), lambda: B.flce_rope_backward(t, t, t),
-                     lambda: B.rope(t, t, t)):
+                     lambda: B.flce_rope_forward(t, t, t), lambda: B.flce_rope_backward(t, t, t)):
             with pytest.raises(ValueError, match=match):
                 call()
