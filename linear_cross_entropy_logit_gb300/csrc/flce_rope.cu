@@ -26,7 +26,7 @@ bool stride_ok(int64_t row, int64_t head, int64_t head_dim) {
 
 template <typename T, int P>
 flce_status launch(const flce_rope_desc* d, const RopeParams& p, dim3 grid, int threads, cudaStream_t st) {
-  const size_t smem = (size_t)p.tokens_per_block * p.rot_dim * sizeof(float);
+  const size_t smem = (size_t)threads * kRopeStage<T, P> + (size_t)p.tokens_per_block * p.rot_dim * sizeof(float);
   return d->interleaved ? host::launch(rope_kernel<T, P, true>, grid, threads, smem, st, p)
                         : host::launch(rope_kernel<T, P, false>, grid, threads, smem, st, p);
 }

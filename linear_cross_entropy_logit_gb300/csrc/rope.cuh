@@ -10,9 +10,10 @@
 // half turns, off by 2^-25 at most.
 //
 // About 4 flops a value: bound by HBM.  A block computes the cosines and sines of its
-// tokens once, in shared memory.  A thread holds both halves of P pairs of a head, so
-// that every value is read once, 16 bytes at a time, and turns the same pairs of several
-// heads of one token with angles that stay in its registers.
+// tokens once, in shared memory, while the heads are on their way there: each thread
+// copies what it turns itself.  It has both halves of P pairs of a head, so that every value is
+// read once, 16 bytes at a time, and turns the same pairs of several heads of one token with
+// angles that stay in its registers.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -60,47 +61,38 @@ __device__ __forceinline__ float2 rope_angle(int64_t position, double inv_freq) 
   return make_float2(c + bad, s + bad);
 }
 
-// Where the values of a unit lie in its head, and how they are paired.
-template <typename T, int P, bool PAIRS>
-struct RopeHead {
-  Raw<T, P> r[2];
-  __device__ __forceinline__ void load(const T* in, int a0, int a1) {
-    r[0].load(in + a0);
-    r[1].load(in + a1);
-  }
-  __device__ __forceinline__ void turn_and_store(T* out, int a0, int a1, const uint64_t (&c)[P / 2],
-                                                 const uint64_t (&s)[P / 2], bool turns) const {
-    uint64_t v[P];
+// Turns the values of a unit, in twos: those of its first run, then of its second.
+template <int P, bool PAIRS>
+__device__ __forceinline__ void rope_turn(uint64_t (&v)[P], const uint64_t (&c)[P / 2], const uint64_t (&s)[P / 2]) {
+  if constexpr (PAIRS) {  // (a, b) (c, c) + (b, a) (-s, s)
 #pragma unroll
-    for (int i = 0; i < P; ++i) v[i] = r[i / (P / 2)].pair(i % (P / 2));
-    if (turns) {
-      if constexpr (PAIRS) {  // (a, b) (c, c) + (b, a) (-s, s)
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          float a, b, ci[2], si[2];
-          unpack_f32x2(v[i], a, b);
-          unpack_f32x2(c[i / 2], ci[0], ci[1]);
-          unpack_f32x2(s[i / 2], si[0], si[1]);
-          v[i] = fma_f32x2(pack_f32x2(b, a), pack_f32x2(-si[i & 1], si[i & 1]),
-                           mul_f32x2(v[i], pack_f32x2(ci[i & 1], ci[i & 1])));
-        }
-      } else {  // two pairs at a time
-#pragma unroll
-        for (int i = 0; i < P / 2; ++i) {
-          const uint64_t a = v[i], b = v[i + P / 2], m = mul_f32x2(s[i], pack_f32x2(-1.f, -1.f));
-          v[i] = fma_f32x2(b, m, mul_f32x2(a, c[i]));
-          v[i + P / 2] = fma_f32x2(a, s[i], mul_f32x2(b, c[i]));
-        }
-      }
+    for (int i = 0; i < P; ++i) {
+      float a, b, ci[2], si[2];
+      unpack_f32x2(v[i], a, b);
+      unpack_f32x2(c[i / 2], ci[0], ci[1]);
+      unpack_f32x2(s[i / 2], si[0], si[1]);
+      v[i] = fma_f32x2(pack_f32x2(b, a), pack_f32x2(-si[i & 1], si[i & 1]),
+                       mul_f32x2(v[i], pack_f32x2(ci[i & 1], ci[i & 1])));
     }
-    store_values<T, P>(out + a0, v);
-    store_values<T, P>(out + a1, v + P / 2);
+  } else {  // two pairs at a time
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) {
+      const uint64_t a = v[i], b = v[i + P / 2], m = mul_f32x2(s[i], pack_f32x2(-1.f, -1.f));
+      v[i] = fma_f32x2(b, m, mul_f32x2(a, c[i]));
+      v[i + P / 2] = fma_f32x2(a, s[i], mul_f32x2(b, c[i]));
+    }
   }
-};
+}
+
+// Shared memory of a block: its threads' heads, then the angles.
+template <typename T, int P>
+constexpr int kRopeStage = kRopeHeads<T> * 2 * P * (int)sizeof(T);  // bytes a thread
 
 template <typename T, int P, bool PAIRS>
-__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_constant__ RopeParams p) {
-  extern __shared__ float angles[];  // by token: rot / 2 cosines, rot / 2 sines
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ __align__(16) uint8_t rope_space[];
+  // angles by token: rot / 2 cosines, rot / 2 sines
+  float* angles = reinterpret_cast<float*>(rope_space + blockDim.x * kRopeStage<T, P>);
   const int64_t token0 = (int64_t)blockIdx.x * p.tokens_per_block;
   const int tokens = (int)min((int64_t)p.tokens_per_block, p.tokens - token0), half = p.rot_dim / 2;
   const int group = threadIdx.x / p.units, u = threadIdx.x - group * p.units;
@@ -114,8 +106,26 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_cons
   T* q_out = static_cast<T*>(p.q_out) + token * p.q_heads * p.head_dim;
   T* k_out = static_cast<T*>(p.k_out) + token * p.kv_heads * p.head_dim;
   auto in = [&](int h) { return h < p.q_heads ? q + h * p.q_head : k + (h - p.q_heads) * p.k_head; };
+  constexpr int U = kRopeHeads<T>, kBytes = P * sizeof(T), kCopy = kBytes < 16 ? kBytes : 16;
+  // by head, run, 16 or 8 byte copy and thread
+  auto piece = [&](int i, int run, int copy) {
+    return rope_space + (((i * 2 + run) * (kBytes / kCopy) + copy) * blockDim.x + threadIdx.x) * kCopy;
+  };
+  auto fetch = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (t < tokens && h0 + i * p.slots < heads) {
+        const T* from = in(h0 + i * p.slots);
+#pragma unroll
+        for (int c = 0; c < kBytes / kCopy; ++c) {
+          cp_async<kCopy>(piece(i, 0, c), reinterpret_cast<const uint8_t*>(from + a0) + c * kCopy);
+          cp_async<kCopy>(piece(i, 1, c), reinterpret_cast<const uint8_t*>(from + a1) + c * kCopy);
+        }
+      }
+    cp_async_commit();
+  };
   grid_wait();
-  constexpr int U = kRopeHeads<T>;
+  fetch(slot);
   for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
     const int at = i / half, j = i - at * half;
     const float2 w = rope_angle(p.positions ? p.positions[token0 + at] : token0 + at, p.inv_freq[j]);
@@ -135,17 +145,33 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_cons
     }
   }
   for (int h0 = slot; h0 < heads; h0 += U * p.slots) {
-    RopeHead<T, P, PAIRS> x[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (h0 + i * p.slots < heads) x[i].load(in(h0 + i * p.slots), a0, a1);
+    cp_async_wait<0>();
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int h = h0 + i * p.slots;
-      if (h < heads)
-        x[i].turn_and_store(h < p.q_heads ? q_out + h * p.head_dim : k_out + (h - p.q_heads) * p.head_dim, a0, a1,
-                            c, s, turns);
+      if (h >= heads) break;
+      Raw<T, P> r[2];
+#pragma unroll
+      for (int run = 0; run < 2; ++run)
+#pragma unroll
+        for (int c = 0; c < kBytes / kCopy; ++c) {
+          if constexpr (kCopy == 16) {
+            const uint4 v = *reinterpret_cast<const uint4*>(piece(i, run, c));
+            r[run].w[4 * c] = v.x, r[run].w[4 * c + 1] = v.y, r[run].w[4 * c + 2] = v.z, r[run].w[4 * c + 3] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(piece(i, run, c));
+            r[run].w[0] = v.x, r[run].w[1] = v.y;
+          }
+        }
+      uint64_t v[P];
+#pragma unroll
+      for (int j = 0; j < P; ++j) v[j] = r[j / (P / 2)].pair(j % (P / 2));
+      if (turns) rope_turn<P, PAIRS>(v, c, s);
+      T* out = h < p.q_heads ? q_out + h * p.head_dim : k_out + (h - p.q_heads) * p.head_dim;
+      store_values<T, P>(out + a0, v);
+      store_values<T, P>(out + a1, v + P / 2);
     }
+    if (h0 + U * p.slots < heads) fetch(h0 + U * p.slots);
   }
 }
 
