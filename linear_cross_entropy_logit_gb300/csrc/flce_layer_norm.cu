@@ -96,6 +96,13 @@ flce_status run(Setup& s, Kern kern, const flce_layer_norm_desc* d, int arrays, 
   return host::launch(kern, dim3((unsigned)blocks), split(d).threads, ring_bytes(d, arrays), st, p);
 }
 
+// Rows of a barrier, backward: two where they are floats, which are read from the ring in
+// twice as many loads, and there is room for four (3001 rows of 2304: 43 us, 59 with one); one
+// of bf16, whose registers then leave the compiler more room (8192 rows of 4096: 67.6 us, 73.3
+// with two; forward and backward both).
+template <typename T, int STAGES>
+constexpr int kRows = sizeof(T) == 4 && STAGES == 4 ? 2 : 1;
+
 struct Launch {
   const flce_layer_norm_desc* d;
   const LayerNormParams& p;
@@ -112,8 +119,8 @@ struct Launch {
     }
     const int arrays = p.ds ? 3 : 2;
     const int64_t n = bwd_blocks(d, sms);
-    return p.db_partial ? run(with, layer_norm_bwd<T, C, STAGES, CENTER, true>, d, arrays, n, p, dev, st)
-                        : run(without, layer_norm_bwd<T, C, STAGES, CENTER, false>, d, arrays, n, p, dev, st);
+    return p.db_partial ? run(with, layer_norm_bwd<T, C, STAGES, kRows<T, STAGES>, CENTER, true>, d, arrays, n, p, dev, st)
+                        : run(without, layer_norm_bwd<T, C, STAGES, kRows<T, STAGES>, CENTER, false>, d, arrays, n, p, dev, st);
   }
   template <typename T, int C, int STAGES>
   flce_status pick() const {

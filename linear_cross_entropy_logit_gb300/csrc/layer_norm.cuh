@@ -82,21 +82,26 @@ __device__ __forceinline__ float2 warp_pairs(float a, float b, float2* shared) {
   __syncthreads();
   return lane < warps ? shared[lane] : make_float2(0.f, 0.f);
 }
-// Their sums.  Read by every lane, two warps at a time, and added: shorter than a tree of
-// shuffles, which the forward's weighted sums take (backward of 8192 rows of 4096, bf16:
-// 48 -> 38 us).  `shared` has zeros behind the last warp.
-__device__ __forceinline__ float2 warp_pairs_sum(float a, float b, float2* shared) {
+// Their sums, of ROWS rows.  Every lane reads them, two warps at a time, and adds: shorter than
+// the tree of shuffles that the forward's weighted sums take (backward of 8192 rows of 4096,
+// bf16: 48 -> 43 us).  `shared` has zeros behind an odd last warp.
+template <int ROWS>
+__device__ __forceinline__ void warp_pairs_sum(float2 (&x)[ROWS], float2 (*shared)[kLayerNormWarps]) {
   const int warps = blockDim.x >> 5;
-  if (warps == 1) return make_float2(a, b);
-  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = make_float2(a, b);
+  if (warps == 1) return;
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k)
+    if ((threadIdx.x & 31) == 0) shared[k][threadIdx.x >> 5] = x[k];
   __syncthreads();
-  float2 t = make_float2(0.f, 0.f);
-  for (int i = 0; i < warps; i += 2) {
-    const float4 q = *reinterpret_cast<const float4*>(shared + i);
-    t.x += q.x + q.z;
-    t.y += q.y + q.w;
-  }
-  return t;
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) x[k] = make_float2(0.f, 0.f);
+  for (int i = 0; i < warps; i += 2)
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const float4 q = *reinterpret_cast<const float4*>(&shared[k][i]);
+      x[k].x += q.x + q.z;
+      x[k].y += q.y + q.w;
+    }
 }
 
 // The rows of a persistent block that are on their way, A arrays of each (the last if it is
@@ -138,8 +143,12 @@ struct RowRing {
     cp_async_commit();
     in = in + stage == STAGES * stage ? 0 : in + stage;
   }
-  __device__ __forceinline__ const uint4& at(int a, int c) const { return mine[out + (a * C + c) * blockDim.x]; }
-  __device__ __forceinline__ void next() { out = out + stage == STAGES * stage ? 0 : out + stage; }
+  __device__ __forceinline__ const uint4& at(int a, int c, int row = 0) const {
+    return mine[out + row * stage + (a * C + c) * blockDim.x];
+  }
+  __device__ __forceinline__ void next(int rows = 1) {
+    out = out + rows * stage == STAGES * stage ? 0 : out + rows * stage;
+  }
 };
 
 // A thread's columns of the weight or the bias: held in registers where there are few, else
@@ -268,87 +277,106 @@ __global__ void __maxnreg__(80) layer_norm_fwd(const __grid_constant__ LayerNorm
 
 // Persistent over rows: a thread has the same columns of each, so that the weights'
 // gradients are summed in its registers, in the order of the rows; one partial row per
-// block goes to the workspace.  No atomics: results do not change run to run.  n and g w
-// are held over the row's sums where a thread has few, else made again from the ring.
-template <typename T, int C, int STAGES, bool CENTER, bool BIAS>
+// block goes to the workspace.  No atomics: results do not change run to run.  ROWS rows share
+// a barrier: what one waits for, the other computes.  n and g w are made a second time, from
+// the ring, instead of being held over it.
+template <typename T, int C, int STAGES, int ROWS, bool CENTER, bool BIAS>
 __global__ void __launch_bounds__(kLayerNormThreads) layer_norm_bwd(const __grid_constant__ LayerNormParams p) {
   extern __shared__ uint4 ring_space[];
-  __shared__ __align__(16) float2 shared[2][kLayerNormWarps];
+  __shared__ __align__(16) float2 shared[2][ROWS][kLayerNormWarps];
   constexpr int H = Vec<T>::H;
-  constexpr bool kHeld = Columns<T, C>::kHeld;
+  static_assert(STAGES % ROWS == 0, "the rows of a turn lie together");
   RowRing<C, STAGES, 3> ring(ring_space, p, p.ds != nullptr);
   ring.source(0, p.x, p.x_row / Vec<T>::N);
   ring.source(1, p.dy, p.vectors);
   ring.source(2, p.ds, p.vectors);
   uint64_t dw[C][H] = {}, db[BIAS ? C : 1][H] = {};
-  if (threadIdx.x < 2) shared[threadIdx.x][(blockDim.x >> 5) & (kLayerNormWarps - 1)] = make_float2(0.f, 0.f);
+  if (blockDim.x & 32 && threadIdx.x < 2 * ROWS)  // an odd number of warps: behind the last
+    shared[threadIdx.x & 1][threadIdx.x >> 1][blockDim.x >> 5] = make_float2(0.f, 0.f);
   grid_wait();
+  const int rows = ring.left;
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) ring.fetch();
+  for (int s = 0; s < STAGES - ROWS; ++s) ring.fetch();
   const Columns<T, C> weight(p.w, 1.f, p.vectors);
+  const int64_t step = (int64_t)gridDim.x * p.vectors;
   uint4* out = static_cast<uint4*>(p.out) + (int64_t)blockIdx.x * p.vectors + threadIdx.x;
-  int parity = 0;
-  // of the row after this one, on their way
-  float mean_next = CENTER && blockIdx.x < p.rows ? p.mean[blockIdx.x] : 0.f;
-  float r_next = blockIdx.x < p.rows ? p.rstd[blockIdx.x] : 0.f;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    ring.fetch();
-    const float r = r_next;
-    const uint64_t r2 = pack_f32x2(r, r), m2 = pack_f32x2(-mean_next, -mean_next);
-    if (row + gridDim.x < p.rows) {
-      if (CENTER) mean_next = p.mean[row + gridDim.x];
-      r_next = p.rstd[row + gridDim.x];
-    }
-    cp_async_wait<STAGES - 1>();
-    Vec<T> n[kHeld ? C : 1], gw[kHeld ? C : 1];
-    uint64_t sn = 0, sg = 0;  // sums of g w n, and of g w
-    auto read = [&](int c, Vec<T>& n, Vec<T>& g) {
-      n.unpack(ring.at(0, c));
-      g.unpack(ring.at(1, c));
+  const float *mean = p.mean + blockIdx.x, *rstd = p.rstd + blockIdx.x;
+  float mean_next[ROWS], r_next[ROWS];  // of the rows after these, on their way
+  auto next_stats = [&](int row) {
 #pragma unroll
-      for (int j = 0; j < H; ++j) n.f[j] = mul_f32x2(CENTER ? add_f32x2(n.f[j], m2) : n.f[j], r2);
+    for (int i = 0; i < ROWS; ++i) {
+      const bool in = row + i < rows;
+      mean_next[i] = CENTER && in ? mean[(int64_t)(row + i) * gridDim.x] : 0.f;
+      r_next[i] = in ? rstd[(int64_t)(row + i) * gridDim.x] : 0.f;
+    }
+  };
+  next_stats(0);
+  int parity = 0;
+  for (int row = 0; row < rows; row += ROWS) {
+    uint64_t r2[ROWS], m2[ROWS], sn[ROWS] = {}, sg[ROWS] = {};  // sums of g w n, and of g w
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      ring.fetch();
+      r2[i] = pack_f32x2(r_next[i], r_next[i]);
+      m2[i] = pack_f32x2(-mean_next[i], -mean_next[i]);
+    }
+    next_stats(row + ROWS);
+    cp_async_wait<STAGES - ROWS>();
+    auto read = [&](int i, int c, Vec<T>& n, Vec<T>& g) {
+      n.unpack(ring.at(0, c, i));
+      g.unpack(ring.at(1, c, i));
+#pragma unroll
+      for (int j = 0; j < H; ++j) n.f[j] = mul_f32x2(CENTER ? add_f32x2(n.f[j], m2[i]) : n.f[j], r2[i]);
     };
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if (c * blockDim.x + threadIdx.x >= p.vectors) continue;
-      Vec<T>&nc = n[kHeld ? c : 0], &gc = gw[kHeld ? c : 0];
-      read(c, nc, gc);
-      const Vec<T> w = weight.at(c, p.vectors);
+    for (int i = 0; i < ROWS; ++i) {
+      if (i && row + i >= rows) break;
 #pragma unroll
-      for (int j = 0; j < H; ++j) {
-        dw[c][j] = fma_f32x2(gc.f[j], nc.f[j], dw[c][j]);
-        if (BIAS) db[c][j] = add_f32x2(db[c][j], gc.f[j]);
-        gc.f[j] = mul_f32x2(gc.f[j], w.f[j]);
-        sn = fma_f32x2(gc.f[j], nc.f[j], sn);
-        if (CENTER) sg = add_f32x2(sg, gc.f[j]);
-      }
-    }
-    const float2 w = warp_pairs_sum(lanes(halves(sn)), CENTER ? lanes(halves(sg)) : 0.f, shared[parity]);
-    const float along = -w.x * p.inv_cols, level = -w.y * p.inv_cols;
-    const uint64_t a2 = pack_f32x2(along, along), l2 = pack_f32x2(level, level);
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int i = c * blockDim.x + threadIdx.x;
-      if (i >= p.vectors) continue;
-      Vec<T>&nc = n[kHeld ? c : 0], &gc = gw[kHeld ? c : 0];
-      if constexpr (!kHeld) {
-        read(c, nc, gc);
+      for (int c = 0; c < C; ++c) {
+        if (c * blockDim.x + threadIdx.x >= p.vectors) continue;
+        Vec<T> n, g;
+        read(i, c, n, g);
         const Vec<T> w = weight.at(c, p.vectors);
 #pragma unroll
-        for (int j = 0; j < H; ++j) gc.f[j] = mul_f32x2(gc.f[j], w.f[j]);
+        for (int j = 0; j < H; ++j) {
+          dw[c][j] = fma_f32x2(g.f[j], n.f[j], dw[c][j]);
+          if (BIAS) db[c][j] = add_f32x2(db[c][j], g.f[j]);
+          const uint64_t gw = mul_f32x2(g.f[j], w.f[j]);
+          sn[i] = fma_f32x2(gw, n.f[j], sn[i]);
+          if (CENTER) sg[i] = add_f32x2(sg[i], gw);
+        }
       }
-      Vec<T> d;
-      if (p.ds)
-        d.unpack(ring.at(2, c));
-      else
-        d.fill(0.f);
-#pragma unroll
-      for (int j = 0; j < H; ++j)
-        d.f[j] = fma_f32x2(r2, fma_f32x2(nc.f[j], a2, CENTER ? add_f32x2(gc.f[j], l2) : gc.f[j]), d.f[j]);
-      out[c * blockDim.x] = d.packed();
     }
-    ring.next();
-    out += (int64_t)gridDim.x * p.vectors;
+    float2 sum[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+      sum[i] = make_float2(lanes(halves(sn[i])), CENTER ? lanes(halves(sg[i])) : 0.f);
+    warp_pairs_sum(sum, shared[parity]);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (i && row + i >= rows) break;
+      const float along = -sum[i].x * p.inv_cols, level = -sum[i].y * p.inv_cols;
+      const uint64_t a2 = pack_f32x2(along, along), l2 = pack_f32x2(level, level);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (c * blockDim.x + threadIdx.x >= p.vectors) continue;
+        Vec<T> n, g, d;
+        read(i, c, n, g);
+        const Vec<T> w = weight.at(c, p.vectors);
+        if (p.ds)
+          d.unpack(ring.at(2, c, i));
+        else
+          d.fill(0.f);
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          const uint64_t gw = CENTER ? fma_f32x2(g.f[j], w.f[j], l2) : mul_f32x2(g.f[j], w.f[j]);
+          d.f[j] = fma_f32x2(r2[i], fma_f32x2(n.f[j], a2, gw), d.f[j]);
+        }
+        out[i * step + c * blockDim.x] = d.packed();
+      }
+    }
+    ring.next(ROWS);
+    out += ROWS * step;
     parity ^= 1;
   }
 #pragma unroll
