@@ -273,6 +273,39 @@ def test_gradient_by_differences():
     assert abs(f[0] - f[1] - along) <= 4e-3 * float(dX.double().norm() * (up.double() - down.double()).norm())
 
 
+@pytest.mark.parametrize("grad", [-2.0, 0.0, 1e-30])
+def test_any_upstream_gradient(grad):
+    import torch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    X, W, ids, t = make(150, 64, 700, 6, seed=14)
+    out, (dX, dW), _ = run(B, X, W, ids, t, grad=torch.tensor([grad], device="cuda"))
+    if grad == 0.0:
+        assert not dX.any() and not dW.any()
+    elif grad == 1e-30:  # dX is tiny, not zero: bf16 has fp32's exponents
+        _, (one, _), _ = run(B, X, W, ids, t)
+        assert rel_fro(tensor_f64(dX) / 1e-30, tensor_f64(one)) <= 4e-3
+    else:
+        check(X, W, ids, t, 1.0, None, "mean", out, (dX, dW), grad)
+
+
+def test_calls_on_two_streams_at_once():
+    """Each with its own workspace: the results of calls made alone."""
+    import torch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    inputs = [make(600, 256, 9000, 24, seed=s) for s in (15, 16)]
+    want = [run(B, *a, T=1.2)[:2] for a in inputs]
+    streams = [torch.cuda.Stream() for _ in inputs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for a, s in zip(inputs, streams):
+            with torch.cuda.stream(s):
+                got.append(run(B, *a, T=1.2))
+        torch.cuda.synchronize()
+        for (o, g, err), (wo, wg) in zip(got, want):
+            assert int(err.item()) == 0 and all(torch.equal(a, b) for a, b in zip((*o, *g), (*wo, *wg)))
+
+
 def test_debug_library():
     from linear_cross_entropy_logit_gb300 import binding as B
     X, W, ids, t = make(300, 136, 1500, 21, seed=13)

@@ -122,3 +122,20 @@ def test_what_is_not_finite_stays_in_its_pair():
     same = torch.ones_like(q, dtype=torch.bool)
     same[2, 1, 3] = same[2, 1, 27] = same[4, 0, 50] = False
     assert torch.equal(got[same], want[same]) and got[4, 0, 50] == float("inf") and got[2, 1, 27].isnan()
+
+
+def test_any_frequency():
+    """Negative and large ones turn as the formula says, zero not at all; one that is not
+    finite makes its pairs NaN and no others."""
+    import torch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    q, k = make(7, 2, 1, 16, "fp32", seed=7, fused=False)
+    pos = torch.tensor([0, 1, -3, 50, 999, 12345, -7], device="cuda")
+    f = [-0.25, 30.0, 0.0, 6.5, 1e-9, -12.0, 2.0**-70, 1.0]
+    qo, _ = B.flce_rope_forward(q, k, torch.tensor(f, dtype=torch.float64, device="cuda"), pos)
+    assert near(qo, S.rope(tensor_f64(q), f, pos.tolist()), tensor_f64(q), "fp32")
+    for bad in (float("nan"), float("inf")):
+        f[3] = bad
+        got, _ = B.flce_rope_forward(q, k, torch.tensor(f, dtype=torch.float64, device="cuda"), pos)
+        same = [i for i in range(16) if i % 8 != 3]
+        assert got[..., [3, 11]].isnan().all() and torch.equal(got[..., same], qo[..., same])
