@@ -230,18 +230,61 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   }
 }
 
-// Backward, a warp a row: what the GEMM core needs of it (the mark V of a row that counts, -1
-// of one that does not, and lse - log Q, so that its softmax term is Q p), and dZ at each
-// entry, c / T (Q p - sum of q of the same id), formed in fp32 from the forward's logit and
-// rounded once: the difference of nearly equal p and q keeps its digits.
+// Which rows count, as bits of groups of 64: a block a group, a warp eight rows.
+constexpr int kGroup = 64;
+template <typename T>
+__global__ void __launch_bounds__(256) distill_flags(const __grid_constant__ DistillParams p,
+                                                     unsigned long long* __restrict__ masks) {
+  __shared__ unsigned char bits[kGroup / 8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_wait();
+  unsigned mine = 0;
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = (int64_t)blockIdx.x * kGroup + warp * 8 + i;
+    bool any = false, bad = false;
+    if (row < p.N)
+      for (int k = lane; k < p.K; k += 32) {
+        const int64_t id = p.ids[row * p.K + k];
+        bad |= id >= p.V;
+        any |= entry(id, teacher_logit(p, row * p.K + k, (const T*)nullptr) * p.inv_t);
+      }
+    if (__any_sync(~0u, any) && !__any_sync(~0u, bad)) mine |= 1u << i;
+  }
+  if (lane == 0) bits[warp] = (unsigned char)mine;
+  __syncthreads();
+  if (threadIdx.x) return;
+  unsigned long long m = 0;
+#pragma unroll
+  for (int w = 0; w < kGroup / 8; ++w) m |= (unsigned long long)bits[w] << (8 * w);
+  masks[blockIdx.x] = m;
+}
+
+// Backward, a warp a row.  The rows that count come first, in their order, the others behind
+// them: the GEMMs then walk the former alone (their number is live[0]), and 10% of tokens
+// without entries are 10% less work, wherever they lie.  For a row's place, what the GEMM core
+// needs: its X, the mark V of a row that counts or -1, and lse - log Q, so that its softmax
+// term is Q p; and dZ at each entry, c / T (Q p - sum of q of the same id), formed in fp32
+// from the forward's logit and rounded once: the difference of nearly equal p and q keeps its
+// digits.
 constexpr int kPrepareThreads = 128;
+struct DistillPlaces {
+  const unsigned long long* masks;
+  int* live;      // rows that count
+  int* place;     // N: of each row, or -1 - place of one that does not count
+  uint4* X;       // by place
+  int64_t* marks;
+  float* lse_q;
+  int* ids;       // N x K; -1: no entry
+  uint16_t* dz;
+  float* scale;   // c / T
+};
 template <typename T>
 __global__ void __launch_bounds__(kPrepareThreads)
-    distill_prepare(const __grid_constant__ DistillParams p, const float* __restrict__ lse,
-                    const int* __restrict__ valid_count, const float* __restrict__ grad_loss, int reduction_sum,
-                    float* __restrict__ scale, int64_t* __restrict__ marks, float* __restrict__ lse_q,
-                    int* __restrict__ ids32, uint16_t* __restrict__ dz) {
+    distill_prepare(const __nv_bfloat16* __restrict__ X, const __grid_constant__ DistillParams p,
+                    const float* __restrict__ lse, const int* __restrict__ valid_count,
+                    const float* __restrict__ grad_loss, int reduction_sum, const DistillPlaces out) {
   extern __shared__ int shared[];  // each warp: K ids, K probabilities
+  __shared__ int counts[2][kPrepareThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int* id_of = shared + warp * 2 * p.K;
   float* q_of = reinterpret_cast<float*>(id_of + p.K);
@@ -249,45 +292,82 @@ __global__ void __launch_bounds__(kPrepareThreads)
   const float g = grad_loss ? *grad_loss : 1.f;
   const int nv = reduction_sum ? 1 : *valid_count;
   const float c = nv > 0 ? (float)((double)g * (double)p.inv_t / (double)nv) : 0.f;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *scale = c;
-  const int64_t row = (int64_t)blockIdx.x * (kPrepareThreads / 32) + warp;
+  // rows that count: in the groups before this block's, and in all
+  const int64_t row0 = (int64_t)blockIdx.x * (kPrepareThreads / 32);
+  const int groups = (p.N + kGroup - 1) / kGroup, group = (int)(row0 / kGroup);
+  int before = 0, all = 0;
+  for (int i = threadIdx.x; i < groups; i += kPrepareThreads) {
+    const int n = __popcll(out.masks[i]);
+    all += n;
+    before += i < group ? n : 0;
+  }
+  before = __reduce_add_sync(~0u, before);
+  all = __reduce_add_sync(~0u, all);
+  if (lane == 0) counts[0][warp] = before, counts[1][warp] = all;
+  __syncthreads();
+  before = all = 0;
+#pragma unroll
+  for (int i = 0; i < kPrepareThreads / 32; ++i) before += counts[0][i], all += counts[1][i];
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *out.scale = c;
+    *out.live = all;
+  }
+  const int64_t row = row0 + warp;
   if (row >= p.N) return;
+  const unsigned long long mask = out.masks[group];
+  const int in_group = (int)(row % kGroup);
+  const bool counts_here = mask >> in_group & 1;
+  const int rank = before + __popcll(mask & ((1ull << in_group) - 1));
+  const int64_t place = counts_here ? rank : all + ((int)row - rank);
+  const uint4* from = reinterpret_cast<const uint4*>(X + row * p.H);
+  uint4* to = out.X + place * (p.H / 8);
+#pragma unroll 8
+  for (int i = lane; i < p.H / 8; i += 32) to[i] = from[i];
   const TeacherRow tr = teacher_row<T>(p, row, lane);
   for (int k = lane; k < p.K; k += 32) {
     const int64_t id = p.ids[row * p.K + k];
     const float t = teacher_logit(p, row * p.K + k, (const T*)nullptr) * p.inv_t;
-    const bool in = tr.valid && entry(id, t);
+    const bool in = counts_here && entry(id, t);
     id_of[k] = in ? (int)id : -1;
     q_of[k] = in ? expf(t - tr.tl) : 0.f;
   }
   __syncwarp();
   const float l = lse[row];
   if (lane == 0) {
-    marks[row] = tr.valid ? p.V : -1;
-    lse_q[row] = tr.valid ? l - logf(tr.Q) : 0.f;
+    out.place[row] = counts_here ? (int)place : -1 - (int)place;
+    out.marks[place] = counts_here ? p.V : -1;
+    out.lse_q[place] = counts_here ? l - logf(tr.Q) : 0.f;
   }
   for (int k = lane; k < p.K; k += 32) {
     const int id = id_of[k];
     float same = 0.f;
     for (int j = 0; j < p.K; ++j) same += id_of[j] == id ? q_of[j] : 0.f;
     const float d = fmaf(tr.Q, expf(p.logits[row * p.K + k] * p.inv_t - l), -same);
-    ids32[row * p.K + k] = id;
-    dz[row * p.K + k] = __bfloat16_as_ushort(__float2bfloat16_rn(c * d));
+    out.ids[place * p.K + k] = id;
+    out.dz[place * p.K + k] = __bfloat16_as_ushort(__float2bfloat16_rn(c * d));
   }
 }
 
-// dX of few tokens: the sum of the parts' rows, `pitch` values apart, in their order.
-__global__ void __launch_bounds__(256) distill_dx(const float4* __restrict__ parts, int k_parts, int64_t pitch4,
-                                                  uint2* __restrict__ dX, int64_t n4) {
+// dX of each row from its place in the fp32 sums, of k_parts parts `pitch` values apart, added
+// in their order; zero for a row that does not count.  A block a row.
+__global__ void __launch_bounds__(256) distill_dx(const float4* __restrict__ sums, int k_parts, int64_t pitch4,
+                                                  const int* __restrict__ place, int vectors,
+                                                  uint2* __restrict__ dX) {
   grid_wait();
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
-    float4 t = parts[i];
+  const int at = place[blockIdx.x];
+  const float4* from = sums + (int64_t)at * vectors;
+  uint2* to = dX + (int64_t)blockIdx.x * vectors;
+  for (int i = threadIdx.x; i < vectors; i += 256) {
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (at >= 0) {
+      t = from[i];
 #pragma unroll 4
-    for (int k = 1; k < k_parts; ++k) {
-      const float4 v = parts[k * pitch4 + i];
-      t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+      for (int k = 1; k < k_parts; ++k) {
+        const float4 v = from[k * pitch4 + i];
+        t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+      }
     }
-    dX[i] = make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+    to[i] = make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
   }
 }
 

@@ -687,10 +687,7 @@ struct DistillCall {
   DistillParams p;
   // in the workspace: forward, per row; backward, per row and per entry
   DistillRow* rows;
-  int64_t* marks;
-  float* lse_q;
-  int* ids32;
-  uint16_t* dz;
+  DistillPlaces at;
   bool dw_bf16;
   // dX in parts of the contraction, where its tiles are few: rows of the parts in dx_parts
   int k_parts;
@@ -914,16 +911,18 @@ flce_status run_forward(const Common& c, const Plan& pl, int dev, int sms, const
   return loss_finalize(c, pl, block_loss, block_valid, loss, valid_count);
 }
 
-// Per row of a distillation's backward: marks for the GEMM core, dZ at the entries, and c.
+// What a distillation's backward needs of its rows, those that count first.
 flce_status distill_rows_backward(const Common& c, const float* lse, const int32_t* valid_count,
-                                  const float* grad_loss, float* scale) {
+                                  const float* grad_loss) {
   const DistillCall& d = *c.distill;
+  const bool bf16 = d.desc->teacher_dtype == FLCE_BF16;
+  FLCE_TRY(host::launch(bf16 ? distill_flags<__nv_bfloat16> : distill_flags<float>,
+                        dim3((unsigned)ceil_div(std::max<int64_t>(c.N, 1), kGroup)), 256, 0, c.st, d.p,
+                        const_cast<unsigned long long*>(d.at.masks)));
   const unsigned blocks = (unsigned)ceil_div(std::max<int64_t>(c.N, 1), kPrepareThreads / 32);
-  const size_t smem = (size_t)kPrepareThreads / 32 * 2 * d.p.K * 4;
-  const int sum = c.reduction == FLCE_SUM;
-  return host::launch(d.desc->teacher_dtype == FLCE_BF16 ? distill_prepare<__nv_bfloat16> : distill_prepare<float>,
-                      dim3(blocks), kPrepareThreads, smem, c.st, d.p, lse, valid_count, grad_loss, sum, scale,
-                      d.marks, d.lse_q, d.ids32, d.dz);
+  return host::launch(bf16 ? distill_prepare<__nv_bfloat16> : distill_prepare<float>, dim3(blocks), kPrepareThreads,
+                      (size_t)kPrepareThreads / 32 * 2 * d.p.K * 4, c.st, static_cast<const __nv_bfloat16*>(c.X), d.p,
+                      lse, valid_count, grad_loss, (int)(c.reduction == FLCE_SUM), d.at);
 }
 
 // The entries of a chunk put into its dZ.
@@ -931,8 +930,8 @@ flce_status distill_chunk(const Common& c, int sms, int64_t v0, int64_t w, int64
   const DistillCall& d = *c.distill;
   const int64_t entries = c.N * d.p.K;
   const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(entries, 256), 8 * sms);
-  return host::launch(distill_scatter, dim3(blocks), 256, 0, c.st, static_cast<const int*>(d.ids32),
-                      static_cast<const uint16_t*>(d.dz), entries, d.p.K, (int)v0, (int)w, pitch,
+  return host::launch(distill_scatter, dim3(blocks), 256, 0, c.st, static_cast<const int*>(d.at.ids),
+                      static_cast<const uint16_t*>(d.at.dz), entries, d.p.K, (int)v0, (int)w, pitch,
                       static_cast<uint16_t*>(dz));
 }
 
@@ -944,8 +943,10 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
   float* dW = static_cast<float*>(dW_out);
   const bool dw_bf16 = c.distill && c.distill->dw_bf16;
   if (c.distill) {
-    FLCE_TRY(distill_rows_backward(c, lse, valid_count, grad_loss, scale));
-    lse = c.distill->lse_q;
+    FLCE_TRY(distill_rows_backward(c, lse, valid_count, grad_loss));
+    lse = c.distill->at.lse_q;
+    scale = c.distill->at.scale;
+    Xb = c.distill->at.X;
   } else {
     grad_scale_kernel<<<1, 1, 0, c.st>>>(valid_count, grad_loss, c.reduction == FLCE_SUM, scale);
     ++g_launches;
@@ -1015,7 +1016,10 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
     p3.col_limit = (int)w;
     p3.smoothing = c.smoothing;
     p3.z_loss = c.z_loss;
-    if (c.distill) p3.z_log2e = LOG2E * c.distill->p.inv_t;
+    if (c.distill) {
+      p3.z_log2e = LOG2E * c.distill->p.inv_t;
+      p3.live_m = c.distill->at.live;
+    }
     p3.row_list = sk.list;
     p3.row_count = sk.count;
     p3.list_cap = pl.n_blocks128;
@@ -1179,6 +1183,7 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
       p4.num_units = p4.m_blocks * h_blocks;
       p4.m_fastest = 0;
       p4.reduce_add = accumulate ? 1 : 0;
+      if (c.distill) p4.live_k = c.distill->at.live;
       p4.k_list = sk.list;
       p4.k_count = sk.count;
       p4.k_per_entry = tile_rows(pair) / BK;
@@ -1211,6 +1216,7 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
       p5.num_units = m_blocks_tok * h_blocks;
       p5.m_fastest = 0;
       p5.reduce_add = ci > 0 ? 1 : 0;
+      if (c.distill) p5.live_m = c.distill->at.live;
       p5.row_list = sk.list;
       p5.row_count = sk.count;
       p5.list_cap = pl.n_blocks128;
@@ -1242,12 +1248,11 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
                                                       tmDxAcc, p5, c.st, 3)));
     }
   }
-  if (k_parts > 1) {
-    const int64_t n4 = N * H / 4;
-    return host::launch(distill_dx, dim3((unsigned)std::min<int64_t>(ceil_div(n4, 256), 8 * sms)), 256, 0, c.st,
-                        reinterpret_cast<const float4*>(c.distill->dx_parts), k_parts, (int64_t)pl.m_pad * H / 4,
-                        static_cast<uint2*>(dX), n4);
-  }
+  if (c.distill)
+    return host::launch(distill_dx, dim3((unsigned)N), 256, 0, c.st,
+                        reinterpret_cast<const float4*>(k_parts > 1 ? c.distill->dx_parts : dx_acc), k_parts,
+                        (int64_t)pl.m_pad * H / 4, static_cast<const int*>(c.distill->at.place), (int)(H / 4),
+                        static_cast<uint2*>(dX));
   if (c.dtype == FLCE_BF16 && !c.dx_partial_f32) {
     const size_t n4 = (size_t)N * H / 4;
     dx_finalize_bf16_kernel<<<convert_blocks(n4, sms), CONVERT_THREADS, 0, c.st>>>(
@@ -1741,7 +1746,7 @@ Tuning distill_tuning() {
 // The loss's plan, and behind it the backward's rows and entries.
 struct DistillPlan {
   Plan pl;
-  size_t off_rows, off_marks, off_lse_q, off_ids, off_dz, off_dx_parts, total;
+  size_t off_rows, off_masks, off_live, off_place, off_x, off_marks, off_lse_q, off_ids, off_dz, off_dx_parts, total;
   int k_parts;
 };
 // Parts of dX's contraction: as many as give each CTA pair a unit, of eight k-blocks at least.
@@ -1759,6 +1764,10 @@ bool distill_plan(const flce_distill_desc* d, int mode, DistillPlan* out) {
   };
   region(&out->off_rows, (mode & FLCE_MODE_FWD) ? d->N * sizeof(DistillRow) : 0);
   const size_t n = (mode & FLCE_MODE_BWD) ? (size_t)d->N : 0;
+  region(&out->off_masks, ceil_div(std::max<int64_t>(n, 1), kGroup) * sizeof(unsigned long long));
+  region(&out->off_live, sizeof(int));
+  region(&out->off_place, n * sizeof(int));
+  region(&out->off_x, n * d->H * 2);
   region(&out->off_marks, n * sizeof(int64_t));
   region(&out->off_lse_q, n * sizeof(float));
   region(&out->off_ids, n * d->K * sizeof(int));
@@ -1790,10 +1799,15 @@ flce_status distill_call(const flce_distill_desc* d, int mode, const void* X, co
                     DistillParams{ids, teacher, teacher_lse, logits, (int)d->N, (int)d->K, (int)d->H, (int)d->V,
                                   1.f / d->temperature, err_word},
                     reinterpret_cast<DistillRow*>(base + pl->off_rows),
-                    reinterpret_cast<int64_t*>(base + pl->off_marks),
-                    reinterpret_cast<float*>(base + pl->off_lse_q),
-                    reinterpret_cast<int*>(base + pl->off_ids),
-                    reinterpret_cast<uint16_t*>(base + pl->off_dz),
+                    DistillPlaces{reinterpret_cast<unsigned long long*>(base + pl->off_masks),
+                                  reinterpret_cast<int*>(base + pl->off_live),
+                                  reinterpret_cast<int*>(base + pl->off_place),
+                                  reinterpret_cast<uint4*>(base + pl->off_x),
+                                  reinterpret_cast<int64_t*>(base + pl->off_marks),
+                                  reinterpret_cast<float*>(base + pl->off_lse_q),
+                                  reinterpret_cast<int*>(base + pl->off_ids),
+                                  reinterpret_cast<uint16_t*>(base + pl->off_dz),
+                                  reinterpret_cast<float*>(base + pl->pl.off_scalars)},
                     d->dw_dtype == FLCE_BF16,
                     pl->k_parts,
                     reinterpret_cast<float*>(base + pl->off_dx_parts)};
@@ -1801,7 +1815,7 @@ flce_status distill_call(const flce_distill_desc* d, int mode, const void* X, co
   // (a column that does not exist, so that no target is taken off) and -1 for one that
   // does not.
   const flce_options o = defaults(-1, 0.f, d->reduction);
-  *c = make_common(X, W, (mode & FLCE_MODE_BWD) ? dc->marks : nullptr, d->N, d->H, d->V, FLCE_BF16, &o, ws,
+  *c = make_common(X, W, (mode & FLCE_MODE_BWD) ? dc->at.marks : nullptr, d->N, d->H, d->V, FLCE_BF16, &o, ws,
                    ws_bytes, err_word, stream);
   c->row_loss = row_loss;
   c->vocab_total = d->V + 1;

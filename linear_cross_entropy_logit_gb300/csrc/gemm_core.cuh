@@ -126,6 +126,8 @@ struct GemmParams {
   // units of TILE_M rows).  When k_list is set, the contraction walks only the
   // token blocks it lists (*k_count entries of k_per_entry k-blocks each); a
   // tile with no active k-block is written as zeros.
+  const int* live_m;  // as well without the lists, as a device count of rows, the first of D:
+  const int* live_k;  // units walk no row blocks, the contraction no k-blocks beyond them
   const int* row_list;
   const int* row_count;
   const int* k_list;
@@ -177,8 +179,16 @@ struct UnitSpace {
   int num_units;
 };
 
+// EVEN: row blocks are taken in twos (the host has seen that their full number is even).
+template <bool EXT, int TILE_M, bool EVEN>
 __device__ __forceinline__ UnitSpace unit_space(const GemmParams& p) {
-  if (p.row_list) {
+  if (p.live_m) {
+    int mb = (max(1, *p.live_m) + TILE_M - 1) / TILE_M;
+    if (EVEN) mb += mb & 1;
+    if (!dbg_ok(mb <= p.m_blocks, p.err_word)) mb = p.m_blocks;
+    return {mb, p.num_units / p.m_blocks * mb};
+  }
+  if (EXT && p.row_list) {
     int cnt = *p.row_count;
     if (!dbg_ok(cnt >= 0 && cnt <= p.list_cap, p.err_word)) cnt = 0;
     return {cnt, cnt * p.n_groups};
@@ -234,6 +244,7 @@ __device__ __forceinline__ void unit_coords(const GemmParams& p, const UnitSpace
 
 // Number of k-blocks the contraction walks, and the i-th of them.
 __device__ __forceinline__ int kblock_count(const GemmParams& p, int num_kb) {
+  if (p.live_k) return min(num_kb, (max(1, *p.live_k) + BK - 1) / BK);
   if (!p.k_list) return num_kb;
   int cnt = *p.k_count;
   if (!dbg_ok(cnt >= 0 && cnt <= p.list_cap, p.err_word)) cnt = 0;
@@ -428,12 +439,12 @@ __device__ __forceinline__ void staged_store(uint32_t buf, uint8_t* staging, int
 // the same row block and column groups 2h, 2h+1 (group length 1).  The host
 // only launches QUAD when these pairings cover the grid exactly.
 template <bool SHARE_B>
-__device__ __forceinline__ void unit_coords_quad(const GemmParams& p, int u, int& mb, int& nb0,
+__device__ __forceinline__ void unit_coords_quad(const GemmParams& p, const UnitSpace& us, int u, int& mb, int& nb0,
                                                  int& nb1, int& g) {
   const int i = u & 1;
   const int v = u >> 1;
   if constexpr (SHARE_B) {
-    const int mh = p.m_blocks >> 1;
+    const int mh = us.m_blocks >> 1;
     int mbh;
     if (p.m_fastest) {
       const int band_h = p.m_band >> 1;
@@ -585,8 +596,8 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
   const uint32_t tmem_base = *tmem_slot;
   const WaitCtx ctx{abort_flag, p.err_word, p.timeout_ns};
   const int num_kb_all = (p.k_size + BK - 1) / BK;
-  const int num_kb = EXT ? kblock_count(p, num_kb_all) : num_kb_all;
-  const UnitSpace us = EXT ? unit_space(p) : UnitSpace{p.m_blocks, p.num_units};
+  const int num_kb = EXT || p.live_k ? kblock_count(p, num_kb_all) : num_kb_all;
+  const UnitSpace us = unit_space<EXT, Cfg::TILE_M, QUAD && SHARE_B>(p);
 
   const int parts = EPI == Epi::kStorePart ? p.k_parts : 1;  // units of a tile
 
@@ -605,7 +616,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
       for (int u = pair_id; u < us.num_units && ok; u += num_pairs) {
         int mb, nb0, nb1, g;
         if constexpr (QUAD)
-          unit_coords_quad<SHARE_B>(p, u, mb, nb0, nb1, g);
+          unit_coords_quad<SHARE_B>(p, us, u, mb, nb0, nb1, g);
         else
           unit_coords<EXT>(p, us, u / parts, mb, nb0, nb1, g);
         const KRange kr = k_range<EPI>(p, u, num_kb);
@@ -749,7 +760,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
       for (int u = pair_id; u < us.num_units && ok; u += num_pairs) {
         int mb, nb0, nb1, g;
         if constexpr (QUAD)
-          unit_coords_quad<SHARE_B>(p, u, mb, nb0, nb1, g);
+          unit_coords_quad<SHARE_B>(p, us, u, mb, nb0, nb1, g);
         else
           unit_coords<EXT>(p, us, u / parts, mb, nb0, nb1, g);
         const KRange kr = k_range<EPI>(p, u, num_kb);
@@ -823,7 +834,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
     for (int u = pair_id; u < us.num_units && ok; u += num_pairs) {
       int mb, nb0, nb1, g;
       if constexpr (QUAD)
-        unit_coords_quad<SHARE_B>(p, u, mb, nb0, nb1, g);
+        unit_coords_quad<SHARE_B>(p, us, u, mb, nb0, nb1, g);
       else
         unit_coords<EXT>(p, us, u / parts, mb, nb0, nb1, g);
       const int row = mb * Cfg::TILE_M + row_in_tile;

@@ -129,6 +129,25 @@ def test_several_row_blocks_with_and_without_multicast(multicast):
     check(X, W, ids, t, 1.1, None, "mean", out, grads)
 
 
+@pytest.mark.parametrize("pattern", ["one", "last", "prompts", "half", "most", "three_blocks"])
+@pytest.mark.parametrize("N", [1024, 1100])
+def test_rows_that_do_not_count_lie_anywhere(N, pattern):
+    """One row that counts, the last ones, all but prompts, every second, all but a few; an odd
+    number of row blocks where they are walked in twos."""
+    import torch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    B.flce_set_vocab_chunk(2048)
+    X, W, ids, t = make(N, 128, 6000, 7, seed=N, odd_rows=False)
+    at = torch.arange(N)
+    counts = {"one": at == 777, "last": at >= N - 65, "prompts": at % 300 >= 140, "half": at % 2 == 0,
+              "most": at % 97 != 5, "three_blocks": at % 16 < 11}[pattern]
+    ids[~counts.cuda()] = -1
+    out, (dX, dW), err = run(B, X, W, ids, t, 1.4)
+    assert int(err.item()) == 0 and int(out[3].item()) == int(counts.sum())
+    check(X, W, ids, t, 1.4, None, "mean", out, (dX, dW))
+    assert not dX[~counts.cuda()].any()
+
+
 def test_one_row_of_loss_each():
     import torch
     from linear_cross_entropy_logit_gb300 import binding as B

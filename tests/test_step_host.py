@@ -107,7 +107,7 @@ def test_workspaces(B):  # noqa: F811
     N, V, K = 8192, 128256, 64
     loss = B.flce_workspace_size(N, 4096, V, B.FLCE_BF16, B.MODE_FWD_BWD)
     size = B.flce_distill_workspace_size(N, 4096, V, K)
-    assert loss < size <= loss + N * (K * 6 + 28) + 6 * 256
+    assert loss < size <= loss + N * (K * 6 + 33 + 2 * 4096) + 10 * 256
 
 
 def test_frequencies():
