@@ -1749,11 +1749,14 @@ struct DistillPlan {
   size_t off_rows, off_masks, off_live, off_place, off_x, off_marks, off_lse_q, off_ids, off_dz, off_dx_parts, total;
   int k_parts;
 };
-// Parts of dX's contraction: as many as give each CTA pair a unit, of eight k-blocks at least.
+// Parts of dX's contraction: as many as give each CTA pair a unit, of eight k-blocks at least,
+// and each a part of the first chunk (the later ones, no wider, have no more), which writes
+// what those add to.
 int dx_parts(const Plan& p) {
   const int64_t tiles = ceil_div(std::max<int64_t>(p.N, 1), 2 * BM) * ceil_div(p.H, BN);
-  const int64_t most = std::min<int64_t>({device_pairs() / tiles, ceil_div(std::min(p.chunk, p.V), BK) / 8, 32});
-  return (int)std::max<int64_t>(1, most);
+  const int64_t num_kb = ceil_div(std::min(p.chunk, p.V), BK);
+  const int64_t most = std::min<int64_t>({device_pairs() / tiles, num_kb / 8, 32});
+  return most <= 1 ? 1 : (int)ceil_div(num_kb, ceil_div(num_kb, most));
 }
 bool distill_plan(const flce_distill_desc* d, int mode, DistillPlan* out) {
   if (!distill_ok(d) || !make_plan(d->N, d->H, d->V, FLCE_BF16, mode, distill_tuning(), &out->pl)) return false;
@@ -1788,8 +1791,8 @@ flce_status distill_call(const flce_distill_desc* d, int mode, const void* X, co
   if (!distill_ok(d)) return FLCE_ERR_ARG;
   if (d->dtype != FLCE_BF16) return FLCE_ERR_UNSUPPORTED;
   if (!err_word || !aligned(err_word, 4) || !W || !aligned(W, 16)) return FLCE_ERR_ARG;
-  if (!aligned(X, 16) || !aligned(ids, 8) || !aligned(teacher, d->teacher_dtype == FLCE_BF16 ? 2 : 4) || !aligned(teacher_lse, 4) ||
-      !aligned(logits, 4) || !aligned(row_loss, 4))
+  if (!aligned(X, 16) || !aligned(ids, 8) || !aligned(teacher, d->teacher_dtype == FLCE_BF16 ? 2 : 4) ||
+      !aligned(teacher_lse, 4) || !aligned(logits, 4) || !aligned(row_loss, 4))
     return FLCE_ERR_ARG;
   if (d->N > 0 && (!X || !ids || !teacher || !logits)) return FLCE_ERR_ARG;
   if (!distill_plan(d, mode, pl)) return FLCE_ERR_ARG;

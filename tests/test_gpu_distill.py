@@ -85,9 +85,22 @@ def check(X, W, ids, t, T, tl, reduction, out, grads, grad=1.0):
 
 
 def run(B, X, W, ids, t, T=1.0, reduction="mean", tl=None, grad=None, **kw):
-    *out, err = B.flce_distill_forward(X, W, ids, t, T, reduction, teacher_lse=tl)
+    """Forward and backward, with workspaces and outputs full of NaN."""
+    import torch
+    (N, H), V, K = X.shape, W.shape[0], ids.shape[1]
+
+    def workspace(mode):
+        return torch.full((B.flce_distill_workspace_size(N, H, V, K, mode),), 255, dtype=torch.uint8, device="cuda")
+
+    def junk(*shape, dtype=torch.float32):
+        return torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+
+    *out, err = B.flce_distill_forward(X, W, ids, t, T, reduction, teacher_lse=tl, loss=junk(1), lse=junk(N),
+                                       logits=junk(N, K), workspace_buf=workspace(B.MODE_FWD))
+    kw.setdefault("dW", junk(V, H, dtype=torch.bfloat16))
     dX, dW, _ = B.flce_distill_backward(X, W, ids, t, *out[1:], T, reduction, teacher_lse=tl, grad_loss=grad,
-                                        err_word=err, **kw)
+                                        err_word=err, dX=junk(N, H, dtype=torch.bfloat16),
+                                        workspace_buf=workspace(B.MODE_BWD), **kw)
     return out, (dX, dW), err
 
 
@@ -102,6 +115,10 @@ CASES = [  # N, H, V, K, T, teacher's type, tail, reduction, chunk
     (700, 1024, 3001, 50, 1.0, "fp32", False, "mean", 768),
     (1030, 264, 8000, 64, 1.3, "bf16", False, "mean", 2048),
     (20, 64, 2000, 1024, 1.0, "fp32", False, "mean", 0),
+    # dX in parts of the contraction: 204 and 108 k-blocks, which 25 and 13 parts
+    # would not divide
+    (20, 64, 26200, 4, 1.0, "fp32", False, "mean", 13056),
+    (90, 520, 14000, 4, 1.0, "fp32", False, "mean", 6912),
 ]
 
 
