@@ -37,6 +37,7 @@ def make(R, H, dtype, seed=0, pad=0):
 CASES = [  # rows, columns: one value a lane to several vectors a thread, odd row counts
     (1, 8), (3, 16), (7, 64), (130, 96), (33, 256), (65, 264), (1, 4096), (1000, 520), (9, 2304), (5, 5000),
     (700, 1024), (3, 8192), (2, 16384), (4, 16376), (2500, 128),
+    (20003, 1032),  # many rows for each block that is there at once
 ]
 
 
