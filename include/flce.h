@@ -468,7 +468,8 @@ flce_status flce_attention_backward(const flce_attention_desc* desc, const void*
  *   s = x + residual, rounded to dtype and stored (x itself without a residual),
  *   n = (s - mu) / sqrt(mean((s - mu)^2) + eps), mu = mean(s), or 0 for rms,
  *   y = weight * n + bias
- * No error word: nothing that the inputs hold is an error. */
+ * No error word: nothing that the inputs hold is an error.  Sums are float: a row whose
+ * squares add up beyond 3e38 norms to zeros. */
 typedef struct {
   size_t struct_size;            /* sizeof(flce_layer_norm_desc) */
   int64_t rows;

@@ -99,17 +99,18 @@ struct DistillRow {
 // of two bf16 are exact; the tensor cores' sums are off by up to 4e-6 at H = 4096, these by
 // 1e-7), and the row's part of the loss.  A warp takes four entries at a time, so that eight
 // loads of 512 bytes are in flight; the row of X stays in L1.
-// Bound by the reads of the rows of W, 4.3 GB for 8192 tokens of 64 entries at H = 4096: 563 us
+// Bound by the reads of the rows of W, 4.3 GB for 8192 tokens of 64 entries at H = 4096: 680 us
 // alone.  So it is launched ahead of the forward GEMM, which does not read its results, and
 // lets it start at once: two small blocks a SM find room beside the GEMM's and read
-// while that computes.
+// while that computes (V = 128256, forward and backward: 20.77 -> 20.06 ms).
 constexpr int kRowsThreads = 256, kRowsBlocks = 2;  // blocks of an SM
 template <typename T>
 __global__ void __launch_bounds__(kRowsThreads, 4) distill_rows(const __nv_bfloat16* X, const __nv_bfloat16* W,
                                                              const __grid_constant__ DistillParams p,
-                                                             DistillRow* rows) {
+                                                             DistillRow* rows, unsigned* merged) {
   extern __shared__ float z_of[];  // two rows of K logits
   launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *merged = 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vectors = p.H / 8;
   constexpr int U = 4, kWarps = kRowsThreads / 32;
   int turn = 0;
@@ -176,14 +177,18 @@ __global__ void __launch_bounds__(kRowsThreads, 4) distill_rows(const __nv_bfloa
 
 // lse of each row from the vocabulary groups' partials, and its loss: a block MERGE_ROWS rows,
 // as lse_merge_kernel, but a warp for every 32nd group: with few tokens there are few
-// blocks, and each waits for its reads (64 tokens, 501 groups: 30 -> 10 us).  All orders are
-// fixed.
+// blocks, and each waits for its reads (64 tokens, 501 groups: 30 -> 10 us).  The block that
+// ends last adds the blocks' sums.  All orders are fixed, whichever that is.
 constexpr int kMergeWarps = 32;
 __global__ void __launch_bounds__(32 * kMergeWarps)
     distill_merge(const float4* __restrict__ partials, int n_groups, int m_pad, int N,
                   const DistillRow* __restrict__ rows, float* __restrict__ lse_out, float* __restrict__ row_loss,
-                  double* __restrict__ block_loss, int* __restrict__ block_valid) {
+                  double* block_loss, int* block_valid, unsigned* merged, int reduction_sum,
+                  float* __restrict__ loss_out, int* __restrict__ valid_out) {
   __shared__ float2 part[kMergeWarps][MERGE_ROWS];
+  __shared__ double loss_of[kMergeWarps];
+  __shared__ int valid_of[kMergeWarps];
+  __shared__ bool last;
   const int r = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int row = blockIdx.x * MERGE_ROWS + r;
   grid_wait();
@@ -199,34 +204,60 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     }
   part[warp][r] = make_float2(m, sum);
   __syncthreads();
-  if (warp) return;
   double loss = 0.0;
   int valid = 0;
-  if (row < N) {
-    float top = -INFINITY, total = 0.f;
+  auto warp_total = [&] {
 #pragma unroll
-    for (int k = 0; k < kMergeWarps; ++k) top = fmaxf(top, part[k][r].x);
-#pragma unroll
-    for (int k = 0; k < kMergeWarps; ++k)
-      if (part[k][r].x > -INFINITY) total += part[k][r].y * ex2_approx(part[k][r].x - top);
-    const float lse = (top + log2f(total)) * LN2;
-    lse_out[row] = lse;
-    const DistillRow d = rows[row];
-    valid = d.valid;
-    if (valid) {
-      loss = d.rest;
-      if (!(d.Q == 0.f)) loss += (double)d.Q * (double)(lse - d.tl);
+    for (int o = 16; o > 0; o >>= 1) {
+      loss += __shfl_xor_sync(~0u, loss, o);
+      valid += __shfl_xor_sync(~0u, valid, o);
     }
-    if (row_loss) row_loss[row] = (float)loss;
-  }
+  };
+  if (warp == 0) {
+    if (row < N) {
+      float top = -INFINITY, total = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    loss += __shfl_xor_sync(~0u, loss, o);
-    valid += __shfl_xor_sync(~0u, valid, o);
+      for (int k = 0; k < kMergeWarps; ++k) top = fmaxf(top, part[k][r].x);
+#pragma unroll
+      for (int k = 0; k < kMergeWarps; ++k)
+        if (part[k][r].x > -INFINITY) total += part[k][r].y * ex2_approx(part[k][r].x - top);
+      const float lse = (top + log2f(total)) * LN2;
+      lse_out[row] = lse;
+      const DistillRow d = rows[row];
+      valid = d.valid;
+      if (valid) {
+        loss = d.rest;
+        if (!(d.Q == 0.f)) loss += (double)d.Q * (double)(lse - d.tl);
+      }
+      if (row_loss) row_loss[row] = (float)loss;
+    }
+    warp_total();
+    if (r == 0) {
+      block_loss[blockIdx.x] = loss;
+      block_valid[blockIdx.x] = valid;
+      __threadfence();
+      last = atomicAdd(merged, 1u) == gridDim.x - 1;
+    }
   }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  loss = 0.0;
+  valid = 0;
+  for (int b = threadIdx.x; b < gridDim.x; b += 32 * kMergeWarps) {
+    loss += __ldcg(block_loss + b);
+    valid += __ldcg(block_valid + b);
+  }
+  warp_total();
+  if (r == 0) loss_of[warp] = loss, valid_of[warp] = valid;
+  __syncthreads();
+  if (warp) return;
+  loss = loss_of[r];
+  valid = valid_of[r];
+  warp_total();
   if (r == 0) {
-    block_loss[blockIdx.x] = loss;
-    block_valid[blockIdx.x] = valid;
+    *loss_out = (float)(reduction_sum ? loss : valid > 0 ? loss / (double)valid : 0.0);
+    *valid_out = valid;
   }
 }
 

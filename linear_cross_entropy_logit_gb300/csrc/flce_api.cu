@@ -687,6 +687,7 @@ struct DistillCall {
   DistillParams p;
   // in the workspace: forward, per row; backward, per row and per entry
   DistillRow* rows;
+  unsigned* merged;  // blocks of the merge that have ended
   DistillPlaces at;
   bool dw_bf16;
   // dX in parts of the contraction, where its tiles are few: rows of the parts in dx_parts
@@ -806,16 +807,6 @@ flce_status cast_inputs(const Common& c, const Plan& pl, int sms, const void** X
   return FLCE_OK;
 }
 
-flce_status loss_finalize(const Common& c, const Plan& pl, const double* block_loss, const int* block_valid,
-                          float* loss, int32_t* valid_count) {
-  loss_finalize_kernel<<<1, MERGE_THREADS, 0, c.st>>>(block_loss, block_valid,
-                                                       c.N > 0 ? pl.merge_blocks : 0,
-                                                       c.reduction == FLCE_SUM, loss, valid_count);
-  ++g_launches;
-  FLCE_CUDA(cudaGetLastError());
-  return FLCE_OK;
-}
-
 // The student's logits at a distillation's entries and what the rows' losses take from them.
 template <typename T>
 flce_status launch_rows(const Common& c, int dev, int sms, const void* Xb, const void* Wb) {
@@ -831,7 +822,7 @@ flce_status launch_rows(const Common& c, int dev, int sms, const void* Xb, const
   if (ks.err != cudaSuccess) return cuda_fail(ks.err, "cudaFuncSetAttribute");
   const unsigned blocks = (unsigned)std::min<int64_t>(c.N, kRowsBlocks * sms);
   distill_rows<T><<<blocks, kRowsThreads, 2 * (size_t)d.p.K * sizeof(float), c.st>>>(
-      static_cast<const __nv_bfloat16*>(Xb), static_cast<const __nv_bfloat16*>(Wb), d.p, d.rows);
+      static_cast<const __nv_bfloat16*>(Xb), static_cast<const __nv_bfloat16*>(Wb), d.p, d.rows, d.merged);
   ++g_launches;
   FLCE_CUDA(cudaGetLastError());
   return FLCE_OK;
@@ -890,8 +881,8 @@ flce_status run_forward(const Common& c, const Plan& pl, int dev, int sms, const
       FLCE_TRY(host::launch(distill_merge, dim3(pl.merge_blocks), 32 * kMergeWarps, 0, c.st,
                             static_cast<const float4*>(p.partials), pl.n_groups, pl.m_pad, (int)c.N,
                             static_cast<const DistillRow*>(c.distill->rows), lse, c.row_loss, block_loss,
-                            block_valid));
-      return loss_finalize(c, pl, block_loss, block_valid, loss, valid_count);
+                            block_valid, c.distill->merged, (int)(c.reduction == FLCE_SUM), loss, valid_count));
+      return FLCE_OK;
     }
     if (shard_out) {
       // vocabulary shard: one merged partial per row, no loss yet
@@ -908,7 +899,12 @@ flce_status run_forward(const Common& c, const Plan& pl, int dev, int sms, const
     ++g_launches;
     FLCE_CUDA(cudaGetLastError());
   }
-  return loss_finalize(c, pl, block_loss, block_valid, loss, valid_count);
+  loss_finalize_kernel<<<1, MERGE_THREADS, 0, c.st>>>(block_loss, block_valid,
+                                                       c.N > 0 ? pl.merge_blocks : 0,
+                                                       c.reduction == FLCE_SUM, loss, valid_count);
+  ++g_launches;
+  FLCE_CUDA(cudaGetLastError());
+  return FLCE_OK;
 }
 
 // What a distillation's backward needs of its rows, those that count first.
@@ -1802,6 +1798,7 @@ flce_status distill_call(const flce_distill_desc* d, int mode, const void* X, co
                     DistillParams{ids, teacher, teacher_lse, logits, (int)d->N, (int)d->K, (int)d->H, (int)d->V,
                                   1.f / d->temperature, err_word},
                     reinterpret_cast<DistillRow*>(base + pl->off_rows),
+                    reinterpret_cast<unsigned*>(base + pl->pl.off_scalars),
                     DistillPlaces{reinterpret_cast<unsigned long long*>(base + pl->off_masks),
                                   reinterpret_cast<int*>(base + pl->off_live),
                                   reinterpret_cast<int*>(base + pl->off_place),
