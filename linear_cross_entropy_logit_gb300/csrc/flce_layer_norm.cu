@@ -119,17 +119,24 @@ struct Launch {
   cudaStream_t st;
   bool bwd;
 
-  template <typename T, int C, int STAGES, bool CENTER>
-  flce_status pick() const {
-    static Setup fwd, with, without;
-    if (!bwd) {
-      const int arrays = p.residual ? 2 : 1;
-      return run(fwd, layer_norm_fwd<T, C, STAGES, CENTER>, d, arrays, fwd_blocks(d, p.residual, sms), p, dev, st);
-    }
+  template <typename T, int C, int STAGES, bool CENTER, bool BIAS>
+  flce_status backward() const {
+    static Setup part;
     const int arrays = p.ds ? 3 : 2;
     const int64_t n = bwd_blocks(d, sms);
-    return p.db_partial ? run(with, layer_norm_bwd<T, C, STAGES, kRows<T, STAGES>, CENTER, true>, d, arrays, n, p, dev, st)
-                        : run(without, layer_norm_bwd<T, C, STAGES, kRows<T, STAGES>, CENTER, false>, d, arrays, n, p, dev, st);
+    if constexpr (sizeof(T) == 2) {
+      static Setup full;
+      if (split(d).threads * C == vectors(d))
+        return run(full, layer_norm_bwd<T, C, STAGES, kRows<T, STAGES>, CENTER, BIAS, true>, d, arrays, n, p, dev, st);
+    }
+    return run(part, layer_norm_bwd<T, C, STAGES, kRows<T, STAGES>, CENTER, BIAS, false>, d, arrays, n, p, dev, st);
+  }
+  template <typename T, int C, int STAGES, bool CENTER>
+  flce_status pick() const {
+    static Setup fwd;
+    if (bwd) return p.db_partial ? backward<T, C, STAGES, CENTER, true>() : backward<T, C, STAGES, CENTER, false>();
+    return run(fwd, layer_norm_fwd<T, C, STAGES, CENTER>, d, p.residual ? 2 : 1, fwd_blocks(d, p.residual, sms), p,
+               dev, st);
   }
   template <typename T, int C, int STAGES>
   flce_status pick() const {
