@@ -183,7 +183,9 @@ struct Columns {
 // Persistent over rows, C vectors of a row a thread, STAGES rows in the ring.  Each warp takes
 // its own part's mean m_w and sum of squares s_w around it; the row's are
 //   mean = sum n_w m_w / n,   sum s_w + sum n_w (m_w - mean)^2:
-// one barrier a row, and nothing cancels.
+// one barrier a row, and nothing cancels.  16384 rows of 4096 in bf16, RMS with a residual: 537 MB
+// in 79.4 us, 6760 GB/s; 8192 rows, layer norm: 134 MB in 25.5, 5260, where barriers and issue
+// (54%) of three rows a SM count too.
 template <typename T, int C, int STAGES, bool CENTER>
 __global__ void __maxnreg__(80) layer_norm_fwd(const __grid_constant__ LayerNormParams p) {
   extern __shared__ uint4 ring_space[];
@@ -277,7 +279,9 @@ __global__ void __maxnreg__(80) layer_norm_fwd(const __grid_constant__ LayerNorm
 
 // Persistent over rows: a thread has the same columns of each, so that the weights'
 // gradients are summed in its registers, in the order of the rows; one partial row per
-// block goes to the workspace.  No atomics: results do not change run to run.  ROWS rows share
+// block goes to the workspace.  No atomics: results do not change run to run.  8192 rows of
+// 4096 in bf16: 201 MB, and 10 of partial rows, in 37 us, 5700 GB/s: two rows at once a SM, as
+// many as the sums' registers leave room for.  ROWS rows share
 // a barrier: what one waits for, the other computes.  n and g w are made a second time, from
 // the ring, instead of being held over it.  FULL: the row fills C vectors of every thread, none is
 // asked whether it is there (16384 rows of 4096 in bf16, RMS: 75 -> 69 us; not taken for floats,
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(kLayerNormThreads) layer_norm_bwd(const __grid
 }
 
 // dw, db = sums of the blocks' partial rows: 32 columns a block, 32 rows at a time,
-// added in a fixed order.
+// added in a fixed order.  304 rows of 4096, twice: 10 MB from L2 in 5 us, mostly latency.
 __global__ void __launch_bounds__(1024) layer_norm_dw(const float* dw_partial, const float* db_partial, int rows,
                                                       int cols, float* dw, float* db) {
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
