@@ -366,7 +366,8 @@ flce_status flce_distill_forward(const flce_distill_desc* desc, const void* X, c
                                  int32_t* err_word, void* stream);
 
 /* dX (dtype) and dW (dw_dtype; += when accumulating) from the forward's inputs and its lse,
- * logits and valid_count. */
+ * logits and valid_count.  One of them may be NULL: it is not computed (a frozen unembedding
+ * matrix saves a third of the backward). */
 flce_status flce_distill_backward(const flce_distill_desc* desc, const void* X, const void* W, const int64_t* ids,
                                   const void* teacher, const float* teacher_lse, const float* lse,
                                   const float* logits, const int32_t* valid_count, const float* grad_loss, void* dX,

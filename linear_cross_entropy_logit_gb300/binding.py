@@ -1129,20 +1129,23 @@ def flce_distill_forward(X, W, ids, teacher_logits, temperature: float = 1.0, re
 
 def flce_distill_backward(X, W, ids, teacher_logits, lse, logits, valid_count, temperature: float = 1.0,
                           reduction: str = "mean", *, teacher_lse=None, grad_loss=None, dX=None, dW=None,
-                          accumulate_dW: bool = False, workspace_buf=None, err_word=None, stream=None):
+                          accumulate_dW: bool = False, need_dX: bool = True, need_dW: bool = True,
+                          workspace_buf=None, err_word=None, stream=None):
     """Gradients (dX [N, H] bf16, dW [V, H], err_word) of flce_distill_forward.  dW is bf16, or
-    the caller's float32 tensor, which alone can be accumulated into."""
+    the caller's float32 tensor, which alone can be accumulated into.  A gradient that is not
+    needed is not computed, and None."""
     if stream is not None:
         return _with_stream(stream, flce_distill_backward, X, W, ids, teacher_logits, lse, logits, valid_count,
                             temperature, reduction, teacher_lse=teacher_lse, grad_loss=grad_loss, dX=dX, dW=dW,
-                            accumulate_dW=accumulate_dW, workspace_buf=workspace_buf, err_word=err_word)
+                            accumulate_dW=accumulate_dW, need_dX=need_dX, need_dW=need_dW,
+                            workspace_buf=workspace_buf, err_word=err_word)
     f32 = torch.float32
     dw_dtype = f32 if dW is not None and dW.dtype is f32 else torch.bfloat16
     d, dev, teacher = _distill_args(X, W, ids, teacher_logits, temperature, reduction, teacher_lse, dw_dtype)
     if accumulate_dW and (dW is None or dw_dtype is not f32):
         raise ValueError("accumulate_dW needs an existing float32 dW")
-    dX, p_dx = _output("dX", dX, X, X.shape, torch.bfloat16, dev)
-    dW, p_dw = _output("dW", dW, X, W.shape, dw_dtype, dev)
+    dX, p_dx = _output("dX", dX, X, X.shape, torch.bfloat16, dev) if need_dX else (None, None)
+    dW, p_dw = _output("dW", dW, X, W.shape, dw_dtype, dev) if need_dW else (None, None)
     p_grad = None if grad_loss is None else _array("grad_loss", grad_loss, (1,), f32, dev)
     L = lib()
     need = L.flce_distill_workspace_size(d, MODE_BWD) if workspace_buf is None else 0
@@ -1364,7 +1367,8 @@ class _LinearDistillation(torch.autograd.Function):
         temperature, reduction, err = ctx.cfg
         dX, dW, _ = flce_distill_backward(X, W, ids, teacher_logits, lse, logits, valid, temperature, reduction,
                                           teacher_lse=teacher_lse,
-                                          grad_loss=g.reshape(1).to(torch.float32).contiguous(), err_word=err)
+                                          grad_loss=g.reshape(1).to(torch.float32).contiguous(), err_word=err,
+                                          need_dX=ctx.needs_input_grad[0], need_dW=ctx.needs_input_grad[1])
         return dX, dW, None, None, None, None, None, None
 
 

@@ -951,7 +951,7 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
     FLCE_CUDA(cudaGetLastError());
   }
   if (c.N == 0) {
-    if (!accumulate)
+    if (dW_out && !accumulate)
       FLCE_CUDA(cudaMemsetAsync(dW_out, 0, (size_t)c.V * c.H * (dw_bf16 ? 2 : 4), c.st));
     return FLCE_OK;
   }
@@ -965,6 +965,7 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
   // X as the K-major A operand of the dZ recompute: 128-row boxes (pairs, the
   // merged launches) or 64-row boxes (QUAD walks)
   const int k_parts = c.distill ? c.distill->k_parts : 1;
+  const bool want_dw = dW_out != nullptr, want_dx = dX != nullptr;  // a distillation may leave one out
   CUtensorMap tmX_k, tmX_k64, tmX_mn, tmDxAcc;
   FLCE_TRY(map_kmajor(&tmX_k, Xb, H, N, H, BM));
   FLCE_TRY(map_kmajor(&tmX_k64, Xb, H, N, H, 64));
@@ -1158,7 +1159,9 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
       FLCE_TRY(map_mnmajor(&tmWc_mn, Wc, H, w, H));
       FLCE_TRY(map_dz_store(&tmDzSt, dz, w, N, Cv));
       FLCE_TRY(map_mnmajor(&tmDz_mn, dz, w, N, Cv));
-      if (dw_bf16)
+      if (!want_dw)
+        tmDw = tmDzSt;  // not used
+      else if (dw_bf16)
         FLCE_TRY(map_dz_store(&tmDw, static_cast<uint16_t*>(dW_out) + v0 * H, H, w, H));
       else
         FLCE_TRY(map_f32_out(&tmDw, dW + v0 * H, H, w, H));
@@ -1196,12 +1199,13 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
       p4.err_word = c.err_word;
       p4.timeout_ns = kTimeoutNs;
       const Walk w4 = pick_walk(c.tun, pair, ext, p4);
-      if (dw_bf16)
+      if (want_dw && dw_bf16)
         FLCE_TRY((launch_pair<Epi::kStoreBf16, true, true>(w4, dev, sms, tmDz_mn, tmX_mn, tmDw, p4, c.st, 2)));
-      else
+      else if (want_dw)
         FLCE_TRY((launch_tile<Epi::kStore, true, true>(pair, ext, w4, dev, sms, tmDz_mn, tmX_mn, tmDw, p4, c.st,
                                                        2)));
 
+      if (!want_dx) continue;
       // K5: dX_acc (+)= dZ_chunk W[v0:v0+w, :]   (K = w vocabulary columns)
       GemmParams p5{};
       p5.m_size = (int)N;
@@ -1246,6 +1250,7 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
                                                       tmDxAcc, p5, c.st, 3)));
     }
   }
+  if (!want_dx) return FLCE_OK;
   if (c.distill)
     return host::launch(distill_dx, dim3((unsigned)N), 256, 0, c.st,
                         reinterpret_cast<const float4*>(k_parts > 1 ? c.distill->dx_parts : dx_acc), k_parts,
@@ -1866,9 +1871,9 @@ flce_status flce_distill_backward(const flce_distill_desc* d, const void* X, con
   FLCE_TRY(distill_call(d, FLCE_MODE_BWD, X, W, ids, teacher, teacher_lse, const_cast<float*>(logits), nullptr,
                         workspace, ws_bytes, err_word, stream, &c, &dc, &pl));
   if (!valid_count || !aligned(valid_count, 4) || !aligned(grad_loss, 4) || !aligned(lse, 4)) return FLCE_ERR_ARG;
-  if (!dW || !aligned(dW, 16) || !aligned(dX, 16)) return FLCE_ERR_ARG;
+  if ((!dW && !dX && d->N > 0) || !aligned(dW, 16) || !aligned(dX, 16)) return FLCE_ERR_ARG;
   if (accumulate_dW && d->dw_dtype != FLCE_FP32) return FLCE_ERR_ARG;
-  if (d->N > 0 && (!lse || !dX)) return FLCE_ERR_ARG;
+  if (d->N > 0 && !lse) return FLCE_ERR_ARG;
   int dev, sms;
   FLCE_TRY(host::device(&dev, &sms));
   return run_backward(c, pl.pl, dev, sms, X, W, lse, valid_count, grad_loss, dX, dW, accumulate_dW);

@@ -293,6 +293,27 @@ def test_autograd():
     check(X, W, ids, t, 2.0, None, "mean", out, grads, 4.0)
 
 
+@pytest.mark.parametrize("N,H,V", [(300, 128, 2000), (20, 64, 30000)])
+def test_a_gradient_that_is_not_needed_is_left_out(N, H, V):
+    """Of frozen hidden states or a frozen matrix; the other one has the same bits."""
+    import torch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    X, W, ids, t = make(N, H, V, 8, seed=17)
+    *out, err = B.flce_distill_forward(X, W, ids, t)
+    dX, dW, _ = B.flce_distill_backward(X, W, ids, t, *out[1:])
+    launches = B.last_launch_count()
+    a, none, _ = B.flce_distill_backward(X, W, ids, t, *out[1:], need_dW=False)
+    assert none is None and torch.equal(a, dX) and B.last_launch_count() < launches
+    none, b, _ = B.flce_distill_backward(X, W, ids, t, *out[1:], need_dX=False)
+    assert none is None and torch.equal(b, dW) and B.last_launch_count() < launches
+    h = X.clone().requires_grad_()
+    B.linear_distillation(h, W, ids, t).backward()
+    assert torch.equal(h.grad, dX) and W.grad is None
+    w = W.clone().requires_grad_()
+    B.linear_distillation(X, w, ids, t).backward()
+    assert torch.equal(w.grad, dW)
+
+
 def test_gradient_by_differences():
     """The loss moves along a direction as the gradient says: with bf16 hidden states a step
     of one unit in the last place of every value, 2^-8 of them, of a fp64 loss."""

@@ -46,7 +46,7 @@ def calls(B, kind, d):  # noqa: F811
 
 
 POINTERS = {"distill": (10, 11), "norm": (8, 9), "rope": (6, 6)}
-OPTIONAL = {"distill": ({4, 6}, {4, 8}), "norm": ({1, 2, 3, 5}, {2, 5, 8}), "rope": ({3}, {3})}
+OPTIONAL = {"distill": ({4, 6}, {4, 8, 9, 10}), "norm": ({1, 2, 3, 5}, {2, 5, 8}), "rope": ({3}, {3})}
 MAKE = {"distill": distill, "norm": norm, "rope": rope}
 BAD = [("distill", c) for c in (
     {"struct_size": 8}, {"N": -1}, {"N": 2**31}, {"H": 12}, {"H": 0}, {"V": 0}, {"V": 2**31}, {"K": 0}, {"K": 1025},
@@ -90,6 +90,11 @@ def test_fp32_distillation_and_accumulating_into_bf16_are_refused(B):  # noqa: F
     assert forward([P] * 10) == backward([P] * 11) == B.FLCE_ERR_UNSUPPORTED
     d = ctypes.byref(distill(B))
     assert B.lib().flce_distill_backward(d, *[P] * 11, 1, P, 1 << 40, P, None) == B.FLCE_ERR_ARG
+
+
+def test_a_distillation_without_any_gradient_is_refused(B):  # noqa: F811
+    _, backward = calls(B, "distill", distill(B))
+    assert backward([P] * 9 + [None, None]) == B.FLCE_ERR_ARG
 
 
 def test_workspaces(B):  # noqa: F811
