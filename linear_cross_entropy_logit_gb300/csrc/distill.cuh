@@ -121,14 +121,20 @@ __global__ void __launch_bounds__(kRowsThreads, 4) distill_rows(const __nv_bfloa
       const uint4* w[U];
       bool live[U];
       uint64_t sum[U];
+      int64_t any = -1;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t id = k0 + u < p.K ? p.ids[row * p.K + k0 + u] : -1;
         live[u] = id >= 0 && id < p.V;
+        if (live[u]) any = id;
         w[u] = reinterpret_cast<const uint4*>(W + (live[u] ? id : 0) * p.H);
         sum[u] = 0;
       }
-      // entries that are none read row 0 too: loads without branches between them
+      // loads without branches between them: what is no entry reads another's row (2001 tokens, 6%
+      // without entries and others with few: 213 -> 211 us; all read row 0 before)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (!live[u]) w[u] = reinterpret_cast<const uint4*>(W + any * p.H);
       auto step = [&](int i) {
         const uint4 x = x_row[i];
         uint4 v[U];
@@ -144,8 +150,9 @@ __global__ void __launch_bounds__(kRowsThreads, 4) distill_rows(const __nv_bfloa
                                pack_u32x2(vs[j] << 16, vs[j] & 0xffff0000u), sum[u]);
         }
       };
+      if (any >= 0)
 #pragma unroll 2
-      for (int i = lane; i < vectors; i += 32) step(i);
+        for (int i = lane; i < vectors; i += 32) step(i);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float a, b;

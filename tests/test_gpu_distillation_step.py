@@ -140,6 +140,45 @@ def test_calls_in_a_row_see_each_others_results(T, H, V, K, heads, D):
         assert all(torch.equal(a, b) for a, b in zip(chain(lambda: None), want))
 
 
+def test_a_captured_step_replays():
+    """Forward and gradients through autograd in a CUDA graph, on new inputs in the captured
+    buffers: the bits of the same step made eagerly."""
+    import torch
+    from distillation_step import Block, packed_batch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    torch.manual_seed(2)
+    block = Block(256, 4, 2, 64, 1500)
+    batch, prompt = packed_batch(300, 3, 256)
+    ids = torch.randint(0, 1500, (300, 6), device="cuda")
+    ids[prompt] = -1
+    logits = torch.randn(300, 6, device="cuda")
+    err, weights = B.new_err_word("cuda"), list(block.parameters())
+
+    def step():
+        loss = B.linear_distillation(block(*batch, err), block.vocab, ids, logits, 1.2, err_word=err)
+        return [loss.detach(), *torch.autograd.grad(loss, weights)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for k in range(2):
+        batch[0].mul_(-0.7)
+        logits.add_(torch.randn_like(logits))
+        ids[100 + k] = -1
+        graph.replay()
+        got = [t.clone() for t in out]
+        want = step()
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_second_derivatives_are_refused():
     import torch
     from linear_cross_entropy_logit_gb300 import binding as B

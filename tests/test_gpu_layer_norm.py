@@ -133,6 +133,12 @@ def test_in_place_and_given_outputs():
         g = ds.clone()
         dx2, dw2, _ = B.flce_layer_norm_backward(dy, s, w, mean, rstd, dsum=g, dx=g)
         assert dx2 is g and torch.equal(g, dx) and torch.equal(dw, dw2)
+        g = dy.clone()
+        B.flce_layer_norm_backward(g, s, w, mean, rstd, dsum=ds, dx=g)
+        assert torch.equal(g, dx)
+        acc = x.contiguous().clone()
+        B.flce_layer_norm_forward(acc, w, b, EPS, residual=res, sum_out=acc)
+        assert torch.equal(acc, s)
 
 
 def test_no_rows_and_same_bits():
