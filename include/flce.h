@@ -353,7 +353,8 @@ typedef struct {
 /* Bytes of the workspace of a forward or a backward (FLCE_MODE_FWD, _BWD; _FWD_BWD for one
  * that serves both), with the process-wide vocabulary chunk width; 0 on an invalid desc.  The
  * backward's holds one N x Cv chunk of dZ, Cv at most half of V rounded up to a multiple of
- * 256, and a copy of X in which the tokens that count come first. */
+ * 256 (all of V where that is 32 MB at most), and a copy of X in which the tokens that count
+ * come first. */
 size_t flce_distill_workspace_size(const flce_distill_desc* desc, int mode);
 
 /* ids: int64, N x K; teacher: N x K logits; teacher_lse: float N, or NULL.  Writes the loss,

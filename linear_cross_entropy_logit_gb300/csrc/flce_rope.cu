@@ -67,7 +67,8 @@ flce_status run(const flce_rope_desc* d, const void* q, const void* k, const dou
   // leave SMs idle; the heads of a single token are then shared by as many threads as
   // there are.
   const int groups = kRopeThreads / p.units, heads = p.q_heads + p.kv_heads;
-  const int fit = groups / std::min(groups, (int)host::ceil_div(heads, d->dtype == FLCE_BF16 ? kRopeHeads<__nv_bfloat16> : kRopeHeads<float>));
+  const int in_flight = d->dtype == FLCE_BF16 ? kRopeHeads<__nv_bfloat16> : kRopeHeads<float>;
+  const int fit = groups / std::min(groups, (int)host::ceil_div(heads, in_flight));
   p.tokens_per_block = (int)std::max<int64_t>(1, std::min<int64_t>(fit, d->tokens / (2 * sms)));
   p.slots = std::min(groups / p.tokens_per_block, heads);
   const int threads = p.units * p.slots * p.tokens_per_block;
