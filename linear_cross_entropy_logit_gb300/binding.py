@@ -1054,8 +1054,8 @@ def flce_rope_forward(q, k, inv_freq, positions=None, *, magnitude: float = 1.0,
     """Rotary positions of q [T, Hq, D] and k [T, Hk, D] (views are fine): the first
     2 * len(inv_freq) values of each head turned by positions * inv_freq and multiplied by
     magnitude, in pairs (j, j + rot_dim / 2), or (2j, 2j + 1) when interleaved.  Returns
-    (q_out, k_out), contiguous.  inv_freq: float64, any (see rope_frequencies); positions:
-    int64 [T] or None (0, 1, 2, ...), any."""
+    (q_out, k_out), contiguous.  inv_freq: float64, a multiple of 4 of them, any (see
+    rope_frequencies); positions: int64 [T] or None (0, 1, 2, ...), any."""
     if stream is not None:
         return _with_stream(stream, flce_rope_forward, q, k, inv_freq, positions, magnitude=magnitude,
                             interleaved=interleaved, q_out=q_out, k_out=k_out)
