@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(256) distill_flags(const __grid_constant__ Dis
 // Backward, a warp a row.  The rows that count come first, in their order, the others behind
 // them: the GEMMs then walk the former alone (their number is live[0]), and 10% of tokens
 // without entries are 10% less work, wherever they lie.  For a row's place, what the GEMM core
-// needs: its X, the mark V of a row that counts or -1, and lse - log Q, so that its softmax
+// needs: its X, the mark V of a row with a softmax term or -1, and lse - log Q, so that this
 // term is Q p; and dZ at each entry, c / T (Q p - sum of q of the same id), formed in fp32
 // from the forward's logit and rounded once: the difference of nearly equal p and q keeps its
 // digits.  8192 tokens, H = 4096, 64 entries: 30 us, 134 MB of X in and out and chains of reads.
@@ -371,10 +371,12 @@ __global__ void __launch_bounds__(kPrepareThreads)
   }
   __syncwarp();
   const float l = lse[row];
+  // a row whose entries all have probability 0 counts, but has no softmax term (its log Q is none)
+  const bool weighs = counts_here && !(tr.Q == 0.f);
   if (lane == 0) {
     out.place[row] = counts_here ? (int)place : -1 - (int)place;
-    out.marks[place] = counts_here ? p.V : -1;
-    out.lse_q[place] = counts_here ? l - logf(tr.Q) : 0.f;
+    out.marks[place] = weighs ? p.V : -1;
+    out.lse_q[place] = weighs ? l - logf(tr.Q) : 0.f;
   }
   for (int k = lane; k < p.K; k += 32) {
     const int id = id_of[k];

@@ -1825,9 +1825,9 @@ flce_status distill_call(const flce_distill_desc* d, int mode, const void* X, co
                     d->dw_dtype == FLCE_BF16,
                     pl->k_parts,
                     reinterpret_cast<float*>(base + pl->off_dx_parts)};
-  // The GEMM core's labels: none forward; backward the rows' marks, V for one that counts
-  // (a column that does not exist, so that no target is taken off) and -1 for one that
-  // does not.
+  // The GEMM core's labels: none forward; backward the rows' marks, V for one with a softmax
+  // term (a column that does not exist, so that no target is taken off) and -1 for one
+  // without.
   const flce_options o = defaults(-1, 0.f, d->reduction);
   *c = make_common(X, W, (mode & FLCE_MODE_BWD) ? dc->at.marks : nullptr, d->N, d->H, d->V, FLCE_BF16, &o, ws,
                    ws_bytes, err_word, stream);
