@@ -376,7 +376,9 @@ __global__ void __launch_bounds__(kPrepareThreads)
   if (lane == 0) {
     out.place[row] = counts_here ? (int)place : -1 - (int)place;
     out.marks[place] = weighs ? p.V : -1;
-    out.lse_q[place] = weighs ? l - logf(tr.Q) : 0.f;
+    // without a term, lse itself: its exponentials are taken all the same where the scale is
+    // negative, and have to be finite before they are multiplied by 0
+    out.lse_q[place] = weighs ? l - logf(tr.Q) : l;
   }
   for (int k = lane; k < p.K; k += 32) {
     const int id = id_of[k];

@@ -46,3 +46,22 @@ def test_entries_far_below_the_teachers_sum(where, grad, chunk):
         assert not out[0].any() and int(out[3].item()) == 298 and not grads[0].any() and not grads[1].any()
     else:
         check(X, W, ids, t, T, tl, "mean", out, grads, grad)
+
+
+@pytest.mark.parametrize("pattern", ["end", "between"])
+@pytest.mark.parametrize("grad", [-2.0, 2.0])
+def test_large_logits_of_tokens_that_do_not_count(grad, pattern):
+    """Their z / T pass what an exponential holds, 88; with either sign of the upstream
+    gradient they leave no trace."""
+    import torch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    X, W, ids, t = make(150, 64, 700, 6, seed=22, odd_rows=False)
+    at = torch.arange(150, device="cuda")
+    out_of = at >= 80 if pattern == "end" else at % 15 < 7
+    assert int(out_of.sum()) == 70
+    ids[out_of] = -1
+    T = 0.01
+    assert float((X.float() @ W.float().T / T)[out_of].amax(-1).min()) > 89.0
+    out, (dX, dW), err = run(B, X, W, ids, t, T, grad=torch.tensor([grad], device="cuda"))
+    assert int(err.item()) == 0 and not dX[out_of].any()
+    check(X, W, ids, t, T, None, "mean", out, (dX, dW), grad)
