@@ -332,7 +332,8 @@ flce_status flce_backward_vocab_shard(const void* X, const void* W_shard, const 
  *   l_i  = sum_k q_ik (log q_ik - log p_i,id_ik),  p = softmax(z / T) over all V
  *   loss = sum_i l_i / N_valid (mean) or sum_i l_i (sum)
  *   dZ_ij = c / T (p_ij sum_k q_ik - sum of q_ik with id_ik = j)
- * A negative id, or a logit of -infinity, is no entry; entries of the same id add up.
+ * A negative id, or a logit of -infinity, is no entry; the lowest finite value of the type is
+ * one like any other.  Entries of the same id add up.
  * A token without entries does not count (a prompt's, padding): no loss, zero dX, not in
  * N_valid; nor does one with an id of V or more, which is reported as FLCE_ERR_LABEL.
  * The hidden states of tokens that do not count must be finite all the same (0 times

@@ -4,6 +4,8 @@
 //   q_ik  = exp(t_ik / T - tl_i),  tl_i = log sum_k exp(t_ik / T), or the teacher's own
 //   l_i   = sum_k q_ik (log q_ik - log p_ik)
 //         = sum_k q_ik (t_ik - z_ik) / T + Q_i (lse_i - tl_i),   Q_i = sum_k q_ik
+// (t and tl may both be taken relative to the row's largest t: they are, without the teacher's
+// own tl, so that its logits may lie anywhere and reach to the ends of their type)
 //   dZ_ij = c / T (Q_i exp(z_ij / T - lse_i) - sum of q_ik with id_ik = j)
 //
 // The GEMM core takes lse and the first term of dZ from logits that it never
@@ -38,7 +40,10 @@ __device__ __forceinline__ float teacher_logit(const DistillParams& p, int64_t i
 struct TeacherRow {
   bool valid;  // it has entries, and none outside the vocabulary
   bool error;  // one is
+  float top;   // what t and tl are relative to: the largest t of the entries, or 0
   float tl, Q;
+  // t / T relative to top; -infinity where the difference is more than a float holds
+  __device__ __forceinline__ float scaled(float t, float inv_t) const { return (t - top) * inv_t; }
 };
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -62,7 +67,7 @@ __device__ __forceinline__ TeacherRow teacher_row(const DistillParams& p, int64_
   bool any = false, bad = false, nan = false;
   for (int k = lane; k < p.K; k += 32) {
     const int64_t id = p.ids[row * p.K + k];
-    const float t = teacher_logit(p, row * p.K + k, (const T*)nullptr) * p.inv_t;
+    const float t = teacher_logit(p, row * p.K + k, (const T*)nullptr);
     bad |= id >= p.V;
     if (entry(id, t)) {
       any = true;
@@ -74,23 +79,26 @@ __device__ __forceinline__ TeacherRow teacher_row(const DistillParams& p, int64_
   r.valid = __any_sync(~0u, any) && !r.error;
   nan = __any_sync(~0u, nan);
   m = warp_max(m);
+  r.top = p.teacher_lse ? 0.f : m;
+  r.tl = p.teacher_lse ? p.teacher_lse[row] : 0.f;
   float s = 0.f;
-  // relative to the largest, or to the teacher's own sum
-  if (p.teacher_lse) m = p.teacher_lse[row];
   for (int k = lane; k < p.K; k += 32) {
-    const float t = teacher_logit(p, row * p.K + k, (const T*)nullptr) * p.inv_t;
-    if (entry(p.ids[row * p.K + k], t)) s += expf(t - m);
+    const float t = teacher_logit(p, row * p.K + k, (const T*)nullptr);
+    if (entry(p.ids[row * p.K + k], t)) s += expf(r.scaled(t, p.inv_t) - r.tl);
   }
   s = warp_sum(s);
-  r.tl = p.teacher_lse ? m : m + logf(s);
-  r.Q = p.teacher_lse ? s : 1.f;
+  r.Q = 1.f;
+  if (p.teacher_lse)
+    r.Q = s;
+  else
+    r.tl = logf(s);
   if (nan) r.tl = r.Q = __int_as_float(0x7fc00000);
   return r;
 }
 
 // What a row's loss needs beside lse: l = rest + Q (lse - tl) for a row that counts.
 struct DistillRow {
-  float rest;  // sum of q (t - z) / T
+  float rest;  // sum of q (t - z) / T, t as tl relative to the row's top
   float tl, Q;
   int valid;
 };
@@ -171,10 +179,10 @@ __global__ void __launch_bounds__(kRowsThreads, 4) distill_rows(const __nv_bfloa
     if (tr.error && lane == 0) record_error(p.err_word, kErrLabel);
     float rest = 0.f;
     for (int k = lane; k < p.K; k += 32) {
-      const float t = teacher_logit(p, row * p.K + k, (const T*)nullptr) * p.inv_t;
+      const float t = teacher_logit(p, row * p.K + k, (const T*)nullptr);
       if (tr.valid && entry(p.ids[row * p.K + k], t)) {
-        const float q = expf(t - tr.tl);
-        if (!(q == 0.f)) rest = fmaf(q, t - z[k] * p.inv_t, rest);
+        const float u = tr.scaled(t, p.inv_t), q = expf(u - tr.tl);
+        if (!(q == 0.f)) rest = fmaf(q, u - z[k] * p.inv_t, rest);
       }
     }
     rest = warp_sum(rest);
@@ -284,7 +292,7 @@ __global__ void __launch_bounds__(256) distill_flags(const __grid_constant__ Dis
       for (int k = lane; k < p.K; k += 32) {
         const int64_t id = p.ids[row * p.K + k];
         bad |= id >= p.V;
-        any |= entry(id, teacher_logit(p, row * p.K + k, (const T*)nullptr) * p.inv_t);
+        any |= entry(id, teacher_logit(p, row * p.K + k, (const T*)nullptr));
       }
     if (__any_sync(~0u, any) && !__any_sync(~0u, bad)) mine |= 1u << i;
   }
@@ -364,10 +372,10 @@ __global__ void __launch_bounds__(kPrepareThreads)
   const TeacherRow tr = teacher_row<T>(p, row, lane);
   for (int k = lane; k < p.K; k += 32) {
     const int64_t id = p.ids[row * p.K + k];
-    const float t = teacher_logit(p, row * p.K + k, (const T*)nullptr) * p.inv_t;
+    const float t = teacher_logit(p, row * p.K + k, (const T*)nullptr);
     const bool in = counts_here && entry(id, t);
     id_of[k] = in ? (int)id : -1;
-    q_of[k] = in ? expf(t - tr.tl) : 0.f;
+    q_of[k] = in ? expf(tr.scaled(t, p.inv_t) - tr.tl) : 0.f;
   }
   __syncwarp();
   const float l = lse[row];

@@ -65,9 +65,10 @@ def teacher(ids, t, temperature, V, teacher_lse=None):
     there &= valid[:, None]
     t = np.where(there, t, -np.inf)
     if teacher_lse is None:
-        m = np.where(valid, t.max(-1, initial=-np.inf), 0.0)
+        # relative to the largest, before the sum's logarithm could be lost in it
+        t = t - np.where(valid, t.max(-1, initial=-np.inf), 0.0)[:, None]
         with np.errstate(divide="ignore"):
-            tl = m + np.log(np.exp(t - m[:, None]).sum(-1))
+            tl = np.log(np.exp(t).sum(-1))
         tl = np.where(valid, tl, 0.0)
     else:
         tl = f64(teacher_lse)

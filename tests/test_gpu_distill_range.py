@@ -65,3 +65,46 @@ def test_large_logits_of_tokens_that_do_not_count(grad, pattern):
     out, (dX, dW), err = run(B, X, W, ids, t, T, grad=torch.tensor([grad], device="cuda"))
     assert int(err.item()) == 0 and not dX[out_of].any()
     check(X, W, ids, t, T, None, "mean", out, (dX, dW), grad)
+
+
+def test_a_teachers_logits_may_lie_anywhere():
+    """Probabilities go by differences: logits moved together by a number that moves them
+    exactly give the same bits."""
+    import torch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    X, W, ids, t = make(130, 64, 700, 12, seed=23)
+    t = (t * 8).round() / 8
+    for T in (1.0, 0.7):
+        want = run(B, X, W, ids, t, T)
+        check(X, W, ids, t, T, None, "mean", *want[:2])
+        for by in (2.0**19, -(2.0**19)):
+            moved = t + by
+            assert torch.equal(moved - by, t)
+            got = run(B, X, W, ids, moved, T)
+            for a, b in zip((*want[0], *want[1]), (*got[0], *got[1])):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [0.5, 1.0, 2.0])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_entries_of_the_types_lowest_value(dtype, T):
+    """They are entries, without weight next to any other; a row that has nothing else has them
+    all alike."""
+    import torch
+    from linear_cross_entropy_logit_gb300 import binding as B
+    X, W, ids, t = make(90, 64, 700, 12, dtype, seed=24, odd_rows=False)
+    lowest = torch.finfo(t.dtype).min
+    low, masked = t.clone(), t.clone()
+    low[::3, 4:], masked[::3, 4:] = lowest, -float("inf")
+    low[1::9], masked[1::9] = lowest, 0.0
+    low[2::9, 1:], masked[2::9, 1:] = lowest, -float("inf")  # as far apart as the type goes
+    low[2::9, 0], masked[2::9, 0] = -lowest, 0.0
+    out, grads, err = run(B, X, W, ids, low, T)
+    assert int(err.item()) == 0 and int(out[3].item()) == 90
+    check(X, W, ids, masked, T, None, "mean", out, grads)
+    # against the teacher's own sum they weigh nothing, and the row counts
+    tl = torch.logsumexp(masked.float() / T, -1) + 0.1
+    low[2::9, 0] = 0.0
+    out, grads, _ = run(B, X, W, ids, low, T, tl=tl)
+    assert int(out[3].item()) == 90 and not grads[0][1::9].any()
+    check(X, W, ids, low, T, tl, "mean", out, grads)
