@@ -20,8 +20,9 @@ inline int64_t merge_block_count(int64_t N) {
 
 // One slice of one row's vocabulary-group partials: groups slice,
 // slice + MERGE_SLICES, ... merged online into (max*log2e, sum rescaled to
-// that max, target logit, logit sum).  A group with no column (-inf max)
-// adds nothing to the sum.
+// that max, target logit, logit sum).  A partial that stands for no group (-inf
+// max) adds nothing to the sum; a group without a finite logit has a finite max
+// and the sum 0, or NaN.
 __device__ __forceinline__ float4 merge_slice(const float4* __restrict__ partials, int n_groups,
                                               int m_pad, int row, int slice) {
   float m = -INFINITY, s = 0.f, zy = 0.f, zs = 0.f;

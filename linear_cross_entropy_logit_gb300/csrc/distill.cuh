@@ -212,9 +212,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 #pragma unroll 4
     for (int g = warp; g < n_groups; g += kMergeWarps) {
       const float4 q = partials[(size_t)g * m_pad + row];
-      const float top = fmaxf(m, q.x);
-      // a group without a column (maximum -infinity) adds nothing
-      sum = sum * (m > -INFINITY ? ex2_approx(m - top) : 0.f) + (q.x > -INFINITY ? q.y * ex2_approx(q.x - top) : 0.f);
+      const float top = fmaxf(m, q.x);  // finite: so are the groups' maxima
+      sum = sum * ex2_approx(m - top) + q.y * ex2_approx(q.x - top);
       m = top;
     }
   part[warp][r] = make_float2(m, sum);
@@ -235,7 +234,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       for (int k = 0; k < kMergeWarps; ++k) top = fmaxf(top, part[k][r].x);
 #pragma unroll
       for (int k = 0; k < kMergeWarps; ++k)
-        if (part[k][r].x > -INFINITY) total += part[k][r].y * ex2_approx(part[k][r].x - top);
+        total += part[k][r].y * ex2_approx(part[k][r].x - top);  // a warp without groups has 0 at -infinity
       const float lse = (top + log2f(total)) * LN2;
       lse_out[row] = lse;
       const DistillRow d = rows[row];

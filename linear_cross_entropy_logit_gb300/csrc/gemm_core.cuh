@@ -57,6 +57,7 @@
 //          its own, which are added in a fixed order afterwards.
 // kLse and kDz take exp(z / T) for any temperature T: z_log2e is log2(e) / T.
 #pragma once
+#include <cfloat>
 #include <cstdint>
 #include <cuda.h>
 #include "ptx.cuh"
@@ -842,8 +843,10 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap& tmA, const CUtensor
       if constexpr (EPI == Epi::kStorePart) store_row0 += u % p.k_parts * p.part_rows;
       const bool row_ok = row < p.m_size;
 
-      // Per-row state for kLse (natural-log max is m2 / log2(e)).
-      float m2 = -INFINITY, ssum = 0.f, zy = 0.f, zsum = 0.f;
+      // Per-row state for kLse (natural-log max is m2 / log2(e)).  The maximum starts at a float's
+      // lowest, not at -infinity: logits of -infinity, and columns that do not exist, then add
+      // 0, and a NaN, which no maximum sees, is still NaN in the sum.
+      float m2 = -FLT_MAX, ssum = 0.f, zy = 0.f, zsum = 0.f;
       long long label = 0;
       if constexpr (EPI == Epi::kLse || EPI == Epi::kDz)
         label = row_ok && (EPI == Epi::kDz || p.labels) ? (long long)p.labels[row]
