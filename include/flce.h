@@ -510,7 +510,9 @@ flce_status flce_layer_norm_backward(const flce_layer_norm_desc* desc, const voi
  * the others as they are.  R turns pair j, (j, j + rot_dim/2) or (2j, 2j + 1) when
  * interleaved, by position * inv_freq[j] (device double, rot_dim/2): any frequencies,
  * so also those of a context scaled past the trained length.  The angle is taken modulo
- * one turn in 64-bit integers: any position, a negative one too, is as exact as 0. */
+ * one turn in 64-bit integers, of a frequency held in multiples of 2^-64 of a turn: off by less
+ * than |position| * 2^-64 turns for frequencies up to 4 (half the frequency times that above),
+ * which up to positions of 2^39 is below float's own rounding, 2e-7. */
 typedef struct {
   size_t struct_size;            /* sizeof(flce_rope_desc) */
   int64_t tokens, q_heads, kv_heads;

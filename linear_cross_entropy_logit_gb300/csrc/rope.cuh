@@ -3,11 +3,12 @@
 // R turns pair j by position * inv_freq[j]: pair (j, j + rot/2), or (2j, 2j + 1) when
 // interleaved.  The backward is the same with the negative angle.
 //
-// Angles are taken in turns, as 64-bit fractions of one: position * round(2^64 f),
-// f = inv_freq / 2 pi, wraps around as the angle does.  f has 64 bits itself, so that
-// a position of a million is as exact as one of ten; integers take it from inv_freq's
-// bits, the fp64 pipe is slow here.  Cosine and sine take the angle as a float of
-// half turns, off by 2^-25 at most.
+// Angles are taken in turns, as 64-bit fractions of one: position * (2^64 f), f = inv_freq / 2 pi,
+// wraps around as the angle does.  2^64 f is cut off to an integer (for inv_freq from 4 on, to as
+// many bits of it as 64 bits of f leave), so that the angle is off by less than |position| *
+// 2^-64 * max(1, inv_freq / 2) turns: nothing for a position of a million, 2e-7 radians at 2^39,
+// 2e-4 at 2^49.  Integers take f from inv_freq's bits, the fp64 pipe is slow here.  Cosine and
+// sine take the angle as a float of half turns, off by 2^-25 at most.
 //
 // About 4 flops a value: bound by HBM.  A block computes the cosines and sines of its
 // tokens once, in shared memory, while the heads are on their way there: each thread
@@ -41,7 +42,7 @@ constexpr int kRopeThreads = 256;  // at most: slots x tokens x units of them wo
 template <typename T>
 constexpr int kRopeHeads = sizeof(T) == 2 ? 4 : 2;
 
-// inv_freq / 2 pi in turns, modulo one, as a 64-bit fraction: its 53 bits times
+// inv_freq / 2 pi in turns, modulo one, as a 64-bit fraction, cut off: its 53 bits times
 // 2^66 / 2 pi, shifted by its exponent.
 __device__ __forceinline__ uint64_t rope_step(double inv_freq) {
   const uint64_t bits = (uint64_t)__double_as_longlong(inv_freq);
