@@ -363,7 +363,8 @@ __global__ void __launch_bounds__(kPrepareThreads)
   const int in_group = (int)(row % kGroup);
   const bool counts_here = mask >> in_group & 1;
   const int rank = before + __popcll(mask & ((1ull << in_group) - 1));
-  const int64_t place = counts_here ? rank : all + ((int)row - rank);
+  int64_t place = counts_here ? rank : all + ((int)row - rank);
+  if (!dbg_ok(place >= 0 && place < p.N, p.err_word)) place = 0;
   const uint4* from = reinterpret_cast<const uint4*>(X + row * p.H);
   uint4* to = out.X + place * (p.H / 8);
 #pragma unroll 8

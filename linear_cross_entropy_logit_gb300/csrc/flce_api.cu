@@ -298,15 +298,25 @@ bool make_plan(int64_t N, int64_t H, int64_t V, flce_dtype dtype, int mode, cons
 }
 
 #ifdef FLCE_DEBUG
-// Debug build: the regions a call of `mode` uses lie inside the plan's total,
-// in ascending order, without overlap, and the dZ chunk width is at most half
-// the vocabulary (or the 256-column minimum).
-bool plan_regions_ok(const Plan& p, flce_dtype dtype, int mode) {
-  struct R {
-    size_t off, bytes;
-  };
+// Debug build: regions lie inside [begin, total), in ascending order, without overlap.
+struct Region {
+  size_t off, bytes;
+};
+bool regions_ok(const std::vector<Region>& rs, size_t begin, size_t total) {
+  size_t end = begin;
+  for (const Region& r : rs) {
+    if (r.off < end || r.off % kAlign != 0 || r.off + r.bytes > total) return false;
+    end = r.off + r.bytes;
+  }
+  return true;
+}
+
+// Debug build: the regions a call of `mode` uses, and the dZ chunk width: at most half the
+// vocabulary (or the 256-column minimum), with few_chunks half of it in whole tiles, or
+// all of it where dZ is small.
+bool plan_regions_ok(const Plan& p, flce_dtype dtype, int mode, bool few_chunks = false) {
   const size_t n1 = (size_t)std::max<int64_t>(p.N, 1);
-  std::vector<R> rs;
+  std::vector<Region> rs;
   rs.push_back({p.off_scalars, kAlign});
   rs.push_back({p.off_blocks, (size_t)(2 * p.n_blocks128 + 1) * sizeof(int)});
   if (mode & FLCE_MODE_FWD) {
@@ -326,12 +336,9 @@ bool plan_regions_ok(const Plan& p, flce_dtype dtype, int mode) {
     rs.push_back({p.off_xcast, (size_t)p.N * p.H * 2});
     rs.push_back({p.off_wcast, (size_t)p.V * p.H * 2});
   }
-  size_t end = 0;
-  for (const R& r : rs) {
-    if (r.off < end || r.off % kAlign != 0 || r.off + r.bytes > p.total) return false;
-    end = r.off + r.bytes;
-  }
-  return p.chunk >= 256 && p.chunk % 256 == 0 && p.chunk <= std::max<int64_t>(256, p.V / 2) &&
+  int64_t widest = std::max<int64_t>(256, p.V / 2);
+  if (few_chunks) widest = (int64_t)n1 * p.V * 2 <= kOneChunk ? ceil_div(p.V, 256) * 256 : ceil_div(p.V, 512) * 256;
+  return regions_ok(rs, 0, p.total) && p.chunk >= 256 && p.chunk % 256 == 0 && p.chunk <= widest &&
          p.n_chunks * p.chunk >= p.V && (int64_t)p.m_pad >= p.N;
 }
 #endif
@@ -1240,6 +1247,14 @@ flce_status run_backward(const Common& c, const Plan& pl, int dev, int sms, cons
         p5.k_parts = (int)ceil_div(num_kb, p5.part_kb);
         p5.part_rows = pl.m_pad;
         p5.num_units *= p5.k_parts;
+#ifdef FLCE_DEBUG
+        // each part has k-blocks and rows of its own, those of the first chunk all rows
+        if (p5.k_parts > k_parts || (ci == 0 && p5.k_parts != k_parts) || p5.m_blocks * tile_rows(true) > p5.part_rows ||
+            (p5.k_parts - 1) * p5.part_kb >= num_kb || p5.k_parts * p5.part_kb < num_kb) {
+          g_last_cuda_error = "debug build: parts of a contraction overlap or leave some of it out";
+          return FLCE_ERR_BOUNDS;
+        }
+#endif
         Walk wp;
         wp.overlap = c.tun.overlap;
         FLCE_TRY(map_kmajor(&tmDz_k, dz, w, N, Cv, a_box_rows(wp)));
@@ -1791,6 +1806,25 @@ bool distill_plan(const flce_distill_desc* d, int mode, DistillPlan* out) {
   return true;
 }
 
+#ifdef FLCE_DEBUG
+// Debug build: the loss's regions and the distillation's behind them.
+bool distill_regions_ok(const DistillPlan& p, const flce_distill_desc* d, int mode) {
+  const size_t rows = (mode & FLCE_MODE_FWD) ? (size_t)d->N : 0, n = (mode & FLCE_MODE_BWD) ? (size_t)d->N : 0;
+  return plan_regions_ok(p.pl, FLCE_BF16, mode, true) &&
+         regions_ok({{p.off_rows, rows * sizeof(DistillRow)},
+                     {p.off_masks, (n + kGroup - 1) / kGroup * sizeof(unsigned long long)},
+                     {p.off_live, sizeof(int)},
+                     {p.off_place, n * sizeof(int)},
+                     {p.off_x, n * d->H * 2},
+                     {p.off_marks, n * sizeof(int64_t)},
+                     {p.off_lse_q, n * sizeof(float)},
+                     {p.off_ids, n * d->K * sizeof(int)},
+                     {p.off_dz, n * d->K * sizeof(uint16_t)},
+                     {p.off_dx_parts, p.k_parts > 1 ? (size_t)p.k_parts * p.pl.m_pad * d->H * sizeof(float) : 0}},
+                    p.pl.total, p.total);
+}
+#endif
+
 // Checks what both directions share and fills the call.
 flce_status distill_call(const flce_distill_desc* d, int mode, const void* X, const void* W, const int64_t* ids,
                          const void* teacher, const float* teacher_lse, float* logits, float* row_loss,
@@ -1807,6 +1841,12 @@ flce_status distill_call(const flce_distill_desc* d, int mode, const void* X, co
   if (d->N > 0 && (!X || !ids || !teacher || !logits)) return FLCE_ERR_ARG;
   if (!distill_plan(d, mode, pl)) return FLCE_ERR_ARG;
   if (!ws || !aligned(ws, kAlign) || ws_bytes < pl->total) return FLCE_ERR_WORKSPACE;
+#ifdef FLCE_DEBUG
+  if (!distill_regions_ok(*pl, d, mode)) {
+    g_last_cuda_error = "debug build: workspace plan regions overlap or overrun";
+    return FLCE_ERR_BOUNDS;
+  }
+#endif
   uint8_t* base = static_cast<uint8_t*>(ws);
   *dc = DistillCall{d,
                     DistillParams{ids, teacher, teacher_lse, logits, (int)d->N, (int)d->K, (int)d->H, (int)d->V,
@@ -1844,7 +1884,11 @@ extern "C" {
 
 size_t flce_distill_workspace_size(const flce_distill_desc* d, int mode) {
   DistillPlan pl;
-  return distill_plan(d, mode, &pl) ? pl.total : 0;
+  if (!distill_plan(d, mode, &pl)) return 0;
+#ifdef FLCE_DEBUG
+  if (!distill_regions_ok(pl, d, mode)) return 0;  // no workspace, no call
+#endif
+  return pl.total;
 }
 
 flce_status flce_distill_forward(const flce_distill_desc* d, const void* X, const void* W, const int64_t* ids,
