@@ -1327,7 +1327,8 @@ def layer_norm(x, weight, bias=None, eps: float = 1e-5, *, residual=None, rms: b
     shape (y, x + residual)."""
     if residual is not None and residual.shape != x.shape:
         raise ValueError(f"residual {tuple(residual.shape)} must have the shape of x {tuple(x.shape)}")
-    return _LayerNorm.apply(x, residual, weight, bias, eps, rms)
+    return _LayerNorm.apply(x, residual, None if weight is None else _aligned(weight),
+                            None if bias is None else _aligned(bias), eps, rms)
 
 
 class _Rope(torch.autograd.Function):
