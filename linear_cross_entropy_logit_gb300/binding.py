@@ -1283,8 +1283,10 @@ def _dense_rows(t):
     return t if one == 1 and row >= t.shape[1] and row % 8 == 0 and t.data_ptr() % 16 == 0 else _aligned(t)
 
 
-def _dense_heads(t):
+def _dense_heads(name, t):
     """The same of [tokens, heads, head_dim]."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
     row, head, one = t.stride()
     ok = one == 1 and head >= t.shape[2] and row > 0 and row % 8 == 0 and head % 8 == 0 and t.data_ptr() % 16 == 0
     return t if ok else _aligned(t)
@@ -1342,13 +1344,13 @@ class _Rope(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, gq, gk):
         inv_freq, positions = ctx.saved_tensors
-        return (*flce_rope_backward(_dense_heads(gq), _dense_heads(gk), inv_freq, positions, **ctx.cfg),
+        return (*flce_rope_backward(_dense_heads("dq_out", gq), _dense_heads("dk_out", gk), inv_freq, positions, **ctx.cfg),
                 None, None, None, None)
 
 
 def rope(q, k, inv_freq, positions=None, *, magnitude: float = 1.0, interleaved: bool = False):
     """Autograd entry of flce_rope_forward: (q_out, k_out)."""
-    return _Rope.apply(_dense_heads(q), _dense_heads(k), inv_freq, positions, magnitude, interleaved)
+    return _Rope.apply(_dense_heads("q", q), _dense_heads("k", k), inv_freq, positions, magnitude, interleaved)
 
 
 class _LinearDistillation(torch.autograd.Function):
