@@ -360,8 +360,8 @@ size_t flce_distill_workspace_size(const flce_distill_desc* desc, int mode);
 
 /* ids: int64, N x K; teacher: N x K logits; teacher_lse: float N, or NULL.  Writes the loss,
  * the rows' losses (row_loss, NULL to leave out), lse_i = log sum_j exp(z_ij / T) of every
- * row, the student's logits z at the ids (float, N x K; 0 where there is no entry) and
- * N_valid. */
+ * row, the student's logits z at the ids (float, N x K; 0 where the id is none of the
+ * vocabulary's) and N_valid.  A NaN among a token's logits makes its lse and loss NaN. */
 flce_status flce_distill_forward(const flce_distill_desc* desc, const void* X, const void* W, const int64_t* ids,
                                  const void* teacher, const float* teacher_lse, float* loss, float* row_loss,
                                  float* lse, float* logits, int32_t* valid_count, void* workspace, size_t ws_bytes,

@@ -1344,8 +1344,9 @@ class _Rope(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, gq, gk):
         inv_freq, positions = ctx.saved_tensors
-        return (*flce_rope_backward(_dense_heads("dq_out", gq), _dense_heads("dk_out", gk), inv_freq, positions, **ctx.cfg),
-                None, None, None, None)
+        dq, dk = flce_rope_backward(_dense_heads("dq_out", gq), _dense_heads("dk_out", gk), inv_freq, positions,
+                                    **ctx.cfg)
+        return dq, dk, None, None, None, None
 
 
 def rope(q, k, inv_freq, positions=None, *, magnitude: float = 1.0, interleaved: bool = False):

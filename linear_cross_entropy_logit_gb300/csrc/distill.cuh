@@ -23,7 +23,7 @@ struct DistillParams {
   const int64_t* ids;        // N x K; negative: no entry
   const void* teacher;       // N x K logits
   const float* teacher_lse;  // N, or null
-  float* logits;             // N x K: the student's at the ids, 0 where there is none
+  float* logits;             // N x K: the student's at the ids, 0 where the id is none of V
   int N, K, H, V;
   float inv_t;               // 1 / T
   int* err_word;
