@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 #pragma unroll 4
     for (int g = warp; g < n_groups; g += kMergeWarps) {
       const float4 q = partials[(size_t)g * m_pad + row];
-      const float top = fmaxf(m, q.x);  // finite: so are the groups' maxima
+      const float top = fmaxf(m, q.x);  // above -infinity, as every group's maximum is
       sum = sum * ex2_approx(m - top) + q.y * ex2_approx(q.x - top);
       m = top;
     }
